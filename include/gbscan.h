@@ -58,8 +58,9 @@
 extern "C" {
 #endif
 
-/* Element types. */
-enum gb_dtype { GB_I32 = 0, GB_U32 = 1, GB_I64 = 2, GB_U64 = 3, GB_F32 = 4, GB_F64 = 5 };
+/* Element types.  GB_BF16 and GB_F16 are for the language-model operators at the end of
+ * this file (with GB_F32); the scans, compaction and packing do not take them. */
+enum gb_dtype { GB_I32 = 0, GB_U32 = 1, GB_I64 = 2, GB_U64 = 3, GB_F32 = 4, GB_F64 = 5, GB_BF16 = 6, GB_F16 = 7 };
 
 /* Associative operators ([PS] "Exclusive Prefix Sum": an operator (+) with an
  * identity I; "Other Applications": max for visibility; [AK]: the accumulate API's
@@ -364,6 +365,124 @@ void gb_set_wait_limit_ns(uint64_t ns);
  * run out.  -1 (the default) turns it off.  Process-wide.
  */
 void gb_set_stalled_tile(int64_t tile);
+
+/* ---- Language-model operators ------------------------------------------------------
+ *
+ * The gated linear recurrence (a scan of affine maps over time), layer norm, and log
+ * probabilities of given tokens, each with its gradient.  dtype is GB_F32, GB_BF16 or
+ * GB_F16; all arithmetic, states, statistics and sums are fp32, and each output of a
+ * 16-bit type is rounded once, to nearest even.  Results do not vary from run to run.
+ *
+ * Arrays have unit stride along their last axis and any non-negative strides (in
+ * elements) along the others; element (b, t, c) is at p + b*stride_b + t*stride_t + c.
+ * Pointers are aligned to their element type; rows aligned to 16 bytes are faster.
+ * Outputs must not overlap inputs unless stated, nor their own rows each other.  The
+ * conventions at the top of this file hold otherwise, except that these calls clear no
+ * status words and have no in-kernel waits.  Errors: GB_ERR_INVALID (null or misaligned
+ * pointer, negative size or stride, bad option), GB_ERR_UNSUPPORTED (dtype),
+ * GB_ERR_RANGE (channels, cols or vocab above 2^30, or a grid past 2^31 - 1 blocks),
+ * GB_ERR_TEMP, GB_ERR_CUDA.
+ */
+
+/*
+ * Gated linear recurrence over time of a (batch, length, channels) array:
+ *   a_t = sigmoid(f_t),   u_t = sigmoid(i_t), or 1 - a_t where i is NULL,
+ *   h_t = a_t h_{t-1} + u_t x_t,   h_{-1} = h0, or 0 where h0 is NULL.
+ *   strides   host array (batch, time) of x, f, i, h in this order, or NULL: contiguous
+ *   h0        (batch, channels) fp32, contiguous, or NULL
+ *   starts    (batch, length) bytes, contiguous, or NULL: nonzero marks the first token
+ *             of a document; the state before it is dropped (h_{t-1} counts as 0)
+ *   h         (batch, length, channels)
+ *   last      (batch, channels) fp32, contiguous, or NULL: the state after the last token
+ *             (h0 where length = 0), unrounded
+ */
+int gb_recurrence(int dtype, int64_t batch, int64_t length, int64_t channels, const void* x, const void* f,
+                  const void* i, const int64_t* strides, const float* h0, const uint8_t* starts, void* h,
+                  float* last, void* stream);
+
+/*
+ * Its gradient.  dh is the gradient of h, dlast that of `last` (NULL: 0), h what the
+ * forward call wrote (as stored, so its rounding is the forward's):
+ *   g_t = dh_t + a_{t+1} g_{t+1} (+ dlast at the end),   dx_t = u_t g_t,
+ *   df_t = a_t (1 - a_t) h_{t-1} g_t,   di_t = u_t (1 - u_t) x_t g_t,
+ *   and without i   df_t = a_t (1 - a_t) (h_{t-1} - x_t) g_t.
+ *   strides   host array (batch, time) of dh, x, f, i, h, dx, df, di, or NULL: contiguous
+ *   di        required with i, ignored without
+ *   dh0       (batch, channels) fp32, contiguous, or NULL: the gradient of h0
+ */
+int gb_recurrence_backward(int dtype, int64_t batch, int64_t length, int64_t channels, const void* dh, const void* x,
+                           const void* f, const void* i, const void* h, const int64_t* strides, const float* h0,
+                           const uint8_t* starts, const float* dlast, void* dx, void* df, void* di, float* dh0,
+                           void* stream);
+
+/*
+ * One token for each of `batch` rows: row b moves state s = slots[b] of the pool on,
+ *   state_s = a state_s + u x_b,   h_b = state_s.
+ *   strides   host array (row strides) of x, f, i, h, or NULL: contiguous
+ *   state     (pool, channels) fp32, contiguous, updated in place
+ *   slots     `batch` int32, or NULL: row b uses state b (batch <= pool).  A negative slot
+ *             is padding: h_b = 0 and no state moves.  A slot past the pool is treated so
+ *             too and reported as GB_ERR_RANGE by gb_device_error.  Slots of one call are
+ *             distinct.
+ */
+int gb_recurrence_step(int dtype, int64_t batch, int64_t channels, const void* x, const void* f, const void* i,
+                       const int64_t* strides, float* state, int64_t pool, const int32_t* slots, void* h,
+                       void* stream);
+
+/*
+ * Layer norm of each row:  y = (x - mean) rstd w + b,  rstd = 1 / sqrt(var + eps), var the
+ * mean square deviation.
+ *   w, b          (cols) of param_dtype (dtype or GB_F32), contiguous, or NULL: 1 and 0
+ *   mean, rstd    (rows) fp32, written
+ */
+int gb_layer_norm(int dtype, int param_dtype, int64_t rows, int64_t cols, const void* x, int64_t x_stride,
+                  const void* w, const void* b, float eps, void* y, int64_t y_stride, float* mean, float* rstd,
+                  void* stream);
+
+/*
+ * Its gradient, from the forward call's mean and rstd:  n = (x - mean) rstd, g = dy w,
+ *   dx = rstd (g - mean(g) - n mean(g n)),   dw = sum over rows of dy n,   db = of dy.
+ *   dw, db        (cols) of param_dtype, or NULL: not computed
+ *   temp          scratch of gb_layer_norm_temp_bytes(rows, cols) bytes, 256-byte aligned,
+ *                 or NULL (see the conventions); not used where dw and db are NULL
+ */
+int gb_layer_norm_backward(int dtype, int param_dtype, int64_t rows, int64_t cols, const void* dy, int64_t dy_stride,
+                           const void* x, int64_t x_stride, const float* mean, const float* rstd, const void* w,
+                           void* dx, int64_t dx_stride, void* dw, void* db, void* temp, size_t temp_bytes,
+                           void* stream);
+size_t gb_layer_norm_temp_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Log probabilities of one given token a row of logits, with the row's entropy and its
+ * most likely alternatives:
+ *   lse = log sum_j exp(x_j),   logprob = x_target - lse,   p_j = exp(x_j - lse),
+ *   entropy = -sum_j p_j log p_j.
+ *   targets       (rows) of GB_I32 or GB_I64 (target_dtype).  A negative target is ignored:
+ *                 its logprob is 0.  One past the vocabulary is ignored too, and reported as
+ *                 GB_ERR_RANGE by gb_device_error.
+ *   logprob, entropy, lse   (rows) fp32, written
+ *   top           0 .. 32 (at most vocab): how many alternatives
+ *   top_values    (rows, top) fp32: their log probabilities, in falling order
+ *   top_ids       (rows, top) int32: their indices; ties go to the lower index
+ * A logit of -inf is masked: p_j = 0, and it adds nothing.  Where a row has nothing left,
+ * lse, logprob and top_values are -inf, entropy is 0 and top_ids are 0, 1, ...  A NaN or
+ * +inf logit makes lse, entropy, logprob and top_values NaN (a NaN ranks first).
+ */
+int gb_token_logprobs(int dtype, int64_t rows, int64_t vocab, const void* logits, int64_t stride, const void* targets,
+                      int target_dtype, float* logprob, float* entropy, float* lse, int top, float* top_values,
+                      int32_t* top_ids, void* stream);
+
+/*
+ * Its gradient, from the forward call's lse and entropy:
+ *   dlogits_j = dlogprob ([j = target] - p_j) - dentropy p_j (log p_j + entropy).
+ *   dlogprob, dentropy  (rows) fp32 or NULL: 0 (entropy may be NULL with dentropy)
+ *   dlogits             may be the logits themselves (same stride): overwritten
+ * Rows with an ignored target take no dlogprob; rows with nothing left get zeros.
+ */
+int gb_token_logprobs_backward(int dtype, int64_t rows, int64_t vocab, const void* logits, int64_t stride,
+                               const void* targets, int target_dtype, const float* lse, const float* entropy,
+                               const float* dlogprob, const float* dentropy, void* dlogits, int64_t dstride,
+                               void* stream);
 
 #ifdef __cplusplus
 }

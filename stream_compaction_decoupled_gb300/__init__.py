@@ -1,4 +1,6 @@
-"""Device-wide prefix sums and stream compaction for the GB300 (sm_103a).
+"""Device-wide prefix sums and stream compaction for the GB300 (sm_103a),
+with the language-model operators that are scans, selections and reductions beside them
+(``recurrence``, ``layer_norm``, ``token_logprobs`` and their gradients, in lm.py).
 
 A thin binding over the C ABI of ``libgbscan.so`` (declared in include/gbscan.h):
 every function marshals torch tensors into device pointers, sizes and the current
@@ -18,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgbscan.so")
 
 # Mirrors of the enums in include/gbscan.h.
-I32, U32, I64, U64, F32, F64 = range(6)
+I32, U32, I64, U64, F32, F64, BF16, F16 = range(8)
 ADD, MAX, MIN, MUL, AFFINE = range(5)
 LT, LE, GT, GE, EQ, NE, BIT_CLEAR = range(7)
 KIND_SCAN, KIND_BATCHED_AXIS1, KIND_BATCHED_AXIS0, KIND_COMPACT, KIND_PACK, KIND_REDUCE_THEN_SCAN, \
@@ -31,6 +33,7 @@ _NP_OF = {I32: np.int32, U32: np.uint32, I64: np.int64, U64: np.uint64, F32: np.
 
 # Exported symbols and their ctypes signatures (the whole of include/gbscan.h).
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f = ctypes.c_float
 SIGNATURES = {
     "gb_scan_inclusive": (_i, [_i, _i, _i, _vp, _vp, _i64, _vp, _sz, _vp]),
     "gb_scan_exclusive": (_i, [_i, _i, _i, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
@@ -53,6 +56,15 @@ SIGNATURES = {
     "gb_scan_inclusive_noalloc": (_i, [_i, _i, _vp, _vp, _i64, _vp]),
     "gb_scan_inclusive_host": (_i, [_i, _i, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
     "gb_host_scan_work_bytes": (_sz, [_i, _i64, _i64]),
+    "gb_recurrence": (_i, [_i, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "gb_recurrence_backward": (_i, [_i, _i64, _i64, _i64] + [_vp] * 14),
+    "gb_recurrence_step": (_i, [_i, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "gb_layer_norm": (_i, [_i, _i, _i64, _i64, _vp, _i64, _vp, _vp, _f, _vp, _i64, _vp, _vp, _vp]),
+    "gb_layer_norm_backward": (_i, [_i, _i, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "gb_layer_norm_temp_bytes": (_sz, [_i64, _i64]),
+    "gb_token_logprobs": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
+    "gb_token_logprobs_backward": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
 }
 
 _lib = None
@@ -370,3 +382,18 @@ def scan_segmented(x, flags, op: str = "add", inclusive: bool = True, init=None,
                                     tp, tb, _stream(x, stream)), "gb_scan_segmented")
     del keep
     return out
+
+
+# The language-model operators (lm.py) are looked up on first use: they import torch,
+# which this module itself does not.
+_LM = ("recurrence", "recurrence_backward", "recurrence_step", "layer_norm", "layer_norm_backward",
+       "token_logprobs", "token_logprobs_backward", "TokenLogprobs")
+
+
+def __getattr__(name):
+    if name in _LM:
+        from . import lm
+        for n in _LM:
+            globals()[n] = getattr(lm, n)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -7,6 +7,7 @@
 #include <type_traits>
 #include <vector>
 
+#include "abi.h"
 #include "common.cuh"
 #include "gbscan.h"
 #include "launch.h"
@@ -99,15 +100,7 @@ int make_ctx(void* stream, LaunchCtx& ctx) {
   return GB_OK;
 }
 
-// Caller-supplied scratch, or stream-ordered scratch freed when the call ends.
-struct Temp {
-  void* p = nullptr;
-  bool owned = false;
-  cudaStream_t s = nullptr;
-  ~Temp() {
-    if (owned && p) cudaFreeAsync(p, s);
-  }
-};
+using gbs::Temp;
 
 // The call's own error word lives in its scratch header (cleared by the call's
 // status clear), so gb_last_device_error(temp, ...) reports what this call found.
@@ -372,6 +365,16 @@ int run_comparator(int stf, int dtype, int op, int inclusive, const void* in, vo
 }
 
 }  // namespace
+
+namespace gbs {
+
+int abi_ctx(void* stream, LaunchCtx& ctx) { return make_ctx(stream, ctx); }
+int abi_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+int abi_temp(void* temp, size_t temp_bytes, size_t need, cudaStream_t s, Temp& t) {
+  return get_temp(temp, temp_bytes, need, s, t);
+}
+
+}  // namespace gbs
 
 extern "C" {
 

@@ -1,0 +1,135 @@
+// lm.cuh -- device helpers of the language-model operators (recurrence, layer norm,
+// token log probabilities): 16-byte vectors of fp32 / bf16 / fp16 values widened to
+// fp32, the approximate exponential and reciprocal, asynchronous copies into shared
+// memory, thread-block clusters.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace gbs {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- element types: all arithmetic is in fp32, each output is rounded once ----------
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+template <class T> __device__ __forceinline__ T narrow(float v);
+template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+
+// V consecutive values (V = 1, or 16 bytes' worth) as they lie in memory.
+template <class T, int V> struct Pack {
+  static_assert(V == 1 || V * sizeof(T) == 16, "one value or 16 bytes");
+  alignas(V == 1 ? sizeof(T) : 16) T v[V];
+};
+template <class T, int V> __device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
+  Pack<T, V> r;
+  if constexpr (V == 1) {
+    r.v[0] = *p;
+  } else {
+    const uint4 u = *(const uint4*)p;
+    memcpy(r.v, &u, 16);
+  }
+  return r;
+}
+template <class T, int V> __device__ __forceinline__ void st_pack(T* p, const Pack<T, V>& x) {
+  if constexpr (V == 1) {
+    *p = x.v[0];
+  } else {
+    uint4 u;
+    memcpy(&u, x.v, 16);
+    *(uint4*)p = u;
+  }
+}
+template <class T, int V> __device__ __forceinline__ void widen_pack(const Pack<T, V>& x, float (&f)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; ++k) f[k] = widen(x.v[k]);
+}
+template <class T, int V> __device__ __forceinline__ Pack<T, V> narrow_pack(const float (&f)[V]) {
+  Pack<T, V> r;
+#pragma unroll
+  for (int k = 0; k < V; ++k) r.v[k] = narrow<T>(f[k]);
+  return r;
+}
+
+// ---- approximate functions (PTX instructions, a few units in the last place) ---------
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// min / max that keep a NaN operand (fminf and fmaxf drop it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// ---- asynchronous copies of 16 bytes, tracked by the issuing thread ------------------
+
+// Copies 16 bytes to shared memory, or writes 16 zero bytes there when `live` is false
+// (nothing is read then; src must still be a valid address to form).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- clusters ------------------------------------------------------------------------
+
+// All threads of all CTAs of the cluster: what was written before the barrier, in any of
+// their shared memories, is visible after it.  A hardware barrier over CTAs that the GPU
+// schedules together, not a spin.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The shared-memory address, in CTA `rank` of the cluster, of the variable at `p` here.
+__device__ __forceinline__ unsigned cluster_addr(const void* p, unsigned rank) {
+  unsigned a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float ld_cluster_f32(unsigned addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned ld_cluster_u32(unsigned addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long ld_cluster_u64(unsigned addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+}  // namespace gbs
