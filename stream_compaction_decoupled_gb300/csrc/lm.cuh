@@ -59,6 +59,11 @@ template <class T, int V> __device__ __forceinline__ Pack<T, V> narrow_pack(cons
   return r;
 }
 
+// Two consecutive 16-bit values.
+template <class T> struct Pair {
+  T x, y;
+};
+
 // ---- approximate functions (PTX instructions, a few units in the last place) ---------
 
 __device__ __forceinline__ float ex2(float x) {
@@ -91,6 +96,10 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool live
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
                : "memory");
 }
+// Copies the first `bytes` (1 .. 16) of 16 bytes and writes zeros for the rest.
+__device__ __forceinline__ void cp_async_part(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -115,6 +124,10 @@ __device__ __forceinline__ unsigned cluster_addr(const void* p, unsigned rank) {
   unsigned a;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
+}
+__device__ __forceinline__ void st_cluster_f4(unsigned addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ float ld_cluster_f32(unsigned addr) {
   float v;

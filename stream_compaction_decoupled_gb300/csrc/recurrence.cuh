@@ -3,17 +3,22 @@
 // its gradient, and its form for one token a call.
 //
 // Step t is the affine map y -> a_t y + b_t (b = u x), and maps compose associatively:
-// (A1, B1) then (A2, B2) is (A1 A2, A2 B1 + B2).  A CTA owns W channels of one batch
-// row for all of time and takes it tile by tile; the threads of a tile split its rows,
-// each composes its own R rows, the threads' maps are composed across the warp and the
-// CTA, and each thread then replays its rows from the state it starts from.  Every input
-// is read once and every output written once, and the composition order is fixed, so a
-// call's results do not vary from run to run.
+// (A1, B1) then (A2, B2) is (A1 A2, A2 B1 + B2).  A CTA owns 64 channels of one batch row
+// for all of time and takes them tile by tile.  The 8 warps of a tile split its rows, a
+// lane holds 2 channels: each thread composes the maps of its R rows, the warps' maps meet
+// in shared memory, and each thread replays its rows from the state they start from.  Every
+// input is read once and every output written once, and the composition order is fixed, so
+// results do not vary from run to run.
 //
-// Where B*D/W CTAs would leave SMs idle, a cluster of C CTAs shares the strip: its CTAs
-// take C consecutive tiles at a time and exchange their tiles' maps through distributed
-// shared memory, one cluster barrier per round.  No CTA waits on another outside that
-// hardware barrier, and no global scratch is needed.
+// Tiles reach shared memory by asynchronous copies of 16 bytes, STAGES - 1 tiles ahead of
+// the one in hand.  Rows may start anywhere: where they are not all on 16-byte boundaries
+// (EDGE) the copies start at the boundary below each row's first channel and each lane
+// picks its channels out at the row's offset; a copy never reads outside its row.
+//
+// Where B*D/64 CTAs would leave SMs idle, a cluster of C CTAs shares the strip: its CTAs
+// take C consecutive tiles at a time and send each other their tiles' maps through
+// distributed shared memory, one cluster barrier per round.  No CTA waits on another
+// outside that hardware barrier, and no global scratch is needed.
 //
 // The gradient runs the same scan backwards in time.  With g_t = dL/dh_t (all paths) and
 // c_t = a_t g_t,   g_t = dh_t + c_{t+1}   and   c_t = a_t c_{t+1} + a_t dh_t,
@@ -49,389 +54,355 @@ template <class T> struct RecArgs {
   int D, strips;  // strips of W channels per batch row
 };
 
-// Geometry.  V channels a thread (16 bytes, or 1 where rows are not 16-byte aligned),
-// LANES threads of a warp side by side along the channels, the other lanes and the warps
-// along time, R consecutive rows a thread.
-template <int V_, int LANES_, int R_, int STAGES_> struct RecGeom {
-  static constexpr int V = V_, LANES = LANES_, R = R_, STAGES = STAGES_;
-  static constexpr int NT = 256, WARPS = NT / 32;
-  static constexpr int W = V * LANES;
-  static constexpr int GROUPS = 32 / LANES;
-  static constexpr int L = WARPS * GROUPS * R;  // rows of a tile
-};
+// sigmoid(z) alone: 1 / (1 + exp(-z)); exp(-z) may overflow to infinity, which gives 0.
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+
 constexpr int kRecMaxCluster = 8;
 
-template <class G> struct RecShared {
-  float a[G::WARPS][G::W], b[G::WARPS][G::W];  // the map of each warp's rows
-  float from[G::WARPS][G::W];                  // the state each warp starts from
-  float ca[2][G::W], cb[2][G::W];              // the CTA's map of this round and the last
+// R rows a thread, so that a tile of one array is 8 KB whatever the type.
+template <class T, bool EDGE_, int STAGES_> struct RecGeom {
+  static constexpr bool EDGE = EDGE_;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int NT = 256, WARPS = NT / 32, W = 64;
+  static constexpr int V = 16 / sizeof(T);
+  static constexpr int R = 16 / sizeof(T);
+  static constexpr int L = WARPS * R;                        // rows of a tile
+  static constexpr int CHUNKS = W / V + (EDGE ? 1 : 0);      // 16-byte copies of a row
+  static constexpr int PITCH = CHUNKS * 16;                  // bytes of a row in shared memory
+  static constexpr int ARRAY = L * PITCH;
+  static constexpr int ITERS = (L * CHUNKS + NT - 1) / NT;   // copies of a thread for one array
 };
 
-// The state `in` that each thread's first row starts from, given the map (A, B) of its R
-// rows and, in threads tid < W, the state `carry` before the cluster's rows of this
-// round; updates `carry` to the state after them.  All threads call it.
-template <class G>
-__device__ __forceinline__ void rec_carry(float (&A)[G::V], float (&B)[G::V], float (&in)[G::V], RecShared<G>& sh,
-                                          float& carry, unsigned C, unsigned rank, int round) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c0 = (lane % G::LANES) * G::V;
-#pragma unroll
-  for (int d = G::LANES; d < 32; d *= 2) {
-#pragma unroll
-    for (int k = 0; k < G::V; ++k) {
-      const float pa = __shfl_up_sync(0xffffffffu, A[k], d), pb = __shfl_up_sync(0xffffffffu, B[k], d);
-      if (lane >= d) {
-        B[k] = fmaf(A[k], pb, B[k]);
-        A[k] *= pa;
-      }
+// The maps of two channels.
+struct RecShared {
+  float4 warp[2][8][32];                  // (A, B) of each warp's rows, by lane; two rounds in turn
+  float4 cta[2][kRecMaxCluster][32];      // of each CTA's tile
+};
+
+// One array of one strip: `p` is (b, t = 0, d0).
+template <class T> struct RecStrip {
+  const T* p;
+  long long st;
+};
+
+// Copies row `t` of the strip, or nothing where `on` is false, into row `r` of its tile:
+// this thread's share, chunk c.
+template <class T, class G>
+__device__ __forceinline__ void rec_copy(unsigned char* tile, const RecStrip<T>& s, int r, int c, long long t, bool on,
+                                         int d0, int D) {
+  unsigned char* dst = tile + r * G::PITCH + c * 16;
+  const T* row = s.p + (on ? t : 0) * s.st;
+  if constexpr (!G::EDGE) {
+    const bool live = on && d0 + c * G::V < D;
+    cp_async16(dst, live ? row + c * G::V : s.p, live);
+  } else {
+    const int off = (int)((uintptr_t)row % 16 / sizeof(T));
+    const int e = c * G::V - off, ch = d0 + e;  // the chunk's first channel
+    if (!on || e >= G::W || ch >= D) return;    // none of it is used
+    if (ch >= 0) {
+      const int n = D - ch < G::V ? D - ch : G::V;
+      cp_async_part(dst, row + e, n * (int)sizeof(T));
+    } else {  // the row begins inside the chunk
+      for (int k = -ch; k < G::V && ch + k < D; ++k) ((T*)dst)[k] = row[e + k];
     }
   }
-  if (lane >= 32 - G::LANES) {
-#pragma unroll
-    for (int k = 0; k < G::V; ++k) {
-      sh.a[warp][c0 + k] = A[k];
-      sh.b[warp][c0 + k] = B[k];
-    }
-  }
-  // From here on the map of the rows before this thread's in its warp.
-#pragma unroll
-  for (int k = 0; k < G::V; ++k) {
-    if constexpr (G::GROUPS > 1) {
-      const float pa = __shfl_up_sync(0xffffffffu, A[k], G::LANES), pb = __shfl_up_sync(0xffffffffu, B[k], G::LANES);
-      A[k] = lane < G::LANES ? 1.f : pa;
-      B[k] = lane < G::LANES ? 0.f : pb;
-    } else {
-      A[k] = 1.f;
-      B[k] = 0.f;
-    }
-  }
-  __syncthreads();
-  float wa[G::WARPS], wb[G::WARPS];
-  if (tid < G::W) {
-#pragma unroll
-    for (int w = 0; w < G::WARPS; ++w) {
-      wa[w] = sh.a[w][tid];
-      wb[w] = sh.b[w][tid];
-    }
-  }
-  float start = carry;
-  if (C > 1) {
-    const int slot = round & 1;
-    if (tid < G::W) {
-      float ta = 1.f, tb = 0.f;
-#pragma unroll
-      for (int w = 0; w < G::WARPS; ++w) {
-        tb = fmaf(wa[w], tb, wb[w]);
-        ta *= wa[w];
-      }
-      sh.ca[slot][tid] = ta;
-      sh.cb[slot][tid] = tb;
-    }
-    // Two slots in turn: a CTA writes a slot again only after the next round's barrier,
-    // which every reader of the slot reaches after its reads.
-    cluster_sync();
-    if (tid < G::W) {
-      float ra[kRecMaxCluster], rb[kRecMaxCluster];
-#pragma unroll
-      for (unsigned r = 0; r < kRecMaxCluster; ++r) {
-        if (r < C) {
-          ra[r] = ld_cluster_f32(cluster_addr(&sh.ca[slot][tid], r));
-          rb[r] = ld_cluster_f32(cluster_addr(&sh.cb[slot][tid], r));
-        }
-      }
-#pragma unroll
-      for (unsigned r = 0; r < kRecMaxCluster; ++r) {
-        if (r < C) {
-          if (r == rank) start = carry;
-          carry = fmaf(ra[r], carry, rb[r]);
-        }
-      }
-    }
-  }
-  if (tid < G::W) {
-    float s = start;
-#pragma unroll
-    for (int w = 0; w < G::WARPS; ++w) {
-      sh.from[w][tid] = s;
-      s = fmaf(wa[w], s, wb[w]);
-    }
-    if (C == 1) carry = s;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < G::V; ++k) in[k] = fmaf(A[k], sh.from[warp][c0 + k], B[k]);
 }
 
-// Where a thread's values of one array in one tile are: staged in shared memory by its
-// own asynchronous copies (16-byte packs), or read straight from global memory.
-template <class T, class G, int NA> struct RecStage {
-  static constexpr size_t kSlot = (size_t)G::R * G::NT * 16;  // one array
-  static constexpr size_t kStage = kSlot * NA;
-  static constexpr size_t kBytes = G::V == 1 ? 0 : kStage * G::STAGES;
-};
+// The two channels of this lane in row `r` of a tile, which holds row `t` of the strip.
+template <class T, class G>
+__device__ __forceinline__ float2 rec_pair(const unsigned char* tile, const RecStrip<T>& s, int r, int lane, long long t) {
+  const unsigned char* row = tile + r * G::PITCH;
+  if constexpr (!G::EDGE) {
+    if constexpr (sizeof(T) == 4) {
+      return *(const float2*)(row + lane * 8);
+    } else {
+      Pair<T> q;
+      const unsigned u = *(const unsigned*)(row + lane * 4);
+      memcpy(&q, &u, 4);
+      return make_float2(widen(q.x), widen(q.y));
+    }
+  } else {
+    const unsigned off = (unsigned)((uintptr_t)(s.p + t * s.st) % 16);
+    const T* q = (const T*)(row + off) + 2 * lane;
+    return make_float2(widen(q[0]), widen(q[1]));
+  }
+}
+
+// Writes the two channels ch, ch + 1 of a row; `p` points at the first.
+template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, float2 v, int ch, int D) {
+  if constexpr (!EDGE) {
+    if (ch < D) {
+      if constexpr (sizeof(T) == 4) {
+        *(float2*)p = v;
+      } else {
+        const Pair<T> q = {narrow<T>(v.x), narrow<T>(v.y)};
+        unsigned u;
+        memcpy(&u, &q, 4);
+        *(unsigned*)p = u;
+      }
+    }
+  } else {
+    if (ch < D) p[0] = narrow<T>(v.x);
+    if (ch + 1 < D) p[1] = narrow<T>(v.y);
+  }
+}
+
+// The states (two channels) that this warp's first row starts from, given the map m of its
+// rows and the states `carry` before the cluster's rows of this round; moves `carry` past
+// them.  All threads of the CTA call it.
+__device__ __forceinline__ float2 rec_exchange(float4 m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
+                                               int turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sh.warp[turn][warp][lane] = m;
+  __syncthreads();
+  if (C == 1) {
+    float2 s = carry, in = carry;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float4 q = sh.warp[turn][w][lane];
+      if (w == warp) in = s;
+      s = make_float2(fmaf(q.x, s.x, q.y), fmaf(q.z, s.y, q.w));
+    }
+    carry = s;
+    return in;
+  }
+  float4 all = make_float4(1.f, 0.f, 1.f, 0.f), before = all;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float4 q = sh.warp[turn][w][lane];
+    if (w == warp) before = all;
+    all = make_float4(all.x * q.x, fmaf(q.x, all.y, q.y), all.z * q.z, fmaf(q.z, all.w, q.w));
+  }
+  // Warp r sends the CTA's map to CTA r.  A CTA writes a slot again two rounds later, past
+  // a barrier that its reader reaches after reading it.
+  if ((unsigned)warp < C) st_cluster_f4(cluster_addr(&sh.cta[turn][rank][lane], (unsigned)warp), all);
+  cluster_sync();
+  float2 s = carry, start = carry;
+#pragma unroll
+  for (unsigned r = 0; r < kRecMaxCluster; ++r) {
+    if (r < C) {
+      const float4 q = sh.cta[turn][r][lane];
+      if (r == rank) start = s;
+      s = make_float2(fmaf(q.x, s.x, q.y), fmaf(q.z, s.y, q.w));
+    }
+  }
+  carry = s;
+  return make_float2(fmaf(before.x, start.x, before.y), fmaf(before.z, start.y, before.w));
+}
+
+// Appends the map (a, b) of one row to m, for both channels.
+__device__ __forceinline__ void rec_append(float4& m, float2 a, float2 b) {
+  m = make_float4(m.x * a.x, fmaf(a.x, m.y, b.x), m.z * a.y, fmaf(a.y, m.w, b.y));
+}
 
 template <class T, bool GATE, class G>
-__global__ void __launch_bounds__(G::NT) rec_forward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
-  using S = RecStage<T, G, GATE ? 3 : 2>;
-  constexpr int V = G::V, R = G::R;
-  extern __shared__ __align__(16) unsigned char stage_mem[];
-  __shared__ RecShared<G> sh;
+__global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+  constexpr int R = G::R, NA = GATE ? 3 : 2;
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ RecShared sh;
   pdl_entry();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
   const long long b = strip / a.strips;
-  const int d0 = (int)(strip % a.strips) * G::W;
-  const int ch = d0 + (lane % G::LANES) * V;
-  const bool live = ch < a.D;
-  const int group = warp * G::GROUPS + lane / G::LANES;
-  // The first row of this thread in its CTA's first tile.
-  const long long row0 = (long long)rank * G::L + group * R;
-  const long long step = (long long)C * G::L;
-  const long long rounds = (a.T_ + step - 1) / step;
-  const int chs = live ? ch : 0;  // an address that exists
-  const T* x = a.x + b * a.xb + chs;
-  const T* f = a.f + b * a.fb + chs;
-  const T* g = GATE ? a.i + b * a.ib + chs : nullptr;
-  T* y = a.y + b * a.yb + chs;
+  const int d0 = (int)(strip % a.strips) * G::W, ch = d0 + 2 * lane;
+  const long long step = (long long)C * G::L, rounds = (a.T_ + step - 1) / step;
+  const long long tile0 = (long long)rank * G::L;
+  const RecStrip<T> x = {a.x + b * a.xb + d0, a.xt}, f = {a.f + b * a.fb + d0, a.ft},
+                    g = {GATE ? a.i + b * a.ib + d0 : nullptr, a.it};
+  T* y = a.y + b * a.yb + ch;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
-  float carry = 0.f;
-  if (tid < G::W && d0 + tid < a.D && a.h0) carry = a.h0[b * a.D + d0 + tid];
-
-  auto fetch = [&](long long k) {  // tile of round k into its stage
-    if constexpr (V > 1) {
-      unsigned char* base = stage_mem + (size_t)(k % G::STAGES) * S::kStage + (size_t)tid * 16;
-      const long long t0 = row0 + k * step;
+  auto fetch = [&](long long k) {  // this CTA's tile of round k; one commit group a round
+    if (k < rounds) {
+      unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool on = live && t0 + r < a.T_;
-        const long long t = on ? t0 + r : 0;
-        cp_async16(base + r * G::NT * 16, x + t * a.xt, on);
-        cp_async16(base + S::kSlot + r * G::NT * 16, f + t * a.ft, on);
-        if constexpr (GATE) cp_async16(base + 2 * S::kSlot + r * G::NT * 16, g + t * a.it, on);
+      for (int n = 0; n < G::ITERS; ++n) {
+        const int at = tid + n * G::NT, r = at / G::CHUNKS, c = at % G::CHUNKS;
+        if (G::EDGE && r >= G::L) break;
+        const long long t = tile0 + k * step + r;
+        const bool on = t < a.T_;
+        rec_copy<T, G>(base, x, r, c, t, on, d0, a.D);
+        rec_copy<T, G>(base + G::ARRAY, f, r, c, t, on, d0, a.D);
+        if constexpr (GATE) rec_copy<T, G>(base + 2 * G::ARRAY, g, r, c, t, on, d0, a.D);
       }
-      cp_async_commit();
     }
+    cp_async_commit();
   };
-  if constexpr (V > 1) {
+  auto flags = [&](long long k) -> int {  // lane r < R: whether its warp's row r is a start
+    const long long t = tile0 + k * step + warp * R + lane;
+    return starts && lane < R && t < a.T_ ? starts[t] : 0;
+  };
 #pragma unroll
-    for (int k = 0; k < G::STAGES - 1; ++k) {
-      if (k < rounds) fetch(k);
-      else cp_async_commit();
-    }
+  for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
+  int flag = flags(0);
+  float2 carry = make_float2(0.f, 0.f);
+  if (a.h0) {
+    if (ch < a.D) carry.x = a.h0[b * a.D + ch];
+    if (ch + 1 < a.D) carry.y = a.h0[b * a.D + ch + 1];
   }
+  if (C > 1) cluster_sync();  // the others are there to be written to
+
   for (long long k = 0; k < rounds; ++k) {
-    const long long t0 = row0 + k * step;
-    Pack<T, V> px[R], pf[R], pi[R];
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool on = live && t0 + r < a.T_;
-        const long long t = on ? t0 + r : 0;
-        px[r].v[0] = on ? x[t * a.xt] : narrow<T>(0.f);
-        pf[r].v[0] = on ? f[t * a.ft] : narrow<T>(0.f);
-        if constexpr (GATE) pi[r].v[0] = on ? g[t * a.it] : narrow<T>(0.f);
-      }
-    }
-    bool drop[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) drop[r] = starts && t0 + r < a.T_ && starts[t0 + r] != 0;
-    if constexpr (V > 1) {
-      if (k + G::STAGES - 1 < rounds) fetch(k + G::STAGES - 1);
-      else cp_async_commit();
-      cp_async_wait<G::STAGES - 1>();
-      const unsigned char* base = stage_mem + (size_t)(k % G::STAGES) * S::kStage + (size_t)tid * 16;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        px[r] = ld_pack<T, V>((const T*)(base + r * G::NT * 16));
-        pf[r] = ld_pack<T, V>((const T*)(base + S::kSlot + r * G::NT * 16));
-        if constexpr (GATE) pi[r] = ld_pack<T, V>((const T*)(base + 2 * S::kSlot + r * G::NT * 16));
-      }
-    }
-    float av[R][V], bv[R][V], A[V], B[V], in[V];
+    const long long t0 = tile0 + k * step + warp * R;
+    cp_async_wait<G::STAGES - 2>();
+    __syncthreads();  // the tile is in; the one before it has been read by all
+    fetch(k + G::STAGES - 1);
+    const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
+    flag = flags(k + 1);
+    const unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
+    float2 av[R], bv[R];
+    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float xs[V], fs[V], is[V];
-      widen_pack(px[r], xs);
-      widen_pack(pf[r], fs);
-      if constexpr (GATE) widen_pack(pi[r], is);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        float s, u;
-        sigmoid_both(fs[c], s, u);
+      // Past the end the map is the identity, so that `carry` ends as the last state.
+      av[r] = make_float2(1.f, 1.f);
+      bv[r] = make_float2(0.f, 0.f);
+      if (t0 + r < a.T_) {
+        const int row = warp * R + r;
+        const float2 xs = rec_pair<T, G>(base, x, row, lane, t0 + r);
+        const float2 fs = rec_pair<T, G>(base + G::ARRAY, f, row, lane, t0 + r);
+        float2 u;
         if constexpr (GATE) {
-          float unused;
-          sigmoid_both(is[c], u, unused);
+          const float2 is = rec_pair<T, G>(base + 2 * G::ARRAY, g, row, lane, t0 + r);
+          av[r] = make_float2(sigmoid(fs.x), sigmoid(fs.y));
+          u = make_float2(sigmoid(is.x), sigmoid(is.y));
+        } else {
+          sigmoid_both(fs.x, av[r].x, u.x);
+          sigmoid_both(fs.y, av[r].y, u.y);
         }
-        // Past the end the map is the identity, so that `carry` ends as the last state.
-        const bool on = t0 + r < a.T_;
-        av[r][c] = drop[r] ? 0.f : on ? s : 1.f;
-        bv[r][c] = on ? u * xs[c] : 0.f;
-        A[c] = r ? A[c] * av[r][c] : av[r][c];
-        B[c] = r ? fmaf(av[r][c], B[c], bv[r][c]) : bv[r][c];
+        if (drop >> r & 1) av[r] = make_float2(0.f, 0.f);
+        bv[r] = make_float2(u.x * xs.x, u.y * xs.y);
       }
+      rec_append(m, av[r], bv[r]);
     }
-    rec_carry<G>(A, B, in, sh, carry, C, rank, (int)(k & 1));
+    float2 s = rec_exchange(m, carry, sh, C, rank, (int)(k & 1));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) in[c] = fmaf(av[r][c], in[c], bv[r][c]);
-      if (live && t0 + r < a.T_) st_pack(y + (t0 + r) * a.yt, narrow_pack<T, V>(in));
+      if (t0 + r < a.T_) {
+        s = make_float2(fmaf(av[r].x, s.x, bv[r].x), fmaf(av[r].y, s.y, bv[r].y));
+        rec_store<T, G::EDGE>(y + (t0 + r) * a.yt, s, ch, a.D);
+      }
     }
   }
-  if (a.last && rank == 0 && tid < G::W && d0 + tid < a.D) a.last[b * a.D + d0 + tid] = carry;
-  if (C > 1) cluster_sync();  // no CTA leaves while another may read its shared memory
+  if (a.last && rank == 0 && warp == 0) {
+    if (ch < a.D) a.last[b * a.D + ch] = carry.x;
+    if (ch + 1 < a.D) a.last[b * a.D + ch + 1] = carry.y;
+  }
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
 template <class T, bool GATE, class G>
-__global__ void __launch_bounds__(G::NT) rec_backward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
-  using S = RecStage<T, G, GATE ? 5 : 4>;
-  constexpr int V = G::V, R = G::R;
-  extern __shared__ __align__(16) unsigned char stage_mem[];
-  __shared__ RecShared<G> sh;
+__global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+  constexpr int R = G::R, NA = GATE ? 5 : 4;
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ RecShared sh;
   pdl_entry();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
   const long long b = strip / a.strips;
-  const int d0 = (int)(strip % a.strips) * G::W;
-  const int ch = d0 + (lane % G::LANES) * V;
-  const bool live = ch < a.D;
-  const int group = warp * G::GROUPS + lane / G::LANES;
-  const long long row0 = (long long)rank * G::L + group * R;
-  const long long step = (long long)C * G::L;
-  const long long rounds = (a.T_ + step - 1) / step;
-  const int chs = live ? ch : 0;
-  const T* x = a.x + b * a.xb + chs;
-  const T* f = a.f + b * a.fb + chs;
-  const T* g = GATE ? a.i + b * a.ib + chs : nullptr;
-  const T* h = a.h + b * a.hb + chs;
-  const T* dh = a.dh + b * a.dhb + chs;
+  const int d0 = (int)(strip % a.strips) * G::W, ch = d0 + 2 * lane;
+  const long long step = (long long)C * G::L, rounds = (a.T_ + step - 1) / step;
+  const long long tile0 = (long long)rank * G::L;
+  const RecStrip<T> f = {a.f + b * a.fb + d0, a.ft}, dh = {a.dh + b * a.dhb + d0, a.dht},
+                    x = {a.x + b * a.xb + d0, a.xt}, h = {a.h + b * a.hb + d0, a.ht},
+                    g = {GATE ? a.i + b * a.ib + d0 : nullptr, a.it};
+  T *dx = a.dx + b * a.dxb + ch, *df = a.df + b * a.dfb + ch, *di = GATE ? a.di + b * a.dib + ch : nullptr;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
-  float carry = 0.f;
-  if (tid < G::W && d0 + tid < a.D && a.dlast) carry = a.dlast[b * a.D + d0 + tid];
-
   auto fetch = [&](long long k) {
-    if constexpr (V > 1) {
-      unsigned char* base = stage_mem + (size_t)(k % G::STAGES) * S::kStage + (size_t)tid * 16;
-      const long long p0 = row0 + k * step;
+    if (k < rounds) {
+      unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool on = live && p0 + r < a.T_;
-        const long long t = on ? a.T_ - 1 - (p0 + r) : 0;
-        unsigned char* q = base + r * G::NT * 16;
-        cp_async16(q, f + t * a.ft, on);
-        cp_async16(q + S::kSlot, dh + t * a.dht, on);
-        cp_async16(q + 2 * S::kSlot, x + t * a.xt, on);
-        cp_async16(q + 3 * S::kSlot, h + (t > 0 ? t - 1 : 0) * a.ht, on && t > 0);
-        if constexpr (GATE) cp_async16(q + 4 * S::kSlot, g + t * a.it, on);
+      for (int n = 0; n < G::ITERS; ++n) {
+        const int at = tid + n * G::NT, r = at / G::CHUNKS, c = at % G::CHUNKS;
+        if (G::EDGE && r >= G::L) break;
+        const long long t = a.T_ - 1 - (tile0 + k * step + r);
+        const bool on = t >= 0;
+        rec_copy<T, G>(base, f, r, c, t, on, d0, a.D);
+        rec_copy<T, G>(base + G::ARRAY, dh, r, c, t, on, d0, a.D);
+        rec_copy<T, G>(base + 2 * G::ARRAY, x, r, c, t, on, d0, a.D);
+        rec_copy<T, G>(base + 3 * G::ARRAY, h, r, c, t - 1, t > 0, d0, a.D);
+        if constexpr (GATE) rec_copy<T, G>(base + 4 * G::ARRAY, g, r, c, t, on, d0, a.D);
       }
-      cp_async_commit();
     }
+    cp_async_commit();
   };
-  if constexpr (V > 1) {
+  auto flags = [&](long long k) -> int {
+    const long long t = a.T_ - 1 - (tile0 + k * step + warp * R + lane);
+    return starts && lane < R && t >= 0 ? starts[t] : 0;
+  };
 #pragma unroll
-    for (int k = 0; k < G::STAGES - 1; ++k) {
-      if (k < rounds) fetch(k);
-      else cp_async_commit();
-    }
+  for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
+  int flag = flags(0);
+  float2 carry = make_float2(0.f, 0.f), first = carry;
+  if (a.dlast) {
+    if (ch < a.D) carry.x = a.dlast[b * a.D + ch];
+    if (ch + 1 < a.D) carry.y = a.dlast[b * a.D + ch + 1];
   }
-  for (long long k = 0; k < rounds; ++k) {
-    const long long p0 = row0 + k * step;
-    const unsigned char* base = nullptr;
-    Pack<T, V> px[R], pf[R], pi[R], ph[R], pd[R];
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool on = live && p0 + r < a.T_;
-        const long long t = on ? a.T_ - 1 - (p0 + r) : 0;
-        const T zero = narrow<T>(0.f);
-        pf[r].v[0] = on ? f[t * a.ft] : zero;
-        pd[r].v[0] = on ? dh[t * a.dht] : zero;
-        px[r].v[0] = on ? x[t * a.xt] : zero;
-        ph[r].v[0] = on && t > 0 ? h[(t - 1) * a.ht] : zero;
-        if constexpr (GATE) pi[r].v[0] = on ? g[t * a.it] : zero;
-      }
-    }
-    bool drop[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) drop[r] = starts && p0 + r < a.T_ && starts[a.T_ - 1 - (p0 + r)] != 0;
-    if constexpr (V > 1) {
-      if (k + G::STAGES - 1 < rounds) fetch(k + G::STAGES - 1);
-      else cp_async_commit();
-      cp_async_wait<G::STAGES - 1>();
-      base = stage_mem + (size_t)(k % G::STAGES) * S::kStage + (size_t)tid * 16;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        pf[r] = ld_pack<T, V>((const T*)(base + r * G::NT * 16));
-        pd[r] = ld_pack<T, V>((const T*)(base + S::kSlot + r * G::NT * 16));
-      }
-    }
-    float av[R][V], A[V], B[V], in[V];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float fs[V], ds[V];
-      widen_pack(pf[r], fs);
-      widen_pack(pd[r], ds);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        float s, u;
-        sigmoid_both(fs[c], s, u);
-        const bool on = p0 + r < a.T_;
-        av[r][c] = drop[r] ? 0.f : on ? s : 1.f;
-        const float bv = on ? av[r][c] * ds[c] : 0.f;
-        A[c] = r ? A[c] * av[r][c] : av[r][c];
-        B[c] = r ? fmaf(av[r][c], B[c], bv) : bv;
-      }
-    }
-    rec_carry<G>(A, B, in, sh, carry, C, rank, (int)(k & 1));
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long t = a.T_ - 1 - (p0 + r);
-      if (V > 1) {
-        px[r] = ld_pack<T, V>((const T*)(base + 2 * S::kSlot + r * G::NT * 16));
-        ph[r] = ld_pack<T, V>((const T*)(base + 3 * S::kSlot + r * G::NT * 16));
-        if constexpr (GATE) pi[r] = ld_pack<T, V>((const T*)(base + 4 * S::kSlot + r * G::NT * 16));
-      }
-      float xs[V], fs[V], is[V], hs[V], ds[V], ox[V], of[V], oi[V];
-      widen_pack(px[r], xs);
-      widen_pack(pf[r], fs);
-      widen_pack(ph[r], hs);
-      widen_pack(pd[r], ds);
-      if constexpr (GATE) widen_pack(pi[r], is);
-      if (t == 0 && a.h0 && live) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) hs[c] = a.h0[b * a.D + ch + c];
-      }
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float gt = ds[c] + in[c];  // dL/dh_t
-        float s, s1, u, u1;
-        sigmoid_both(fs[c], s, s1);
-        const float before = drop[r] ? 0.f : hs[c];
-        if constexpr (GATE) {
-          sigmoid_both(is[c], u, u1);
-          of[c] = s * s1 * before * gt;
-          oi[c] = u * u1 * xs[c] * gt;
-          ox[c] = u * gt;
-        } else {
-          of[c] = s * s1 * (before - xs[c]) * gt;
-          ox[c] = s1 * gt;
-        }
-        in[c] = av[r][c] * gt;
-      }
-      if (live && t >= 0) {
-        st_pack(a.dx + b * a.dxb + ch + t * a.dxt, narrow_pack<T, V>(ox));
-        st_pack(a.df + b * a.dfb + ch + t * a.dft, narrow_pack<T, V>(of));
-        if constexpr (GATE) st_pack(a.di + b * a.dib + ch + t * a.dit, narrow_pack<T, V>(oi));
-      }
-    }
+  if (a.h0) {
+    if (ch < a.D) first.x = a.h0[b * a.D + ch];
+    if (ch + 1 < a.D) first.y = a.h0[b * a.D + ch + 1];
   }
-  if (a.dh0 && rank == 0 && tid < G::W && d0 + tid < a.D) a.dh0[b * a.D + d0 + tid] = carry;
   if (C > 1) cluster_sync();
+
+  for (long long k = 0; k < rounds; ++k) {
+    const long long t0 = a.T_ - 1 - (tile0 + k * step + warp * R);  // this warp's rows: t0, t0 - 1, ...
+    cp_async_wait<G::STAGES - 2>();
+    __syncthreads();
+    fetch(k + G::STAGES - 1);
+    const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
+    flag = flags(k + 1);
+    const unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
+    float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
+    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = s1[r] = make_float2(0.f, 0.f);
+      if (t0 - r >= 0) {
+        const int row = warp * R + r;
+        const float2 fs = rec_pair<T, G>(base, f, row, lane, t0 - r);
+        const float2 ds = rec_pair<T, G>(base + G::ARRAY, dh, row, lane, t0 - r);
+        sigmoid_both(fs.x, s[r].x, s1[r].x);
+        sigmoid_both(fs.y, s[r].y, s1[r].y);
+        const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
+        rec_append(m, av, make_float2(av.x * ds.x, av.y * ds.y));
+      }
+    }
+    float2 c = rec_exchange(m, carry, sh, C, rank, (int)(k & 1));  // c_{t+1} of the warp's first row
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long t = t0 - r;
+      if (t < 0) break;
+      const int row = warp * R + r;
+      const float2 ds = rec_pair<T, G>(base + G::ARRAY, dh, row, lane, t);
+      const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, x, row, lane, t);
+      float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, h, row, lane, t - 1) : first;
+      const bool dropped = drop >> r & 1;
+      if (dropped) hs = make_float2(0.f, 0.f);
+      const float2 gt = make_float2(ds.x + c.x, ds.y + c.y);  // dL/dh_t
+      const float2 fg = make_float2(s[r].x * s1[r].x * gt.x, s[r].y * s1[r].y * gt.y);
+      if constexpr (GATE) {
+        const float2 is = rec_pair<T, G>(base + 4 * G::ARRAY, g, row, lane, t);
+        float2 u, u1;
+        sigmoid_both(is.x, u.x, u1.x);
+        sigmoid_both(is.y, u.y, u1.y);
+        const float2 ug = make_float2(u.x * gt.x, u.y * gt.y);
+        rec_store<T, G::EDGE>(dx + t * a.dxt, ug, ch, a.D);
+        rec_store<T, G::EDGE>(df + t * a.dft, make_float2(fg.x * hs.x, fg.y * hs.y), ch, a.D);
+        rec_store<T, G::EDGE>(di + t * a.dit, make_float2(ug.x * u1.x * xs.x, ug.y * u1.y * xs.y), ch, a.D);
+      } else {
+        rec_store<T, G::EDGE>(dx + t * a.dxt, make_float2(s1[r].x * gt.x, s1[r].y * gt.y), ch, a.D);
+        rec_store<T, G::EDGE>(df + t * a.dft, make_float2(fg.x * (hs.x - xs.x), fg.y * (hs.y - xs.y)), ch, a.D);
+      }
+      c = dropped ? make_float2(0.f, 0.f) : make_float2(s[r].x * gt.x, s[r].y * gt.y);
+    }
+  }
+  if (a.dh0 && rank == 0 && warp == 0) {
+    if (ch < a.D) a.dh0[b * a.D + ch] = carry.x;
+    if (ch + 1 < a.D) a.dh0[b * a.D + ch + 1] = carry.y;
+  }
 }
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
@@ -535,14 +506,13 @@ template <class G> unsigned rec_cluster(long long strips, long long T_, int num_
   return c;
 }
 
-template <class T, class G, int NA, class K>
+template <class G, int NA, class T, class K>
 cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const LaunchCtx& ctx) {
   const long long strips = (j.D + G::W - 1) / G::W;
   const unsigned C = rec_cluster<G>(strips * j.B, j.T, ctx.num_sms);
   a.strips = (int)strips;
-  const size_t smem = RecStage<T, G, NA>::kBytes;
-  cudaError_t e = cudaSuccess;
-  if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int smem = G::STAGES * NA * G::ARRAY;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   profile_before(ctx);
   e = launch_pdl_cluster(kernel, (unsigned)(strips * j.B * C), G::NT, C, smem, ctx.stream, a, C);
@@ -550,32 +520,29 @@ cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const Lau
   return e;
 }
 
-template <class T> cudaError_t launch_recurrence(const RecurrenceJob& j, const LaunchCtx& ctx) {
-  constexpr int V = 16 / sizeof(T);
-  using GV = RecGeom<V, 8, 4, 2>;
-  using GS = RecGeom<1, 32, 8, 1>;
+template <class T, bool EDGE> cudaError_t rec_forward(const RecurrenceJob& j, const LaunchCtx& ctx) {
+  using G = RecGeom<T, EDGE, 3>;
   const RecArgs<T> a = rec_args<T>(j);
-  const bool wide = j.D % V == 0 && rows16<T>(j.x, j.B, j.T) && rows16<T>(j.f, j.B, j.T) &&
-                    rows16<T>(j.i, j.B, j.T) && rows16<T>(j.h, j.B, j.T);
-  if (j.i.p)
-    return wide ? rec_launch<T, GV, 3>(rec_forward_kernel<T, true, GV>, j, a, ctx)
-                : rec_launch<T, GS, 3>(rec_forward_kernel<T, true, GS>, j, a, ctx);
-  return wide ? rec_launch<T, GV, 2>(rec_forward_kernel<T, false, GV>, j, a, ctx)
-              : rec_launch<T, GS, 2>(rec_forward_kernel<T, false, GS>, j, a, ctx);
+  return j.i.p ? rec_launch<G, 3>(rec_forward_kernel<T, true, G>, j, a, ctx)
+               : rec_launch<G, 2>(rec_forward_kernel<T, false, G>, j, a, ctx);
+}
+template <class T, bool EDGE> cudaError_t rec_backward(const RecurrenceJob& j, const LaunchCtx& ctx) {
+  using G = RecGeom<T, EDGE, 2>;
+  const RecArgs<T> a = rec_args<T>(j);
+  return j.i.p ? rec_launch<G, 5>(rec_backward_kernel<T, true, G>, j, a, ctx)
+               : rec_launch<G, 4>(rec_backward_kernel<T, false, G>, j, a, ctx);
+}
+
+template <class T> cudaError_t launch_recurrence(const RecurrenceJob& j, const LaunchCtx& ctx) {
+  bool even = j.D % (16 / sizeof(T)) == 0;
+  for (const SeqArray* s : {&j.x, &j.f, &j.i, &j.h}) even = even && rows16<T>(*s, j.B, j.T);
+  return even ? rec_forward<T, false>(j, ctx) : rec_forward<T, true>(j, ctx);
 }
 
 template <class T> cudaError_t launch_recurrence_backward(const RecurrenceJob& j, const LaunchCtx& ctx) {
-  constexpr int V = 16 / sizeof(T);
-  using GV = RecGeom<V, 8, 2, 2>;
-  using GS = RecGeom<1, 32, 4, 1>;
-  const RecArgs<T> a = rec_args<T>(j);
-  bool wide = j.D % V == 0;
-  for (const SeqArray* s : {&j.x, &j.f, &j.i, &j.h, &j.dh, &j.dx, &j.df, &j.di}) wide = wide && rows16<T>(*s, j.B, j.T);
-  if (j.i.p)
-    return wide ? rec_launch<T, GV, 5>(rec_backward_kernel<T, true, GV>, j, a, ctx)
-                : rec_launch<T, GS, 5>(rec_backward_kernel<T, true, GS>, j, a, ctx);
-  return wide ? rec_launch<T, GV, 4>(rec_backward_kernel<T, false, GV>, j, a, ctx)
-              : rec_launch<T, GS, 4>(rec_backward_kernel<T, false, GS>, j, a, ctx);
+  bool even = j.D % (16 / sizeof(T)) == 0;
+  for (const SeqArray* s : {&j.x, &j.f, &j.i, &j.h, &j.dh, &j.dx, &j.df, &j.di}) even = even && rows16<T>(*s, j.B, j.T);
+  return even ? rec_backward<T, false>(j, ctx) : rec_backward<T, true>(j, ctx);
 }
 
 template <class T, bool GATE, int V>
