@@ -378,9 +378,9 @@ void gb_set_stalled_tile(int64_t tile);
  * Pointers are aligned to their element type; rows aligned to 16 bytes are faster.
  * Outputs must not overlap inputs unless stated, nor their own rows each other.  The
  * conventions at the top of this file hold otherwise, except that these calls clear no
- * status words and have no in-kernel waits.  Errors: GB_ERR_INVALID (null or misaligned
+ * status words.  Errors: GB_ERR_INVALID (null or misaligned
  * pointer, negative size or stride, bad option), GB_ERR_UNSUPPORTED (dtype),
- * GB_ERR_RANGE (channels, cols or vocab above 2^30, or a grid past 2^31 - 1 blocks),
+ * GB_ERR_RANGE (length, channels, cols or vocab above 2^30, or a grid past 2^31 - 1 blocks),
  * GB_ERR_TEMP, GB_ERR_CUDA.
  */
 

@@ -90,11 +90,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // ---- asynchronous copies of 16 bytes, tracked by the issuing thread ------------------
 
-// Copies 16 bytes to shared memory, or writes 16 zero bytes there when `live` is false
-// (nothing is read then; src must still be a valid address to form).
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 // Copies the first `bytes` (1 .. 16) of 16 bytes and writes zeros for the rest.
 __device__ __forceinline__ void cp_async_part(void* dst, const void* src, int bytes) {
@@ -125,9 +122,13 @@ __device__ __forceinline__ unsigned cluster_addr(const void* p, unsigned rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void st_cluster_f4(unsigned addr, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
+// Stores 16 bytes in another CTA's shared memory and counts them on an mbarrier there.
+__device__ __forceinline__ void st_async_f4(unsigned addr, float4 v, unsigned bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+      "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)),
+      "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ float ld_cluster_f32(unsigned addr) {
   float v;

@@ -13,7 +13,7 @@ namespace {
 using gbs::LaunchCtx;
 using gbs::SeqArray;
 
-constexpr long long kMaxWidth = 1ll << 30;   // channels, columns, vocabulary
+constexpr long long kMaxWidth = 1ll << 30;   // channels, tokens, columns, vocabulary
 constexpr long long kMaxGrid = 0x7fffffffll;
 
 size_t lm_size(int dtype) {
@@ -53,8 +53,8 @@ int finish(cudaError_t e) { return e == cudaSuccess ? GB_OK : gbs::abi_cuda_fail
 int check_sizes(int dtype, long long B, long long T, long long D) {
   if (B < 0 || T < 0 || D < 0) return GB_ERR_INVALID;
   if (!lm_size(dtype)) return GB_ERR_UNSUPPORTED;
-  if (D > kMaxWidth || (long double)B * T * D > 9.0e17L) return GB_ERR_RANGE;
-  // The narrowest strip is 32 channels, the largest cluster 8 CTAs.
+  if (D > kMaxWidth || T > kMaxWidth || (long double)B * T * D > 9.0e17L) return GB_ERR_RANGE;
+  // The narrowest strip is 56 channels, the largest cluster 8 CTAs.
   if ((long double)B * ((D + 31) / 32) * 8 > (long double)kMaxGrid) return GB_ERR_RANGE;
   return GB_OK;
 }

@@ -12,13 +12,16 @@
 //
 // Tiles reach shared memory by asynchronous copies of 16 bytes, STAGES - 1 tiles ahead of
 // the one in hand.  Rows may start anywhere: where they are not all on 16-byte boundaries
-// (EDGE) the copies start at the boundary below each row's first channel and each lane
-// picks its channels out at the row's offset; a copy never reads outside its row.
+// (EDGE) a strip is narrower by one copy's worth, so that from the boundary below its first
+// channel it still fits the same copies, and each lane picks its channels out at the row's
+// offset.  A copy never reads outside its row.
 //
 // Where B*D/64 CTAs would leave SMs idle, a cluster of C CTAs shares the strip: its CTAs
 // take C consecutive tiles at a time and send each other their tiles' maps through
-// distributed shared memory, one cluster barrier per round.  No CTA waits on another
-// outside that hardware barrier, and no global scratch is needed.
+// distributed shared memory: asynchronous stores that complete on the receiver's mbarrier,
+// which needs no fence behind the CTA's outstanding writes of h as a cluster barrier does.
+// The CTAs of a cluster are scheduled together, so the wait ends; it is bounded all the
+// same (GB_ERR_TIMEOUT).  No global scratch is needed.
 //
 // The gradient runs the same scan backwards in time.  With g_t = dL/dh_t (all paths) and
 // c_t = a_t g_t,   g_t = dh_t + c_{t+1}   and   c_t = a_t c_{t+1} + a_t dh_t,
@@ -50,8 +53,9 @@ template <class T> struct RecArgs {
   const float *h0, *dlast;
   const uint8_t* starts;
   float *last, *dh0;
-  long long T_;
-  int D, strips;  // strips of W channels per batch row
+  int T_, D, strips;  // strips of W channels per batch row
+  ErrSink err;
+  unsigned long long wait_ns;
 };
 
 // sigmoid(z) alone: 1 / (1 + exp(-z)); exp(-z) may overflow to infinity, which gives 0.
@@ -63,54 +67,66 @@ constexpr int kRecMaxCluster = 8;
 template <class T, bool EDGE_, int STAGES_> struct RecGeom {
   static constexpr bool EDGE = EDGE_;
   static constexpr int STAGES = STAGES_;
-  static constexpr int NT = 256, WARPS = NT / 32, W = 64;
-  static constexpr int V = 16 / sizeof(T);
+  static constexpr int NT = 256, WARPS = NT / 32;
+  static constexpr int V = 16 / sizeof(T);                   // values of a copy
   static constexpr int R = 16 / sizeof(T);
   static constexpr int L = WARPS * R;                        // rows of a tile
-  static constexpr int CHUNKS = W / V + (EDGE ? 1 : 0);      // 16-byte copies of a row
+  static constexpr int W = EDGE ? 64 - V : 64;               // channels of a strip
+  static constexpr int CHUNKS = 64 / V;                      // copies of a row
   static constexpr int PITCH = CHUNKS * 16;                  // bytes of a row in shared memory
   static constexpr int ARRAY = L * PITCH;
-  static constexpr int ITERS = (L * CHUNKS + NT - 1) / NT;   // copies of a thread for one array
+  static constexpr int ROWS = NT / CHUNKS;                   // rows that the CTA copies at once
+  static_assert(L == 2 * ROWS, "each thread copies two rows' chunks of each array");
 };
 
-// The maps of two channels.
+// The maps (A, B of two channels) that threads exchange; two rounds in turn.
 struct RecShared {
-  float4 warp[2][8][32];                  // (A, B) of each warp's rows, by lane; two rounds in turn
-  float4 cta[2][kRecMaxCluster][32];      // of each CTA's tile
+  float4 warp[2][8][32];              // of each warp's rows
+  float4 cta[2][kRecMaxCluster][32];  // of each CTA's tile
+  unsigned long long bar[2];          // the cluster's maps have arrived
 };
 
-// One array of one strip: `p` is (b, t = 0, d0).
-template <class T> struct RecStrip {
-  const T* p;
-  long long st;
-};
-
-// Copies row `t` of the strip, or nothing where `on` is false, into row `r` of its tile:
-// this thread's share, chunk c.
-template <class T, class G>
-__device__ __forceinline__ void rec_copy(unsigned char* tile, const RecStrip<T>& s, int r, int c, long long t, bool on,
-                                         int d0, int D) {
-  unsigned char* dst = tile + r * G::PITCH + c * 16;
-  const T* row = s.p + (on ? t : 0) * s.st;
-  if constexpr (!G::EDGE) {
-    const bool live = on && d0 + c * G::V < D;
-    cp_async16(dst, live ? row + c * G::V : s.p, live);
-  } else {
-    const int off = (int)((uintptr_t)row % 16 / sizeof(T));
-    const int e = c * G::V - off, ch = d0 + e;  // the chunk's first channel
-    if (!on || e >= G::W || ch >= D) return;    // none of it is used
-    if (ch >= 0) {
-      const int n = D - ch < G::V ? D - ch : G::V;
-      cp_async_part(dst, row + e, n * (int)sizeof(T));
-    } else {  // the row begins inside the chunk
-      for (int k = -ch; k < G::V && ch + k < D; ++k) ((T*)dst)[k] = row[e + k];
+// What a thread copies of one array: the row p rows after the strip's first in scan order
+// (dir = 1: t = p; dir = -1: t = T - 1 - p), and where its copies go.
+template <class T, class G> struct RecCopy {
+  const char* src;       // row (tile, tid / CHUNKS); EVEN: its chunk
+  long long half, step;  // bytes from row r to r + ROWS, and to the next round's row
+  __device__ __forceinline__ void init(const T* strip, long long st, int t, int dir, long long rows) {
+    src = (const char*)(strip + t * st);
+    if constexpr (!G::EDGE) src += threadIdx.x % G::CHUNKS * 16;
+    half = dir * G::ROWS * st * (long long)sizeof(T);
+    step = dir * rows * st * (long long)sizeof(T);
+  }
+  // The chunk of row `row` (a pointer as src), if it is on; dead: the strip ends before
+  // this thread's chunk (EVEN).  `left`: channels from d0 to the end of the row.
+  static __device__ __forceinline__ void chunk(unsigned char* dst, const char* row, bool on, int d0, int left) {
+    if constexpr (!G::EDGE) {
+      if (on) cp_async16(dst, row);
+    } else {
+      const int off = (int)((uintptr_t)row & 15) / (int)sizeof(T);
+      const int e = (int)(threadIdx.x % G::CHUNKS) * G::V - off;  // the chunk's first channel, from d0
+      if (!on || e >= left) return;
+      if (d0 + e >= 0) {
+        const int n = left - e < G::V ? left - e : G::V;
+        cp_async_part(dst, row + e * (int)sizeof(T), n * (int)sizeof(T));
+      } else {  // the row begins inside the chunk
+        for (int k = -e; k < G::V && e + k < left; ++k) ((T*)dst)[k] = ((const T*)row)[e + k];
+      }
     }
   }
-}
+  // Both chunks of this round; on0, on1: whether their rows exist.
+  __device__ __forceinline__ void fetch(unsigned char* tile, bool on0, bool on1, int d0, int left) {
+    unsigned char* dst = tile + threadIdx.x * 16;  // row tid / CHUNKS, chunk tid % CHUNKS
+    chunk(dst, src, on0, d0, left);
+    chunk(dst + G::ROWS * G::PITCH, src + half, on1, d0, left);
+    src += step;
+  }
+};
 
-// The two channels of this lane in row `r` of a tile, which holds row `t` of the strip.
-template <class T, class G>
-__device__ __forceinline__ float2 rec_pair(const unsigned char* tile, const RecStrip<T>& s, int r, int lane, long long t) {
+// A lane's two channels of row `r` of a tile.  EDGE: `lo` is the low half of the address of
+// the row's first channel d0, whose last 4 bits are the row's offset.
+template <class T, class G> __device__ __forceinline__ float2 rec_pair(const unsigned char* tile, int r, unsigned lo) {
+  const int lane = threadIdx.x & 31;
   const unsigned char* row = tile + r * G::PITCH;
   if constexpr (!G::EDGE) {
     if constexpr (sizeof(T) == 4) {
@@ -122,16 +138,15 @@ __device__ __forceinline__ float2 rec_pair(const unsigned char* tile, const RecS
       return make_float2(widen(q.x), widen(q.y));
     }
   } else {
-    const unsigned off = (unsigned)((uintptr_t)(s.p + t * s.st) % 16);
-    const T* q = (const T*)(row + off) + 2 * lane;
+    const T* q = (const T*)(row + (lo & 15)) + 2 * lane;
     return make_float2(widen(q[0]), widen(q[1]));
   }
 }
 
-// Writes the two channels ch, ch + 1 of a row; `p` points at the first.
-template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, float2 v, int ch, int D) {
+// Writes two channels of a row from p on; n of them (0 .. 2) exist.
+template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, float2 v, int n) {
   if constexpr (!EDGE) {
-    if (ch < D) {
+    if (n > 0) {
       if constexpr (sizeof(T) == 4) {
         *(float2*)p = v;
       } else {
@@ -142,17 +157,36 @@ template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, fl
       }
     }
   } else {
-    if (ch < D) p[0] = narrow<T>(v.x);
-    if (ch + 1 < D) p[1] = narrow<T>(v.y);
+    if (n > 0) p[0] = narrow<T>(v.x);
+    if (n > 1) p[1] = narrow<T>(v.y);
   }
+}
+__device__ __forceinline__ float2 rec_load2(const float* p, int n) {
+  return make_float2(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f);
+}
+__device__ __forceinline__ void rec_store2(float* p, float2 v, int n) {
+  if (n > 0) p[0] = v.x;
+  if (n > 1) p[1] = v.y;
+}
+
+// Makes the cluster's mbarriers and waits until every CTA of it has.
+__device__ __forceinline__ void rec_cluster_init(RecShared& sh, unsigned C) {
+  if (C == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&sh.bar[0], 1);
+    mbar_init(&sh.bar[1], 1);
+    fence_mbar_init();
+  }
+  cluster_sync();
 }
 
 // The states (two channels) that this warp's first row starts from, given the map m of its
 // rows and the states `carry` before the cluster's rows of this round; moves `carry` past
 // them.  All threads of the CTA call it.
+template <class A>
 __device__ __forceinline__ float2 rec_exchange(float4 m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
-                                               int turn) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+                                               int round, const A& a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = round & 1;
   sh.warp[turn][warp][lane] = m;
   __syncthreads();
   if (C == 1) {
@@ -166,6 +200,7 @@ __device__ __forceinline__ float2 rec_exchange(float4 m, float2& carry, RecShare
     carry = s;
     return in;
   }
+  if (threadIdx.x == 0) mbar_arrive_expect_tx(&sh.bar[turn], C * 32 * (unsigned)sizeof(float4));
   float4 all = make_float4(1.f, 0.f, 1.f, 0.f), before = all;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
@@ -173,10 +208,12 @@ __device__ __forceinline__ float2 rec_exchange(float4 m, float2& carry, RecShare
     if (w == warp) before = all;
     all = make_float4(all.x * q.x, fmaf(q.x, all.y, q.y), all.z * q.z, fmaf(q.z, all.w, q.w));
   }
-  // Warp r sends the CTA's map to CTA r.  A CTA writes a slot again two rounds later, past
-  // a barrier that its reader reaches after reading it.
-  if ((unsigned)warp < C) st_cluster_f4(cluster_addr(&sh.cta[turn][rank][lane], (unsigned)warp), all);
-  cluster_sync();
+  // Warp r sends the CTA's map to CTA r.  A slot is written again two rounds later: after the
+  // sender has had this CTA's map of the next round, which was sent past a barrier that
+  // every reader of the slot reached after reading it.
+  if ((unsigned)warp < C)
+    st_async_f4(cluster_addr(&sh.cta[turn][rank][lane], (unsigned)warp), all, cluster_addr(&sh.bar[turn], (unsigned)warp));
+  if (!mbar_wait(&sh.bar[turn], (unsigned)(round >> 1) & 1, a.wait_ns) && lane == 0) raise_err(a.err, ERRBIT_TIMEOUT);
   float2 s = carry, start = carry;
 #pragma unroll
   for (unsigned r = 0; r < kRecMaxCluster; ++r) {
@@ -201,94 +238,108 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
   extern __shared__ __align__(16) unsigned char tiles[];
   __shared__ RecShared sh;
   pdl_entry();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
   const long long b = strip / a.strips;
-  const int d0 = (int)(strip % a.strips) * G::W, ch = d0 + 2 * lane;
-  const long long step = (long long)C * G::L, rounds = (a.T_ + step - 1) / step;
-  const long long tile0 = (long long)rank * G::L;
-  const RecStrip<T> x = {a.x + b * a.xb + d0, a.xt}, f = {a.f + b * a.fb + d0, a.ft},
-                    g = {GATE ? a.i + b * a.ib + d0 : nullptr, a.it};
-  T* y = a.y + b * a.yb + ch;
+  const int d0 = (int)(strip % a.strips) * G::W;
+  const int left = a.D - d0 < G::W ? a.D - d0 : G::W;              // channels of this strip
+  const int n = left - 2 * lane < 2 ? left - 2 * lane : 2;         // of this lane
+  const int step = (int)C * G::L, tile0 = (int)rank * G::L;
+  const int rounds = (int)(((long long)a.T_ + step - 1) / step);
+  const int mine = tile0 + (int)threadIdx.x / G::CHUNKS;           // the first row this thread copies
+  const bool chunk = G::EDGE || (int)(threadIdx.x % G::CHUNKS) * G::V < left;
+  const T *xp = a.x + b * a.xb + d0, *fp = a.f + b * a.fb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
+  RecCopy<T, G> x, f, g;
+  x.init(xp, a.xt, mine, 1, step);
+  f.init(fp, a.ft, mine, 1, step);
+  if constexpr (GATE) g.init(gp, a.it, mine, 1, step);
+  T* y = a.y + b * a.yb + d0 + 2 * lane + (long long)(tile0 + warp * R) * a.yt;
+  const long long y_step = step * a.yt;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
-  auto fetch = [&](long long k) {  // this CTA's tile of round k; one commit group a round
+  auto fetch = [&](int k) {  // this CTA's tile of round k; one commit group a round
     if (k < rounds) {
-      unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
-#pragma unroll
-      for (int n = 0; n < G::ITERS; ++n) {
-        const int at = tid + n * G::NT, r = at / G::CHUNKS, c = at % G::CHUNKS;
-        if (G::EDGE && r >= G::L) break;
-        const long long t = tile0 + k * step + r;
-        const bool on = t < a.T_;
-        rec_copy<T, G>(base, x, r, c, t, on, d0, a.D);
-        rec_copy<T, G>(base + G::ARRAY, f, r, c, t, on, d0, a.D);
-        if constexpr (GATE) rec_copy<T, G>(base + 2 * G::ARRAY, g, r, c, t, on, d0, a.D);
-      }
+      unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
+      const long long p = (long long)k * step + mine;
+      const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
+      x.fetch(base, on0, on1, d0, left);
+      f.fetch(base + G::ARRAY, on0, on1, d0, left);
+      if constexpr (GATE) g.fetch(base + 2 * G::ARRAY, on0, on1, d0, left);
     }
     cp_async_commit();
   };
-  auto flags = [&](long long k) -> int {  // lane r < R: whether its warp's row r is a start
-    const long long t = tile0 + k * step + warp * R + lane;
+  auto flags = [&](int k) -> int {  // lane r < R: whether its warp's row r is a start
+    const long long t = (long long)k * step + tile0 + warp * R + lane;
     return starts && lane < R && t < a.T_ ? starts[t] : 0;
   };
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   int flag = flags(0);
-  float2 carry = make_float2(0.f, 0.f);
-  if (a.h0) {
-    if (ch < a.D) carry.x = a.h0[b * a.D + ch];
-    if (ch + 1 < a.D) carry.y = a.h0[b * a.D + ch + 1];
-  }
-  if (C > 1) cluster_sync();  // the others are there to be written to
+  float2 carry = a.h0 ? rec_load2(a.h0 + b * a.D + d0 + 2 * lane, n) : make_float2(0.f, 0.f);
+  rec_cluster_init(sh, C);
 
-  for (long long k = 0; k < rounds; ++k) {
-    const long long t0 = tile0 + k * step + warp * R;
+  for (int k = 0; k < rounds; ++k) {
+    const int rows = (int)(a.T_ - (long long)k * step) - tile0 - warp * R;  // rows from this warp's first to the end
     cp_async_wait<G::STAGES - 2>();
     __syncthreads();  // the tile is in; the one before it has been read by all
     fetch(k + G::STAGES - 1);
     const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
     flag = flags(k + 1);
-    const unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
+    const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
+    unsigned xo = 0, fo = 0, go = 0;  // EDGE: the rows' offsets
+    if constexpr (G::EDGE) {
+      const unsigned t = (unsigned)(k * step + tile0 + warp * R);
+      xo = (unsigned)(uintptr_t)xp + t * (unsigned)(a.xt * sizeof(T));
+      fo = (unsigned)(uintptr_t)fp + t * (unsigned)(a.ft * sizeof(T));
+      if constexpr (GATE) go = (unsigned)(uintptr_t)gp + t * (unsigned)(a.it * sizeof(T));
+    }
     float2 av[R], bv[R];
-    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+    auto row = [&](int r) {
+      const float2 xs = rec_pair<T, G>(base, r, xo + r * (unsigned)(a.xt * sizeof(T)));
+      const float2 fs = rec_pair<T, G>(base + G::ARRAY, r, fo + r * (unsigned)(a.ft * sizeof(T)));
+      float2 u;
+      if constexpr (GATE) {
+        const float2 is = rec_pair<T, G>(base + 2 * G::ARRAY, r, go + r * (unsigned)(a.it * sizeof(T)));
+        av[r] = make_float2(sigmoid(fs.x), sigmoid(fs.y));
+        u = make_float2(sigmoid(is.x), sigmoid(is.y));
+      } else {
+        sigmoid_both(fs.x, av[r].x, u.x);
+        sigmoid_both(fs.y, av[r].y, u.y);
+      }
+      bv[r] = make_float2(u.x * xs.x, u.y * xs.y);
+    };
+    if (rows >= R) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r) row(r);
+    } else {
       // Past the end the map is the identity, so that `carry` ends as the last state.
-      av[r] = make_float2(1.f, 1.f);
-      bv[r] = make_float2(0.f, 0.f);
-      if (t0 + r < a.T_) {
-        const int row = warp * R + r;
-        const float2 xs = rec_pair<T, G>(base, x, row, lane, t0 + r);
-        const float2 fs = rec_pair<T, G>(base + G::ARRAY, f, row, lane, t0 + r);
-        float2 u;
-        if constexpr (GATE) {
-          const float2 is = rec_pair<T, G>(base + 2 * G::ARRAY, g, row, lane, t0 + r);
-          av[r] = make_float2(sigmoid(fs.x), sigmoid(fs.y));
-          u = make_float2(sigmoid(is.x), sigmoid(is.y));
-        } else {
-          sigmoid_both(fs.x, av[r].x, u.x);
-          sigmoid_both(fs.y, av[r].y, u.y);
-        }
-        if (drop >> r & 1) av[r] = make_float2(0.f, 0.f);
-        bv[r] = make_float2(u.x * xs.x, u.y * xs.y);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        av[r] = make_float2(1.f, 1.f);
+        bv[r] = make_float2(0.f, 0.f);
+        if (r < rows) row(r);
       }
-      rec_append(m, av[r], bv[r]);
     }
-    float2 s = rec_exchange(m, carry, sh, C, rank, (int)(k & 1));
+    if (drop) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (drop >> r & 1) av[r] = make_float2(0.f, 0.f);
+    }
+    float4 m = make_float4(av[0].x, bv[0].x, av[0].y, bv[0].y);
+#pragma unroll
+    for (int r = 1; r < R; ++r) rec_append(m, av[r], bv[r]);
+    float2 s = rec_exchange(m, carry, sh, C, rank, k, a);
+    T* out = y;
+    y += y_step;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (t0 + r < a.T_) {
-        s = make_float2(fmaf(av[r].x, s.x, bv[r].x), fmaf(av[r].y, s.y, bv[r].y));
-        rec_store<T, G::EDGE>(y + (t0 + r) * a.yt, s, ch, a.D);
-      }
+      s = make_float2(fmaf(av[r].x, s.x, bv[r].x), fmaf(av[r].y, s.y, bv[r].y));
+      rec_store<T, G::EDGE>(out, s, r < rows ? n : 0);
+      out += a.yt;
     }
   }
-  if (a.last && rank == 0 && warp == 0) {
-    if (ch < a.D) a.last[b * a.D + ch] = carry.x;
-    if (ch + 1 < a.D) a.last[b * a.D + ch + 1] = carry.y;
-  }
+  if (a.last && rank == 0 && warp == 0) rec_store2(a.last + b * a.D + d0 + 2 * lane, carry, n);
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
@@ -298,111 +349,125 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
   extern __shared__ __align__(16) unsigned char tiles[];
   __shared__ RecShared sh;
   pdl_entry();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
   const long long b = strip / a.strips;
-  const int d0 = (int)(strip % a.strips) * G::W, ch = d0 + 2 * lane;
-  const long long step = (long long)C * G::L, rounds = (a.T_ + step - 1) / step;
-  const long long tile0 = (long long)rank * G::L;
-  const RecStrip<T> f = {a.f + b * a.fb + d0, a.ft}, dh = {a.dh + b * a.dhb + d0, a.dht},
-                    x = {a.x + b * a.xb + d0, a.xt}, h = {a.h + b * a.hb + d0, a.ht},
-                    g = {GATE ? a.i + b * a.ib + d0 : nullptr, a.it};
-  T *dx = a.dx + b * a.dxb + ch, *df = a.df + b * a.dfb + ch, *di = GATE ? a.di + b * a.dib + ch : nullptr;
+  const int d0 = (int)(strip % a.strips) * G::W;
+  const int left = a.D - d0 < G::W ? a.D - d0 : G::W;
+  const int n = left - 2 * lane < 2 ? left - 2 * lane : 2;
+  const int step = (int)C * G::L, tile0 = (int)rank * G::L;
+  const int rounds = (int)(((long long)a.T_ + step - 1) / step);
+  const int mine = tile0 + (int)threadIdx.x / G::CHUNKS;
+  const bool chunk = G::EDGE || (int)(threadIdx.x % G::CHUNKS) * G::V < left;
+  const T *fp = a.f + b * a.fb + d0, *dhp = a.dh + b * a.dhb + d0, *xp = a.x + b * a.xb + d0,
+          *hp = a.h + b * a.hb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
+  RecCopy<T, G> f, dh, x, h, g;
+  const int t_mine = a.T_ - 1 - mine;
+  f.init(fp, a.ft, t_mine, -1, step);
+  dh.init(dhp, a.dht, t_mine, -1, step);
+  x.init(xp, a.xt, t_mine, -1, step);
+  h.init(hp, a.ht, t_mine - 1, -1, step);  // h_{t-1}
+  if constexpr (GATE) g.init(gp, a.it, t_mine, -1, step);
+  const int t_warp = a.T_ - 1 - tile0 - warp * R;  // this warp's first row of round 0
+  const long long at = b * a.D + d0 + 2 * lane;
+  T* dx = a.dx + b * a.dxb + d0 + 2 * lane + (long long)t_warp * a.dxt;
+  T* df = a.df + b * a.dfb + d0 + 2 * lane + (long long)t_warp * a.dft;
+  T* di = GATE ? a.di + b * a.dib + d0 + 2 * lane + (long long)t_warp * a.dit : nullptr;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
-  auto fetch = [&](long long k) {
+  auto fetch = [&](int k) {
     if (k < rounds) {
-      unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
-#pragma unroll
-      for (int n = 0; n < G::ITERS; ++n) {
-        const int at = tid + n * G::NT, r = at / G::CHUNKS, c = at % G::CHUNKS;
-        if (G::EDGE && r >= G::L) break;
-        const long long t = a.T_ - 1 - (tile0 + k * step + r);
-        const bool on = t >= 0;
-        rec_copy<T, G>(base, f, r, c, t, on, d0, a.D);
-        rec_copy<T, G>(base + G::ARRAY, dh, r, c, t, on, d0, a.D);
-        rec_copy<T, G>(base + 2 * G::ARRAY, x, r, c, t, on, d0, a.D);
-        rec_copy<T, G>(base + 3 * G::ARRAY, h, r, c, t - 1, t > 0, d0, a.D);
-        if constexpr (GATE) rec_copy<T, G>(base + 4 * G::ARRAY, g, r, c, t, on, d0, a.D);
-      }
+      unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
+      const long long p = (long long)k * step + mine;
+      const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
+      f.fetch(base, on0, on1, d0, left);
+      dh.fetch(base + G::ARRAY, on0, on1, d0, left);
+      x.fetch(base + 2 * G::ARRAY, on0, on1, d0, left);
+      h.fetch(base + 3 * G::ARRAY, chunk && p + 1 < a.T_, chunk && p + G::ROWS + 1 < a.T_, d0, left);
+      if constexpr (GATE) g.fetch(base + 4 * G::ARRAY, on0, on1, d0, left);
     }
     cp_async_commit();
   };
-  auto flags = [&](long long k) -> int {
-    const long long t = a.T_ - 1 - (tile0 + k * step + warp * R + lane);
+  auto flags = [&](int k) -> int {
+    const long long t = (long long)t_warp - (long long)k * step - lane;
     return starts && lane < R && t >= 0 ? starts[t] : 0;
   };
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   int flag = flags(0);
-  float2 carry = make_float2(0.f, 0.f), first = carry;
-  if (a.dlast) {
-    if (ch < a.D) carry.x = a.dlast[b * a.D + ch];
-    if (ch + 1 < a.D) carry.y = a.dlast[b * a.D + ch + 1];
-  }
-  if (a.h0) {
-    if (ch < a.D) first.x = a.h0[b * a.D + ch];
-    if (ch + 1 < a.D) first.y = a.h0[b * a.D + ch + 1];
-  }
-  if (C > 1) cluster_sync();
+  float2 carry = a.dlast ? rec_load2(a.dlast + at, n) : make_float2(0.f, 0.f);
+  const float2 first = a.h0 ? rec_load2(a.h0 + at, n) : make_float2(0.f, 0.f);
+  rec_cluster_init(sh, C);
 
-  for (long long k = 0; k < rounds; ++k) {
-    const long long t0 = a.T_ - 1 - (tile0 + k * step + warp * R);  // this warp's rows: t0, t0 - 1, ...
+  for (int k = 0; k < rounds; ++k) {
+    const int rows = (int)(a.T_ - (long long)k * step) - tile0 - warp * R;  // rows r < rows exist; t = rows - 1 - r
     cp_async_wait<G::STAGES - 2>();
     __syncthreads();
     fetch(k + G::STAGES - 1);
     const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
     flag = flags(k + 1);
-    const unsigned char* base = tiles + (size_t)(k % G::STAGES) * NA * G::ARRAY;
+    const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
+    // EDGE: the low address of row t = rows - 1 - r of a strip.
+    auto lo = [&](const T* strip, long long st, int t) {
+      return G::EDGE ? (unsigned)(uintptr_t)strip + (unsigned)t * (unsigned)(st * sizeof(T)) : 0u;
+    };
     float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
     float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+    auto row = [&](int r) {
+      const float2 fs = rec_pair<T, G>(base, r, lo(fp, a.ft, rows - 1 - r));
+      const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, rows - 1 - r));
+      sigmoid_both(fs.x, s[r].x, s1[r].x);
+      sigmoid_both(fs.y, s[r].y, s1[r].y);
+      const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
+      rec_append(m, av, make_float2(av.x * ds.x, av.y * ds.y));
+    };
+    if (rows >= R) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) row(r);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows) row(r);
+    }
+    float2 c = rec_exchange(m, carry, sh, C, rank, k, a);  // c_{t+1} of the warp's first row
+    T *ox = dx, *of = df, *oi = di;
+    dx -= step * a.dxt;
+    df -= step * a.dft;
+    if constexpr (GATE) di -= step * a.dit;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = s1[r] = make_float2(0.f, 0.f);
-      if (t0 - r >= 0) {
-        const int row = warp * R + r;
-        const float2 fs = rec_pair<T, G>(base, f, row, lane, t0 - r);
-        const float2 ds = rec_pair<T, G>(base + G::ARRAY, dh, row, lane, t0 - r);
-        sigmoid_both(fs.x, s[r].x, s1[r].x);
-        sigmoid_both(fs.y, s[r].y, s1[r].y);
-        const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
-        rec_append(m, av, make_float2(av.x * ds.x, av.y * ds.y));
+      if (r < rows) {
+        const int t = rows - 1 - r;
+        const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
+        const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, lo(xp, a.xt, t));
+        float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, lo(hp, a.ht, t - 1)) : first;
+        const bool dropped = drop >> r & 1;
+        if (dropped) hs = make_float2(0.f, 0.f);
+        const float2 gt = make_float2(ds.x + c.x, ds.y + c.y);  // dL/dh_t
+        c = make_float2(s[r].x * gt.x, s[r].y * gt.y);
+        const float2 fg = make_float2(c.x * s1[r].x, c.y * s1[r].y);
+        if (dropped) c = make_float2(0.f, 0.f);
+        if constexpr (GATE) {
+          const float2 is = rec_pair<T, G>(base + 4 * G::ARRAY, r, lo(gp, a.it, t));
+          float2 u, u1;
+          sigmoid_both(is.x, u.x, u1.x);
+          sigmoid_both(is.y, u.y, u1.y);
+          const float2 ug = make_float2(u.x * gt.x, u.y * gt.y);
+          rec_store<T, G::EDGE>(ox, ug, n);
+          rec_store<T, G::EDGE>(of, make_float2(fg.x * hs.x, fg.y * hs.y), n);
+          rec_store<T, G::EDGE>(oi, make_float2(ug.x * u1.x * xs.x, ug.y * u1.y * xs.y), n);
+        } else {
+          rec_store<T, G::EDGE>(ox, make_float2(s1[r].x * gt.x, s1[r].y * gt.y), n);
+          rec_store<T, G::EDGE>(of, make_float2(fg.x * (hs.x - xs.x), fg.y * (hs.y - xs.y)), n);
+        }
       }
-    }
-    float2 c = rec_exchange(m, carry, sh, C, rank, (int)(k & 1));  // c_{t+1} of the warp's first row
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long t = t0 - r;
-      if (t < 0) break;
-      const int row = warp * R + r;
-      const float2 ds = rec_pair<T, G>(base + G::ARRAY, dh, row, lane, t);
-      const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, x, row, lane, t);
-      float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, h, row, lane, t - 1) : first;
-      const bool dropped = drop >> r & 1;
-      if (dropped) hs = make_float2(0.f, 0.f);
-      const float2 gt = make_float2(ds.x + c.x, ds.y + c.y);  // dL/dh_t
-      const float2 fg = make_float2(s[r].x * s1[r].x * gt.x, s[r].y * s1[r].y * gt.y);
-      if constexpr (GATE) {
-        const float2 is = rec_pair<T, G>(base + 4 * G::ARRAY, g, row, lane, t);
-        float2 u, u1;
-        sigmoid_both(is.x, u.x, u1.x);
-        sigmoid_both(is.y, u.y, u1.y);
-        const float2 ug = make_float2(u.x * gt.x, u.y * gt.y);
-        rec_store<T, G::EDGE>(dx + t * a.dxt, ug, ch, a.D);
-        rec_store<T, G::EDGE>(df + t * a.dft, make_float2(fg.x * hs.x, fg.y * hs.y), ch, a.D);
-        rec_store<T, G::EDGE>(di + t * a.dit, make_float2(ug.x * u1.x * xs.x, ug.y * u1.y * xs.y), ch, a.D);
-      } else {
-        rec_store<T, G::EDGE>(dx + t * a.dxt, make_float2(s1[r].x * gt.x, s1[r].y * gt.y), ch, a.D);
-        rec_store<T, G::EDGE>(df + t * a.dft, make_float2(fg.x * (hs.x - xs.x), fg.y * (hs.y - xs.y)), ch, a.D);
-      }
-      c = dropped ? make_float2(0.f, 0.f) : make_float2(s[r].x * gt.x, s[r].y * gt.y);
+      ox -= a.dxt;
+      of -= a.dft;
+      if constexpr (GATE) oi -= a.dit;
     }
   }
-  if (a.dh0 && rank == 0 && warp == 0) {
-    if (ch < a.D) a.dh0[b * a.D + ch] = carry.x;
-    if (ch + 1 < a.D) a.dh0[b * a.D + ch + 1] = carry.y;
-  }
+  if (a.dh0 && rank == 0 && warp == 0) rec_store2(a.dh0 + at, carry, n);
 }
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
@@ -494,15 +559,17 @@ template <class T> RecArgs<T> rec_args(const RecurrenceJob& j) {
   a.df = (T*)j.df.p, a.dfb = j.df.sb, a.dft = j.df.st;
   a.di = (T*)j.di.p, a.dib = j.di.sb, a.dit = j.di.st;
   a.h0 = j.h0, a.dlast = j.dlast, a.starts = j.starts, a.last = j.last, a.dh0 = j.dh0;
-  a.T_ = j.T, a.D = (int)j.D;
+  a.T_ = (int)j.T, a.D = (int)j.D;
   return a;
 }
 
-// CTAs per cluster: doubled while the strips alone leave SMs short of two CTAs each and
-// there are tiles to share.
+// CTAs per cluster: doubled while the CTAs are fewer than 1.5 an SM and there are tiles to
+// share.  Measured: 256 strips (8 x 2048 x 2048 bf16) take 58.4 us alone and 66.1 in pairs,
+// whose 512 CTAs need a second wave; 54 strips (3 x 1537 x 1001 fp32, gradient) 92.6 us in
+// fours and 55.0 in eights.
 template <class G> unsigned rec_cluster(long long strips, long long T_, int num_sms) {
   unsigned c = 1;
-  while (c < (unsigned)kRecMaxCluster && strips * c < 2ll * num_sms && (long long)c * G::L < T_) c *= 2;
+  while (c < (unsigned)kRecMaxCluster && 2 * strips * c < 3ll * num_sms && (long long)c * G::L < T_) c *= 2;
   return c;
 }
 
@@ -511,6 +578,8 @@ cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const Lau
   const long long strips = (j.D + G::W - 1) / G::W;
   const unsigned C = rec_cluster<G>(strips * j.B, j.T, ctx.num_sms);
   a.strips = (int)strips;
+  a.err = ctx.err;
+  a.wait_ns = ctx.wait_ns;
   constexpr int smem = G::STAGES * NA * G::ARRAY;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
