@@ -45,7 +45,13 @@ __device__ __forceinline__ void sigmoid_both(float z, float& s, float& c) {
   s = rcp(1.f + e);
   c = e * s;
 }
-
+__device__ __forceinline__ void sigmoid_both(float2 z, float2& s, float2& c) {
+  const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
+  const float2 e = make_float2(ex2(min_nan(x.x, 125.f)), ex2(min_nan(x.y, 125.f)));
+  const float2 d = add2(e, make_float2(1.f, 1.f));
+  s = make_float2(rcp(d.x), rcp(d.y));
+  c = mul2(e, s);
+}
 template <class T> struct RecArgs {
   const T *x, *f, *i, *h, *dh;  // backward reads h and dh
   T *y, *dx, *df, *di;          // forward writes y
@@ -58,8 +64,13 @@ template <class T> struct RecArgs {
   unsigned long long wait_ns;
 };
 
-// sigmoid(z) alone: 1 / (1 + exp(-z)); exp(-z) may overflow to infinity, which gives 0.
+// sigmoid(z) alone: exp(-z) may overflow to infinity, which gives 0.
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
+__device__ __forceinline__ float2 sigmoid(float2 z) {
+  const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
+  const float2 d = add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
 
 constexpr int kRecMaxCluster = 8;
 
@@ -79,10 +90,21 @@ template <class T, bool EDGE_, int STAGES_> struct RecGeom {
   static_assert(L == 2 * ROWS, "each thread copies two rows' chunks of each array");
 };
 
-// The maps (A, B of two channels) that threads exchange; two rounds in turn.
+// Two channels' map y -> a y + b.
+struct RecMap {
+  float2 a, b;
+};
+__device__ __forceinline__ float2 rec_apply(RecMap m, float2 s) { return fma2(m.a, s, m.b); }
+// m, then q.
+__device__ __forceinline__ RecMap rec_then(RecMap m, RecMap q) { return {mul2(m.a, q.a), fma2(q.a, m.b, q.b)}; }
+__device__ __forceinline__ float4 rec_pack(RecMap m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
+__device__ __forceinline__ RecMap rec_unpack(float4 q) { return {make_float2(q.x, q.y), make_float2(q.z, q.w)}; }
+
+// What threads exchange; two rounds in turn.
 struct RecShared {
-  float4 warp[2][8][32];              // of each warp's rows
-  float4 cta[2][kRecMaxCluster][32];  // of each CTA's tile
+  float4 warp[2][8][32];              // the map of each warp's rows
+  float4 cta[2][kRecMaxCluster][32];  // the map of each CTA's tile
+  float2 carry[2][32];                // C = 1: the state before the round's rows
   unsigned long long bar[2];          // the cluster's maps have arrived
 };
 
@@ -181,55 +203,49 @@ __device__ __forceinline__ void rec_cluster_init(RecShared& sh, unsigned C) {
 }
 
 // The states (two channels) that this warp's first row starts from, given the map m of its
-// rows and the states `carry` before the cluster's rows of this round; moves `carry` past
-// them.  All threads of the CTA call it.
+// rows.  `carry` is the state before the cluster's rows of this round, moved past them in
+// warp 7 (C = 1, where the others read it from shared memory) or in all (C > 1).  All
+// threads of the CTA call it.
 template <class A>
-__device__ __forceinline__ float2 rec_exchange(float4 m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
+__device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
                                                int round, const A& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = round & 1;
-  sh.warp[turn][warp][lane] = m;
-  __syncthreads();
+  if (warp < 7) sh.warp[turn][warp][lane] = rec_pack(m);
   if (C == 1) {
-    float2 s = carry, in = carry;
+    if (warp == 7) sh.carry[turn][lane] = carry;
+    __syncthreads();
+    float2 s = sh.carry[turn][lane];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float4 q = sh.warp[turn][w][lane];
-      if (w == warp) in = s;
-      s = make_float2(fmaf(q.x, s.x, q.y), fmaf(q.z, s.y, q.w));
-    }
-    carry = s;
-    return in;
+    for (int w = 0; w < 7; ++w)
+      if (w < warp) s = rec_apply(rec_unpack(sh.warp[turn][w][lane]), s);
+    if (warp == 7) carry = rec_apply(m, s);
+    return s;
   }
-  if (threadIdx.x == 0) mbar_arrive_expect_tx(&sh.bar[turn], C * 32 * (unsigned)sizeof(float4));
-  float4 all = make_float4(1.f, 0.f, 1.f, 0.f), before = all;
+  __syncthreads();
+  RecMap before = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    const float4 q = sh.warp[turn][w][lane];
-    if (w == warp) before = all;
-    all = make_float4(all.x * q.x, fmaf(q.x, all.y, q.y), all.z * q.z, fmaf(q.z, all.w, q.w));
+  for (int w = 0; w < 7; ++w)
+    if (w < warp) before = rec_then(before, rec_unpack(sh.warp[turn][w][lane]));
+  if (warp == 7) {
+    // The CTA's map goes to every CTA of the cluster.  A slot is written again two rounds
+    // later: after the sender has had this CTA's map of the next round, which was sent past
+    // a barrier that every reader of the slot reached after reading it.
+    if (lane == 0) mbar_arrive_expect_tx(&sh.bar[turn], C * 32 * (unsigned)sizeof(float4));
+    const float4 all = rec_pack(rec_then(before, m));
+    for (unsigned r = 0; r < C; ++r)
+      st_async_f4(cluster_addr(&sh.cta[turn][rank][lane], r), all, cluster_addr(&sh.bar[turn], r));
   }
-  // Warp r sends the CTA's map to CTA r.  A slot is written again two rounds later: after the
-  // sender has had this CTA's map of the next round, which was sent past a barrier that
-  // every reader of the slot reached after reading it.
-  if ((unsigned)warp < C)
-    st_async_f4(cluster_addr(&sh.cta[turn][rank][lane], (unsigned)warp), all, cluster_addr(&sh.bar[turn], (unsigned)warp));
   if (!mbar_wait(&sh.bar[turn], (unsigned)(round >> 1) & 1, a.wait_ns) && lane == 0) raise_err(a.err, ERRBIT_TIMEOUT);
   float2 s = carry, start = carry;
 #pragma unroll
   for (unsigned r = 0; r < kRecMaxCluster; ++r) {
     if (r < C) {
-      const float4 q = sh.cta[turn][r][lane];
       if (r == rank) start = s;
-      s = make_float2(fmaf(q.x, s.x, q.y), fmaf(q.z, s.y, q.w));
+      s = rec_apply(rec_unpack(sh.cta[turn][r][lane]), s);
     }
   }
   carry = s;
-  return make_float2(fmaf(before.x, start.x, before.y), fmaf(before.z, start.y, before.w));
-}
-
-// Appends the map (a, b) of one row to m, for both channels.
-__device__ __forceinline__ void rec_append(float4& m, float2 a, float2 b) {
-  m = make_float4(m.x * a.x, fmaf(a.x, m.y, b.x), m.z * a.y, fmaf(a.y, m.w, b.y));
+  return rec_apply(before, start);
 }
 
 template <class T, bool GATE, class G>
@@ -298,16 +314,14 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     auto row = [&](int r) {
       const float2 xs = rec_pair<T, G>(base, r, xo + r * (unsigned)(a.xt * sizeof(T)));
       const float2 fs = rec_pair<T, G>(base + G::ARRAY, r, fo + r * (unsigned)(a.ft * sizeof(T)));
-      float2 u;
       if constexpr (GATE) {
-        const float2 is = rec_pair<T, G>(base + 2 * G::ARRAY, r, go + r * (unsigned)(a.it * sizeof(T)));
-        av[r] = make_float2(sigmoid(fs.x), sigmoid(fs.y));
-        u = make_float2(sigmoid(is.x), sigmoid(is.y));
+        av[r] = sigmoid(fs);
+        bv[r] = mul2(sigmoid(rec_pair<T, G>(base + 2 * G::ARRAY, r, go + r * (unsigned)(a.it * sizeof(T)))), xs);
       } else {
-        sigmoid_both(fs.x, av[r].x, u.x);
-        sigmoid_both(fs.y, av[r].y, u.y);
+        float2 u;
+        sigmoid_both(fs, av[r], u);
+        bv[r] = mul2(u, xs);
       }
-      bv[r] = make_float2(u.x * xs.x, u.y * xs.y);
     };
     if (rows >= R) {
 #pragma unroll
@@ -326,20 +340,27 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
       for (int r = 0; r < R; ++r)
         if (drop >> r & 1) av[r] = make_float2(0.f, 0.f);
     }
-    float4 m = make_float4(av[0].x, bv[0].x, av[0].y, bv[0].y);
+    RecMap m = {av[0], bv[0]};
 #pragma unroll
-    for (int r = 1; r < R; ++r) rec_append(m, av[r], bv[r]);
+    for (int r = 1; r < R; ++r) m = rec_then(m, {av[r], bv[r]});
     float2 s = rec_exchange(m, carry, sh, C, rank, k, a);
     T* out = y;
     y += y_step;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      s = make_float2(fmaf(av[r].x, s.x, bv[r].x), fmaf(av[r].y, s.y, bv[r].y));
-      rec_store<T, G::EDGE>(out, s, r < rows ? n : 0);
+    auto write = [&](int r) {
+      s = fma2(av[r], s, bv[r]);
+      rec_store<T, G::EDGE>(out, s, n);
       out += a.yt;
+    };
+    if (rows >= R) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) write(r);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows) write(r);
     }
   }
-  if (a.last && rank == 0 && warp == 0) rec_store2(a.last + b * a.D + d0 + 2 * lane, carry, n);
+  if (a.last && rank == 0 && warp == 7) rec_store2(a.last + b * a.D + d0 + 2 * lane, carry, n);
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
@@ -413,14 +434,13 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       return G::EDGE ? (unsigned)(uintptr_t)strip + (unsigned)t * (unsigned)(st * sizeof(T)) : 0u;
     };
     float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
-    float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
+    RecMap m = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
     auto row = [&](int r) {
-      const float2 fs = rec_pair<T, G>(base, r, lo(fp, a.ft, rows - 1 - r));
       const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, rows - 1 - r));
-      sigmoid_both(fs.x, s[r].x, s1[r].x);
-      sigmoid_both(fs.y, s[r].y, s1[r].y);
+      sigmoid_both(rec_pair<T, G>(base, r, lo(fp, a.ft, rows - 1 - r)), s[r], s1[r]);
       const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
-      rec_append(m, av, make_float2(av.x * ds.x, av.y * ds.y));
+      // a c + a dh = a (c + dh), so the map's b is a (b + dh).
+      m = {mul2(m.a, av), mul2(av, add2(m.b, ds))};
     };
     if (rows >= R) {
 #pragma unroll
@@ -435,39 +455,42 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     dx -= step * a.dxt;
     df -= step * a.dft;
     if constexpr (GATE) di -= step * a.dit;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r < rows) {
-        const int t = rows - 1 - r;
-        const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
-        const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, lo(xp, a.xt, t));
-        float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, lo(hp, a.ht, t - 1)) : first;
-        const bool dropped = drop >> r & 1;
-        if (dropped) hs = make_float2(0.f, 0.f);
-        const float2 gt = make_float2(ds.x + c.x, ds.y + c.y);  // dL/dh_t
-        c = make_float2(s[r].x * gt.x, s[r].y * gt.y);
-        const float2 fg = make_float2(c.x * s1[r].x, c.y * s1[r].y);
-        if (dropped) c = make_float2(0.f, 0.f);
-        if constexpr (GATE) {
-          const float2 is = rec_pair<T, G>(base + 4 * G::ARRAY, r, lo(gp, a.it, t));
-          float2 u, u1;
-          sigmoid_both(is.x, u.x, u1.x);
-          sigmoid_both(is.y, u.y, u1.y);
-          const float2 ug = make_float2(u.x * gt.x, u.y * gt.y);
-          rec_store<T, G::EDGE>(ox, ug, n);
-          rec_store<T, G::EDGE>(of, make_float2(fg.x * hs.x, fg.y * hs.y), n);
-          rec_store<T, G::EDGE>(oi, make_float2(ug.x * u1.x * xs.x, ug.y * u1.y * xs.y), n);
-        } else {
-          rec_store<T, G::EDGE>(ox, make_float2(s1[r].x * gt.x, s1[r].y * gt.y), n);
-          rec_store<T, G::EDGE>(of, make_float2(fg.x * (hs.x - xs.x), fg.y * (hs.y - xs.y)), n);
-        }
+    auto write = [&](int r) {
+      const int t = rows - 1 - r;
+      const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
+      const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, lo(xp, a.xt, t));
+      float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, lo(hp, a.ht, t - 1)) : first;
+      const bool dropped = drop >> r & 1;
+      if (dropped) hs = make_float2(0.f, 0.f);
+      const float2 gt = add2(ds, c);  // dL/dh_t
+      c = mul2(s[r], gt);
+      const float2 fg = mul2(c, s1[r]);
+      if (dropped) c = make_float2(0.f, 0.f);
+      if constexpr (GATE) {
+        float2 u, u1;
+        sigmoid_both(rec_pair<T, G>(base + 4 * G::ARRAY, r, lo(gp, a.it, t)), u, u1);
+        const float2 ug = mul2(u, gt);
+        rec_store<T, G::EDGE>(ox, ug, n);
+        rec_store<T, G::EDGE>(of, mul2(fg, hs), n);
+        rec_store<T, G::EDGE>(oi, mul2(mul2(ug, u1), xs), n);
+      } else {
+        rec_store<T, G::EDGE>(ox, mul2(s1[r], gt), n);
+        rec_store<T, G::EDGE>(of, mul2(fg, make_float2(hs.x - xs.x, hs.y - xs.y)), n);
       }
       ox -= a.dxt;
       of -= a.dft;
       if constexpr (GATE) oi -= a.dit;
+    };
+    if (rows >= R) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) write(r);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows) write(r);
     }
   }
-  if (a.dh0 && rank == 0 && warp == 0) rec_store2(a.dh0 + at, carry, n);
+  if (a.dh0 && rank == 0 && warp == 7) rec_store2(a.dh0 + at, carry, n);
 }
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
