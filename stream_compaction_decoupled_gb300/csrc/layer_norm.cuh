@@ -5,14 +5,20 @@
 //   g = dy w:  dx = rstd (g - mean(g) - n mean(g n)),   dw = sum_rows dy n,  db = sum_rows dy.
 //
 // A row is held in the registers of TPR threads, so it is read once: the mean first, then
-// the centred squares (no cancellation), then y.  CTAs are persistent: CTA c takes rows
-// c + G k (G the grid, a multiple of 8), which has two uses.  The weight is loaded once a
-// CTA, and the gradient's sums over rows stay in registers until the CTA is done; one row
-// of partial sums a CTA is then reduced by a second, small launch, in a fixed order.  And
-// every row of a CTA starts at the same offset from a 16-byte boundary, whatever the width
-// (the offset repeats after at most 8 rows), so an odd width is read in whole 16-byte
-// packs too: the packs are laid over the row shifted by the offset, and only the first
-// and the last of a row are read value by value.
+// the centred squares (no cancellation), then y.
+//
+// Rows on 16-byte boundaries (EDGE false) are read and written in whole packs.  Forward,
+// such rows take one group of threads each, in no order: the weight comes from L1 and the
+// many resident CTAs keep the memory busy.  Otherwise CTAs are persistent: CTA c takes rows
+// c + G k (G the grid, a multiple of 8).  Every row of a CTA then starts at the same offset
+// from a 16-byte boundary, whatever the width (the offset repeats after at most 8 rows), so
+// an odd width is read in whole packs too: they are laid over the row shifted by the
+// offset, only the first and the last of a row are read value by value, and the weight,
+// shifted alike, is loaded once a CTA.
+//
+// The gradient's sums over rows stay in the registers of a persistent CTA until it is done;
+// one row of partial sums a CTA is then reduced by a second, small launch, in a fixed
+// order, so that results do not vary from run to run.
 #pragma once
 
 #include "lm.cuh"
@@ -33,26 +39,25 @@ template <class T, class P> struct NormArgs {
 };
 
 // V values a pack, TPR threads a row, NV packs a thread, NT threads a CTA.
-template <int V_, int TPR_, int NV_> struct NormGeom {
-  static constexpr int V = V_, TPR = TPR_, NV = NV_;
-  static constexpr int NT = TPR < 256 ? 256 : TPR;
+template <int V_, int TPR_, int NV_, int NT_, bool EDGE_> struct NormGeom {
+  static constexpr int V = V_, TPR = TPR_, NV = NV_, NT = NT_;
+  static constexpr bool EDGE = EDGE_;
   static constexpr int ROWS = NT / TPR;       // rows a CTA takes at a time
   static constexpr int WARPS = TPR / 32;      // warps of a row
-  // Whether the weight (and in the forward pass the next row, in the backward the row
-  // between its two passes) is held in registers.  At 32 values a thread there is no room:
-  // what is needed is read again, from L1 or L2.
-  static constexpr bool HOLD = NV * V <= 16;
-  // Where the gradient's sums over rows are kept: in registers, or, at 512 threads a row
-  // (128 registers a thread at most), in shared memory, each thread's own.
-  static constexpr bool SUMS_IN_SMEM = TPR >= 512;
-  static constexpr size_t SUMS_BYTES = SUMS_IN_SMEM ? (size_t)NT * NV * V * 2 * sizeof(float) : 0;
+  static constexpr int STEP = TPR * V;        // values between a thread's packs
 };
 
 // Values e0 .. e0 + V - 1 of a row of D values, the first of them at p; those outside the
 // row read as zero and are not written.
-template <class T, int V> __device__ __forceinline__ Pack<T, V> norm_load(const T* p, int e0, int D, bool on) {
+template <class T, class G> __device__ __forceinline__ Pack<T, G::V> norm_load(const T* p, int e0, int D, bool on) {
+  constexpr int V = G::V;
   Pack<T, V> r;
-  if (on && e0 >= 0 && e0 + V <= D) {
+  if constexpr (!G::EDGE) {
+    if (on && e0 < D) r = ld_pack<T, V>(p);
+    else
+#pragma unroll
+      for (int c = 0; c < V; ++c) r.v[c] = narrow<T>(0.f);
+  } else if (on && e0 >= 0 && e0 + V <= D) {
     r = ld_pack<T, V>(p);
   } else {
 #pragma unroll
@@ -60,13 +65,36 @@ template <class T, int V> __device__ __forceinline__ Pack<T, V> norm_load(const 
   }
   return r;
 }
-template <class T, int V> __device__ __forceinline__ void norm_store(T* p, int e0, int D, const Pack<T, V>& v) {
-  if (e0 >= 0 && e0 + V <= D) {
+template <class T, class G>
+__device__ __forceinline__ void norm_store(T* p, int e0, int D, const Pack<T, G::V>& v) {
+  if constexpr (!G::EDGE) {
+    if (e0 < D) st_pack(p, v);
+  } else if (e0 >= 0 && e0 + G::V <= D) {
     st_pack(p, v);
   } else {
 #pragma unroll
-    for (int c = 0; c < V; ++c)
+    for (int c = 0; c < G::V; ++c)
       if ((unsigned)(e0 + c) < (unsigned)D) p[c] = v.v[c];
+  }
+}
+// V parameters from e0 on; `none` outside the row and where p is null.
+template <class P, class G>
+__device__ __forceinline__ void norm_params(P (&r)[G::V], const P* p, int e0, int D, float none) {
+  if constexpr (!G::EDGE) {
+    if (p && e0 < D) {
+      constexpr int N = 16 / sizeof(P);
+#pragma unroll
+      for (int c = 0; c < G::V; c += N) {
+        const uint4 u = *(const uint4*)(p + e0 + c);
+        memcpy(r + c, &u, 16);
+      }
+      return;
+    }
+#pragma unroll
+    for (int c = 0; c < G::V; ++c) r[c] = narrow<P>(none);
+  } else {
+#pragma unroll
+    for (int c = 0; c < G::V; ++c) r[c] = p && (unsigned)(e0 + c) < (unsigned)D ? p[e0 + c] : narrow<P>(none);
   }
 }
 
@@ -84,7 +112,8 @@ template <class G> __device__ __forceinline__ float2 norm_sum(float2 v, NormShar
   if constexpr (G::WARPS > 1) {
     const int sub = threadIdx.x / G::TPR, w = threadIdx.x % G::TPR / 32;
     if (threadIdx.x % 32 == 0) sh.red[turn][sub][w] = v;
-    __syncthreads();
+    if constexpr (G::ROWS == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(sub + 1), "n"(G::TPR) : "memory");  // the row's own threads
     v = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < G::WARPS; ++k) {
@@ -97,192 +126,322 @@ template <class G> __device__ __forceinline__ float2 norm_sum(float2 v, NormShar
   return v;
 }
 
-template <class T, class P, class G>
-__global__ void __launch_bounds__(G::NT) norm_forward_kernel(const __grid_constant__ NormArgs<T, P> a) {
+// One row's statistics and output from its values in registers (zero outside the row).
+template <class T, class P, class G, class W>
+__device__ __forceinline__ void norm_row(float (&x)[G::NV][G::V], const NormArgs<T, P>& a, long long row, bool live,
+                                         int e0, NormShared<G>& sh, int& turn, W&& params) {
   constexpr int V = G::V, NV = G::NV;
-  __shared__ NormShared<G> sh;
-  pdl_entry();
-  const int t = threadIdx.x % G::TPR, sub = threadIdx.x / G::TPR;
-  const long long first = blockIdx.x;
-  if (first >= a.N) return;
-  const int off = (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T));
-  const int e0 = t * V - off;  // this thread's first value; its packs are kStep apart
-  constexpr int kStep = G::TPR * V;
-  P w[NV][V], b[NV][V];
-  auto affine = [&](int i) {
+  const float inv = 1.f / (float)a.D;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int c = 0; c < V; ++c) s += x[i][c];
+  const float mean = norm_sum<G>(make_float2(s, 0.f), sh, turn).x * inv;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool pack = e0 + i * G::STEP < a.D;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      const int e = e0 + i * kStep + c;
-      const bool in = (unsigned)e < (unsigned)a.D;
-      w[i][c] = in && a.w ? a.w[e] : narrow<P>(1.f);
-      b[i][c] = in && a.b ? a.b[e] : narrow<P>(0.f);
+      const bool in = G::EDGE ? (unsigned)(e0 + i * G::STEP + c) < (unsigned)a.D : pack;
+      x[i][c] = in ? x[i][c] - mean : 0.f;
+      q = fmaf(x[i][c], x[i][c], q);
     }
-  };
-  if constexpr (G::HOLD) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) affine(i);
   }
-  const float inv = 1.f / (float)a.D;
-  int turn = 0;
-  Pack<T, V> px[NV];
-  auto load = [&](long long row) {
-    const T* p = a.x + row * a.xs + e0;
+  const float rstd = 1.f / sqrtf(norm_sum<G>(make_float2(q, 0.f), sh, turn).x * inv + a.eps);
+  if (!live) return;
+  if (threadIdx.x % G::TPR == 0) {
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+  }
+  T* y = a.y + row * a.ys + e0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) px[i] = norm_load<T, V>(p + i * kStep, e0 + i * kStep, a.D, row < a.N);
-  };
-  const long long G_ = gridDim.x;
-  if constexpr (G::HOLD) load(first + G_ * sub);
-  for (long long base = first; base < a.N; base += G_ * G::ROWS) {
-    const long long row = base + G_ * sub;
-    const bool live = row < a.N;
-    float x[NV][V];
-    if constexpr (!G::HOLD) load(row);
+  for (int i = 0; i < NV; ++i) {
+    P w[V], b[V];
+    params(i, w, b);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) widen_pack(px[i], x[i]);
-    if constexpr (G::HOLD) load(row + G_ * G::ROWS);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int c = 0; c < V; ++c) s += x[i][c];
-    const float mean = norm_sum<G>(make_float2(s, 0.f), sh, turn).x * inv;
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        x[i][c] = (unsigned)(e0 + i * kStep + c) < (unsigned)a.D ? x[i][c] - mean : 0.f;
-        q = fmaf(x[i][c], x[i][c], q);
-      }
-    const float var = norm_sum<G>(make_float2(q, 0.f), sh, turn).x * inv;
-    const float rstd = 1.f / sqrtf(var + a.eps);
-    if (!live) continue;
-    if (t == 0) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (!G::HOLD) affine(i);
-#pragma unroll
-      for (int c = 0; c < V; ++c) x[i][c] = fmaf(x[i][c] * rstd, widen(w[i][c]), widen(b[i][c]));
-      norm_store<T, V>(a.y + row * a.ys + e0 + i * kStep, e0 + i * kStep, a.D, narrow_pack<T, V>(x[i]));
-    }
+    for (int c = 0; c < V; ++c) x[i][c] = fmaf(x[i][c] * rstd, widen(w[c]), widen(b[c]));
+    norm_store<T, G>(y + i * G::STEP, e0 + i * G::STEP, a.D, narrow_pack<T, V>(x[i]));
   }
 }
 
+// Rows on 16-byte boundaries.
+template <class T, class P, class G>
+__global__ void __launch_bounds__(G::NT) norm_forward_kernel(const __grid_constant__ NormArgs<T, P> a) {
+  static_assert(!G::EDGE, "whole packs");
+  __shared__ NormShared<G> sh;
+  pdl_entry();
+  const int e0 = (int)(threadIdx.x % G::TPR) * G::V;
+  const long long row = (long long)blockIdx.x * G::ROWS + threadIdx.x / G::TPR;
+  const bool live = row < a.N;
+  const T* p = a.x + row * a.xs + e0;
+  Pack<T, G::V> px[G::NV];
+#pragma unroll
+  for (int i = 0; i < G::NV; ++i) px[i] = norm_load<T, G>(p + i * G::STEP, e0 + i * G::STEP, a.D, live);
+  float x[G::NV][G::V];
+#pragma unroll
+  for (int i = 0; i < G::NV; ++i) widen_pack(px[i], x[i]);
+  int turn = 0;
+  norm_row<T, P, G>(x, a, row, live, e0, sh, turn, [&](int i, P(&w)[G::V], P(&b)[G::V]) {
+    norm_params<P, G>(w, a.w, e0 + i * G::STEP, a.D, 1.f);
+    norm_params<P, G>(b, a.b, e0 + i * G::STEP, a.D, 0.f);
+  });
+}
+
+// A thread's packs of the rows it takes in turn, in shared memory that is its own: filled
+// by asynchronous copies STAGES - 1 rows ahead, so that the row in hand costs no registers
+// until it is read and the memory stays busy between the reductions.  Packs outside the row
+// hold zeros.  No barrier: a thread reads what it copied.
+template <class T, class G, int ARRAYS, int STAGES_> struct NormRing {
+  static constexpr int STAGES = STAGES_;
+  static constexpr int SLOT = G::NT * 16;                       // one pack of every thread
+  static constexpr int STAGE = ARRAYS * G::NV * SLOT;
+  static constexpr int BYTES = STAGES * STAGE;
+  unsigned char* mem;
+  int e0, D;
+  __device__ __forceinline__ unsigned char* slot(int stage, int array, int i) const {
+    return mem + stage * STAGE + (array * G::NV + i) * SLOT + threadIdx.x * 16;
+  }
+  __device__ __forceinline__ void init(void* smem, int e0_, int D_) {
+    mem = (unsigned char*)smem, e0 = e0_, D = D_;
+    for (int at = threadIdx.x; at < BYTES / 16; at += G::NT) ((uint4*)mem)[at] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+  }
+  // The row's pack i: p is where value e0 of the row is.
+  __device__ __forceinline__ void copy(int stage, int array, int i, const T* p) const {
+    const int e = e0 + i * G::STEP;
+    if (e >= D) return;
+    unsigned char* dst = slot(stage, array, i);
+    if constexpr (!G::EDGE) {
+      cp_async16(dst, p + i * G::STEP);
+    } else if (e >= 0) {
+      const int n = D - e < G::V ? D - e : G::V;
+      cp_async_part(dst, p + i * G::STEP, n * (int)sizeof(T));
+    } else {  // the row begins inside the pack
+      for (int c = -e; c < G::V && e + c < D; ++c) ((T*)dst)[c] = p[i * G::STEP + c];
+    }
+  }
+  __device__ __forceinline__ void read(int stage, int array, int i, float (&v)[G::V]) const {
+    widen_pack(ld_pack<T, G::V>((const T*)slot(stage, array, i)), v);
+  }
+};
+
+// A thread's parameters, laid over the row as its packs are, in shared memory of its own.
+template <class P, class G> struct NormParams {
+  static constexpr int CHUNKS = G::V * (int)sizeof(P) / 16;
+  static constexpr int BYTES = G::NT * G::NV * G::V * (int)sizeof(P);
+  unsigned char* mem;
+  __device__ __forceinline__ void init(void* smem, const P* p, int e0, int D, float none) {
+    mem = (unsigned char*)smem + threadIdx.x * 16;
+#pragma unroll
+    for (int i = 0; i < G::NV; ++i) {
+      P r[G::V];
+      norm_params<P, G>(r, p, e0 + i * G::STEP, D, none);
+#pragma unroll
+      for (int k = 0; k < CHUNKS; ++k) memcpy(mem + (i * CHUNKS + k) * G::NT * 16, (const char*)r + k * 16, 16);
+    }
+  }
+  __device__ __forceinline__ void get(int i, P (&r)[G::V]) const {
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) {
+      const uint4 u = *(const uint4*)(mem + (i * CHUNKS + k) * G::NT * 16);
+      memcpy((char*)r + k * 16, &u, 16);
+    }
+  }
+};
+
+// Rows at any offset: persistent, the parameters in shared memory.
+template <class T, class P, class G, int STAGES>
+__global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_constant__ NormArgs<T, P> a) {
+  constexpr int V = G::V, NV = G::NV;
+  using Ring = NormRing<T, G, 1, STAGES>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ NormShared<G> sh;
+  pdl_entry();
+  const long long first = blockIdx.x, grid = gridDim.x;
+  if (first >= a.N) return;
+  const int t = threadIdx.x % G::TPR, sub = threadIdx.x / G::TPR;
+  const int e0 = t * V - (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T));
+  Ring ring;
+  ring.init(smem, e0, a.D);
+  NormParams<P, G> ws, bs;
+  ws.init(smem + Ring::BYTES, a.w, e0, a.D, 1.f);
+  bs.init(smem + Ring::BYTES + NormParams<P, G>::BYTES, a.b, e0, a.D, 0.f);
+  const long long r0 = first + grid * sub, hop = grid * G::ROWS;
+  auto fetch = [&](long long row, int stage) {
+    if (row < a.N) {
+      const T* p = a.x + row * a.xs + e0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ring.copy(stage, 0, i, p);
+    }
+    cp_async_commit();
+  };
+  for (int k = 0; k < STAGES - 1; ++k) fetch(r0 + k * hop, k);
+  int turn = 0, stage = 0;
+  for (long long row = r0; row < a.N; row += hop) {
+    fetch(row + (STAGES - 1) * hop, (stage + STAGES - 1) % STAGES);
+    cp_async_wait<STAGES - 1>();
+    float x[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ring.read(stage, 0, i, x[i]);
+    stage = (stage + 1) % STAGES;
+    norm_row<T, P, G>(x, a, row, true, e0, sh, turn, [&](int i, P(&w)[V], P(&b)[V]) {
+      ws.get(i, w);
+      bs.get(i, b);
+    });
+  }
+}
+
+// The gradient: persistent, one CTA an SM, x and dy through the ring, the sums over rows in
+// registers.  At 32 values a thread those would take too many: db's are in shared memory
+// then, each thread's own, and the weight comes from L1 in place of shared memory.
+template <class T, class P, class G> struct NormBackwardSmem {
+  static constexpr bool BIG = G::NV * G::V > 16;
+  static constexpr bool AGAIN = BIG || G::NT > 512;  // n and g are worked out twice, not kept
+  static constexpr int ROOM = 220 * 1024, ROW = NormRing<T, G, 2, 1>::BYTES;
+  static constexpr int REST = BIG ? G::NT * G::NV * G::V * (int)sizeof(float) : NormParams<P, G>::BYTES;
+  static constexpr int STAGES = (ROOM - REST) / ROW < 3 ? (ROOM - REST) / ROW : 3;
+  static constexpr int BYTES = STAGES * ROW + REST;
+  static_assert(STAGES >= 1, "fits");
+};
 template <class T, class P, class G>
 __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_constant__ NormArgs<T, P> a) {
-  constexpr int V = G::V, NV = G::NV;
-  constexpr int kSums = G::SUMS_IN_SMEM ? 1 : NV * V;
+  using S = NormBackwardSmem<T, P, G>;
+  constexpr int V = G::V, NV = G::NV, N = NV * V, STAGES = S::STAGES;
+  constexpr bool BIG = S::BIG, AGAIN = S::AGAIN;
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ NormShared<G> sh;
-  __shared__ float fold[G::ROWS > 1 ? G::NT * NV * V : 1];
-  extern __shared__ float sums_mem[];
   pdl_entry();
   const int t = threadIdx.x % G::TPR, sub = threadIdx.x / G::TPR;
-  const long long first = blockIdx.x;
-  const int off = first < a.N ? (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T)) : 0;
+  const long long first = blockIdx.x, grid = gridDim.x;
+  const int off = G::EDGE && first < a.N ? (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T)) : 0;
   const int e0 = t * V - off;
-  constexpr int kStep = G::TPR * V;
-  float dw_[kSums], db_[kSums];
-  auto dw = [&](int k) -> float& {
-    if constexpr (G::SUMS_IN_SMEM) return sums_mem[k * G::NT + threadIdx.x];
-    else return dw_[k];
-  };
-  auto db = [&](int k) -> float& {
-    if constexpr (G::SUMS_IN_SMEM) return sums_mem[(NV * V + k) * G::NT + threadIdx.x];
+  NormRing<T, G, 2, STAGES> ring;
+  ring.init(smem, e0, a.D);
+  float2 dw[N / 2], db_[BIG ? 1 : N / 2];
+  float2* db_mem = (float2*)(smem + STAGES * S::ROW) + threadIdx.x;
+  auto db = [&](int k) -> float2& {
+    if constexpr (BIG) return db_mem[k * G::NT];
     else return db_[k];
   };
-  constexpr int kHeld = G::HOLD ? NV : 1;
-  P pw[kHeld][V];
-  auto weight = [&](int i) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const int e = e0 + i * kStep + c;
-      pw[i % kHeld][c] = a.w && (unsigned)e < (unsigned)a.D ? a.w[e] : narrow<P>(1.f);
-    }
+  for (int k = 0; k < N / 2; ++k) dw[k] = db(k) = make_float2(0.f, 0.f);
+  NormParams<P, G> ws;
+  if constexpr (!BIG) ws.init(smem + STAGES * S::ROW, a.w, e0, a.D, 1.f);
+  auto weight = [&](int i, P(&w)[V]) {
+    if constexpr (BIG) norm_params<P, G>(w, a.w, e0 + i * G::STEP, a.D, 1.f);
+    else ws.get(i, w);
   };
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int c = 0; c < V; ++c) dw(i * V + c) = db(i * V + c) = 0.f;
-    if constexpr (G::HOLD) weight(i);
-  }
   const float inv = 1.f / (float)a.D;
-  int turn = 0;
-  const long long G_ = gridDim.x;
-  for (long long base = first; base < a.N; base += G_ * G::ROWS) {
-    const long long row = base + G_ * sub;
-    const bool live = row < a.N;
-    const T *x_at = a.x + row * a.xs + e0, *dy_at = a.dy + row * a.dys + e0;
-    Pack<T, V> px[kHeld], pd[kHeld];
-    auto load = [&](int i) {
-      px[i % kHeld] = norm_load<T, V>(x_at + i * kStep, e0 + i * kStep, a.D, live);
-      pd[i % kHeld] = norm_load<T, V>(dy_at + i * kStep, e0 + i * kStep, a.D, live);
+  const long long r0 = first + grid * sub, hop = grid * G::ROWS;
+  auto fetch = [&](long long row, int stage) {
+    if (row < a.N) {
+      const T *x = a.x + row * a.xs + e0, *dy = a.dy + row * a.dys + e0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        ring.copy(stage, 0, i, x);
+        ring.copy(stage, 1, i, dy);
+      }
+    }
+    cp_async_commit();
+  };
+  auto load_stats = [&](long long row) {
+    return row < a.N ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.f, 0.f);
+  };
+  for (int k = 0; k < STAGES - 1; ++k) fetch(r0 + k * hop, k);
+  float2 next = load_stats(r0);
+  int turn = 0, stage = 0;
+  for (long long row = r0; row < a.N; row += hop) {
+    fetch(row + (STAGES - 1) * hop, (stage + STAGES - 1) % STAGES);
+    const float mean = next.x, rstd = next.y;
+    next = load_stats(row + hop);
+    cp_async_wait<STAGES - 1>();
+    // n and g = dy w of pack i, two values at a time.
+    const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+    auto terms = [&](int i, float2 (&n)[V / 2], float2 (&d)[V / 2], float2 (&g)[V / 2]) {
+      float x[V], y[V];
+      P w[V];
+      ring.read(stage, 0, i, x);
+      ring.read(stage, 1, i, y);  // zero outside the row
+      weight(i, w);
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        n[c] = mul2(add2(make_float2(x[2 * c], x[2 * c + 1]), m2), r2);
+        d[c] = make_float2(y[2 * c], y[2 * c + 1]);
+        g[c] = mul2(d[c], make_float2(widen(w[2 * c]), widen(w[2 * c + 1])));
+      }
     };
-    if constexpr (G::HOLD) {
+    float2 n[AGAIN ? 1 : NV][V / 2], g[AGAIN ? 1 : NV][V / 2];
+    float2 sg = make_float2(0.f, 0.f), sgn = sg;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load(i);
-    }
-    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll kHeld
     for (int i = 0; i < NV; ++i) {
-      float x[V], d[V];
-      if constexpr (!G::HOLD) load(i), weight(i);
-      widen_pack(px[i % kHeld], x);
-      widen_pack(pd[i % kHeld], d);  // zero outside the row
+      const int q = AGAIN ? 0 : i;
+      float2 d[V / 2];
+      terms(i, n[q], d, g[q]);
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float n = (x[c] - mean) * rstd;
-        dw(i * V + c) = fmaf(d[c], n, dw(i * V + c));
-        db(i * V + c) += d[c];
-        const float g = d[c] * widen(pw[i % kHeld][c]);
-        s.x += g;
-        s.y = fmaf(g, n, s.y);
+      for (int c = 0; c < V / 2; ++c) {
+        const int k = i * (V / 2) + c;
+        dw[k] = fma2(d[c], n[q][c], dw[k]);
+        db(k) = add2(db(k), d[c]);
+        sg = add2(sg, g[q][c]);
+        sgn = fma2(g[q][c], n[q][c], sgn);
       }
     }
-    s = norm_sum<G>(s, sh, turn);
-    const float mg = s.x * inv, mgn = s.y * inv;
-    if (!live) continue;
-#pragma unroll kHeld
-    for (int i = 0; i < NV; ++i) {
-      float x[V], d[V];
-      if constexpr (!G::HOLD) load(i), weight(i);
-      widen_pack(px[i % kHeld], x);
-      widen_pack(pd[i % kHeld], d);
+    const float2 s = norm_sum<G>(make_float2(sg.x + sg.y, sgn.x + sgn.y), sh, turn);
+    const float2 mg = make_float2(-s.x * inv, -s.x * inv), mgn = make_float2(-s.y * inv, -s.y * inv);
+    T* dx = a.dx + row * a.dxs + e0;
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float n = (x[c] - mean) * rstd;
-        d[c] = (fmaf(-n, mgn, d[c] * widen(pw[i % kHeld][c])) - mg) * rstd;
+    for (int i = 0; i < NV; ++i) {
+      const int q = AGAIN ? 0 : i;
+      if constexpr (AGAIN) {
+        float2 d[V / 2];
+        terms(i, n[0], d, g[0]);
       }
-      norm_store<T, V>(a.dx + row * a.dxs + e0 + i * kStep, e0 + i * kStep, a.D, narrow_pack<T, V>(d));
+      float o[V];
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        const float2 v = mul2(add2(fma2(n[q][c], mgn, g[q][c]), mg), r2);
+        o[2 * c] = v.x, o[2 * c + 1] = v.y;
+      }
+      norm_store<T, G>(dx + i * G::STEP, e0 + i * G::STEP, a.D, narrow_pack<T, V>(o));
     }
+    stage = (stage + 1) % STAGES;
   }
   if (!a.part) return;
   float* part = a.part + (size_t)blockIdx.x * 2 * a.D;
+  auto sum = [&](int which, int k) {
+    const float2 v = which ? db(k / 2) : dw[k / 2];
+    return k % 2 ? v.y : v.x;
+  };
+  if constexpr (G::ROWS == 1) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-#pragma unroll
-    for (int k = 0; k < NV * V; ++k) {
-      const float v = which ? db(k) : dw(k);
-      const int e = e0 + k / V * kStep + k % V;
-      if constexpr (G::ROWS > 1) fold[k * G::NT + threadIdx.x] = v;
-      else if ((unsigned)e < (unsigned)a.D) part[(size_t)which * a.D + e] = v;
-    }
-    if constexpr (G::ROWS > 1) {
-      __syncthreads();
-      if (sub == 0) {
-#pragma unroll
-        for (int k = 0; k < NV * V; ++k) {
-          float v = 0.f;
-#pragma unroll
-          for (int r = 0; r < G::ROWS; ++r) v += fold[k * G::NT + r * G::TPR + t];
-          const int e = e0 + k / V * kStep + k % V;
-          if ((unsigned)e < (unsigned)a.D) part[(size_t)which * a.D + e] = v;
-        }
+    for (int k = 0; k < N; ++k) {
+      const int e = e0 + k / V * G::STEP + k % V;
+      if ((unsigned)e < (unsigned)a.D) {
+        part[e] = sum(0, k);
+        part[(size_t)a.D + e] = sum(1, k);
       }
+    }
+  } else {
+    // The CTA's groups of threads, one after another; the ring's memory is free now.
+    static_assert(NormRing<T, G, 2, STAGES>::BYTES >= N * G::NT * (int)sizeof(float), "the sums fit");
+    float* fold = (float*)smem;
+    cp_async_wait<0>();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
       __syncthreads();
+#pragma unroll
+      for (int k = 0; k < N; ++k) fold[k * G::NT + threadIdx.x] = sum(which, k);
+      __syncthreads();
+      for (int at = threadIdx.x; at < N * G::TPR; at += G::NT) {
+        const int k = at / G::TPR, q = at % G::TPR;
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < G::ROWS; ++r) v += fold[k * G::NT + r * G::TPR + q];
+        const int e = q * V - off + k / V * G::STEP + k % V;
+        if ((unsigned)e < (unsigned)a.D) part[(size_t)which * a.D + e] = v;
+      }
     }
   }
 }
@@ -291,7 +450,7 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
 // the passes (from L2).  Rows too long for registers, and arrays whose rows start at
 // different offsets from a 16-byte boundary, come here.
 constexpr int kNormLongThreads = 512;
-using NormLongGeom = NormGeom<1, kNormLongThreads, 1>;
+using NormLongGeom = NormGeom<1, kNormLongThreads, 1, kNormLongThreads, true>;
 
 template <class T, class P>
 __global__ void __launch_bounds__(kNormLongThreads) norm_forward_long_kernel(const __grid_constant__ NormArgs<T, P> a) {
@@ -371,24 +530,25 @@ __global__ void __launch_bounds__(256) norm_columns_long_kernel(const __grid_con
   part[a.D + col] = db;
 }
 
-// dw and db from `count` rows of partial sums: 32 columns a CTA, 8 threads a column.
+// dw and db from `count` rows of partial sums: 32 columns a CTA, 16 threads a column, whose
+// loads are all in flight together.
 template <class P>
-__global__ void __launch_bounds__(256) norm_fold_kernel(const float* part, int count, int D, P* dw, P* db) {
-  __shared__ float red[8][33];
+__global__ void __launch_bounds__(512) norm_fold_kernel(const float* part, int count, int D, P* dw, P* db) {
+  __shared__ float red[16][33];
   pdl_entry();
   const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
   const int at = blockIdx.x * 32 + lane;  // a column of (dw, db) side by side
   float s = 0.f;
   if (at < 2 * D) {
-#pragma unroll 8
-    for (int p = g; p < count; p += 8) s += part[(size_t)p * 2 * D + at];
+#pragma unroll 10
+    for (int p = g; p < count; p += 16) s += part[(size_t)p * 2 * D + at];
   }
   red[g][lane] = s;
   __syncthreads();
   if (g == 0 && at < 2 * D) {
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][lane];
+    for (int k = 0; k < 16; ++k) s += red[k][lane];
     P* out = at < D ? dw : db;
     if (out) out[at < D ? at : at - D] = narrow<P>(s);
   }
@@ -414,77 +574,119 @@ template <class T, class P> NormArgs<T, P> norm_args(const LayerNormJob& j) {
   return a;
 }
 
-// Calls f(geometry) with the first geometry that holds a row of D values at any offset,
-// or f(nullptr) where none does.
-template <class T, class F> cudaError_t norm_geometry(long long D, F&& f) {
-  constexpr int V = 16 / sizeof(T);
-  const long long packs = (D + 2 * (V - 1)) / V;  // at the worst offset
-  if (packs <= 32 * (8 / V)) return f((NormGeom<V, 32, 8 / V>*)nullptr);
-  if (packs <= 32 * (16 / V)) return f((NormGeom<V, 32, 16 / V>*)nullptr);
-  if (packs <= 128 * (16 / V)) return f((NormGeom<V, 128, 16 / V>*)nullptr);
-  if (packs <= 256 * (16 / V)) return f((NormGeom<V, 256, 16 / V>*)nullptr);
-  if (packs <= 512 * (16 / V)) return f((NormGeom<V, 512, 16 / V>*)nullptr);
-  if (packs <= 512 * (32 / V)) return f((NormGeom<V, 512, 32 / V>*)nullptr);
-  return f((void*)nullptr);
+// Whether the rows of an array all start on 16-byte boundaries.
+template <class T> bool norm_rows16(const void* p, long long stride, long long N) {
+  return (uintptr_t)p % 16 == 0 && (N <= 1 || stride * (long long)sizeof(T) % 16 == 0);
 }
+inline bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// CTAs: enough for every row, at most `most`; a multiple of 8 (see the top of the file).
-inline unsigned norm_grid(long long N, int rows, long long most) {
-  long long g = (N + rows - 1) / rows;
-  if (g > most) g = most;
+// CTAs of a persistent kernel: enough for every row, at most `most`; a multiple of 8.
+inline unsigned norm_grid(long long N, long long most) {
+  const long long g = N < most ? N : most;
   return (unsigned)((g + 7) / 8 * 8);
 }
 
 template <class T, class P> cudaError_t launch_layer_norm(const LayerNormJob& j, const LaunchCtx& ctx) {
+  constexpr int V = 16 / sizeof(T);
   const NormArgs<T, P> a = norm_args<T, P>(j);
-  profile_before(ctx);
+  const bool even = j.D % V == 0 && norm_rows16<T>(j.x, j.xs, j.N) && norm_rows16<T>(j.y, j.ys, j.N) && on16(j.w) && on16(j.b);
   const bool wide = same_offsets<T>(j.x, j.xs, j.y, j.ys, j.N);
-  cudaError_t e = norm_geometry<T>(wide ? j.D : 0x7fffffff, [&](auto* gp) {
+  const long long packs = even ? j.D / V : (j.D + 2 * (V - 1)) / V;  // EDGE: at the worst offset
+  auto run = [&](auto* gp) {
     using G = std::remove_pointer_t<decltype(gp)>;
-    if constexpr (std::is_void_v<G>)
-      return launch_pdl(norm_forward_long_kernel<T, P>, norm_grid(j.N, 1, 4ll * ctx.num_sms), kNormLongThreads, 0,
-                        ctx.stream, a);
+    if constexpr (G::EDGE) {
+      constexpr int room = 220 * 1024;
+      constexpr int row = NormRing<T, G, 1, 1>::BYTES, params = 2 * NormParams<P, G>::BYTES;
+      constexpr int STAGES = (room - params) / row < 3 ? (room - params) / row : 3;
+      constexpr int smem = STAGES * row + params;
+      static_assert(STAGES >= 1 && smem <= room, "fits");
+      auto kernel = norm_forward_edge_kernel<T, P, G, STAGES>;
+      const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      // Two CTAs an SM where their shared memory allows (227 KB, 1 KB of each reserved).
+      const long long ctas = smem <= 112 * 1024 && G::NT <= 512 ? 2 : 1;
+      return r != cudaSuccess ? r : launch_pdl(kernel, norm_grid(j.N, ctas * ctx.num_sms), G::NT, smem, ctx.stream, a);
+    }
     else
-      return launch_pdl(norm_forward_kernel<T, P, G>, norm_grid(j.N, G::ROWS, 1024ll / G::NT * ctx.num_sms), G::NT, 0,
-                        ctx.stream, a);
-  });
+      return launch_pdl(norm_forward_kernel<T, P, G>, (unsigned)((j.N + G::ROWS - 1) / G::ROWS), G::NT, 0, ctx.stream, a);
+  };
+  cudaError_t e;
+  profile_before(ctx);
+  if (even && packs <= 4096 && j.N <= 0x7fffffffll) {
+    if (packs <= 32) e = run((NormGeom<V, 32, 1, 128, false>*)nullptr);
+    else if (packs <= 64) e = run((NormGeom<V, 32, 2, 128, false>*)nullptr);
+    else if (packs <= 128) e = run((NormGeom<V, 32, 4, 128, false>*)nullptr);
+    else if (packs <= 256) e = run((NormGeom<V, 64, 4, 128, false>*)nullptr);
+    else if (packs <= 512) e = run((NormGeom<V, 128, 4, 128, false>*)nullptr);
+    else if (packs <= 1024) e = run((NormGeom<V, 256, 4, 256, false>*)nullptr);
+    else if (packs <= 2048) e = run((NormGeom<V, 512, 4, 512, false>*)nullptr);
+    else e = run((NormGeom<V, 1024, 4, 1024, false>*)nullptr);
+  } else if (wide && packs <= 512 * (16 / V)) {
+    constexpr int U = 16 / V;  // 16 values a thread
+    if (packs <= 32 * U) e = run((NormGeom<V, 32, U, 512, true>*)nullptr);
+    else if (packs <= 128 * U) e = run((NormGeom<V, 128, U, 512, true>*)nullptr);
+    else if (packs <= 256 * U) e = run((NormGeom<V, 256, U, 512, true>*)nullptr);
+    else e = run((NormGeom<V, 512, U, 512, true>*)nullptr);
+  } else if (wide && packs <= 1024 * (16 / V)) {
+    e = run((NormGeom<V, 1024, 16 / V, 1024, true>*)nullptr);
+  } else {
+    e = launch_pdl(norm_forward_long_kernel<T, P>, norm_grid(j.N, 4ll * ctx.num_sms), kNormLongThreads, 0, ctx.stream, a);
+  }
   profile_after(ctx);
   return e;
 }
 
 template <class T, class P> cudaError_t launch_layer_norm_backward(const LayerNormJob& j, const LaunchCtx& ctx) {
+  constexpr int V = 16 / sizeof(T);
   NormArgs<T, P> a = norm_args<T, P>(j);
   const bool sums = j.dw || j.db;
   a.part = sums ? (float*)j.temp : nullptr;
-  int count = 0;
-  profile_before(ctx);
+  const bool even = j.D % V == 0 && norm_rows16<T>(j.x, j.xs, j.N) && norm_rows16<T>(j.dy, j.dys, j.N) &&
+                    norm_rows16<T>(j.dx, j.dxs, j.N) && on16(j.w);
   const bool wide = same_offsets<T>(j.x, j.xs, j.dy, j.dys, j.N) && same_offsets<T>(j.x, j.xs, j.dx, j.dxs, j.N);
-  cudaError_t e = norm_geometry<T>(wide ? j.D : 0x7fffffff, [&](auto* gp) {
+  const long long packs = even ? j.D / V : (j.D + 2 * (V - 1)) / V;
+  long long most = ctx.num_sms / 8 * 8;
+  if (most > kNormMaxParts) most = kNormMaxParts;
+  if (most < 8) most = 8;
+  int count = 0;
+  auto run = [&](auto* gp) {
     using G = std::remove_pointer_t<decltype(gp)>;
-    if constexpr (std::is_void_v<G>) {
-      cudaError_t r = launch_pdl(norm_backward_long_kernel<T, P>, norm_grid(j.N, 1, 4ll * ctx.num_sms),
-                                 kNormLongThreads, 0, ctx.stream, a);
-      if (r != cudaSuccess || !sums) return r;
+    constexpr int smem = NormBackwardSmem<T, P, G>::BYTES;
+    auto kernel = norm_backward_kernel<T, P, G>;
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const unsigned grid = norm_grid(j.N, most);
+    count = (int)grid;
+    return r != cudaSuccess ? r : launch_pdl(kernel, grid, G::NT, smem, ctx.stream, a);
+  };
+  auto pick = [&](auto edge) {
+    constexpr bool E = decltype(edge)::value;
+    constexpr int U = 16 / V;  // 16 values a thread
+    if (packs <= 32 * U) return run((NormGeom<V, 32, U, 512, E>*)nullptr);
+    if (packs <= 128 * U) return run((NormGeom<V, 128, U, 512, E>*)nullptr);
+    if (packs <= 256 * U) return run((NormGeom<V, 256, U, 512, E>*)nullptr);
+    if (packs <= 512 * U) return run((NormGeom<V, 512, U, 512, E>*)nullptr);
+    // Longer rows; at any offset the wider one would spill.
+    if constexpr (E) return run((NormGeom<V, 768, U, 768, true>*)nullptr);
+    else return run((NormGeom<V, 512, 2 * U, 512, false>*)nullptr);
+  };
+  cudaError_t e;
+  profile_before(ctx);
+  if (even && packs <= 512 * (32 / V)) {
+    e = pick(std::false_type{});
+  } else if (wide && packs <= 768 * (16 / V)) {
+    e = pick(std::true_type{});
+  } else {
+    e = launch_pdl(norm_backward_long_kernel<T, P>, norm_grid(j.N, 4ll * ctx.num_sms), kNormLongThreads, 0, ctx.stream, a);
+    if (e == cudaSuccess && sums) {
       const long long blocks = (j.D + 255) / 256;
       long long ranges = (8ll * ctx.num_sms + blocks - 1) / blocks;
       if (ranges > j.N) ranges = j.N;
       if (ranges > kNormMaxParts) ranges = kNormMaxParts;
       count = (int)ranges;
-      return launch_pdl(norm_columns_long_kernel<T, P>, (unsigned)(blocks * ranges), 256, 0, ctx.stream, a, count);
-    } else {
-      long long most = 512ll / G::NT * ctx.num_sms;
-      if (most > kNormMaxParts) most = kNormMaxParts;
-      const unsigned grid = norm_grid(j.N, G::ROWS, most / 8 * 8);
-      count = (int)grid;
-      auto kernel = norm_backward_kernel<T, P, G>;
-      cudaError_t r = cudaSuccess;
-      if (G::SUMS_BYTES)
-        r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::SUMS_BYTES);
-      return r != cudaSuccess ? r : launch_pdl(kernel, grid, G::NT, G::SUMS_BYTES, ctx.stream, a);
+      e = launch_pdl(norm_columns_long_kernel<T, P>, (unsigned)(blocks * ranges), 256, 0, ctx.stream, a, count);
     }
-  });
+  }
   if (e == cudaSuccess && sums)
-    e = launch_pdl(norm_fold_kernel<P>, (unsigned)((2 * j.D + 31) / 32), 256, 0, ctx.stream, (const float*)j.temp,
+    e = launch_pdl(norm_fold_kernel<P>, (unsigned)((2 * j.D + 31) / 32), 512, 0, ctx.stream, (const float*)j.temp,
                    count, (int)j.D, (P*)j.dw, (P*)j.db);
   profile_after(ctx);
   return e;
