@@ -6,20 +6,25 @@
 //   lower index, with their log probabilities;
 //   gradient:  dx_j = dlogprob ([j = target] - p_j) - dentropy p_j (log p_j + entropy).
 //
-// Each row is read once.  A thread keeps the running maximum m of its values and, relative
-// to it, s = sum e^d and t = sum e^d d with d = x - m; when m grows by D, t becomes
-// e^-D (t - s D) and s becomes e^-D s.  Then  lse = m + log s  and  entropy = log s - t/s,
-// which loses nothing to cancellation.  A masked logit (-inf) has e^d = 0 and d is held at a
-// finite floor, so that its product is 0 and not a NaN; a NaN or +inf logit
-// makes the row's results NaN.
+// Each row is read once.  In base 2, a thread keeps a reference M near the largest
+// x log2(e) so far and, relative to it, s = sum 2^d and t = sum 2^d d with
+// d = x log2(e) - M (one fused multiply-add).  M follows the maximum only when that has
+// grown by more than 8, which costs no accuracy and almost never happens after a thread's
+// first values; s and t are then multiplied by 2^(M - M'), t moved first.  At the end
+//   lse = ln 2 (M + log2 s),   entropy = ln 2 (log2 s - t / s),
+// which loses nothing to cancellation.  Values are held at a floor (-2^126, or fp16's
+// lowest), so that a masked logit (-inf) gives 2^d = 0 and a product of 0, not a NaN.
+// Rows for which this does not do (nothing above the floor, values near the top of the
+// range, a NaN) are read again by the careful form in lp_careful.
 //
-// The alternatives are found in the same pass, as a compaction: a value enters a buffer
-// in shared memory if its key (the value in the high half, the index reversed in the low
-// half: unique, so ties are settled) reaches a threshold that K values are known to reach.
-// The first threshold is the K-th largest of 64 group maxima of the first tile, so a few
-// dozen values pass of each tile; the buffer is sorted once at the end.  When it would
-// overflow, it is sorted down to K, the threshold rises past the K-th, and what the tile
-// could not place is offered again.
+// The alternatives are found in the same pass, as a compaction.  A value's key (the value
+// in the high half, the index reversed in the low half: unique, so ties are settled) is
+// compared with a threshold that K values are known to reach: at first the K-th largest
+// of 64 group maxima of the first tile.  The test is one comparison a pack of 16 bytes;
+// packs that pass, a few dozen of a tile, go to a list in shared memory.  The list is
+// expanded into keys after the first, second, fourth, eighth ... tile, where it is full,
+// and at the end; the K largest are kept, in order, and the threshold rises past the K-th.
+// (With the doublings about K packs pass between one and the next, K log2(tiles) in all.)
 //
 // With few rows a cluster of CTAs shares each row, slice by slice; CTA 0 of the cluster
 // reads the others' sums and lists through distributed shared memory.
@@ -48,12 +53,16 @@ template <class T> struct LogprobArgs {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpPacks = 4;        // packs of a thread in a tile
+constexpr int kLpGradPacks = 4;    // and in a block of the gradient
 constexpr int kLpGroups = 64;      // groups of threads whose maxima give the first threshold
-constexpr int kLpBuffer = 2048;    // keys
+constexpr int kLpStages = 2;       // tiles in shared memory
+constexpr int kLpList = 256;       // packs
+constexpr int kLpKeys = 1024;      // keys
 constexpr int kLpMaxCluster = 8;
-// Differences from a maximum stop here: e^d has long been 0 in fp32, and products with
-// d stay finite, so that 0 times them is 0.
+// Natural-log differences from a maximum stop here: e^d has long been 0 in fp32, and
+// products with d stay finite, so that 0 times them is 0.
 constexpr float kLpFloor = -1000.f;
+constexpr float kLpSlack = 8.f;    // how far values may rise above the reference, in base 2
 
 __device__ __forceinline__ long long lp_target(const void* targets, int is64, long long row) {
   return is64 ? ((const long long*)targets)[row] : (long long)((const int*)targets)[row];
@@ -73,32 +82,116 @@ __device__ __forceinline__ unsigned long long lp_key(float x, int index) {
   return (unsigned long long)lp_order(x) << 32 | (0x7fffffffu - (unsigned)index);
 }
 
-// Running sums relative to the maximum.
+// The floor under the values of a type, and a pack held at it.
+template <class T> struct LpType;
+template <> struct LpType<float> {
+  static constexpr float kFloor = -8.507059173023462e37f;  // -2^126
+  static __device__ __forceinline__ float hold(Pack<float, 4>& p) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) p.v[c] = max_nan(p.v[c], kFloor);
+    return max_nan(max_nan(p.v[0], p.v[1]), max_nan(p.v[2], p.v[3]));
+  }
+};
+template <> struct LpType<__nv_bfloat16> {
+  static constexpr float kFloor = -8.507059173023462e37f;
+  static __device__ __forceinline__ unsigned max2(unsigned a, unsigned b) {
+    unsigned d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float hold(Pack<__nv_bfloat16, 8>& p) {
+    uint4 u;
+    memcpy(&u, &p, 16);
+    constexpr unsigned f = 0xfe80fe80u;
+    u = make_uint4(max2(u.x, f), max2(u.y, f), max2(u.z, f), max2(u.w, f));
+    memcpy(&p, &u, 16);
+    const unsigned m = max2(max2(u.x, u.y), max2(u.z, u.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <> struct LpType<__half> {
+  static constexpr float kFloor = -65504.f;
+  static __device__ __forceinline__ unsigned max2(unsigned a, unsigned b) {
+    unsigned d;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float hold(Pack<__half, 8>& p) {
+    uint4 u;
+    memcpy(&u, &p, 16);
+    constexpr unsigned f = 0xfbfffbffu;
+    u = make_uint4(max2(u.x, f), max2(u.y, f), max2(u.z, f), max2(u.w, f));
+    memcpy(&p, &u, 16);
+    const unsigned m = max2(max2(u.x, u.y), max2(u.z, u.w));
+    __half2 h;
+    memcpy(&h, &m, 4);
+    const float2 q = __half22float2(h);
+    return max_nan(q.x, q.y);
+  }
+};
+
+// Sums relative to a reference m, in base 2 (or, in lp_careful, natural units).
 struct LpSums {
   float m, s, t;
 };
-// Multiplies by e^(m_old - m_new) and moves t to the new maximum.
-__device__ __forceinline__ void lp_rebase(LpSums& a, float m) {
-  const float d = max_nan(a.m - m, kLpFloor), k = ex2(d * kLog2e);
+template <bool BASE2> __device__ __forceinline__ void lp_rebase(LpSums& a, float m) {
+  const float d = max_nan(a.m - m, kLpFloor), k = ex2(BASE2 ? d : d * kLog2e);
   a.t = k * fmaf(a.s, d, a.t);
   a.s *= k;
   a.m = m;
 }
-__device__ __forceinline__ LpSums lp_join(LpSums a, LpSums b) {
+template <bool BASE2> __device__ __forceinline__ LpSums lp_join(LpSums a, LpSums b) {
   const float m = max_nan(a.m, b.m);
-  lp_rebase(a, m);
-  lp_rebase(b, m);
+  lp_rebase<BASE2>(a, m);
+  lp_rebase<BASE2>(b, m);
   return {m, a.s + b.s, a.t + b.t};
 }
 
 struct LpShared {
-  unsigned long long keys[kLpBuffer];
+  unsigned long long keys[kLpKeys];
+  unsigned long long best[256];  // the K largest, then those of the cluster
+  uint4 list[kLpList];
+  int list_at[kLpList];          // the index of each pack's first value
   unsigned long long group[kLpGroups];
   LpSums warp[kLpThreads / 32];
-  LpSums sums;  // the CTA's
+  LpSums sums;                   // the CTA's
   unsigned long long tau;
-  int count;
+  int listed, count;
 };
+
+// The CTA's sums from its threads', in a fixed order; ends with a barrier.
+template <bool BASE2> __device__ __forceinline__ void lp_reduce(LpSums v, LpShared& sh) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    LpSums o;
+    o.m = __shfl_xor_sync(0xffffffffu, v.m, d);
+    o.s = __shfl_xor_sync(0xffffffffu, v.s, d);
+    o.t = __shfl_xor_sync(0xffffffffu, v.t, d);
+    v = lp_join<BASE2>(v, o);
+  }
+  if (threadIdx.x % 32 == 0) sh.warp[threadIdx.x / 32] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    LpSums r = sh.warp[0];
+    for (int w = 1; w < kLpThreads / 32; ++w) r = lp_join<BASE2>(r, sh.warp[w]);
+    sh.sums = r;
+  }
+  __syncthreads();
+}
+
+// The sums of a whole row value by value, in natural units with differences taken first:
+// for values near the ends of the range.  A row with nothing left ends with s = 0.
+template <class T> __device__ void lp_careful(const T* x, int V, LpShared& sh) {
+  LpSums v = {-FLT_MAX, 0.f, 0.f};
+  for (int j = threadIdx.x; j < V; j += kLpThreads) {
+    const float q = widen(x[j]);
+    if (q > v.m) lp_rebase<false>(v, q);
+    const float d = max_nan(q - v.m, kLpFloor), e = ex2(d * kLog2e);
+    v.s += e;
+    v.t = fmaf(e, d, v.t);
+  }
+  lp_reduce<false>(v, sh);
+}
 
 // Sorts keys[0 .. n) in falling order (n is padded with zeros to a power of two).  All
 // threads of the CTA call it, after a barrier; ends with a barrier.
@@ -123,12 +216,39 @@ __device__ __forceinline__ void lp_sort(unsigned long long* keys, int n) {
   }
 }
 
+// The K largest of keys[0 .. n) to out[0 .. K) in falling order, zeros where there are
+// fewer.  Few keys are placed by counting the larger ones, 256 / n threads a key; more are
+// sorted.  All threads of the CTA call it after a barrier; ends with a barrier.
+__device__ __forceinline__ void lp_select(unsigned long long* keys, int n, int K, unsigned long long* out) {
+  const int tid = threadIdx.x;
+  if (n <= 256) {
+    const int per = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, at = tid / per;
+    const unsigned long long mine = at < n ? keys[at] : 0;
+    int above = 0;
+    if (at < n) {
+#pragma unroll 4
+      for (int j = tid % per; j < n; j += per) above += keys[j] > mine;
+    }
+    for (int d = 1; d < per; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
+    __syncthreads();  // keys and out may be the same
+    if (tid >= n && tid < K) out[tid] = 0;
+    if (at < n && tid % per == 0 && above < K) out[above] = mine;
+  } else {
+    lp_sort(keys, n);
+    if (tid < K) out[tid] = keys[tid];
+  }
+  __syncthreads();
+}
+
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_constant__ LogprobArgs<T> a, unsigned C) {
+__global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_constant__ LogprobArgs<T> a, unsigned C) {
   constexpr int V = 16 / sizeof(T), U = kLpPacks, NT = kLpThreads;
+  constexpr float kFloor = LpType<T>::kFloor;
+  static_assert(kLpStages == 2, "two tiles in turn");
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ LpShared sh;
   pdl_entry();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const long long row = blockIdx.x / C;
   const T* x = a.logits + row * a.stride;
@@ -151,149 +271,166 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
     if (target >= 0) xt = widen(x[target]);
   }
   if (TOP && tid == 0) {
+    sh.listed = 0;
     sh.count = 0;
     sh.tau = 0;
   }
 
-  Pack<T, V> next[U];
-  auto load = [&](int p) {
+  // A thread's packs of a tile, copied one tile ahead into shared memory of its own.
+  auto slot = [&](int stage, int u) { return ring + ((stage * U + u) * NT + tid) * 16; };
+  auto fetch = [&](int p, int stage) {
+    if (p > 0 && p + U * NT < p1) {  // whole packs of the row
+      const T* q = x + ((p + tid) * V - off);
 #pragma unroll
+      for (int u = 0; u < U; ++u) cp_async16(slot(stage, u), q + u * NT * V);
+      cp_async_commit();
+      return;
+    }
+#pragma unroll 1
     for (int u = 0; u < U; ++u) {
-      const int j = p + u * NT + tid;
-      const int e0 = j * V - off;  // packs fit in 31 bits of values: V <= 2^31 - 1 - 16
+      const int j = p + u * NT + tid, e0 = j * V - off;
       if (j < p1 && e0 >= 0 && e0 + V <= a.V) {
-        next[u] = ld_pack<T, V>(x + e0);
-      } else {
-#pragma unroll
+        cp_async16(slot(stage, u), x + e0);
+      } else if (p < p1) {  // the row's ends, and what lies past the slice
+        T* dst = (T*)slot(stage, u);
+#pragma unroll 1
         for (int c = 0; c < V; ++c)
-          next[u].v[c] = j < p1 && (unsigned)(e0 + c) < (unsigned)a.V ? x[e0 + c] : narrow<T>(-INFINITY);
+          dst[c] = j < p1 && (unsigned)(e0 + c) < (unsigned)a.V ? x[e0 + c] : narrow<T>(-INFINITY);
       }
     }
+    cp_async_commit();
   };
-  LpSums sums = {-FLT_MAX, 0.f, 0.f};
-  if (p0 < p1) load(p0);
-  for (int p = p0; p < p1; p += U * NT) {
-    float v[U][V];
+  // Expands the listed packs into keys and empties the list; `last`: leaves the K largest in
+  // sh.best, else keeps them among the keys and raises the threshold past the K-th.  Called
+  // after a barrier, ends with one.
+  auto flush = [&](bool last) {
+    const int listed = sh.listed < kLpList ? sh.listed : kLpList;
+    for (int q0 = 0; q0 < listed * V; q0 += kLpKeys / 2) {
+      const unsigned long long tau = sh.tau;
+      if (sh.count > kLpKeys / 2) {  // uniform: count changes between barriers only
+        lp_select(sh.keys, sh.count, a.K, sh.best);
+        if (tid < a.K) sh.keys[tid] = sh.best[tid];
+        if (tid == 0) sh.count = a.K;
+      }
+      __syncthreads();
+      for (int q = q0 + tid; q < listed * V && q < q0 + kLpKeys / 2; q += NT) {
+        const int i = sh.list_at[q / V] + q % V;
+        const unsigned long long k = lp_key(widen(((const T*)sh.list)[q]), i);
+        if ((unsigned)i < (unsigned)end && k >= tau) sh.keys[atomicAdd(&sh.count, 1)] = k;
+      }
+      __syncthreads();
+    }
+    lp_select(sh.keys, sh.count, a.K, sh.best);
+    if (!last) {
+      const int n = sh.count < a.K ? sh.count : a.K;
+      __syncthreads();
+      if (tid < n) sh.keys[tid] = sh.best[tid];
+      if (tid == 0) {
+        sh.count = n;
+        sh.listed = 0;
+        if (n == a.K) sh.tau = sh.best[n - 1] + 1;
+      }
+      __syncthreads();
+    }
+  };
+
+  // Sets the threshold to the K-th largest of 64 groups' largest keys.
+  auto first_threshold = [&](unsigned long long k) {
+    constexpr int per_group = NT / kLpGroups;
 #pragma unroll
-    for (int u = 0; u < U; ++u) widen_pack(next[u], v[u]);
-    if (p + U * NT < p1) load(p + U * NT);
-    float best[U];  // the largest of each pack
+    for (int d = 1; d < per_group; d *= 2) {
+      const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
+      k = o > k ? o : k;
+    }
+    if (tid % per_group == 0) sh.group[tid / per_group] = k;
+    __syncthreads();
+    const unsigned long long mine = sh.group[tid / per_group];
+    int above = 0;
+#pragma unroll
+    for (int g = 0; g < kLpGroups; g += per_group) above += sh.group[g + tid % per_group] > mine;
+#pragma unroll
+    for (int d = 1; d < per_group; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
+    if (tid % per_group == 0 && above == a.K - 1 && mine) sh.tau = mine;
+    __syncthreads();
+  };
+
+  float ref = kFloor * kLog2e;
+  float2 s2 = make_float2(0.f, 0.f), t2 = s2;
+  float bar = -INFINITY;  // the threshold's value
+  int stage = 0, tile = 1;
+  fetch(p0, 0);
+  for (int p = p0; p < p1; p += U * NT, ++tile) {
+    fetch(p + U * NT, stage ^ 1);
+    cp_async_wait<1>();
+    unsigned todo = 0;                // packs that reach the threshold's value
+    unsigned long long most = 0;      // first tile: a key that some value here reaches
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float g = v[u][0];
+      Pack<T, V> held = ld_pack<T, V>((const T*)slot(stage, u));
+      const float best = LpType<T>::hold(held);
+      if (TOP && !(best < bar)) todo |= 1u << u;
+      if (TOP && p == p0) {
+        // A pack is known to hold a value of at least its largest (the floor may stand for
+        // -inf) at an index no later than its last.
+        const int j = p + u * NT + tid;
+        int i = j * V - off + V - 1;
+        if (i >= end) i = end - 1;
+        const unsigned long long q = j < p1 ? lp_key(best <= kFloor ? -INFINITY : best, i) : 0;
+        most = q > most ? q : most;
+      }
+      const float top = best * kLog2e;
+      if (top > ref + kLpSlack) {
+        const float d = max_nan(ref - top, kLpFloor), k = ex2(d);
+        const float2 k2 = make_float2(k, k), d2 = make_float2(d, d);
+        t2 = mul2(k2, fma2(s2, d2, t2));
+        s2 = mul2(s2, k2);
+        ref = top;
+      }
+      const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-ref, -ref);
 #pragma unroll
-      for (int c = 1; c < V; ++c) g = max_nan(g, v[u][c]);
-      best[u] = g;
-      if (g > sums.m) lp_rebase(sums, g);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float d = max_nan(v[u][c] - sums.m, kLpFloor), e = ex2(d * kLog2e);
-        sums.s += e;
-        sums.t = fmaf(e, d, sums.t);
+      for (int c = 0; c < V; c += 2) {
+        const float2 d2 = fma2(make_float2(widen(held.v[c]), widen(held.v[c + 1])), l2, r2);
+        const float2 e2 = make_float2(ex2(d2.x), ex2(d2.y));
+        s2 = add2(s2, e2);
+        t2 = fma2(e2, d2, t2);
       }
     }
     if constexpr (TOP) {
-      auto index = [&](int u, int c) { return (p + u * NT + tid) * V - off + c; };
-      auto inside = [&](int i) { return (unsigned)i < (unsigned)end; };
-      // Raises the threshold to the K-th largest of 64 group maxima of this tile.
-      auto tighten = [&]() {
-        // This thread's largest value, at its first place inside the slice.
-        float top = best[0];
-#pragma unroll
-        for (int u = 1; u < U; ++u) top = max_nan(top, best[u]);
-        int at = -1;
-#pragma unroll
-        for (int u = U - 1; u >= 0; --u)
-#pragma unroll
-          for (int c = V - 1; c >= 0; --c)
-            if ((v[u][c] == top || v[u][c] != v[u][c]) && inside(index(u, c))) at = index(u, c);
-        unsigned long long k = at < 0 ? 0 : lp_key(top, at);
-        constexpr int per_group = NT / kLpGroups;
-#pragma unroll
-        for (int d = 1; d < per_group; d *= 2) {
-          const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
-          k = o > k ? o : k;
-        }
-        if (tid % per_group == 0) sh.group[tid / per_group] = k;
-        __syncthreads();
-        // Each group's rank among the maxima, counted by its threads together.
-        const unsigned long long mine = sh.group[tid / per_group];
-        int above = 0;
-        for (int g = tid % per_group; g < kLpGroups; g += per_group) above += sh.group[g] > mine;
-#pragma unroll
-        for (int d = 1; d < per_group; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
-        if (tid % per_group == 0 && above == a.K - 1 && mine > sh.tau) sh.tau = mine;
-        __syncthreads();
-      };
-      // Sorts the buffer down to the K largest and raises the threshold past the K-th.
-      auto compress = [&]() {
-        const int n = sh.count < kLpBuffer ? sh.count : kLpBuffer;
-        __syncthreads();
-        lp_sort(sh.keys, n);
-        if (tid == 0) {
-          sh.count = n < a.K ? n : a.K;
-          if (n >= a.K && sh.keys[a.K - 1] + 1 > sh.tau) sh.tau = sh.keys[a.K - 1] + 1;
-        }
-        __syncthreads();
-      };
-      if (p == p0) {
-        __syncthreads();  // count and tau are set
-        tighten();
-      }
-      unsigned in = 0;  // which of this thread's values have entered the buffer
-      static_assert(U * V <= 32, "one bit a value");
+      if (p == p0) first_threshold(most);
       for (;;) {
+        // Which of those do so with their index counted, into the list.
         const unsigned long long tau = sh.tau;
-        const float bar = tau ? lp_unorder((unsigned)(tau >> 32)) : -INFINITY;
-        bool full = false;
-        // Few packs hold a value at or above the bar: theirs are read again (from L1 or
-        // L2), which keeps this path's registers and code small.
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (best[u] < bar) continue;
 #pragma unroll 1
-          for (int c = 0; c < V; ++c) {
-            const int i = index(u, c);
-            if (!inside(i) || in >> (u * V + c) & 1) continue;
-            const unsigned long long k = lp_key(widen(x[i]), i);
-            if (k < tau) continue;
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kLpBuffer) {
-              sh.keys[at] = k;
-              in |= 1u << (u * V + c);
-            } else {
-              full = true;
+        for (unsigned left = todo; left; left &= left - 1) {
+          const int u = __ffs(left) - 1, j = p + u * NT + tid, e0 = j * V - off;
+          const T* q = (const T*)slot(stage, u);
+          float m = widen(q[0]);
+#pragma unroll 1
+          for (int c = 1; c < V; ++c) m = max_nan(m, widen(q[c]));
+          bool placed = true;
+          if (j < p1 && lp_key(m, e0 > 0 ? e0 : 0) >= tau) {
+            const int at = atomicAdd(&sh.listed, 1);
+            placed = at < kLpList;
+            if (placed) {
+              sh.list[at] = *(const uint4*)q;
+              sh.list_at[at] = e0;
             }
           }
+          if (placed) todo &= ~(1u << u);
         }
-        // Each time round the buffer takes at least kLpBuffer - K more of the tile, so
-        // this ends after a few rounds at most.
-        if (!__syncthreads_or(full)) break;
-        compress();
+        // Each time round the list takes kLpList packs more of the tile's.
+        const bool full = __syncthreads_or(todo != 0);
+        if (full || ((tile & (tile - 1)) == 0 && p + U * NT < p1)) {
+          flush(false);
+          bar = sh.tau ? lp_unorder((unsigned)(sh.tau >> 32)) : -INFINITY;
+        }
+        if (!full) break;
       }
     }
+    stage ^= 1;
   }
-
-  // The CTA's sums, in a fixed order.
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    LpSums o;
-    o.m = __shfl_xor_sync(0xffffffffu, sums.m, d);
-    o.s = __shfl_xor_sync(0xffffffffu, sums.s, d);
-    o.t = __shfl_xor_sync(0xffffffffu, sums.t, d);
-    sums = lp_join(sums, o);
-  }
-  if (lane == 0) sh.warp[warp] = sums;
-  __syncthreads();
-  if (tid == 0) {
-    LpSums r = sh.warp[0];
-    for (int w = 1; w < NT / 32; ++w) r = lp_join(r, sh.warp[w]);
-    sh.sums = r;
-  }
-  if constexpr (TOP) {
-    const int n = sh.count < kLpBuffer ? sh.count : kLpBuffer;
-    lp_sort(sh.keys, n);  // begins and ends with a barrier
-  }
+  lp_reduce<true>({ref, s2.x + s2.y, t2.x + t2.y}, sh);
+  if constexpr (TOP) flush(true);
   if (C > 1) {
     cluster_sync();
     if (rank == 0) {
@@ -301,36 +438,49 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const __grid_consta
         LpSums r = sh.sums;
         for (unsigned q = 1; q < C; ++q) {
           const unsigned at = cluster_addr(&sh.sums, q);
-          r = lp_join(r, {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+          r = lp_join<true>(r, {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
         }
         sh.sums = r;
       }
       if constexpr (TOP) {
         for (int i = a.K + tid; i < (int)C * a.K; i += NT)
-          sh.keys[i] = ld_cluster_u64(cluster_addr(&sh.keys[i % a.K], (unsigned)(i / a.K)));
+          sh.best[i] = ld_cluster_u64(cluster_addr(&sh.best[i % a.K], (unsigned)(i / a.K)));
         __syncthreads();
-        lp_sort(sh.keys, (int)C * a.K);
+        lp_select(sh.best, (int)C * a.K, a.K, sh.best);
       }
+      __syncthreads();
     }
     cluster_sync();  // the others' shared memory has been read
-  } else {
-    __syncthreads();
+    if (rank != 0) return;
   }
-  if (rank != 0) return;
-  const LpSums r = sh.sums;
-  const float log_s = logf(r.s);
+  LpSums r = sh.sums;
+  // Nothing above the floor, a reference near the top of the range, or a NaN: read the row
+  // again with care.  (The same for all threads.)
+  const bool careful = !(r.m > kFloor * kLog2e) || r.m > 1e38f || !(r.s < INFINITY);
+  if (careful) {
+    __syncthreads();
+    lp_careful(x, a.V, sh);
+    r = sh.sums;
+  }
+  const float log_s = careful ? logf(r.s) : log2f(r.s);
+  const float lse = careful ? r.m + log_s : kLn2 * (r.m + log_s);
+  auto logprob = [&](float v) {
+    if (careful) return (v - r.m) - log_s;
+    // Far below, where products with log2(e) may overflow, the difference is as exact.
+    const float d = fmaf(v, kLog2e, -r.m);
+    return d > -1024.f ? kLn2 * (d - log_s) : v - lse;
+  };
+  const bool none = r.s == 0.f;  // all -inf
   if (tid == 0) {
-    // A row with nothing left (all -inf) has s = 0: lse -inf, no entropy, logprob -inf.
-    const bool none = r.s == 0.f;
-    a.lse[row] = none ? -INFINITY : r.m + log_s;
-    a.entropy[row] = none ? 0.f : log_s - r.t / r.s;
-    a.logprob[row] = target < 0 ? 0.f : none ? -INFINITY : (xt - r.m) - log_s;
+    a.lse[row] = none ? -INFINITY : lse;
+    a.entropy[row] = none ? 0.f : careful ? log_s - r.t / r.s : kLn2 * (log_s - r.t / r.s);
+    a.logprob[row] = target < 0 ? 0.f : none ? -INFINITY : logprob(xt);
   }
   if constexpr (TOP) {
     if (tid < a.K) {
-      const unsigned long long k = sh.keys[tid];
+      const unsigned long long k = sh.best[tid];
       a.top_ids[row * a.K + tid] = (int32_t)(0x7fffffffu - (unsigned)k);
-      a.top_values[row * a.K + tid] = r.s == 0.f ? -INFINITY : (lp_unorder((unsigned)(k >> 32)) - r.m) - log_s;
+      a.top_values[row * a.K + tid] = none ? -INFINITY : logprob(lp_unorder((unsigned)(k >> 32)));
     }
   }
 }
@@ -349,7 +499,7 @@ template <class T> struct LogprobGradArgs {
 
 template <class T, int V>
 __global__ void __launch_bounds__(kLpThreads) logprob_backward_kernel(const __grid_constant__ LogprobGradArgs<T> a) {
-  constexpr int U = kLpPacks, NT = kLpThreads;
+  constexpr int U = kLpGradPacks, NT = kLpThreads;
   pdl_entry();
   const long long row = blockIdx.x / a.blocks;
   const T* x = a.logits + row * a.stride;
@@ -417,11 +567,13 @@ template <class T> cudaError_t launch_logprob(const LogprobJob& j, const LaunchC
   constexpr long long tile = (long long)kLpThreads * kLpPacks * (16 / sizeof(T));
   unsigned C = 1;
   while (C < (unsigned)kLpMaxCluster && j.N * C < 2ll * ctx.num_sms && C * tile < j.V) C *= 2;
+  auto kernel = j.top ? logprob_kernel<T, true> : logprob_kernel<T, false>;
+  constexpr int smem = kLpStages * kLpPacks * kLpThreads * 16;
+  static_assert(smem + sizeof(LpShared) <= 55 * 1024, "four CTAs an SM");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   profile_before(ctx);
-  const cudaError_t e = j.top ? launch_pdl_cluster(logprob_kernel<T, true>, (unsigned)(j.N * C), kLpThreads, C, 0,
-                                                   ctx.stream, a, C)
-                              : launch_pdl_cluster(logprob_kernel<T, false>, (unsigned)(j.N * C), kLpThreads, C, 0,
-                                                   ctx.stream, a, C);
+  e = launch_pdl_cluster(kernel, (unsigned)(j.N * C), kLpThreads, C, smem, ctx.stream, a, C);
   profile_after(ctx);
   return e;
 }
@@ -442,7 +594,7 @@ template <class T> cudaError_t launch_logprob_backward(const LogprobJob& j, cons
   a.V = (int)j.V;
   const bool wide = (uintptr_t)j.logits % 16 == (uintptr_t)j.dlogits % 16 &&
                     (j.N <= 1 || (j.stride - j.dstride) * (long long)sizeof(T) % 16 == 0);
-  const long long per = (long long)kLpThreads * kLpPacks * (wide ? V : 1);
+  const long long per = (long long)kLpThreads * kLpGradPacks * (wide ? V : 1);
   a.blocks = (int)((j.V + (wide ? V - 1 : 0) + per - 1) / per);  // at the worst offset
   const long long grid = j.N * a.blocks;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
