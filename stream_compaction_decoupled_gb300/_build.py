@@ -72,7 +72,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         for _, log in results:
             print(log)
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results]
+    cmd = [cc] + ARCH + ["-cudart", "shared", "-shared", "-o", tmp] + [o for o, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
