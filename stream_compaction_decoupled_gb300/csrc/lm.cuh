@@ -48,21 +48,56 @@ template <class T, int V> __device__ __forceinline__ void st_pack(T* p, const Pa
     *(uint4*)p = u;
   }
 }
+// Two 16-bit values in a register, as they lie in memory, to and from fp32: one or two
+// instructions a pair (a bf16 is the upper half of an fp32).
+template <class T> __device__ __forceinline__ float2 widen2(unsigned w);
+template <> __device__ __forceinline__ float2 widen2<__nv_bfloat16>(unsigned w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 widen2<__half>(unsigned w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+template <class T> __device__ __forceinline__ unsigned narrow2(float2 v);
+template <> __device__ __forceinline__ unsigned narrow2<__nv_bfloat16>(float2 v) {
+  unsigned w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v.y), "f"(v.x));
+  return w;
+}
+template <> __device__ __forceinline__ unsigned narrow2<__half>(float2 v) {
+  unsigned w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v.y), "f"(v.x));
+  return w;
+}
 template <class T, int V> __device__ __forceinline__ void widen_pack(const Pack<T, V>& x, float (&f)[V]) {
+  if constexpr (V == 8) {
+    unsigned w[4];
+    memcpy(w, &x, 16);
 #pragma unroll
-  for (int k = 0; k < V; ++k) f[k] = widen(x.v[k]);
+    for (int k = 0; k < 4; ++k) {
+      const float2 q = widen2<T>(w[k]);
+      f[2 * k] = q.x;
+      f[2 * k + 1] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = widen(x.v[k]);
+  }
 }
 template <class T, int V> __device__ __forceinline__ Pack<T, V> narrow_pack(const float (&f)[V]) {
   Pack<T, V> r;
+  if constexpr (V == 8) {
+    unsigned w[4];
 #pragma unroll
-  for (int k = 0; k < V; ++k) r.v[k] = narrow<T>(f[k]);
+    for (int k = 0; k < 4; ++k) w[k] = narrow2<T>(make_float2(f[2 * k], f[2 * k + 1]));
+    memcpy(&r, w, 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) r.v[k] = narrow<T>(f[k]);
+  }
   return r;
 }
-
-// Two consecutive 16-bit values.
-template <class T> struct Pair {
-  T x, y;
-};
 
 // ---- approximate functions (PTX instructions, a few units in the last place) ---------
 

@@ -21,10 +21,11 @@
 // in the high half, the index reversed in the low half: unique, so ties are settled) is
 // compared with a threshold that K values are known to reach: at first the K-th largest
 // of 64 group maxima of the first tile.  The test is one comparison a pack of 16 bytes;
-// packs that pass, a few dozen of a tile, go to a list in shared memory.  The list is
-// expanded into keys after the first, second, fourth, eighth ... tile, where it is full,
-// and at the end; the K largest are kept, in order, and the threshold rises past the K-th.
-// (With the doublings about K packs pass between one and the next, K log2(tiles) in all.)
+// packs that pass, a few of a tile, go to a list in shared memory, with no barrier.  The
+// list is expanded into keys after tiles 2, 6, 18, ... and at the end: the K largest are
+// kept, in order, and the threshold rises past the K-th, so that about K packs pass
+// between one time and the next.  Where the list overflows (values that rise along the
+// row), the tiles from there on are gone through again, 256 packs at a time.
 //
 // With few rows a cluster of CTAs shares each row, slice by slice; CTA 0 of the cluster
 // reads the others' sums and lists through distributed shared memory.
@@ -34,6 +35,7 @@
 #pragma once
 
 #include <cfloat>
+#include <climits>
 
 #include "lm.cuh"
 #include "lm.h"
@@ -149,14 +151,15 @@ template <bool BASE2> __device__ __forceinline__ LpSums lp_join(LpSums a, LpSums
 
 struct LpShared {
   unsigned long long keys[kLpKeys];
-  unsigned long long best[256];  // the K largest, then those of the cluster
   uint4 list[kLpList];
   int list_at[kLpList];          // the index of each pack's first value
+  uint4 again[kLpThreads];       // packs read again
   unsigned long long group[kLpGroups];
   LpSums warp[kLpThreads / 32];
   LpSums sums;                   // the CTA's
-  unsigned long long tau;
-  int listed, count;
+  unsigned long long tau, pivot;
+  int listed, count, left;
+  int missed;                    // the first tile (its first pack) that the list had no room for
 };
 
 // The CTA's sums from its threads', in a fixed order; ends with a barrier.
@@ -193,55 +196,71 @@ template <class T> __device__ void lp_careful(const T* x, int V, LpShared& sh) {
   lp_reduce<false>(v, sh);
 }
 
-// Sorts keys[0 .. n) in falling order (n is padded with zeros to a power of two).  All
-// threads of the CTA call it, after a barrier; ends with a barrier.
-__device__ __forceinline__ void lp_sort(unsigned long long* keys, int n) {
-  int size = 32;
-  while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kLpThreads) keys[i] = 0;
-  __syncthreads();
-  for (int k = 2; k <= size; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int p = threadIdx.x; p < size / 2; p += kLpThreads) {
-        const int i = 2 * p - (p & (j - 1)), q = i + j;
-        const unsigned long long x = keys[i], y = keys[q];
-        const bool falling = (i & k) == 0;
-        if (falling ? x < y : x > y) {
-          keys[i] = y;
-          keys[q] = x;
-        }
-      }
-      __syncthreads();
-    }
+// Of 64 groups of threads (a fixed number of neighbours each) the K-th largest of the
+// groups' largest keys, or 0 where fewer than K groups have one.  All threads of the CTA
+// call it; it begins with a write to shared memory and ends with a barrier.
+__device__ __forceinline__ unsigned long long lp_kth_group(unsigned long long k, int K, LpShared& sh) {
+  constexpr int per = kLpThreads / kLpGroups;
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int d = 1; d < per; d *= 2) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
+    k = o > k ? o : k;
   }
+  if (tid % per == 0) sh.group[tid / per] = k;
+  if (tid == 0) sh.pivot = 0;
+  __syncthreads();
+  int above = 0;
+#pragma unroll
+  for (int g = 0; g < kLpGroups; g += per) above += sh.group[g + tid % per] > k;
+#pragma unroll
+  for (int d = 1; d < per; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
+  if (tid % per == 0 && above == K - 1 && k) sh.pivot = k;
+  __syncthreads();
+  return sh.pivot;
 }
 
-// The K largest of keys[0 .. n) to out[0 .. K) in falling order, zeros where there are
-// fewer.  Few keys are placed by counting the larger ones, 256 / n threads a key; more are
-// sorted.  All threads of the CTA call it after a barrier; ends with a barrier.
-__device__ __forceinline__ void lp_select(unsigned long long* keys, int n, int K, unsigned long long* out) {
+// Leaves the K largest of keys[0 .. n) first, in falling order, zeros where there are fewer.
+// Many keys are first thinned: those below the K-th largest of 64 groups' largest go, which
+// leaves at most K n / 64 or so.  The rest are placed by counting the larger ones.  All
+// threads of the CTA call it after a barrier; ends with a barrier.
+__device__ __forceinline__ void lp_select(int n, int K, LpShared& sh) {
   const int tid = threadIdx.x;
-  if (n <= 256) {
-    const int per = n <= 32 ? 8 : n <= 64 ? 4 : n <= 128 ? 2 : 1, at = tid / per;
-    const unsigned long long mine = at < n ? keys[at] : 0;
-    int above = 0;
-    if (at < n) {
-#pragma unroll 4
-      for (int j = tid % per; j < n; j += per) above += keys[j] > mine;
+  constexpr int kMany = 128;
+  while (n > kMany) {
+    constexpr int M = kLpKeys / kLpThreads;
+    unsigned long long mine[M], most = 0;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int at = tid + m * kLpThreads;
+      mine[m] = at < n ? sh.keys[at] : 0;
+      most = mine[m] > most ? mine[m] : most;
     }
-    for (int d = 1; d < per; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
-    __syncthreads();  // keys and out may be the same
-    if (tid >= n && tid < K) out[tid] = 0;
-    if (at < n && tid % per == 0 && above < K) out[above] = mine;
-  } else {
-    lp_sort(keys, n);
-    if (tid < K) out[tid] = keys[tid];
+    const unsigned long long pivot = lp_kth_group(most, K, sh);
+    if (tid == 0) sh.left = 0;
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      if (mine[m] && mine[m] >= pivot) sh.keys[atomicAdd(&sh.left, 1)] = mine[m];
+    __syncthreads();
+    n = sh.left;
   }
+  const int per = n <= 32 ? 8 : n <= 64 ? 4 : 2, at = tid / per;
+  const unsigned long long mine = at < n ? sh.keys[at] : 0;
+  int above = 0;
+  if (at < n) {
+#pragma unroll 4
+    for (int j = tid % per; j < n; j += per) above += sh.keys[j] > mine;
+  }
+  for (int d = 1; d < per; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
+  __syncthreads();
+  if (tid >= n && tid < K) sh.keys[tid] = 0;
+  if (at < n && tid % per == 0 && above < K) sh.keys[above] = mine;
   __syncthreads();
 }
 
 template <class T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_constant__ LogprobArgs<T> a, unsigned C) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_constant__ LogprobArgs<T> a, unsigned C) {
   constexpr int V = 16 / sizeof(T), U = kLpPacks, NT = kLpThreads;
   constexpr float kFloor = LpType<T>::kFloor;
   static_assert(kLpStages == 2, "two tiles in turn");
@@ -260,20 +279,11 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
   const long long end_ = (long long)p1 * V - off;
   const int end = end_ < a.V ? (int)end_ : a.V;  // values of the slice end here
 
-  long long target = -1;
-  float xt = 0.f;
-  if (rank == 0 && tid == 0) {
-    target = lp_target(a.targets, a.targets64, row);
-    if (target >= a.V) {  // no such token: reported, and treated as ignored
-      raise_err(a.err, ERRBIT_RANGE);
-      target = -1;
-    }
-    if (target >= 0) xt = widen(x[target]);
-  }
   if (TOP && tid == 0) {
     sh.listed = 0;
     sh.count = 0;
     sh.tau = 0;
+    sh.missed = INT_MAX;
   }
 
   // A thread's packs of a tile, copied one tile ahead into shared memory of its own.
@@ -300,75 +310,95 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
     }
     cp_async_commit();
   };
-  // Expands the listed packs into keys and empties the list; `last`: leaves the K largest in
-  // sh.best, else keeps them among the keys and raises the threshold past the K-th.  Called
+  // Expands the listed packs before index `before` into keys and empties the list; the K
+  // largest are left among the keys, in order, and the threshold is past the K-th.  Called
   // after a barrier, ends with one.
-  auto flush = [&](bool last) {
+  auto flush = [&](int before) {
     const int listed = sh.listed < kLpList ? sh.listed : kLpList;
     for (int q0 = 0; q0 < listed * V; q0 += kLpKeys / 2) {
       const unsigned long long tau = sh.tau;
-      if (sh.count > kLpKeys / 2) {  // uniform: count changes between barriers only
-        lp_select(sh.keys, sh.count, a.K, sh.best);
-        if (tid < a.K) sh.keys[tid] = sh.best[tid];
+      if (sh.count > kLpKeys / 2) {  // the same for all: it changes between barriers
+        lp_select(sh.count, a.K, sh);
         if (tid == 0) sh.count = a.K;
+        __syncthreads();
       }
-      __syncthreads();
       for (int q = q0 + tid; q < listed * V && q < q0 + kLpKeys / 2; q += NT) {
-        const int i = sh.list_at[q / V] + q % V;
+        const int e0 = sh.list_at[q / V], i = e0 + q % V;
         const unsigned long long k = lp_key(widen(((const T*)sh.list)[q]), i);
-        if ((unsigned)i < (unsigned)end && k >= tau) sh.keys[atomicAdd(&sh.count, 1)] = k;
+        if (e0 < before && (unsigned)i < (unsigned)end && k >= tau) sh.keys[atomicAdd(&sh.count, 1)] = k;
       }
       __syncthreads();
     }
-    lp_select(sh.keys, sh.count, a.K, sh.best);
-    if (!last) {
-      const int n = sh.count < a.K ? sh.count : a.K;
-      __syncthreads();
-      if (tid < n) sh.keys[tid] = sh.best[tid];
-      if (tid == 0) {
-        sh.count = n;
-        sh.listed = 0;
-        if (n == a.K) sh.tau = sh.best[n - 1] + 1;
+    const int n = sh.count;
+    lp_select(n, a.K, sh);
+    if (tid == 0) {
+      sh.listed = 0;
+      if (n >= a.K) {
+        sh.count = a.K;
+        sh.tau = sh.keys[a.K - 1] + 1;
+      }
+    }
+    __syncthreads();
+  };
+  // Puts a pack of this thread's into the list, at q in shared memory; false: no room.
+  auto put = [&](const unsigned char* q, int e0) {
+    const int at = atomicAdd(&sh.listed, 1);
+    if (at >= kLpList) return false;
+    sh.list[at] = *(const uint4*)q;
+    sh.list_at[at] = e0;
+    return true;
+  };
+  // Whether a pack's largest key reaches the threshold.
+  auto reaches = [&](const T* q, int e0) {
+    float m = widen(q[0]);
+#pragma unroll 1
+    for (int c = 1; c < V; ++c) m = max_nan(m, widen(q[c]));
+    return lp_key(m, e0 > 0 ? e0 : 0) >= sh.tau;
+  };
+  // Brings the keys up to date with all packs before `p`.  Called after a barrier, by all.
+  auto settle = [&](int p) {
+    const int from = sh.missed;
+    flush(from == INT_MAX ? INT_MAX : from * V - off);
+    if (from == INT_MAX) return;
+    unsigned char* mine = (unsigned char*)&sh.again[tid];
+    for (int j0 = from; j0 < p && j0 < p1; j0 += NT) {
+      const int j = j0 + tid, e0 = j * V - off;
+      if (j < p && j < p1) {
+#pragma unroll 1
+        for (int c = 0; c < V; ++c)
+          ((T*)mine)[c] = (unsigned)(e0 + c) < (unsigned)a.V ? x[e0 + c] : narrow<T>(-INFINITY);
+        if (reaches((const T*)mine, e0)) put(mine, e0);  // the list is empty: there is room
       }
       __syncthreads();
+      flush(INT_MAX);
     }
-  };
-
-  // Sets the threshold to the K-th largest of 64 groups' largest keys.
-  auto first_threshold = [&](unsigned long long k) {
-    constexpr int per_group = NT / kLpGroups;
-#pragma unroll
-    for (int d = 1; d < per_group; d *= 2) {
-      const unsigned long long o = __shfl_xor_sync(0xffffffffu, k, d);
-      k = o > k ? o : k;
-    }
-    if (tid % per_group == 0) sh.group[tid / per_group] = k;
-    __syncthreads();
-    const unsigned long long mine = sh.group[tid / per_group];
-    int above = 0;
-#pragma unroll
-    for (int g = 0; g < kLpGroups; g += per_group) above += sh.group[g + tid % per_group] > mine;
-#pragma unroll
-    for (int d = 1; d < per_group; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
-    if (tid % per_group == 0 && above == a.K - 1 && mine) sh.tau = mine;
+    if (tid == 0) sh.missed = INT_MAX;
     __syncthreads();
   };
-
   float ref = kFloor * kLog2e;
   float2 s2 = make_float2(0.f, 0.f), t2 = s2;
   float bar = -INFINITY;  // the threshold's value
-  int stage = 0, tile = 1;
+  int stage = 0, tile = 1, next = 2;
   fetch(p0, 0);
+  long long target = -1;
+  float xt = 0.f;
+  if (rank == 0 && tid == 0) {
+    target = lp_target(a.targets, a.targets64, row);
+    if (target >= a.V) {  // no such token: reported, and treated as ignored
+      raise_err(a.err, ERRBIT_RANGE);
+      target = -1;
+    }
+    if (target >= 0) xt = widen(x[target]);
+  }
   for (int p = p0; p < p1; p += U * NT, ++tile) {
     fetch(p + U * NT, stage ^ 1);
     cp_async_wait<1>();
-    unsigned todo = 0;                // packs that reach the threshold's value
+    float bests[U];                   // the largest value of each pack, or the floor
     unsigned long long most = 0;      // first tile: a key that some value here reaches
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Pack<T, V> held = ld_pack<T, V>((const T*)slot(stage, u));
-      const float best = LpType<T>::hold(held);
-      if (TOP && !(best < bar)) todo |= 1u << u;
+      const float best = bests[u] = LpType<T>::hold(held);
       if (TOP && p == p0) {
         // A pack is known to hold a value of at least its largest (the floor may stand for
         // -inf) at an index no later than its last.
@@ -387,50 +417,49 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
         ref = top;
       }
       const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-ref, -ref);
+      float v[V];
+      widen_pack(held, v);
 #pragma unroll
       for (int c = 0; c < V; c += 2) {
-        const float2 d2 = fma2(make_float2(widen(held.v[c]), widen(held.v[c + 1])), l2, r2);
+        const float2 d2 = fma2(make_float2(v[c], v[c + 1]), l2, r2);
         const float2 e2 = make_float2(ex2(d2.x), ex2(d2.y));
         s2 = add2(s2, e2);
         t2 = fma2(e2, d2, t2);
       }
     }
     if constexpr (TOP) {
-      if (p == p0) first_threshold(most);
-      for (;;) {
-        // Which of those do so with their index counted, into the list.
-        const unsigned long long tau = sh.tau;
+      if (p == p0) {
+        const unsigned long long kth = lp_kth_group(most, a.K, sh);
+        if (tid == 0) sh.tau = kth;
+        __syncthreads();
+        bar = sh.tau ? lp_unorder((unsigned)(sh.tau >> 32)) : -INFINITY;
+      }
+      unsigned over = 0, even = 0;  // packs past the threshold's value, and perhaps level with it
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (bests[u] > bar && bests[u] > kFloor) over |= 1u << u;
+        else if (!(bests[u] < bar)) even |= 1u << u;  // the floor may stand for -inf
+      }
+      if (over | even) {
 #pragma unroll 1
-        for (unsigned left = todo; left; left &= left - 1) {
+        for (unsigned left = over | even; left; left &= left - 1) {
           const int u = __ffs(left) - 1, j = p + u * NT + tid, e0 = j * V - off;
-          const T* q = (const T*)slot(stage, u);
-          float m = widen(q[0]);
-#pragma unroll 1
-          for (int c = 1; c < V; ++c) m = max_nan(m, widen(q[c]));
-          bool placed = true;
-          if (j < p1 && lp_key(m, e0 > 0 ? e0 : 0) >= tau) {
-            const int at = atomicAdd(&sh.listed, 1);
-            placed = at < kLpList;
-            if (placed) {
-              sh.list[at] = *(const uint4*)q;
-              sh.list_at[at] = e0;
-            }
-          }
-          if (placed) todo &= ~(1u << u);
+          const unsigned char* q = slot(stage, u);
+          if (j >= p1 || (even >> u & 1 && !reaches((const T*)q, e0))) continue;
+          if (!put(q, e0)) atomicMin(&sh.missed, p);
         }
-        // Each time round the list takes kLpList packs more of the tile's.
-        const bool full = __syncthreads_or(todo != 0);
-        if (full || ((tile & (tile - 1)) == 0 && p + U * NT < p1)) {
-          flush(false);
-          bar = sh.tau ? lp_unorder((unsigned)(sh.tau >> 32)) : -INFINITY;
-        }
-        if (!full) break;
+      }
+      if (tile == next && p + U * NT < p1) {
+        next *= 3;
+        __syncthreads();
+        settle(p + U * NT);
+        bar = sh.tau ? lp_unorder((unsigned)(sh.tau >> 32)) : -INFINITY;
       }
     }
     stage ^= 1;
   }
   lp_reduce<true>({ref, s2.x + s2.y, t2.x + t2.y}, sh);
-  if constexpr (TOP) flush(true);
+  if constexpr (TOP) settle(INT_MAX);
   if (C > 1) {
     cluster_sync();
     if (rank == 0) {
@@ -444,9 +473,9 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
       }
       if constexpr (TOP) {
         for (int i = a.K + tid; i < (int)C * a.K; i += NT)
-          sh.best[i] = ld_cluster_u64(cluster_addr(&sh.best[i % a.K], (unsigned)(i / a.K)));
+          sh.keys[i] = ld_cluster_u64(cluster_addr(&sh.keys[i % a.K], (unsigned)(i / a.K)));
         __syncthreads();
-        lp_select(sh.best, (int)C * a.K, a.K, sh.best);
+        lp_select((int)C * a.K, a.K, sh);
       }
       __syncthreads();
     }
@@ -478,7 +507,7 @@ __global__ void __launch_bounds__(kLpThreads, 3) logprob_kernel(const __grid_con
   }
   if constexpr (TOP) {
     if (tid < a.K) {
-      const unsigned long long k = sh.best[tid];
+      const unsigned long long k = sh.keys[tid];
       a.top_ids[row * a.K + tid] = (int32_t)(0x7fffffffu - (unsigned)k);
       a.top_values[row * a.K + tid] = none ? -INFINITY : logprob(lp_unorder((unsigned)(k >> 32)));
     }

@@ -154,10 +154,7 @@ template <class T, class G> __device__ __forceinline__ float2 rec_pair(const uns
     if constexpr (sizeof(T) == 4) {
       return *(const float2*)(row + lane * 8);
     } else {
-      Pair<T> q;
-      const unsigned u = *(const unsigned*)(row + lane * 4);
-      memcpy(&q, &u, 4);
-      return make_float2(widen(q.x), widen(q.y));
+      return widen2<T>(*(const unsigned*)(row + lane * 4));
     }
   } else {
     const T* q = (const T*)(row + (lo & 15)) + 2 * lane;
@@ -172,10 +169,7 @@ template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, fl
       if constexpr (sizeof(T) == 4) {
         *(float2*)p = v;
       } else {
-        const Pair<T> q = {narrow<T>(v.x), narrow<T>(v.y)};
-        unsigned u;
-        memcpy(&u, &q, 4);
-        *(unsigned*)p = u;
+        *(unsigned*)p = narrow2<T>(v);
       }
     }
   } else {
