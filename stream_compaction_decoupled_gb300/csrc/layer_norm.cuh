@@ -47,8 +47,26 @@ template <int V_, int TPR_, int NV_, int NT_, bool EDGE_> struct NormGeom {
   static constexpr int STEP = TPR * V;        // values between a thread's packs
 };
 
+// Which of a thread's packs lie in a row of D values, all of their values or some.  The
+// same for every row of a CTA, so it is worked out once.
+template <class G> struct NormPacks {
+  unsigned full = 0, part = 0;  // a bit a pack
+  int e0, D;                    // the thread's first value
+  __device__ __forceinline__ NormPacks(int e0_, int D_) : e0(e0_), D(D_) {
+#pragma unroll
+    for (int i = 0; i < G::NV; ++i) {
+      const int e = e0 + i * G::STEP;
+      if (!G::EDGE ? e < D : e >= 0 && e + G::V <= D) full |= 1u << i;
+      else if (G::EDGE && e < D && e + G::V > 0) part |= 1u << i;
+    }
+  }
+  __device__ __forceinline__ bool in(int i, int c) const {  // of a part pack
+    return (unsigned)(e0 + i * G::STEP + c) < (unsigned)D;
+  }
+};
+
 // Values e0 .. e0 + V - 1 of a row of D values, the first of them at p; those outside the
-// row read as zero and are not written.
+// row read as zero.
 template <class T, class G> __device__ __forceinline__ Pack<T, G::V> norm_load(const T* p, int e0, int D, bool on) {
   constexpr int V = G::V;
   Pack<T, V> r;
@@ -65,18 +83,30 @@ template <class T, class G> __device__ __forceinline__ Pack<T, G::V> norm_load(c
   }
   return r;
 }
+// Writes pack i, whose first value goes to p.  A part pack (a thread has two at most, the
+// row's first and its last) only goes to `spare`, shared memory of the thread's own, from
+// where norm_store_parts writes its values one by one: one copy of that code, after the
+// row's registers are free.
 template <class T, class G>
-__device__ __forceinline__ void norm_store(T* p, int e0, int D, const Pack<T, G::V>& v) {
-  if constexpr (!G::EDGE) {
-    if (e0 < D) st_pack(p, v);
-  } else if (e0 >= 0 && e0 + G::V <= D) {
-    st_pack(p, v);
-  } else {
+__device__ __forceinline__ void norm_store(T* p, const NormPacks<G>& k, int i, const float (&v)[G::V],
+                                           unsigned char* spare) {
+  if (k.full >> i & 1) st_pack(p, narrow_pack<T, G::V>(v));
+  else if (G::EDGE && k.part >> i & 1) st_pack((T*)(spare + (i ? G::NT * 16 : 0)), narrow_pack<T, G::V>(v));
+}
+template <class T, class G>
+__device__ __forceinline__ void norm_store_parts(T* row, const NormPacks<G>& k, const unsigned char* spare) {
+  if constexpr (G::EDGE) {
+#pragma unroll 1
+    for (unsigned left = k.part; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const Pack<T, G::V> v = ld_pack<T, G::V>((const T*)(spare + (i ? G::NT * 16 : 0)));
 #pragma unroll
-    for (int c = 0; c < G::V; ++c)
-      if ((unsigned)(e0 + c) < (unsigned)D) p[c] = v.v[c];
+      for (int c = 0; c < G::V; ++c)
+        if (k.in(i, c)) row[k.e0 + i * G::STEP + c] = v.v[c];
+    }
   }
 }
+
 // V parameters from e0 on; `none` outside the row and where p is null.
 template <class P, class G>
 __device__ __forceinline__ void norm_params(P (&r)[G::V], const P* p, int e0, int D, float none) {
@@ -129,7 +159,8 @@ template <class G> __device__ __forceinline__ float2 norm_sum(float2 v, NormShar
 // One row's statistics and output from its values in registers (zero outside the row).
 template <class T, class P, class G, class W>
 __device__ __forceinline__ void norm_row(float (&x)[G::NV][G::V], const NormArgs<T, P>& a, long long row, bool live,
-                                         int e0, NormShared<G>& sh, int& turn, W&& params) {
+                                         const NormPacks<G>& k, unsigned char* spare, NormShared<G>& sh, int& turn,
+                                         W&& params) {
   constexpr int V = G::V, NV = G::NV;
   const float inv = 1.f / (float)a.D;
   float s = 0.f;
@@ -141,13 +172,15 @@ __device__ __forceinline__ void norm_row(float (&x)[G::NV][G::V], const NormArgs
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const bool pack = e0 + i * G::STEP < a.D;
+    const bool full = k.full >> i & 1;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const bool in = G::EDGE ? (unsigned)(e0 + i * G::STEP + c) < (unsigned)a.D : pack;
-      x[i][c] = in ? x[i][c] - mean : 0.f;
-      q = fmaf(x[i][c], x[i][c], q);
+    for (int c = 0; c < V; ++c) x[i][c] = full ? x[i][c] - mean : x[i][c];
+    if (G::EDGE && k.part >> i & 1) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) x[i][c] = k.in(i, c) ? x[i][c] - mean : 0.f;
     }
+#pragma unroll
+    for (int c = 0; c < V; ++c) q = fmaf(x[i][c], x[i][c], q);
   }
   const float rstd = 1.f / sqrtf(norm_sum<G>(make_float2(q, 0.f), sh, turn).x * inv + a.eps);
   if (!live) return;
@@ -155,15 +188,16 @@ __device__ __forceinline__ void norm_row(float (&x)[G::NV][G::V], const NormArgs
     a.mean[row] = mean;
     a.rstd[row] = rstd;
   }
-  T* y = a.y + row * a.ys + e0;
+  T* y = a.y + row * a.ys + k.e0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     P w[V], b[V];
     params(i, w, b);
 #pragma unroll
     for (int c = 0; c < V; ++c) x[i][c] = fmaf(x[i][c] * rstd, widen(w[c]), widen(b[c]));
-    norm_store<T, G>(y + i * G::STEP, e0 + i * G::STEP, a.D, narrow_pack<T, V>(x[i]));
+    norm_store<T, G>(y + i * G::STEP, k, i, x[i], spare);
   }
+  norm_store_parts<T, G>(a.y + row * a.ys, k, spare);
 }
 
 // Rows on 16-byte boundaries.
@@ -183,7 +217,7 @@ __global__ void __launch_bounds__(G::NT) norm_forward_kernel(const __grid_consta
 #pragma unroll
   for (int i = 0; i < G::NV; ++i) widen_pack(px[i], x[i]);
   int turn = 0;
-  norm_row<T, P, G>(x, a, row, live, e0, sh, turn, [&](int i, P(&w)[G::V], P(&b)[G::V]) {
+  norm_row<T, P, G>(x, a, row, live, NormPacks<G>(e0, a.D), nullptr, sh, turn, [&](int i, P(&w)[G::V], P(&b)[G::V]) {
     norm_params<P, G>(w, a.w, e0 + i * G::STEP, a.D, 1.f);
     norm_params<P, G>(b, a.b, e0 + i * G::STEP, a.D, 0.f);
   });
@@ -197,33 +231,44 @@ template <class T, class G, int ARRAYS, int STAGES_> struct NormRing {
   static constexpr int STAGES = STAGES_;
   static constexpr int SLOT = G::NT * 16;                       // one pack of every thread
   static constexpr int STAGE = ARRAYS * G::NV * SLOT;
-  static constexpr int BYTES = STAGES * STAGE;
+  static constexpr int BYTES = STAGES * STAGE + (G::EDGE ? 2 * SLOT : 0);
   unsigned char* mem;
-  int e0, D;
+  __device__ __forceinline__ unsigned char* spare() const { return mem + STAGES * STAGE + threadIdx.x * 16; }
   __device__ __forceinline__ unsigned char* slot(int stage, int array, int i) const {
     return mem + stage * STAGE + (array * G::NV + i) * SLOT + threadIdx.x * 16;
   }
-  __device__ __forceinline__ void init(void* smem, int e0_, int D_) {
-    mem = (unsigned char*)smem, e0 = e0_, D = D_;
+  __device__ __forceinline__ void init(void* smem) {
+    mem = (unsigned char*)smem;
     for (int at = threadIdx.x; at < BYTES / 16; at += G::NT) ((uint4*)mem)[at] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
   }
-  // The row's pack i: p is where value e0 of the row is.
-  __device__ __forceinline__ void copy(int stage, int array, int i, const T* p) const {
-    const int e = e0 + i * G::STEP;
-    if (e >= D) return;
-    unsigned char* dst = slot(stage, array, i);
-    if constexpr (!G::EDGE) {
-      cp_async16(dst, p + i * G::STEP);
-    } else if (e >= 0) {
-      const int n = D - e < G::V ? D - e : G::V;
-      cp_async_part(dst, p + i * G::STEP, n * (int)sizeof(T));
-    } else {  // the row begins inside the pack
-      for (int c = -e; c < G::V && e + c < D; ++c) ((T*)dst)[c] = p[i * G::STEP + c];
+  // The row's pack i: p is where value e0 of the row is, `first` the array's first value.
+  // A part pack is copied up to the row's end, zeros after it; what it holds before the
+  // row's beginning (values of the array between its rows) is masked when it is read.
+  // Only where those would lie before the array are the values taken one by one.
+  __device__ __forceinline__ void copy(int stage, int array, int i, const T* p, const T* first,
+                                       const NormPacks<G>& k) const {
+    if (k.full >> i & 1) {
+      cp_async16(slot(stage, array, i), p + i * G::STEP);
+    } else if (G::EDGE && k.part >> i & 1) {
+      const T* q = p + i * G::STEP;
+      T* dst = (T*)slot(stage, array, i);
+      const int n = k.D - (k.e0 + i * G::STEP);
+      if (q >= first) {
+        cp_async_part(dst, q, (n < G::V ? n : G::V) * (int)sizeof(T));
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < G::V; ++c)
+          if (k.in(i, c)) dst[c] = q[c];
+      }
     }
   }
-  __device__ __forceinline__ void read(int stage, int array, int i, float (&v)[G::V]) const {
+  __device__ __forceinline__ void read(int stage, int array, int i, float (&v)[G::V], const NormPacks<G>& k) const {
     widen_pack(ld_pack<T, G::V>((const T*)slot(stage, array, i)), v);
+    if (G::EDGE && i == 0 && k.e0 < 0) {
+#pragma unroll
+      for (int c = 0; c < G::V; ++c) v[c] = c < -k.e0 ? 0.f : v[c];
+    }
   }
 };
 
@@ -264,7 +309,8 @@ __global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_c
   const int t = threadIdx.x % G::TPR, sub = threadIdx.x / G::TPR;
   const int e0 = t * V - (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T));
   Ring ring;
-  ring.init(smem, e0, a.D);
+  ring.init(smem);
+  const NormPacks<G> packs(e0, a.D);
   NormParams<P, G> ws, bs;
   ws.init(smem + Ring::BYTES, a.w, e0, a.D, 1.f);
   bs.init(smem + Ring::BYTES + NormParams<P, G>::BYTES, a.b, e0, a.D, 0.f);
@@ -273,7 +319,7 @@ __global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_c
     if (row < a.N) {
       const T* p = a.x + row * a.xs + e0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) ring.copy(stage, 0, i, p);
+      for (int i = 0; i < NV; ++i) ring.copy(stage, 0, i, p, a.x, packs);
     }
     cp_async_commit();
   };
@@ -284,9 +330,9 @@ __global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_c
     cp_async_wait<STAGES - 1>();
     float x[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) ring.read(stage, 0, i, x[i]);
+    for (int i = 0; i < NV; ++i) ring.read(stage, 0, i, x[i], packs);
     stage = (stage + 1) % STAGES;
-    norm_row<T, P, G>(x, a, row, true, e0, sh, turn, [&](int i, P(&w)[V], P(&b)[V]) {
+    norm_row<T, P, G>(x, a, row, true, packs, ring.spare(), sh, turn, [&](int i, P(&w)[V], P(&b)[V]) {
       ws.get(i, w);
       bs.get(i, b);
     });
@@ -294,14 +340,17 @@ __global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_c
 }
 
 // The gradient: persistent, one CTA an SM, x and dy through the ring, the sums over rows in
-// registers.  At 32 values a thread those would take too many: db's are in shared memory
-// then, each thread's own, and the weight comes from L1 in place of shared memory.
+// registers.  Where those would take too many (32 values a thread, more than 512
+// threads, or 512 at any offset in fp32), db's are in shared memory, each thread's own, and a row's n and g are worked
+// out twice; at 32 values the weight comes from L1 in place of shared memory.
 template <class T, class P, class G> struct NormBackwardSmem {
   static constexpr bool BIG = G::NV * G::V > 16;
-  static constexpr bool AGAIN = BIG || G::NT > 512;  // n and g are worked out twice, not kept
-  static constexpr int ROOM = 220 * 1024, ROW = NormRing<T, G, 2, 1>::BYTES;
-  static constexpr int REST = BIG ? G::NT * G::NV * G::V * (int)sizeof(float) : NormParams<P, G>::BYTES;
-  static constexpr int STAGES = (ROOM - REST) / ROW < 3 ? (ROOM - REST) / ROW : 3;
+  static constexpr bool TIGHT = BIG || G::NT > 512 || (G::EDGE && G::TPR == 512 && G::V == 4);
+  static constexpr int SUMS = TIGHT ? G::NT * G::NV * G::V * (int)sizeof(float) : 0;
+  static constexpr int ROOM = 220 * 1024, ROW = NormRing<T, G, 2, 1>::STAGE;
+  static constexpr int REST = SUMS + (BIG ? 0 : NormParams<P, G>::BYTES) + NormRing<T, G, 2, 1>::BYTES - ROW;
+  static constexpr int STAGES = (ROOM - REST) / ROW < 5 ? (ROOM - REST) / ROW : 5;
+  using Ring = NormRing<T, G, 2, STAGES>;
   static constexpr int BYTES = STAGES * ROW + REST;
   static_assert(STAGES >= 1, "fits");
 };
@@ -309,26 +358,28 @@ template <class T, class P, class G>
 __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_constant__ NormArgs<T, P> a) {
   using S = NormBackwardSmem<T, P, G>;
   constexpr int V = G::V, NV = G::NV, N = NV * V, STAGES = S::STAGES;
-  constexpr bool BIG = S::BIG, AGAIN = S::AGAIN;
+  constexpr bool BIG = S::BIG, TIGHT = S::TIGHT;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ NormShared<G> sh;
+  __shared__ float2 stats[STAGES][G::NT / 32];
   pdl_entry();
   const int t = threadIdx.x % G::TPR, sub = threadIdx.x / G::TPR;
   const long long first = blockIdx.x, grid = gridDim.x;
   const int off = G::EDGE && first < a.N ? (int)((uintptr_t)(a.x + first * a.xs) % 16 / sizeof(T)) : 0;
   const int e0 = t * V - off;
-  NormRing<T, G, 2, STAGES> ring;
-  ring.init(smem, e0, a.D);
-  float2 dw[N / 2], db_[BIG ? 1 : N / 2];
-  float2* db_mem = (float2*)(smem + STAGES * S::ROW) + threadIdx.x;
+  typename S::Ring ring;
+  ring.init(smem);
+  const NormPacks<G> packs(e0, a.D);
+  float2 dw[N / 2], db_[TIGHT ? 1 : N / 2];
+  float2* db_mem = (float2*)(smem + S::Ring::BYTES) + threadIdx.x;
   auto db = [&](int k) -> float2& {
-    if constexpr (BIG) return db_mem[k * G::NT];
+    if constexpr (TIGHT) return db_mem[k * G::NT];
     else return db_[k];
   };
 #pragma unroll
   for (int k = 0; k < N / 2; ++k) dw[k] = db(k) = make_float2(0.f, 0.f);
   NormParams<P, G> ws;
-  if constexpr (!BIG) ws.init(smem + STAGES * S::ROW, a.w, e0, a.D, 1.f);
+  if constexpr (!BIG) ws.init(smem + S::Ring::BYTES + S::SUMS, a.w, e0, a.D, 1.f);
   auto weight = [&](int i, P(&w)[V]) {
     if constexpr (BIG) norm_params<P, G>(w, a.w, e0 + i * G::STEP, a.D, 1.f);
     else ws.get(i, w);
@@ -338,32 +389,35 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
   auto fetch = [&](long long row, int stage) {
     if (row < a.N) {
       const T *x = a.x + row * a.xs + e0, *dy = a.dy + row * a.dys + e0;
-#pragma unroll
+#pragma unroll(G::EDGE ? 1 : NV)
       for (int i = 0; i < NV; ++i) {
-        ring.copy(stage, 0, i, x);
-        ring.copy(stage, 1, i, dy);
+        ring.copy(stage, 0, i, x, a.x, packs);
+        ring.copy(stage, 1, i, dy, a.dy, packs);
+      }
+      // The row's statistics come the same way, once a warp: an ordinary load among the
+      // copies would be waited for together with all of them (measured: 115.8 us against
+      // 88.9 at 16384 x 4096 bf16, with the loads and with constants).
+      if (threadIdx.x % 32 == 0) {
+        cp_async4(&stats[stage][threadIdx.x / 32].x, a.mean + row);
+        cp_async4(&stats[stage][threadIdx.x / 32].y, a.rstd + row);
       }
     }
     cp_async_commit();
   };
-  auto load_stats = [&](long long row) {
-    return row < a.N ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.f, 0.f);
-  };
   for (int k = 0; k < STAGES - 1; ++k) fetch(r0 + k * hop, k);
-  float2 next = load_stats(r0);
   int turn = 0, stage = 0;
   for (long long row = r0; row < a.N; row += hop) {
     fetch(row + (STAGES - 1) * hop, (stage + STAGES - 1) % STAGES);
-    const float mean = next.x, rstd = next.y;
-    next = load_stats(row + hop);
     cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    const float mean = stats[stage][threadIdx.x / 32].x, rstd = stats[stage][threadIdx.x / 32].y;
     // n and g = dy w of pack i, two values at a time.
     const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
     auto terms = [&](int i, float2 (&n)[V / 2], float2 (&d)[V / 2], float2 (&g)[V / 2]) {
       float x[V], y[V];
       P w[V];
-      ring.read(stage, 0, i, x);
-      ring.read(stage, 1, i, y);  // zero outside the row
+      ring.read(stage, 0, i, x, packs);
+      ring.read(stage, 1, i, y, packs);  // zero outside the row
       weight(i, w);
 #pragma unroll
       for (int c = 0; c < V / 2; ++c) {
@@ -372,11 +426,11 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
         g[c] = mul2(d[c], make_float2(widen(w[2 * c]), widen(w[2 * c + 1])));
       }
     };
-    float2 n[AGAIN ? 1 : NV][V / 2], g[AGAIN ? 1 : NV][V / 2];
+    float2 n[TIGHT ? 1 : NV][V / 2], g[TIGHT ? 1 : NV][V / 2];
     float2 sg = make_float2(0.f, 0.f), sgn = sg;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int q = AGAIN ? 0 : i;
+      const int q = TIGHT ? 0 : i;
       float2 d[V / 2];
       terms(i, n[q], d, g[q]);
 #pragma unroll
@@ -393,8 +447,8 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
     T* dx = a.dx + row * a.dxs + e0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int q = AGAIN ? 0 : i;
-      if constexpr (AGAIN) {
+      const int q = TIGHT ? 0 : i;
+      if constexpr (TIGHT) {
         float2 d[V / 2];
         terms(i, n[0], d, g[0]);
       }
@@ -404,8 +458,9 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
         const float2 v = mul2(add2(fma2(n[q][c], mgn, g[q][c]), mg), r2);
         o[2 * c] = v.x, o[2 * c + 1] = v.y;
       }
-      norm_store<T, G>(dx + i * G::STEP, e0 + i * G::STEP, a.D, narrow_pack<T, V>(o));
+      norm_store<T, G>(dx + i * G::STEP, packs, i, o, ring.spare());
     }
+    norm_store_parts<T, G>(a.dx + row * a.dxs, packs, ring.spare());
     stage = (stage + 1) % STAGES;
   }
   if (!a.part) return;
@@ -425,7 +480,7 @@ __global__ void __launch_bounds__(G::NT) norm_backward_kernel(const __grid_const
     }
   } else {
     // The CTA's groups of threads, one after another; the ring's memory is free now.
-    static_assert(NormRing<T, G, 2, STAGES>::BYTES >= N * G::NT * (int)sizeof(float), "the sums fit");
+    static_assert(S::Ring::BYTES >= N * G::NT * (int)sizeof(float), "the sums fit");
     float* fold = (float*)smem;
     cp_async_wait<0>();
 #pragma unroll
@@ -586,6 +641,20 @@ inline unsigned norm_grid(long long N, long long most) {
   return (unsigned)((g + 7) / 8 * 8);
 }
 
+// Calls f(geometry) with the first of the listed group sizes whose threads hold a row of
+// `packs` packs at NV packs a thread; the last one is taken without asking.  A CTA has at
+// most MOST threads (or one group), and at most 15 groups that meet at named barriers.
+template <int V, int NV, int MOST, bool EDGE, int TPR, int... More, class F>
+cudaError_t norm_pick(long long packs, F&& f) {
+  if constexpr (sizeof...(More) > 0) {
+    if (packs > (long long)TPR * NV) return norm_pick<V, NV, MOST, EDGE, More...>(packs, f);
+  }
+  constexpr int cap = TPR % 3 == 0 && MOST > 768 ? 768 : MOST;  // whole groups, and 85 registers a thread
+  constexpr int fit = cap / TPR < 1 ? 1 : cap / TPR;
+  constexpr int rows = TPR > 32 && fit > 15 ? 15 : fit;
+  return f((NormGeom<V, TPR, NV, TPR * rows, EDGE>*)nullptr);
+}
+
 template <class T, class P> cudaError_t launch_layer_norm(const LayerNormJob& j, const LaunchCtx& ctx) {
   constexpr int V = 16 / sizeof(T);
   const NormArgs<T, P> a = norm_args<T, P>(j);
@@ -594,40 +663,33 @@ template <class T, class P> cudaError_t launch_layer_norm(const LayerNormJob& j,
   const long long packs = even ? j.D / V : (j.D + 2 * (V - 1)) / V;  // EDGE: at the worst offset
   auto run = [&](auto* gp) {
     using G = std::remove_pointer_t<decltype(gp)>;
-    if constexpr (G::EDGE) {
-      constexpr int room = 220 * 1024;
-      constexpr int row = NormRing<T, G, 1, 1>::BYTES, params = 2 * NormParams<P, G>::BYTES;
-      constexpr int STAGES = (room - params) / row < 3 ? (room - params) / row : 3;
-      constexpr int smem = STAGES * row + params;
-      static_assert(STAGES >= 1 && smem <= room, "fits");
-      auto kernel = norm_forward_edge_kernel<T, P, G, STAGES>;
-      const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      // Two CTAs an SM where their shared memory allows (227 KB, 1 KB of each reserved).
-      const long long ctas = smem <= 112 * 1024 && G::NT <= 512 ? 2 : 1;
-      return r != cudaSuccess ? r : launch_pdl(kernel, norm_grid(j.N, ctas * ctx.num_sms), G::NT, smem, ctx.stream, a);
-    }
-    else
-      return launch_pdl(norm_forward_kernel<T, P, G>, (unsigned)((j.N + G::ROWS - 1) / G::ROWS), G::NT, 0, ctx.stream, a);
+    return launch_pdl(norm_forward_kernel<T, P, G>, (unsigned)((j.N + G::ROWS - 1) / G::ROWS), G::NT, 0, ctx.stream, a);
+  };
+  auto run_edge = [&](auto* gp) {
+    using G = std::remove_pointer_t<decltype(gp)>;
+    constexpr int room = 220 * 1024;
+    constexpr int row = NormRing<T, G, 1, 1>::STAGE;
+    constexpr int rest = 2 * NormParams<P, G>::BYTES + NormRing<T, G, 1, 1>::BYTES - row;
+    constexpr int STAGES = (room - rest) / row < 3 ? (room - rest) / row : 3;
+    constexpr int smem = STAGES * row + rest;
+    static_assert(STAGES >= 1 && smem <= room, "fits");
+    auto kernel = norm_forward_edge_kernel<T, P, G, STAGES>;
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // Two CTAs an SM where their shared memory allows (227 KB, 1 KB of each reserved).
+    const long long ctas = smem <= 112 * 1024 && G::NT <= 512 ? 2 : 1;
+    return r != cudaSuccess ? r : launch_pdl(kernel, norm_grid(j.N, ctas * ctx.num_sms), G::NT, smem, ctx.stream, a);
   };
   cudaError_t e;
   profile_before(ctx);
   if (even && packs <= 4096 && j.N <= 0x7fffffffll) {
-    if (packs <= 32) e = run((NormGeom<V, 32, 1, 128, false>*)nullptr);
-    else if (packs <= 64) e = run((NormGeom<V, 32, 2, 128, false>*)nullptr);
-    else if (packs <= 128) e = run((NormGeom<V, 32, 4, 128, false>*)nullptr);
-    else if (packs <= 256) e = run((NormGeom<V, 64, 4, 128, false>*)nullptr);
-    else if (packs <= 512) e = run((NormGeom<V, 128, 4, 128, false>*)nullptr);
-    else if (packs <= 1024) e = run((NormGeom<V, 256, 4, 256, false>*)nullptr);
-    else if (packs <= 2048) e = run((NormGeom<V, 512, 4, 512, false>*)nullptr);
-    else e = run((NormGeom<V, 1024, 4, 1024, false>*)nullptr);
-  } else if (wide && packs <= 512 * (16 / V)) {
+    if (packs <= 32) e = norm_pick<V, 1, 128, false, 32>(packs, run);
+    else if (packs <= 64) e = norm_pick<V, 2, 128, false, 32>(packs, run);
+    else if (packs <= 128) e = norm_pick<V, 4, 128, false, 32>(packs, run);
+    else if (packs <= 256) e = norm_pick<V, 2, 128, false, 128>(packs, run);
+    else e = norm_pick<V, 4, 128, false, 96, 128, 192, 256, 384, 512, 768, 1024>(packs, run);
+  } else if (wide && packs <= 768 * (16 / V)) {
     constexpr int U = 16 / V;  // 16 values a thread
-    if (packs <= 32 * U) e = run((NormGeom<V, 32, U, 512, true>*)nullptr);
-    else if (packs <= 128 * U) e = run((NormGeom<V, 128, U, 512, true>*)nullptr);
-    else if (packs <= 256 * U) e = run((NormGeom<V, 256, U, 512, true>*)nullptr);
-    else e = run((NormGeom<V, 512, U, 512, true>*)nullptr);
-  } else if (wide && packs <= 1024 * (16 / V)) {
-    e = run((NormGeom<V, 1024, 16 / V, 1024, true>*)nullptr);
+    e = norm_pick<V, U, 512, true, 32, 64, 96, 128, 192, 256, 384, 512, 768>(packs, run_edge);
   } else {
     e = launch_pdl(norm_forward_long_kernel<T, P>, norm_grid(j.N, 4ll * ctx.num_sms), kNormLongThreads, 0, ctx.stream, a);
   }
@@ -657,23 +719,15 @@ template <class T, class P> cudaError_t launch_layer_norm_backward(const LayerNo
     count = (int)grid;
     return r != cudaSuccess ? r : launch_pdl(kernel, grid, G::NT, smem, ctx.stream, a);
   };
-  auto pick = [&](auto edge) {
-    constexpr bool E = decltype(edge)::value;
-    constexpr int U = 16 / V;  // 16 values a thread
-    if (packs <= 32 * U) return run((NormGeom<V, 32, U, 512, E>*)nullptr);
-    if (packs <= 128 * U) return run((NormGeom<V, 128, U, 512, E>*)nullptr);
-    if (packs <= 256 * U) return run((NormGeom<V, 256, U, 512, E>*)nullptr);
-    if (packs <= 512 * U) return run((NormGeom<V, 512, U, 512, E>*)nullptr);
-    // Longer rows; at any offset the wider one would spill.
-    if constexpr (E) return run((NormGeom<V, 768, U, 768, true>*)nullptr);
-    else return run((NormGeom<V, 512, 2 * U, 512, false>*)nullptr);
-  };
   cudaError_t e;
   profile_before(ctx);
-  if (even && packs <= 512 * (32 / V)) {
-    e = pick(std::false_type{});
-  } else if (wide && packs <= 768 * (16 / V)) {
-    e = pick(std::true_type{});
+  constexpr int U = 16 / V;  // 16 values a thread
+  if (even && packs <= 512 * U) {
+    e = norm_pick<V, U, 512, false, 32, 64, 96, 128, 192, 256, 384, 512>(packs, run);
+  } else if (even && packs <= 512 * 2 * U) {
+    e = norm_pick<V, 2 * U, 512, false, 384, 512>(packs, run);
+  } else if (wide && packs <= 768 * U) {
+    e = norm_pick<V, U, 512, true, 32, 64, 96, 128, 192, 256, 384, 512, 768>(packs, run);
   } else {
     e = launch_pdl(norm_backward_long_kernel<T, P>, norm_grid(j.N, 4ll * ctx.num_sms), kNormLongThreads, 0, ctx.stream, a);
     if (e == cudaSuccess && sums) {

@@ -279,13 +279,21 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     }
     cp_async_commit();
   };
-  auto flags = [&](int k) -> int {  // lane r < R: whether its warp's row r is a start
-    const long long t = (long long)k * step + tile0 + warp * R + lane;
-    return starts && lane < R && t < a.T_ ? starts[t] : 0;
+  // Which of this warp's rows are starts, for 32 rounds at once: lane l has round k + l's,
+  // a bit a row.  (A load every round would be waited for together with the copies in
+  // flight.)
+  auto flags = [&](int k) {
+    unsigned bits = 0;
+    const long long t = (long long)(k + lane) * step + tile0 + warp * R;
+    if (starts) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) bits |= (t + r < a.T_ && starts[t + r] != 0 ? 1u : 0u) << r;
+    }
+    return bits;
   };
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
-  int flag = flags(0);
+  unsigned marks = 0;
   float2 carry = a.h0 ? rec_load2(a.h0 + b * a.D + d0 + 2 * lane, n) : make_float2(0.f, 0.f);
   rec_cluster_init(sh, C);
 
@@ -294,8 +302,8 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     cp_async_wait<G::STAGES - 2>();
     __syncthreads();  // the tile is in; the one before it has been read by all
     fetch(k + G::STAGES - 1);
-    const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
-    flag = flags(k + 1);
+    if (k % 32 == 0) marks = flags(k);
+    const unsigned drop = __shfl_sync(0xffffffffu, marks, k % 32);
     const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
     unsigned xo = 0, fo = 0, go = 0;  // EDGE: the rows' offsets
     if constexpr (G::EDGE) {
@@ -404,13 +412,18 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     }
     cp_async_commit();
   };
-  auto flags = [&](int k) -> int {
-    const long long t = (long long)t_warp - (long long)k * step - lane;
-    return starts && lane < R && t >= 0 ? starts[t] : 0;
+  auto flags = [&](int k) {  // as in the forward kernel
+    unsigned bits = 0;
+    const long long t = (long long)t_warp - (long long)(k + lane) * step;
+    if (starts) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) bits |= (t - r >= 0 && starts[t - r] != 0 ? 1u : 0u) << r;
+    }
+    return bits;
   };
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
-  int flag = flags(0);
+  unsigned marks = 0;
   float2 carry = a.dlast ? rec_load2(a.dlast + at, n) : make_float2(0.f, 0.f);
   const float2 first = a.h0 ? rec_load2(a.h0 + at, n) : make_float2(0.f, 0.f);
   rec_cluster_init(sh, C);
@@ -420,8 +433,8 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     cp_async_wait<G::STAGES - 2>();
     __syncthreads();
     fetch(k + G::STAGES - 1);
-    const unsigned drop = __ballot_sync(0xffffffffu, flag != 0);
-    flag = flags(k + 1);
+    if (k % 32 == 0) marks = flags(k);
+    const unsigned drop = __shfl_sync(0xffffffffu, marks, k % 32);
     const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
     // EDGE: the low address of row t = rows - 1 - r of a strip.
     auto lo = [&](const T* strip, long long st, int t) {
