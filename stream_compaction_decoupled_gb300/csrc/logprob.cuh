@@ -514,8 +514,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
   }
 }
 
-// The gradient: one read and one write of each logit, U packs a thread.  Where the rows of
-// the two arrays start at different offsets from a 16-byte boundary V is 1.
+// The gradient: one read and one write of each logit, U packs a thread,
+//   dx = -p (w + h (log p + entropy)),   p = exp(x - lse),   and w more at the target
+// (w = dlogprob, h = dentropy).  Values are held at a floor far below any lse but small
+// enough that its products stay finite, so that a masked logit gets 0; rows whose lse is
+// itself near the floor (or -inf, or NaN) take each difference with care instead.  Where
+// the rows of the two arrays start at different offsets from a 16-byte boundary V is 1.
 template <class T> struct LogprobGradArgs {
   const T* logits;
   T* dlogits;
@@ -526,6 +530,21 @@ template <class T> struct LogprobGradArgs {
   int V, blocks;  // blocks of a row
 };
 
+// A pack held at the gradient's floor: -2^66 (fp16: its lowest).
+template <class T, int V> __device__ __forceinline__ void lp_grad_hold(Pack<T, V>& p) {
+  if constexpr (V == 8) {
+    uint4 u;
+    memcpy(&u, &p, 16);
+    constexpr unsigned f = std::is_same<T, __half>::value ? 0xfbfffbffu : 0xe080e080u;
+    u = make_uint4(LpType<T>::max2(u.x, f), LpType<T>::max2(u.y, f), LpType<T>::max2(u.z, f), LpType<T>::max2(u.w, f));
+    memcpy(&p, &u, 16);
+  } else {
+    const float f = std::is_same<T, __half>::value ? -65504.f : -7.378697629483821e19f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) p.v[c] = narrow<T>(max_nan(widen(p.v[c]), f));
+  }
+}
+
 template <class T, int V>
 __global__ void __launch_bounds__(kLpThreads) logprob_backward_kernel(const __grid_constant__ LogprobGradArgs<T> a) {
   constexpr int U = kLpGradPacks, NT = kLpThreads;
@@ -534,11 +553,15 @@ __global__ void __launch_bounds__(kLpThreads) logprob_backward_kernel(const __gr
   const T* x = a.logits + row * a.stride;
   T* dx = a.dlogits + row * a.dstride;
   const int off = V == 1 ? 0 : (int)((uintptr_t)x % 16 / sizeof(T));
-  const int p = (int)(blockIdx.x % a.blocks) * U * NT + threadIdx.x;
+  const int first = ((int)(blockIdx.x % a.blocks) * U * NT + threadIdx.x) * V - off;
+  // All of the row's numbers at once: none waits for another.
+  const long long target = lp_target(a.targets, a.targets64, row);
+  const float lse = a.lse[row], dl = a.dlogprob ? a.dlogprob[row] : 0.f, dh = a.dentropy ? a.dentropy[row] : 0.f,
+              entropy = a.dentropy ? a.entropy[row] : 0.f;
   Pack<T, V> px[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int e0 = (p + u * NT) * V - off;
+    const int e0 = first + u * NT * V;
     if (e0 >= 0 && e0 + V <= a.V) {
       px[u] = ld_pack<T, V>(x + e0);
     } else {
@@ -547,22 +570,42 @@ __global__ void __launch_bounds__(kLpThreads) logprob_backward_kernel(const __gr
         px[u].v[c] = (unsigned)(e0 + c) < (unsigned)a.V ? x[e0 + c] : narrow<T>(-INFINITY);
     }
   }
-  const long long target = lp_target(a.targets, a.targets64, row);
-  const float lse = a.lse[row];
   const bool none = lse == -INFINITY;  // a row with nothing left has no gradient
-  const float w = a.dlogprob && target >= 0 && target < a.V && !none ? a.dlogprob[row] : 0.f;
-  const float h = a.dentropy && !none ? a.dentropy[row] : 0.f, entropy = a.dentropy ? a.entropy[row] : 0.f;
-  const float base = none ? 0.f : lse;
+  const float w = target >= 0 && target < a.V && !none ? dl : 0.f, h = none ? 0.f : dh;
+  const bool careful = !(lse > (std::is_same<T, __half>::value ? -60000.f : -1e18f));
+  const float2 l2 = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
+  // w + h (d + entropy) = h d + c.
+  const float2 h2 = make_float2(-h, -h), c2 = make_float2(-fmaf(h, entropy, w), -fmaf(h, entropy, w));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int e0 = (p + u * NT) * V - off;
+    const int e0 = first + u * NT * V;
     float v[V];
-    widen_pack(px[u], v);
+    if (careful) {
+      widen_pack(px[u], v);
+      const float base = none ? 0.f : lse;
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float lp = max_nan(v[c] - base, kLpFloor);  // -inf: p = 0, and p lp = 0
-      const float q = ex2(lp * kLog2e);
-      v[c] = fmaf(-q, fmaf(h, lp + entropy, w), e0 + c == target ? w : 0.f);
+      for (int c = 0; c < V; ++c) {
+        const float lp = max_nan(v[c] - base, kLpFloor);
+        v[c] = -ex2(lp * kLog2e) * fmaf(h, lp + entropy, w);
+      }
+    } else {
+      lp_grad_hold(px[u]);
+      widen_pack(px[u], v);
+      if constexpr (V == 1) {
+        const float d = v[0] - lse;
+        v[0] = ex2(d * kLog2e) * fmaf(h2.x, d, c2.x);
+      } else {
+#pragma unroll
+        for (int c = 0; c < V; c += 2) {
+          const float2 d = add2(make_float2(v[c], v[c + 1]), l2), y = mul2(d, b2);
+          const float2 g = mul2(make_float2(ex2(y.x), ex2(y.y)), fma2(h2, d, c2));
+          v[c] = g.x, v[c + 1] = g.y;
+        }
+      }
+    }
+    if ((unsigned long long)(target - e0) < (unsigned)V) {  // one pack of the row
+#pragma unroll
+      for (int c = 0; c < V; ++c) v[c] += e0 + c == target ? w : 0.f;
     }
     const Pack<T, V> out = narrow_pack<T, V>(v);
     if (e0 >= 0 && e0 + V <= a.V) {

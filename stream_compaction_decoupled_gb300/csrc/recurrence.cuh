@@ -112,35 +112,43 @@ struct RecShared {
 // (dir = 1: t = p; dir = -1: t = T - 1 - p), and where its copies go.
 template <class T, class G> struct RecCopy {
   const char* src;       // row (tile, tid / CHUNKS); EVEN: its chunk
+  const char* base;      // EDGE: the array's first value
   long long half, step;  // bytes from row r to r + ROWS, and to the next round's row
-  __device__ __forceinline__ void init(const T* strip, long long st, int t, int dir, long long rows) {
+  __device__ __forceinline__ void init(const T* array, const T* strip, long long st, int t, int dir, long long rows) {
     src = (const char*)(strip + t * st);
+    base = (const char*)array;
     if constexpr (!G::EDGE) src += threadIdx.x % G::CHUNKS * 16;
     half = dir * G::ROWS * st * (long long)sizeof(T);
     step = dir * rows * st * (long long)sizeof(T);
   }
-  // The chunk of row `row` (a pointer as src), if it is on; dead: the strip ends before
-  // this thread's chunk (EVEN).  `left`: channels from d0 to the end of the row.
-  static __device__ __forceinline__ void chunk(unsigned char* dst, const char* row, bool on, int d0, int left) {
+  // The chunk of row `row` (a pointer as src), if it is on.  EDGE: the chunk is the c-th
+  // from the boundary below the row's channel d0.  It may begin before the row, in values of
+  // the array that no lane looks at; it ends with the row.  Only where it would begin before
+  // the array are its values taken one by one.
+  __device__ __forceinline__ void chunk(unsigned char* dst, const char* row, bool on, int d0, int left, int D) {
     if constexpr (!G::EDGE) {
       if (on) cp_async16(dst, row);
     } else {
-      const int off = (int)((uintptr_t)row & 15) / (int)sizeof(T);
-      const int e = (int)(threadIdx.x % G::CHUNKS) * G::V - off;  // the chunk's first channel, from d0
-      if (!on || e >= left) return;
-      if (d0 + e >= 0) {
-        const int n = left - e < G::V ? left - e : G::V;
-        cp_async_part(dst, row + e * (int)sizeof(T), n * (int)sizeof(T));
-      } else {  // the row begins inside the chunk
-        for (int k = -e; k < G::V && e + k < left; ++k) ((T*)dst)[k] = ((const T*)row)[e + k];
+      constexpr int es = (int)sizeof(T);
+      const int eb = (int)(threadIdx.x % G::CHUNKS) * 16 - (int)((uintptr_t)row & 15);  // bytes from d0
+      if (!on) return;
+      if (d0 * es + eb >= 0 && d0 * es + eb + 16 <= D * es) {
+        cp_async16(dst, row + eb);
+      } else if (eb < left * es) {  // an end of the row
+        const int e = eb / es, n = left - e < G::V ? left - e : G::V;  // eb is a multiple of es
+        if (row + eb >= base) {
+          cp_async_part(dst, row + eb, n * es);
+        } else {
+          for (int k = -e; k < n; ++k) ((T*)dst)[k] = ((const T*)row)[e + k];
+        }
       }
     }
   }
   // Both chunks of this round; on0, on1: whether their rows exist.
-  __device__ __forceinline__ void fetch(unsigned char* tile, bool on0, bool on1, int d0, int left) {
+  __device__ __forceinline__ void fetch(unsigned char* tile, bool on0, bool on1, int d0, int left, int D) {
     unsigned char* dst = tile + threadIdx.x * 16;  // row tid / CHUNKS, chunk tid % CHUNKS
-    chunk(dst, src, on0, d0, left);
-    chunk(dst + G::ROWS * G::PITCH, src + half, on1, d0, left);
+    chunk(dst, src, on0, d0, left, D);
+    chunk(dst + G::ROWS * G::PITCH, src + half, on1, d0, left, D);
     src += step;
   }
 };
@@ -261,9 +269,9 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
   const bool chunk = G::EDGE || (int)(threadIdx.x % G::CHUNKS) * G::V < left;
   const T *xp = a.x + b * a.xb + d0, *fp = a.f + b * a.fb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
   RecCopy<T, G> x, f, g;
-  x.init(xp, a.xt, mine, 1, step);
-  f.init(fp, a.ft, mine, 1, step);
-  if constexpr (GATE) g.init(gp, a.it, mine, 1, step);
+  x.init(a.x, xp, a.xt, mine, 1, step);
+  f.init(a.f, fp, a.ft, mine, 1, step);
+  if constexpr (GATE) g.init(a.i, gp, a.it, mine, 1, step);
   T* y = a.y + b * a.yb + d0 + 2 * lane + (long long)(tile0 + warp * R) * a.yt;
   const long long y_step = step * a.yt;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
@@ -273,9 +281,9 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
       unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
       const long long p = (long long)k * step + mine;
       const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
-      x.fetch(base, on0, on1, d0, left);
-      f.fetch(base + G::ARRAY, on0, on1, d0, left);
-      if constexpr (GATE) g.fetch(base + 2 * G::ARRAY, on0, on1, d0, left);
+      x.fetch(base, on0, on1, d0, left, a.D);
+      f.fetch(base + G::ARRAY, on0, on1, d0, left, a.D);
+      if constexpr (GATE) g.fetch(base + 2 * G::ARRAY, on0, on1, d0, left, a.D);
     }
     cp_async_commit();
   };
@@ -387,11 +395,11 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
           *hp = a.h + b * a.hb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
   RecCopy<T, G> f, dh, x, h, g;
   const int t_mine = a.T_ - 1 - mine;
-  f.init(fp, a.ft, t_mine, -1, step);
-  dh.init(dhp, a.dht, t_mine, -1, step);
-  x.init(xp, a.xt, t_mine, -1, step);
-  h.init(hp, a.ht, t_mine - 1, -1, step);  // h_{t-1}
-  if constexpr (GATE) g.init(gp, a.it, t_mine, -1, step);
+  f.init(a.f, fp, a.ft, t_mine, -1, step);
+  dh.init(a.dh, dhp, a.dht, t_mine, -1, step);
+  x.init(a.x, xp, a.xt, t_mine, -1, step);
+  h.init(a.h, hp, a.ht, t_mine - 1, -1, step);  // h_{t-1}
+  if constexpr (GATE) g.init(a.i, gp, a.it, t_mine, -1, step);
   const int t_warp = a.T_ - 1 - tile0 - warp * R;  // this warp's first row of round 0
   const long long at = b * a.D + d0 + 2 * lane;
   T* dx = a.dx + b * a.dxb + d0 + 2 * lane + (long long)t_warp * a.dxt;
@@ -404,11 +412,11 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
       const long long p = (long long)k * step + mine;
       const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
-      f.fetch(base, on0, on1, d0, left);
-      dh.fetch(base + G::ARRAY, on0, on1, d0, left);
-      x.fetch(base + 2 * G::ARRAY, on0, on1, d0, left);
-      h.fetch(base + 3 * G::ARRAY, chunk && p + 1 < a.T_, chunk && p + G::ROWS + 1 < a.T_, d0, left);
-      if constexpr (GATE) g.fetch(base + 4 * G::ARRAY, on0, on1, d0, left);
+      f.fetch(base, on0, on1, d0, left, a.D);
+      dh.fetch(base + G::ARRAY, on0, on1, d0, left, a.D);
+      x.fetch(base + 2 * G::ARRAY, on0, on1, d0, left, a.D);
+      h.fetch(base + 3 * G::ARRAY, chunk && p + 1 < a.T_, chunk && p + G::ROWS + 1 < a.T_, d0, left, a.D);
+      if constexpr (GATE) g.fetch(base + 4 * G::ARRAY, on0, on1, d0, left, a.D);
     }
     cp_async_commit();
   };
@@ -441,9 +449,12 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       return G::EDGE ? (unsigned)(uintptr_t)strip + (unsigned)t * (unsigned)(st * sizeof(T)) : 0u;
     };
     float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
+    constexpr bool KEEP = G::EDGE && !GATE;  // keep dh, whose place takes some working out, where registers allow
+    float2 kept[KEEP ? R : 1];
     RecMap m = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
     auto row = [&](int r) {
       const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, rows - 1 - r));
+      if constexpr (KEEP) kept[r] = ds;
       sigmoid_both(rec_pair<T, G>(base, r, lo(fp, a.ft, rows - 1 - r)), s[r], s1[r]);
       const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
       // a c + a dh = a (c + dh), so the map's b is a (b + dh).
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     if constexpr (GATE) di -= step * a.dit;
     auto write = [&](int r) {
       const int t = rows - 1 - r;
-      const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
+      const float2 ds = KEEP ? kept[KEEP ? r : 0] : rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
       const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, lo(xp, a.xt, t));
       float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, lo(hp, a.ht, t - 1)) : first;
       const bool dropped = drop >> r & 1;
@@ -593,14 +604,18 @@ template <class T> RecArgs<T> rec_args(const RecurrenceJob& j) {
   return a;
 }
 
-// CTAs per cluster: doubled while the CTAs are fewer than 1.5 an SM and there are tiles to
-// share.  Measured: 256 strips (8 x 2048 x 2048 bf16) take 58.4 us alone and 66.1 in pairs,
-// whose 512 CTAs need a second wave; 54 strips (3 x 1537 x 1001 fp32, gradient) 92.6 us in
-// fours and 55.0 in eights.
+// CTAs per cluster: as many as keep all CTAs resident at once, two an SM, while there are
+// tiles to share; and two where the strips are a few more than the SMs.  Measured: 54 strips
+// (3 x 1537 x 1001 fp32 gated, gradient) 39.3 us in fives and 47.7 in eights; 128 strips
+// (8 x 2048 x 1024 bf16 gated) 32.8 in pairs and 43.1 in threes; 160 strips (16 x 2048 x 511
+// bf16 gated) 84.0 alone and 76.8 in pairs.
 template <class G> unsigned rec_cluster(long long strips, long long T_, int num_sms) {
-  unsigned c = 1;
-  while (c < (unsigned)kRecMaxCluster && 2 * strips * c < 3ll * num_sms && (long long)c * G::L < T_) c *= 2;
-  return c;
+  long long c = 2ll * num_sms / strips;
+  if (c == 1 && 10 * strips <= 11ll * num_sms) c = 2;
+  const long long tiles = (T_ + G::L - 1) / G::L;
+  if (c > tiles) c = tiles;
+  if (c > kRecMaxCluster) c = kRecMaxCluster;
+  return c < 1 ? 1u : (unsigned)c;
 }
 
 template <class G, int NA, class T, class K>
