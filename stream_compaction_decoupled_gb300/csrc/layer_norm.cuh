@@ -13,8 +13,8 @@
 // c + G k (G the grid, a multiple of 8).  Every row of a CTA then starts at the same offset
 // from a 16-byte boundary, whatever the width (the offset repeats after at most 8 rows), so
 // an odd width is read in whole packs too: they are laid over the row shifted by the
-// offset, only the first and the last of a row are read value by value, and the weight,
-// shifted alike, is loaded once a CTA.
+// offset, the first and the last of a row are cut or masked, and the weight, shifted alike,
+// is loaded once a CTA.
 //
 // The gradient's sums over rows stay in the registers of a persistent CTA until it is done;
 // one row of partial sums a CTA is then reduced by a second, small launch, in a fixed
@@ -340,9 +340,10 @@ __global__ void __launch_bounds__(G::NT) norm_forward_edge_kernel(const __grid_c
 }
 
 // The gradient: persistent, one CTA an SM, x and dy through the ring, the sums over rows in
-// registers.  Where those would take too many (32 values a thread, more than 512
-// threads, or 512 at any offset in fp32), db's are in shared memory, each thread's own, and a row's n and g are worked
-// out twice; at 32 values the weight comes from L1 in place of shared memory.
+// registers.  Where those would take too many (32 values a thread, more than 512 threads,
+// or 512 at any offset in fp32), db's are in shared memory, each thread's own, and a row's
+// n and g are worked out twice; at 32 values the weight comes from L1 in place of shared
+// memory.
 template <class T, class P, class G> struct NormBackwardSmem {
   static constexpr bool BIG = G::NV * G::V > 16;
   static constexpr bool TIGHT = BIG || G::NT > 512 || (G::EDGE && G::TPR == 512 && G::V == 4);
