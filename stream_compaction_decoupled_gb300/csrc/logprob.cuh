@@ -434,13 +434,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
         __syncthreads();
         bar = sh.tau ? lp_unorder((unsigned)(sh.tau >> 32)) : -INFINITY;
       }
-      unsigned over = 0, even = 0;  // packs past the threshold's value, and perhaps level with it
+      float tallest = bests[0];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (bests[u] > bar && bests[u] > kFloor) over |= 1u << u;
-        else if (!(bests[u] < bar)) even |= 1u << u;  // the floor may stand for -inf
-      }
-      if (over | even) {
+      for (int u = 1; u < U; ++u) tallest = max_nan(tallest, bests[u]);
+      if (!(tallest < bar)) {
+        // Packs past the threshold's value, and those perhaps level with it.
+        unsigned over = 0, even = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (bests[u] > bar && bests[u] > kFloor) over |= 1u << u;
+          else if (!(bests[u] < bar)) even |= 1u << u;  // the floor may stand for -inf
+        }
 #pragma unroll 1
         for (unsigned left = over | even; left; left &= left - 1) {
           const int u = __ffs(left) - 1, j = p + u * NT + tid, e0 = j * V - off;
