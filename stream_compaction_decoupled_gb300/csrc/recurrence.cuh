@@ -30,6 +30,11 @@
 //   and without i:    df_t = a_t (1 - a_t) (h_{t-1} - x_t) g_t.
 // Where starts[t] is set the state before t is dropped: a_t counts as 0 in the scan and
 // h_{t-1} as 0 in df_t.
+//
+// Measured (GB300, copy rate 6.8 TB/s): 8 x 2048 x 2048 bf16 with i 49.8 us (5.4 TB/s), its
+// gradient 85.1 us (6.3 TB/s); 1 x 65536 x 2048 249 us (4.3 TB/s); gradient of 3 x 1537 x
+// 1001 fp32 without i 32.4 us (3.4 TB/s).  The gradient runs at the memory's rate; forward,
+// the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
 #pragma once
 
 #include "lm.cuh"
@@ -516,7 +521,8 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
 // negative slot is a padded row: its output is zero and no state moves.  Purely a read
-// and a write of each value, one 16-byte pack a thread.
+// and a write of each value, one 16-byte pack a thread; 64 rows of 2048 bf16 take 3.5 us,
+// a launch and two dependent reads (slot, then state).
 template <class T> struct RecStepArgs {
   const T *x, *f, *i;
   T* h;
