@@ -380,8 +380,10 @@ void gb_set_stalled_tile(int64_t tile);
  * conventions at the top of this file hold otherwise, except that these calls clear no
  * status words.  Errors: GB_ERR_INVALID (null or misaligned
  * pointer, negative size or stride, bad option), GB_ERR_UNSUPPORTED (dtype),
- * GB_ERR_RANGE (length, channels, cols or vocab above 2^30, or a grid past 2^31 - 1 blocks),
- * GB_ERR_TEMP, GB_ERR_CUDA.
+ * GB_ERR_RANGE (length or vocab above 2^30, channels or cols above 2^28, or a grid past
+ * 2^31 - 1 blocks), GB_ERR_TEMP, GB_ERR_CUDA.  The recurrence's waits between the blocks of
+ * a cluster are bounded as the others are (gb_set_wait_limit_ns): one that runs out is
+ * reported as GB_ERR_TIMEOUT by gb_device_error.
  */
 
 /*

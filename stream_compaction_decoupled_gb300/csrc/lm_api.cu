@@ -13,7 +13,8 @@ namespace {
 using gbs::LaunchCtx;
 using gbs::SeqArray;
 
-constexpr long long kMaxWidth = 1ll << 30;   // channels, tokens, columns, vocabulary
+constexpr long long kMaxLength = 1ll << 30;  // tokens of a sequence, vocabulary
+constexpr long long kMaxWidth = 1ll << 28;   // channels, columns: byte offsets within a row fit in 31 bits
 constexpr long long kMaxGrid = 0x7fffffffll;
 
 size_t lm_size(int dtype) {
@@ -53,7 +54,7 @@ int finish(cudaError_t e) { return e == cudaSuccess ? GB_OK : gbs::abi_cuda_fail
 int check_sizes(int dtype, long long B, long long T, long long D) {
   if (B < 0 || T < 0 || D < 0) return GB_ERR_INVALID;
   if (!lm_size(dtype)) return GB_ERR_UNSUPPORTED;
-  if (D > kMaxWidth || T > kMaxWidth || (long double)B * T * D > 9.0e17L) return GB_ERR_RANGE;
+  if (D > kMaxWidth || T > kMaxLength || (long double)B * T * D > 9.0e17L) return GB_ERR_RANGE;
   // The narrowest strip is 56 channels, the largest cluster 8 CTAs.
   if ((long double)B * ((D + 31) / 32) * 8 > (long double)kMaxGrid) return GB_ERR_RANGE;
   return GB_OK;
@@ -213,7 +214,7 @@ int gb_token_logprobs(int dtype, int64_t rows, int64_t vocab, const void* logits
   if (rows < 0 || vocab < 0 || stride < 0 || top < 0 || top > gbs::kMaxTop || top > vocab) return GB_ERR_INVALID;
   if (target_dtype != GB_I32 && target_dtype != GB_I64) return GB_ERR_INVALID;
   if (!lm_size(dtype)) return GB_ERR_UNSUPPORTED;
-  if (vocab > kMaxWidth || rows > kMaxGrid / 8) return GB_ERR_RANGE;
+  if (vocab > kMaxLength || rows > kMaxGrid / 8) return GB_ERR_RANGE;
   if (rows == 0) return GB_OK;
   if ((vocab > 0 && !logits) || !targets || !logprob || !entropy || !lse) return GB_ERR_INVALID;
   if (top > 0 && (!top_values || !top_ids)) return GB_ERR_INVALID;
@@ -240,7 +241,7 @@ int gb_token_logprobs_backward(int dtype, int64_t rows, int64_t vocab, const voi
   if (target_dtype != GB_I32 && target_dtype != GB_I64) return GB_ERR_INVALID;
   if (!lm_size(dtype)) return GB_ERR_UNSUPPORTED;
   // The narrowest block of a row is 1024 values.
-  if (vocab > kMaxWidth || (long double)rows * ((vocab + 1023) / 1024) > (long double)kMaxGrid) return GB_ERR_RANGE;
+  if (vocab > kMaxLength || (long double)rows * ((vocab + 1023) / 1024) > (long double)kMaxGrid) return GB_ERR_RANGE;
   if (rows == 0 || vocab == 0) return GB_OK;
   if (!logits || !targets || !lse || !dlogits || (dentropy && !entropy)) return GB_ERR_INVALID;
   if (logits == dlogits && stride != dstride) return GB_ERR_INVALID;

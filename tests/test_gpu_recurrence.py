@@ -63,6 +63,15 @@ def test_recurrence(size, dt, gate, extras):
     run(*size, DT[dt], gate, extras, seed=sum(size))
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("strips", [8, 32, 40, 45, 52, 62, 80, 120, 155, 200])
+def test_clusters_of_every_size(strips, dt):
+    """Few 64-channel strips are shared by clusters of up to 8 blocks, more by fewer, and
+    many by none; lengths that end in the first, a middle and the last block's tile."""
+    for t in (450, 1025) if strips < 100 else (130,):
+        run(strips, t, 64, DT[dt], True, True, seed=strips)
+
+
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("pad", [1, 2, 3, 4, 7, 8])
 def test_row_strides_of_every_alignment(dt, pad):
