@@ -89,6 +89,14 @@ template <class T, bool EDGE_, int STAGES_> struct RecGeom {
   static constexpr int R = 16 / sizeof(T);
   static constexpr int L = WARPS * R;                        // rows of a tile
   static constexpr int W = EDGE ? 64 - V : 64;               // channels of a strip
+  // A lane's two channels are neighbours, or EDGE 32 apart: there they are loaded and
+  // stored one by one, and the 32 lanes' are neighbours each time.
+  static constexpr int APART = EDGE ? 32 : 1;
+  static __device__ __forceinline__ int first(int lane) { return EDGE ? lane : 2 * lane; }
+  static __device__ __forceinline__ int count(int left) {    // how many of a lane's channels exist
+    const int c = left - first(threadIdx.x & 31);
+    return c > APART ? 2 : c > 0 ? 1 : 0;
+  }
   static constexpr int CHUNKS = 64 / V;                      // copies of a row
   static constexpr int PITCH = CHUNKS * 16;                  // bytes of a row in shared memory
   static constexpr int ARRAY = L * PITCH;
@@ -117,54 +125,63 @@ struct RecShared {
   unsigned long long bar[kRecSlots];          // the cluster's maps have arrived
 };
 
-// What a thread copies of one array: the row p rows after the strip's first in scan order
-// (dir = 1: t = p; dir = -1: t = T - 1 - p), and where its copies go.
+// What a thread copies of one array: a chunk of the row p rows after the strip's first in
+// scan order (dir = 1: t = p; dir = -1: t = T - 1 - p), of the row ROWS later, and of the
+// rows a round of `rows` later.  EDGE: the chunk is the c-th from the boundary below the
+// row's channel d0; ROWS and `rows` times a value's size are multiples of 16, so those rows
+// all have the same offset, and everything about the chunk but its address is known here.
 template <class T, class G> struct RecCopy {
-  const char* src;       // row (tile, tid / CHUNKS); EVEN: its chunk
-  const char* base;      // EDGE: the array's first value
+  static_assert(G::ROWS * sizeof(T) % 16 == 0 && G::L * sizeof(T) % 16 == 0 && G::R * sizeof(T) % 16 == 0, "offsets");
+  const char* src;       // the chunk of row (tile, tid / CHUNKS)
   long long half, step;  // bytes from row r to r + ROWS, and to the next round's row
-  __device__ __forceinline__ void init(const T* array, const T* strip, long long st, int t, int dir, long long rows) {
+  int bytes;             // of a chunk; 0: none of it is in the strip
+  bool low;              // EDGE: it may begin before the array
+  __device__ __forceinline__ void init(const T* strip, long long st, int t, int dir, long long rows, int d0, int left,
+                                       int D) {
+    constexpr int es = (int)sizeof(T);
     src = (const char*)(strip + t * st);
-    base = (const char*)array;
-    if constexpr (!G::EDGE) src += threadIdx.x % G::CHUNKS * 16;
-    half = dir * G::ROWS * st * (long long)sizeof(T);
-    step = dir * rows * st * (long long)sizeof(T);
+    half = dir * G::ROWS * st * (long long)es;
+    step = dir * rows * st * (long long)es;
+    int at = (int)(threadIdx.x % G::CHUNKS) * 16;  // bytes from d0
+    if constexpr (G::EDGE) at -= (int)((uintptr_t)src & 15);
+    src += at;
+    // A chunk ends with the row, where it does not hold 16 bytes of it.
+    bytes = at >= left * es ? 0 : (d0 * es + at + 16 <= D * es ? 16 : left * es - at);
+    low = d0 * es + at < 0;
   }
-  // The chunk of row `row` (a pointer as src), if it is on.  EDGE: the chunk is the c-th
-  // from the boundary below the row's channel d0.  It may begin before the row, in values of
-  // the array that no lane looks at; it ends with the row.  Only where it would begin before
-  // the array are its values taken one by one.
-  __device__ __forceinline__ void chunk(unsigned char* dst, const char* row, bool on, int d0, int left, int D) {
+  // The chunk at `from`, if its row is on.  It may begin before the row, in values of the
+  // array that no lane looks at; where it would begin before the array, it is taken value
+  // by value.
+  __device__ __forceinline__ void chunk(unsigned char* dst, const char* from, bool on, const T* array) const {
     if constexpr (!G::EDGE) {
-      if (on) cp_async16(dst, row);
+      if (on) cp_async16(dst, from);
     } else {
-      constexpr int es = (int)sizeof(T);
-      const int eb = (int)(threadIdx.x % G::CHUNKS) * 16 - (int)((uintptr_t)row & 15);  // bytes from d0
       if (!on) return;
-      if (d0 * es + eb >= 0 && d0 * es + eb + 16 <= D * es) {
-        cp_async16(dst, row + eb);
-      } else if (eb < left * es) {  // an end of the row
-        const int e = eb / es, n = left - e < G::V ? left - e : G::V;  // eb is a multiple of es
-        if (row + eb >= base) {
-          cp_async_part(dst, row + eb, n * es);
-        } else {
-          for (int k = -e; k < n; ++k) ((T*)dst)[k] = ((const T*)row)[e + k];
-        }
+      if (low && from < (const char*)array) {
+        for (int k = 0; k < bytes / (int)sizeof(T); ++k)
+          if ((const T*)from + k >= array) ((T*)dst)[k] = ((const T*)from)[k];
+      } else {
+        cp_async_part(dst, from, bytes);
       }
     }
   }
   // Both chunks of this round; on0, on1: whether their rows exist.
-  __device__ __forceinline__ void fetch(unsigned char* tile, bool on0, bool on1, int d0, int left, int D) {
+  __device__ __forceinline__ void fetch(unsigned char* tile, bool on0, bool on1, const T* array) {
     unsigned char* dst = tile + threadIdx.x * 16;  // row tid / CHUNKS, chunk tid % CHUNKS
-    chunk(dst, src, on0, d0, left, D);
-    chunk(dst + G::ROWS * G::PITCH, src + half, on1, d0, left, D);
+    chunk(dst, src, on0 && bytes > 0, array);
+    chunk(dst + G::ROWS * G::PITCH, src + half, on1 && bytes > 0, array);
     src += step;
   }
 };
 
-// A lane's two channels of row `r` of a tile.  EDGE: `lo` is the low half of the address of
-// the row's first channel d0, whose last 4 bits are the row's offset.
-template <class T, class G> __device__ __forceinline__ float2 rec_pair(const unsigned char* tile, int r, unsigned lo) {
+// The offset of row t of a strip from a 16-byte boundary.  R rows on it is the same, so the
+// warps' r-th rows all have that of the r-th row of all.
+template <class T, class G> __device__ __forceinline__ unsigned rec_offset(const T* strip, long long st, int t) {
+  return G::EDGE ? ((unsigned)(uintptr_t)strip + (unsigned)t * (unsigned)(st * sizeof(T))) & 15 : 0u;
+}
+
+// A lane's two channels of row `r` of a tile, whose offset is `off`.
+template <class T, class G> __device__ __forceinline__ float2 rec_pair(const unsigned char* tile, int r, unsigned off) {
   const int lane = threadIdx.x & 31;
   const unsigned char* row = tile + r * G::PITCH;
   if constexpr (!G::EDGE) {
@@ -174,14 +191,14 @@ template <class T, class G> __device__ __forceinline__ float2 rec_pair(const uns
       return widen2<T>(*(const unsigned*)(row + lane * 4));
     }
   } else {
-    const T* q = (const T*)(row + (lo & 15)) + 2 * lane;
-    return make_float2(widen(q[0]), widen(q[1]));
+    const T* q = (const T*)(row + off) + G::first(lane);
+    return make_float2(widen(q[0]), widen(q[G::APART]));
   }
 }
 
-// Writes two channels of a row from p on; n of them (0 .. 2) exist.
-template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, float2 v, int n) {
-  if constexpr (!EDGE) {
+// Writes a lane's two channels of a row, the first at p; n of them (0 .. 2) exist.
+template <class T, class G> __device__ __forceinline__ void rec_store(T* p, float2 v, int n) {
+  if constexpr (!G::EDGE) {
     if (n > 0) {
       if constexpr (sizeof(T) == 4) {
         *(float2*)p = v;
@@ -191,15 +208,15 @@ template <class T, bool EDGE> __device__ __forceinline__ void rec_store(T* p, fl
     }
   } else {
     if (n > 0) p[0] = narrow<T>(v.x);
-    if (n > 1) p[1] = narrow<T>(v.y);
+    if (n > 1) p[G::APART] = narrow<T>(v.y);
   }
 }
-__device__ __forceinline__ float2 rec_load2(const float* p, int n) {
-  return make_float2(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f);
+template <class G> __device__ __forceinline__ float2 rec_load2(const float* p, int n) {
+  return make_float2(n > 0 ? p[0] : 0.f, n > 1 ? p[G::APART] : 0.f);
 }
-__device__ __forceinline__ void rec_store2(float* p, float2 v, int n) {
+template <class G> __device__ __forceinline__ void rec_store2(float* p, float2 v, int n) {
   if (n > 0) p[0] = v.x;
-  if (n > 1) p[1] = v.y;
+  if (n > 1) p[G::APART] = v.y;
 }
 
 // Makes the cluster's mbarriers and waits until every CTA of it has.
@@ -270,17 +287,16 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
   const long long b = strip / a.strips;
   const int d0 = (int)(strip % a.strips) * G::W;
   const int left = a.D - d0 < G::W ? a.D - d0 : G::W;              // channels of this strip
-  const int n = left - 2 * lane < 2 ? left - 2 * lane : 2;         // of this lane
+  const int n = G::count(left);                                    // of this lane
   const int step = (int)C * G::L, tile0 = (int)rank * G::L;
   const int rounds = (int)(((long long)a.T_ + step - 1) / step);
   const int mine = tile0 + (int)threadIdx.x / G::CHUNKS;           // the first row this thread copies
-  const bool chunk = G::EDGE || (int)(threadIdx.x % G::CHUNKS) * G::V < left;
   const T *xp = a.x + b * a.xb + d0, *fp = a.f + b * a.fb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
   RecCopy<T, G> x, f, g;
-  x.init(a.x, xp, a.xt, mine, 1, step);
-  f.init(a.f, fp, a.ft, mine, 1, step);
-  if constexpr (GATE) g.init(a.i, gp, a.it, mine, 1, step);
-  T* y = a.y + b * a.yb + d0 + 2 * lane + (long long)(tile0 + warp * R) * a.yt;
+  x.init(xp, a.xt, mine, 1, step, d0, left, a.D);
+  f.init(fp, a.ft, mine, 1, step, d0, left, a.D);
+  if constexpr (GATE) g.init(gp, a.it, mine, 1, step, d0, left, a.D);
+  T* y = a.y + b * a.yb + d0 + G::first(lane) + (long long)(tile0 + warp * R) * a.yt;
   const long long y_step = step * a.yt;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
@@ -288,10 +304,10 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     if (k < rounds) {
       unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
       const long long p = (long long)k * step + mine;
-      const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
-      x.fetch(base, on0, on1, d0, left, a.D);
-      f.fetch(base + G::ARRAY, on0, on1, d0, left, a.D);
-      if constexpr (GATE) g.fetch(base + 2 * G::ARRAY, on0, on1, d0, left, a.D);
+      const bool on0 = p < a.T_, on1 = p + G::ROWS < a.T_;
+      x.fetch(base, on0, on1, a.x);
+      f.fetch(base + G::ARRAY, on0, on1, a.f);
+      if constexpr (GATE) g.fetch(base + 2 * G::ARRAY, on0, on1, a.i);
     }
     cp_async_commit();
   };
@@ -310,7 +326,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   unsigned marks = 0;
-  float2 carry = a.h0 ? rec_load2(a.h0 + b * a.D + d0 + 2 * lane, n) : make_float2(0.f, 0.f);
+  float2 carry = a.h0 ? rec_load2<G>(a.h0 + b * a.D + d0 + G::first(lane), n) : make_float2(0.f, 0.f);
   rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
@@ -321,20 +337,13 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     if (k % 32 == 0) marks = flags(k);
     const unsigned drop = __shfl_sync(0xffffffffu, marks, k % 32);
     const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
-    unsigned xo = 0, fo = 0, go = 0;  // EDGE: the rows' offsets
-    if constexpr (G::EDGE) {
-      const unsigned t = (unsigned)(k * step + tile0 + warp * R);
-      xo = (unsigned)(uintptr_t)xp + t * (unsigned)(a.xt * sizeof(T));
-      fo = (unsigned)(uintptr_t)fp + t * (unsigned)(a.ft * sizeof(T));
-      if constexpr (GATE) go = (unsigned)(uintptr_t)gp + t * (unsigned)(a.it * sizeof(T));
-    }
     float2 av[R], bv[R];
     auto row = [&](int r) {
-      const float2 xs = rec_pair<T, G>(base, r, xo + r * (unsigned)(a.xt * sizeof(T)));
-      const float2 fs = rec_pair<T, G>(base + G::ARRAY, r, fo + r * (unsigned)(a.ft * sizeof(T)));
+      const float2 xs = rec_pair<T, G>(base, r, rec_offset<T, G>(xp, a.xt, r));
+      const float2 fs = rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(fp, a.ft, r));
       if constexpr (GATE) {
         av[r] = sigmoid(fs);
-        bv[r] = mul2(sigmoid(rec_pair<T, G>(base + 2 * G::ARRAY, r, go + r * (unsigned)(a.it * sizeof(T)))), xs);
+        bv[r] = mul2(sigmoid(rec_pair<T, G>(base + 2 * G::ARRAY, r, rec_offset<T, G>(gp, a.it, r))), xs);
       } else {
         float2 u;
         sigmoid_both(fs, av[r], u);
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     y += y_step;
     auto write = [&](int r) {
       s = fma2(av[r], s, bv[r]);
-      rec_store<T, G::EDGE>(out, s, n);
+      rec_store<T, G>(out, s, n);
       out += a.yt;
     };
     if (rows >= R) {
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
         if (r < rows) write(r);
     }
   }
-  if (a.last && rank == 0 && warp == 7) rec_store2(a.last + b * a.D + d0 + 2 * lane, carry, n);
+  if (a.last && rank == 0 && warp == 7) rec_store2<G>(a.last + b * a.D + d0 + G::first(lane), carry, n);
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
@@ -394,37 +403,36 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
   const long long b = strip / a.strips;
   const int d0 = (int)(strip % a.strips) * G::W;
   const int left = a.D - d0 < G::W ? a.D - d0 : G::W;
-  const int n = left - 2 * lane < 2 ? left - 2 * lane : 2;
+  const int n = G::count(left);
   const int step = (int)C * G::L, tile0 = (int)rank * G::L;
   const int rounds = (int)(((long long)a.T_ + step - 1) / step);
   const int mine = tile0 + (int)threadIdx.x / G::CHUNKS;
-  const bool chunk = G::EDGE || (int)(threadIdx.x % G::CHUNKS) * G::V < left;
   const T *fp = a.f + b * a.fb + d0, *dhp = a.dh + b * a.dhb + d0, *xp = a.x + b * a.xb + d0,
           *hp = a.h + b * a.hb + d0, *gp = GATE ? a.i + b * a.ib + d0 : nullptr;
   RecCopy<T, G> f, dh, x, h, g;
   const int t_mine = a.T_ - 1 - mine;
-  f.init(a.f, fp, a.ft, t_mine, -1, step);
-  dh.init(a.dh, dhp, a.dht, t_mine, -1, step);
-  x.init(a.x, xp, a.xt, t_mine, -1, step);
-  h.init(a.h, hp, a.ht, t_mine - 1, -1, step);  // h_{t-1}
-  if constexpr (GATE) g.init(a.i, gp, a.it, t_mine, -1, step);
+  f.init(fp, a.ft, t_mine, -1, step, d0, left, a.D);
+  dh.init(dhp, a.dht, t_mine, -1, step, d0, left, a.D);
+  x.init(xp, a.xt, t_mine, -1, step, d0, left, a.D);
+  h.init(hp, a.ht, t_mine - 1, -1, step, d0, left, a.D);  // h_{t-1}
+  if constexpr (GATE) g.init(gp, a.it, t_mine, -1, step, d0, left, a.D);
   const int t_warp = a.T_ - 1 - tile0 - warp * R;  // this warp's first row of round 0
-  const long long at = b * a.D + d0 + 2 * lane;
-  T* dx = a.dx + b * a.dxb + d0 + 2 * lane + (long long)t_warp * a.dxt;
-  T* df = a.df + b * a.dfb + d0 + 2 * lane + (long long)t_warp * a.dft;
-  T* di = GATE ? a.di + b * a.dib + d0 + 2 * lane + (long long)t_warp * a.dit : nullptr;
+  const long long at = b * a.D + d0 + G::first(lane);
+  T* dx = a.dx + b * a.dxb + d0 + G::first(lane) + (long long)t_warp * a.dxt;
+  T* df = a.df + b * a.dfb + d0 + G::first(lane) + (long long)t_warp * a.dft;
+  T* di = GATE ? a.di + b * a.dib + d0 + G::first(lane) + (long long)t_warp * a.dit : nullptr;
   const uint8_t* starts = a.starts ? a.starts + b * a.T_ : nullptr;
 
   auto fetch = [&](int k) {
     if (k < rounds) {
       unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY);
       const long long p = (long long)k * step + mine;
-      const bool on0 = chunk && p < a.T_, on1 = chunk && p + G::ROWS < a.T_;
-      f.fetch(base, on0, on1, d0, left, a.D);
-      dh.fetch(base + G::ARRAY, on0, on1, d0, left, a.D);
-      x.fetch(base + 2 * G::ARRAY, on0, on1, d0, left, a.D);
-      h.fetch(base + 3 * G::ARRAY, chunk && p + 1 < a.T_, chunk && p + G::ROWS + 1 < a.T_, d0, left, a.D);
-      if constexpr (GATE) g.fetch(base + 4 * G::ARRAY, on0, on1, d0, left, a.D);
+      const bool on0 = p < a.T_, on1 = p + G::ROWS < a.T_;
+      f.fetch(base, on0, on1, a.f);
+      dh.fetch(base + G::ARRAY, on0, on1, a.dh);
+      x.fetch(base + 2 * G::ARRAY, on0, on1, a.x);
+      h.fetch(base + 3 * G::ARRAY, p + 1 < a.T_, p + G::ROWS + 1 < a.T_, a.h);
+      if constexpr (GATE) g.fetch(base + 4 * G::ARRAY, on0, on1, a.i);
     }
     cp_async_commit();
   };
@@ -440,8 +448,8 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
 #pragma unroll
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   unsigned marks = 0;
-  float2 carry = a.dlast ? rec_load2(a.dlast + at, n) : make_float2(0.f, 0.f);
-  const float2 first = a.h0 ? rec_load2(a.h0 + at, n) : make_float2(0.f, 0.f);
+  float2 carry = a.dlast ? rec_load2<G>(a.dlast + at, n) : make_float2(0.f, 0.f);
+  const float2 first = a.h0 ? rec_load2<G>(a.h0 + at, n) : make_float2(0.f, 0.f);
   rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
@@ -452,18 +460,14 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     if (k % 32 == 0) marks = flags(k);
     const unsigned drop = __shfl_sync(0xffffffffu, marks, k % 32);
     const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
-    // EDGE: the low address of row t = rows - 1 - r of a strip.
-    auto lo = [&](const T* strip, long long st, int t) {
-      return G::EDGE ? (unsigned)(uintptr_t)strip + (unsigned)t * (unsigned)(st * sizeof(T)) : 0u;
-    };
     float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
     constexpr bool KEEP = G::EDGE && !GATE;  // keep dh, whose place takes some working out, where registers allow
     float2 kept[KEEP ? R : 1];
     RecMap m = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
     auto row = [&](int r) {
-      const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, rows - 1 - r));
+      const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(dhp, a.dht, a.T_ - 1 - r));
       if constexpr (KEEP) kept[r] = ds;
-      sigmoid_both(rec_pair<T, G>(base, r, lo(fp, a.ft, rows - 1 - r)), s[r], s1[r]);
+      sigmoid_both(rec_pair<T, G>(base, r, rec_offset<T, G>(fp, a.ft, a.T_ - 1 - r)), s[r], s1[r]);
       const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
       // a c + a dh = a (c + dh), so the map's b is a (b + dh).
       m = {mul2(m.a, av), mul2(av, add2(m.b, ds))};
@@ -483,9 +487,9 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     if constexpr (GATE) di -= step * a.dit;
     auto write = [&](int r) {
       const int t = rows - 1 - r;
-      const float2 ds = KEEP ? kept[KEEP ? r : 0] : rec_pair<T, G>(base + G::ARRAY, r, lo(dhp, a.dht, t));
-      const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, lo(xp, a.xt, t));
-      float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, lo(hp, a.ht, t - 1)) : first;
+      const float2 ds = KEEP ? kept[KEEP ? r : 0] : rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(dhp, a.dht, a.T_ - 1 - r));
+      const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, rec_offset<T, G>(xp, a.xt, a.T_ - 1 - r));
+      float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, rec_offset<T, G>(hp, a.ht, a.T_ - 2 - r)) : first;
       const bool dropped = drop >> r & 1;
       if (dropped) hs = make_float2(0.f, 0.f);
       const float2 gt = add2(ds, c);  // dL/dh_t
@@ -494,14 +498,14 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       if (dropped) c = make_float2(0.f, 0.f);
       if constexpr (GATE) {
         float2 u, u1;
-        sigmoid_both(rec_pair<T, G>(base + 4 * G::ARRAY, r, lo(gp, a.it, t)), u, u1);
+        sigmoid_both(rec_pair<T, G>(base + 4 * G::ARRAY, r, rec_offset<T, G>(gp, a.it, a.T_ - 1 - r)), u, u1);
         const float2 ug = mul2(u, gt);
-        rec_store<T, G::EDGE>(ox, ug, n);
-        rec_store<T, G::EDGE>(of, mul2(fg, hs), n);
-        rec_store<T, G::EDGE>(oi, mul2(mul2(ug, u1), xs), n);
+        rec_store<T, G>(ox, ug, n);
+        rec_store<T, G>(of, mul2(fg, hs), n);
+        rec_store<T, G>(oi, mul2(mul2(ug, u1), xs), n);
       } else {
-        rec_store<T, G::EDGE>(ox, mul2(s1[r], gt), n);
-        rec_store<T, G::EDGE>(of, mul2(fg, make_float2(hs.x - xs.x, hs.y - xs.y)), n);
+        rec_store<T, G>(ox, mul2(s1[r], gt), n);
+        rec_store<T, G>(of, mul2(fg, make_float2(hs.x - xs.x, hs.y - xs.y)), n);
       }
       ox -= a.dxt;
       of -= a.dft;
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
         if (r < rows) write(r);
     }
   }
-  if (a.dh0 && rank == 0 && warp == 7) rec_store2(a.dh0 + at, carry, n);
+  if (a.dh0 && rank == 0 && warp == 7) rec_store2<G>(a.dh0 + at, carry, n);
 }
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
