@@ -37,6 +37,8 @@
 // the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
 #pragma once
 
+#include <atomic>
+
 #include "lm.cuh"
 #include "lm.h"
 
@@ -638,30 +640,44 @@ template <class T> RecArgs<T> rec_args(const RecurrenceJob& j) {
   return a;
 }
 
-// CTAs per cluster: as many as keep all CTAs resident at once, two an SM, while there are
-// tiles to share; and two where the strips are a few more than the SMs.  Measured: 54 strips
-// (3 x 1537 x 1001 fp32 gated, gradient) 39.3 us in fives and 47.7 in eights; 128 strips
-// (8 x 2048 x 1024 bf16 gated) 32.8 in pairs and 43.1 in threes; 160 strips (16 x 2048 x 511
-// bf16 gated) 84.0 alone and 76.8 in pairs.
-template <class G> unsigned rec_cluster(long long strips, long long T_, int num_sms) {
-  long long c = 2ll * num_sms / strips;
-  if (c == 1 && 10 * strips <= 11ll * num_sms) c = 2;
-  const long long tiles = (T_ + G::L - 1) / G::L;
-  if (c > tiles) c = tiles;
-  if (c > kRecMaxCluster) c = kRecMaxCluster;
-  return c < 1 ? 1u : (unsigned)c;
+// CTAs per cluster.  The strips take as many waves as the clusters that are resident at once
+// leave; a wave lasts as long as its rounds (and one to fill the pipeline), and a round
+// longer the more CTAs exchange their maps.  The estimate's least is taken.  Measured, both
+// directions gated, 5 batch rows of 1500: 60 strips (bf16) 15.2 and 24.1 us in fours, 19.1
+// and 25.1 in fives, of which not all are resident; 155 strips 36.2 and 55.9 alone, 38.1 and
+// 53.7 in pairs, 33.7 and 47.9 in threes; 255 strips 37.1 and 57.9 alone, 45.1 and 66.8 in
+// pairs; 320 strips (fp32) 99.7 and 174 alone, 93.0 and 155 in pairs.
+template <class F> unsigned rec_cluster(long long strips, long long tiles, F&& resident) {
+  unsigned best = 1;
+  double least = 0;
+  for (unsigned c = 1; c <= kRecMaxCluster && c <= tiles; ++c) {
+    const long long fit = resident(c);
+    if (fit < 1) continue;
+    const double t = (double)((strips + fit - 1) / fit) * ((tiles + c - 1) / c + 1) * (1 + 0.12 * (c - 1));
+    if (least == 0 || t < least) best = c, least = t;
+  }
+  return best;
 }
 
 template <class G, int NA, class T, class K>
 cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const LaunchCtx& ctx) {
   const long long strips = (j.D + G::W - 1) / G::W;
-  const unsigned C = rec_cluster<G>(strips * j.B, j.T, ctx.num_sms);
   a.strips = (int)strips;
   a.err = ctx.err;
   a.wait_ns = ctx.wait_ns;
   constexpr int smem = G::STAGES * NA * G::ARRAY;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // What is resident is a property of this kernel (each instance launches one) and the device.
+  static std::atomic<int> known[kRecMaxCluster + 1];
+  const unsigned C = rec_cluster(strips * j.B, (j.T + G::L - 1) / G::L, [&](unsigned c) {
+    int n = known[c].load(std::memory_order_relaxed);
+    if (n == 0) {
+      n = c == 1 ? 2 * ctx.num_sms : clusters_resident(kernel, G::NT, c, smem);
+      known[c].store(n > 0 ? n : -1, std::memory_order_relaxed);
+    }
+    return n;
+  });
   profile_before(ctx);
   e = launch_pdl_cluster(kernel, (unsigned)(strips * j.B * C), G::NT, C, smem, ctx.stream, a, C);
   profile_after(ctx);
