@@ -33,7 +33,7 @@
 //
 // Measured (GB300, copy rate 6.8 TB/s): 8 x 2048 x 2048 bf16 with i 49.8 us (5.4 TB/s), its
 // gradient 85.1 us (6.3 TB/s); 1 x 65536 x 2048 249 us (4.3 TB/s); gradient of 3 x 1537 x
-// 1001 fp32 without i 32.4 us (3.4 TB/s).  The gradient runs at the memory's rate; forward,
+// 1001 fp32 without i 26.7 us (4.2 TB/s).  The gradient runs at the memory's rate; forward,
 // the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
 #pragma once
 
