@@ -322,10 +322,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
     const int listed = sh.listed < kLpList ? sh.listed : kLpList;
     for (int q0 = 0; q0 < listed * V; q0 += kLpKeys / 2) {
       const unsigned long long tau = sh.tau;
-      if (sh.count > kLpKeys / 2) {  // the same for all: it changes between barriers
-        lp_select(sh.count, a.K, sh);
-        if (tid == 0) sh.count = a.K;
+      // A pass adds up to kLpKeys / 2 keys.  The first finds at most K; before a later one the
+      // keys are thinned where there may not be room.  All threads read the count before any
+      // adds to it, so that they take the same way.
+      if (q0 > 0) {
+        const int have = sh.count;
         __syncthreads();
+        if (have > kLpKeys / 2) {
+          lp_select(have, a.K, sh);
+          if (tid == 0) sh.count = a.K;
+          __syncthreads();
+        }
       }
       for (int q = q0 + tid; q < listed * V && q < q0 + kLpKeys / 2; q += NT) {
         const int e0 = sh.list_at[q / V], i = e0 + q % V;
