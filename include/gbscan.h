@@ -362,7 +362,9 @@ void gb_set_wait_limit_ns(uint64_t ns);
 /*
  * Fault injection for tests: the tile with this index (in claim order) of the
  * next single-pass launches never publishes its status, so its successors' waits
- * run out.  -1 (the default) turns it off.  Process-wide.
+ * run out.  In the recurrence it is the tile of each strip of channels, in scan order,
+ * whose map a block does not send to the others of its cluster.  -1 (the default) turns
+ * it off.  Process-wide.
  */
 void gb_set_stalled_tile(int64_t tile);
 
@@ -382,8 +384,9 @@ void gb_set_stalled_tile(int64_t tile);
  * pointer, negative size or stride, bad option), GB_ERR_UNSUPPORTED (dtype),
  * GB_ERR_RANGE (length or vocab above 2^30, channels or cols above 2^28, or a grid past
  * 2^31 - 1 blocks), GB_ERR_TEMP, GB_ERR_CUDA.  The recurrence's waits between the blocks of
- * a cluster are bounded as the others are (gb_set_wait_limit_ns): one that runs out is
- * reported as GB_ERR_TIMEOUT by gb_device_error.
+ * a cluster are bounded as the others are (gb_set_wait_limit_ns): where one runs out its
+ * block waits no more, what the cluster writes from there on is undefined, and
+ * gb_device_error reports GB_ERR_TIMEOUT.
  */
 
 /*

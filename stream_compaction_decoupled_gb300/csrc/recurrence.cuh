@@ -21,7 +21,8 @@
 // distributed shared memory: asynchronous stores that complete on the receiver's mbarrier,
 // which needs no fence behind the CTA's outstanding writes of h as a cluster barrier does.
 // The CTAs of a cluster are scheduled together, so the wait ends; it is bounded all the
-// same (GB_ERR_TIMEOUT).  No global scratch is needed.
+// same (GB_ERR_TIMEOUT): a thread whose wait ran out neither waits nor sends again, and no
+// CTA leaves while others may still send to it.  No global scratch is needed.
 //
 // The gradient runs the same scan backwards in time.  With g_t = dL/dh_t (all paths) and
 // c_t = a_t g_t,   g_t = dh_t + c_{t+1}   and   c_t = a_t c_{t+1} + a_t dh_t,
@@ -78,6 +79,7 @@ template <class T> struct RecArgs {
   int T_, D, strips;  // strips of W channels per batch row
   ErrSink err;
   unsigned long long wait_ns;
+  long long stalled;  // fault injection: the tile whose map is not sent
 };
 
 constexpr int kRecMaxCluster = 8;
@@ -249,13 +251,30 @@ __device__ __forceinline__ void rec_cluster_init(RecShared& sh, unsigned C) {
   cluster_sync();
 }
 
+// Before a CTA of a cluster leaves.  No CTA sends after the barrier, and one whose waits
+// all ended has had everything that was sent to it.  Where a wait ran out (`late`, of this
+// thread) stores may be on their way still: they land within a microsecond or two, and the
+// CTA stays for twenty.
+__device__ __forceinline__ void rec_cluster_leave(unsigned C, bool late) {
+  if (C == 1) return;
+  cluster_sync_relaxed();
+  if (late) {
+    cp_async_wait<0>();
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 20000) __nanosleep(1000);
+  }
+}
+
 // The states (two channels) that this warp's first row starts from, given the map m of its
 // rows.  `carry` is the state before the cluster's rows of this round, moved past them in
-// warp 7 (C = 1, where the others read it from shared memory) or in all (C > 1).  All
-// threads of the CTA call it.
+// warp 7 (C = 1, where the others read it from shared memory) or in all (C > 1).  `late` is
+// set where the wait for the cluster's maps ran out; the rounds left are then gone through
+// without, with whatever the slots hold.  (Leaving the loop instead, by a shared flag read
+// each round, took 10% more time: 8 x 2048 x 2048 bf16 gated 54.8 us against 50.2, its
+// gradient 98.5 against 86.2.)  All threads of the CTA call it.
 template <class A>
 __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
-                                               int round, const A& a) {
+                                               int round, bool& late, const A& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = round & 1, slot = round % kRecSlots;
   if (warp < 7) sh.warp[turn][warp][lane] = rec_pack(m);
   if (C == 1) {
@@ -273,16 +292,20 @@ __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShare
 #pragma unroll
   for (int w = 0; w < 7; ++w)
     if (w < warp) before = rec_then(before, rec_unpack(sh.warp[turn][w][lane]));
-  if (warp == 7) {
+  if (warp == 7 && !late) {
     // The CTA's map goes to every CTA of the cluster.  A slot is written again four rounds
     // later: after the sender has had this CTA's map of a later round, which was sent past
     // a barrier that every reader of the slot reached after reading it.
     if (lane == 0) mbar_arrive_expect_tx(&sh.bar[slot], C * 32 * (unsigned)sizeof(float4));
     const float4 all = rec_pack(rec_then(before, m));
-    for (unsigned r = 0; r < C; ++r)
-      st_async_f4(cluster_addr(&sh.cta[slot][rank][lane], r), all, cluster_addr(&sh.bar[slot], r));
+    if ((long long)round * C + rank != a.stalled)
+      for (unsigned r = 0; r < C; ++r)
+        st_async_f4(cluster_addr(&sh.cta[slot][rank][lane], r), all, cluster_addr(&sh.bar[slot], r));
   }
-  if (!mbar_wait(&sh.bar[slot], (unsigned)(round / kRecSlots) & 1, a.wait_ns) && lane == 0) raise_err(a.err, ERRBIT_TIMEOUT);
+  if (!late && !mbar_wait(&sh.bar[slot], (unsigned)(round / kRecSlots) & 1, a.wait_ns)) {
+    raise_err(a.err, ERRBIT_TIMEOUT);
+    late = true;
+  }
   float2 s = carry, start = carry;
 #pragma unroll
   for (unsigned r = 0; r < kRecMaxCluster; ++r) {
@@ -349,6 +372,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   unsigned marks = 0;
   float2 carry = a.h0 ? rec_load2<G>(a.h0 + b * a.D + d0 + G::first(lane), n) : make_float2(0.f, 0.f);
+  bool late = false;
   rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
@@ -392,7 +416,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     RecMap m = {av[0], bv[0]};
 #pragma unroll
     for (int r = 1; r < R; ++r) m = rec_then(m, {av[r], bv[r]});
-    float2 s = rec_exchange(m, carry, sh, C, rank, k, a);
+    float2 s = rec_exchange(m, carry, sh, C, rank, k, late, a);
     T* out = y;
     y += y_step;
     auto write = [&](int r) {
@@ -410,6 +434,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     }
   }
   if (a.last && rank == 0 && warp == 7) rec_store2<G>(a.last + b * a.D + d0 + G::first(lane), carry, n);
+  rec_cluster_leave(C, late);
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
@@ -475,6 +500,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
   unsigned marks = 0;
   float2 carry = a.dlast ? rec_load2<G>(a.dlast + at, n) : make_float2(0.f, 0.f);
   const float2 first = a.h0 ? rec_load2<G>(a.h0 + at, n) : make_float2(0.f, 0.f);
+  bool late = false;
   rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
@@ -505,7 +531,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       for (int r = 0; r < R; ++r)
         if (r < rows) row(r);
     }
-    float2 c = rec_exchange(m, carry, sh, C, rank, k, a);  // c_{t+1} of the warp's first row
+    float2 c = rec_exchange(m, carry, sh, C, rank, k, late, a);  // c_{t+1} of the warp's first row
     T *ox = dx, *of = df, *oi = di;
     dx -= step * a.dxt;
     df -= step * a.dft;
@@ -547,6 +573,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     }
   }
   if (a.dh0 && rank == 0 && warp == 7) rec_store2<G>(a.dh0 + at, carry, n);
+  rec_cluster_leave(C, late);
 }
 
 // One token: row b moves the state slots[b] of the pool on by one step, in place.  A
@@ -665,6 +692,7 @@ cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const Lau
   a.strips = (int)strips;
   a.err = ctx.err;
   a.wait_ns = ctx.wait_ns;
+  a.stalled = ctx.stalled_tile;
   constexpr int smem = G::STAGES * NA * G::ARRAY;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
