@@ -302,7 +302,7 @@ __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShare
       for (unsigned r = 0; r < C; ++r)
         st_async_f4(cluster_addr(&sh.cta[slot][rank][lane], r), all, cluster_addr(&sh.bar[slot], r));
   }
-  if (!late && !mbar_wait(&sh.bar[slot], (unsigned)(round / kRecSlots) & 1, a.wait_ns)) {
+  if (!late && !mbar_wait_cluster(&sh.bar[slot], (unsigned)(round / kRecSlots) & 1, a.wait_ns)) {
     raise_err(a.err, ERRBIT_TIMEOUT);
     late = true;
   }
