@@ -111,7 +111,9 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two fp32 operations in one instruction (sm_100 and later), each rounded as the scalar one.
+// Two fp32 operations in one instruction (sm_100 and later).  The assembler fuses a product
+// into a sum that follows it (measured: add2(mul2(a, b), c) has the bits of fma2(a, b, c)) in
+// one place and not in another: where bits must be the same, no sum takes a product.
 __device__ __forceinline__ unsigned long long bits2(float2 v) {
   unsigned long long u;
   asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));

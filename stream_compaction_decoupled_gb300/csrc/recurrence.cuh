@@ -30,7 +30,10 @@
 //   dx_t = u_t g_t,   df_t = a_t (1 - a_t) h_{t-1} g_t,   di_t = u_t (1 - u_t) x_t g_t,
 //   and without i:    df_t = a_t (1 - a_t) (h_{t-1} - x_t) g_t.
 // Where starts[t] is set the state before t is dropped: a_t counts as 0 in the scan and
-// h_{t-1} as 0 in df_t.
+// h_{t-1} as 0 in df_t.  0 times an infinity or a NaN does not drop it, though.  It makes a
+// NaN, and what is not finite then never leaves the state again, in any order of composition:
+// the state after the last row tells.  Where that is not finite and there are starts, the
+// strip is gone through a second time (EXACT), its maps dropping the state by selection.
 //
 // Measured (GB300, copy rate 6.8 TB/s): 8 x 2048 x 2048 bf16 with i 49.8 us (5.4 TB/s), its
 // gradient 85.1 us (6.3 TB/s); 1 x 65536 x 2048 249 us (4.3 TB/s); gradient of 3 x 1537 x
@@ -39,6 +42,7 @@
 #pragma once
 
 #include <atomic>
+#include <cmath>
 
 #include "lm.cuh"
 #include "lm.h"
@@ -108,13 +112,24 @@ template <class T, bool EDGE_, int STAGES_> struct RecGeom {
   static_assert(L == 2 * ROWS, "each thread copies two rows' chunks of each array");
 };
 
-// Two channels' map y -> a y + b.
+// Two channels' map y -> a y + b.  EXACT: where a is -0, which no product of sigmoids is, the
+// map drops y whatever it is.
 struct RecMap {
   float2 a, b;
 };
-__device__ __forceinline__ float2 rec_apply(RecMap m, float2 s) { return fma2(m.a, s, m.b); }
+__device__ __forceinline__ float2 rec_drop() { return make_float2(-0.f, -0.f); }
+__device__ __forceinline__ float2 rec_unless(float2 a, float2 v, float drop) {  // v, or `drop` where a is -0
+  return make_float2(__float_as_uint(a.x) == 0x80000000u ? drop : v.x, __float_as_uint(a.y) == 0x80000000u ? drop : v.y);
+}
+template <bool EXACT> __device__ __forceinline__ float2 rec_apply(RecMap m, float2 s) {
+  if constexpr (EXACT) s = rec_unless(m.a, s, 0.f);
+  return fma2(m.a, s, m.b);
+}
 // m, then q.
-__device__ __forceinline__ RecMap rec_then(RecMap m, RecMap q) { return {mul2(m.a, q.a), fma2(q.a, m.b, q.b)}; }
+template <bool EXACT> __device__ __forceinline__ RecMap rec_then(RecMap m, RecMap q) {
+  if constexpr (EXACT) m = {rec_unless(q.a, m.a, 1.f), rec_unless(q.a, m.b, 0.f)};
+  return {mul2(m.a, q.a), fma2(q.a, m.b, q.b)};
+}
 __device__ __forceinline__ float4 rec_pack(RecMap m) { return make_float4(m.a.x, m.a.y, m.b.x, m.b.y); }
 __device__ __forceinline__ RecMap rec_unpack(float4 q) { return {make_float2(q.x, q.y), make_float2(q.z, q.w)}; }
 
@@ -272,7 +287,7 @@ __device__ __forceinline__ void rec_cluster_leave(unsigned C, bool late) {
 // without, with whatever the slots hold.  (Leaving the loop instead, by a shared flag read
 // each round, took 10% more time: 8 x 2048 x 2048 bf16 gated 54.8 us against 50.2, its
 // gradient 98.5 against 86.2.)  All threads of the CTA call it.
-template <class A>
+template <bool EXACT, class A>
 __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShared& sh, unsigned C, unsigned rank,
                                                int round, bool& late, const A& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = round & 1, slot = round % kRecSlots;
@@ -283,21 +298,21 @@ __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShare
     float2 s = sh.carry[turn][lane];
 #pragma unroll
     for (int w = 0; w < 7; ++w)
-      if (w < warp) s = rec_apply(rec_unpack(sh.warp[turn][w][lane]), s);
-    if (warp == 7) carry = rec_apply(m, s);
+      if (w < warp) s = rec_apply<EXACT>(rec_unpack(sh.warp[turn][w][lane]), s);
+    if (warp == 7) carry = rec_apply<EXACT>(m, s);
     return s;
   }
   __syncthreads();
   RecMap before = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int w = 0; w < 7; ++w)
-    if (w < warp) before = rec_then(before, rec_unpack(sh.warp[turn][w][lane]));
+    if (w < warp) before = rec_then<EXACT>(before, rec_unpack(sh.warp[turn][w][lane]));
   if (warp == 7 && !late) {
     // The CTA's map goes to every CTA of the cluster.  A slot is written again four rounds
     // later: after the sender has had this CTA's map of a later round, which was sent past
     // a barrier that every reader of the slot reached after reading it.
     if (lane == 0) mbar_arrive_expect_tx(&sh.bar[slot], C * 32 * (unsigned)sizeof(float4));
-    const float4 all = rec_pack(rec_then(before, m));
+    const float4 all = rec_pack(rec_then<EXACT>(before, m));
     if ((long long)round * C + rank != a.stalled)
       for (unsigned r = 0; r < C; ++r)
         st_async_f4(cluster_addr(&sh.cta[slot][rank][lane], r), all, cluster_addr(&sh.bar[slot], r));
@@ -311,19 +326,36 @@ __device__ __forceinline__ float2 rec_exchange(RecMap m, float2& carry, RecShare
   for (unsigned r = 0; r < kRecMaxCluster; ++r) {
     if (r < C) {
       if (r == rank) start = s;
-      s = rec_apply(rec_unpack(sh.cta[slot][r][lane]), s);
+      s = rec_apply<EXACT>(rec_unpack(sh.cta[slot][r][lane]), s);
     }
   }
   carry = s;
-  return rec_apply(before, start);
+  return rec_apply<EXACT>(before, start);
 }
 
-template <class T, bool GATE, class G>
-__global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+// Whether the strip has to be gone through again: starts, and a state after the last row that
+// is not finite in a channel that exists (n of the lane's).  The same for the whole cluster:
+// with C > 1 every warp has the state of all 64 channels, else warp 7 does.  All threads of the
+// CTA call it; what the round before left in shared memory is free after it.
+__device__ __forceinline__ bool rec_again(const uint8_t* starts, float2 carry, int n, unsigned C) {
+  if (!starts) return false;
+  const bool odd = (n > 0 && !(fabsf(carry.x) < INFINITY)) || (n > 1 && !(fabsf(carry.y) < INFINITY));
+  return __syncthreads_or(odd && (C > 1 || threadIdx.x >= 7 * 32));
+}
+
+// The same number, which the compiler takes for another one: what the second pass derives from
+// it is worked out there, not kept in registers through the first (spills otherwise).
+__device__ __forceinline__ unsigned rec_afresh(unsigned v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
+// One pass over the strip: the state after its last row (warp 7, or with C > 1 every warp).
+// Rounds count on from round0, as the exchange's slots do.
+template <class T, bool GATE, class G, bool EXACT>
+__device__ __forceinline__ float2 rec_forward_pass(const RecArgs<T>& a, unsigned C, unsigned char* tiles, RecShared& sh,
+                                                   int round0, bool& late) {
   constexpr int R = G::R, NA = GATE ? 3 : 2;
-  extern __shared__ __align__(16) unsigned char tiles[];
-  __shared__ RecShared sh;
-  pdl_entry();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
@@ -372,8 +404,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
   for (int k = 0; k < G::STAGES - 1; ++k) fetch(k);
   unsigned marks = 0;
   float2 carry = a.h0 ? rec_load2<G>(a.h0 + b * a.D + d0 + G::first(lane), n) : make_float2(0.f, 0.f);
-  bool late = false;
-  rec_cluster_init(sh, C);
+  if constexpr (!EXACT) rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
     const int rows = (int)(a.T_ - (long long)k * step) - tile0 - warp * R;  // rows from this warp's first to the end
@@ -411,16 +442,16 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
     if (drop) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (drop >> r & 1) av[r] = make_float2(0.f, 0.f);
+        if (drop >> r & 1) av[r] = EXACT ? rec_drop() : make_float2(0.f, 0.f);
     }
     RecMap m = {av[0], bv[0]};
 #pragma unroll
-    for (int r = 1; r < R; ++r) m = rec_then(m, {av[r], bv[r]});
-    float2 s = rec_exchange(m, carry, sh, C, rank, k, late, a);
+    for (int r = 1; r < R; ++r) m = rec_then<EXACT>(m, {av[r], bv[r]});
+    float2 s = rec_exchange<EXACT>(m, carry, sh, C, rank, round0 + k, late, a);
     T* out = y;
     y += y_step;
     auto write = [&](int r) {
-      s = fma2(av[r], s, bv[r]);
+      s = rec_apply<EXACT>({av[r], bv[r]}, s);
       rec_store<T, G>(out, s, n);
       out += a.yt;
     };
@@ -433,17 +464,43 @@ __global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_cons
         if (r < rows) write(r);
     }
   }
-  if (a.last && rank == 0 && warp == 7) rec_store2<G>(a.last + b * a.D + d0 + G::first(lane), carry, n);
+  return carry;
+}
+
+// Where in the array this thread's channels are, for the kernels: those that exist, and the
+// offset of the first in a (batch, channel) array.
+template <class T, class G> __device__ __forceinline__ int rec_where(const RecArgs<T>& a, unsigned C, long long& at) {
+  const unsigned strip = blockIdx.x / C;
+  const int d0 = (int)(strip % a.strips) * G::W;
+  at = (long long)(strip / a.strips) * a.D + d0 + G::first(threadIdx.x & 31);
+  return G::count(a.D - d0 < G::W ? a.D - d0 : G::W);
+}
+template <class T, class G> __device__ __forceinline__ int rec_rounds(const RecArgs<T>& a, unsigned C) {
+  return (int)(((long long)a.T_ + (int)C * G::L - 1) / ((int)C * G::L));
+}
+
+template <class T, bool GATE, class G>
+__global__ void __launch_bounds__(G::NT, 2) rec_forward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ RecShared sh;
+  pdl_entry();
+  bool late = false;
+  float2 carry = rec_forward_pass<T, GATE, G, false>(a, C, tiles, sh, 0, late);
+  long long at;
+  const int n = rec_where<T, G>(a, C, at);
+  if (rec_again(a.starts, carry, n, C)) {
+    const unsigned C2 = rec_afresh(C);
+    carry = rec_forward_pass<T, GATE, G, true>(a, C2, tiles, sh, rec_rounds<T, G>(a, C2), late);
+  }
+  if (a.last && blockIdx.x % C == 0 && threadIdx.x >= 7 * 32) rec_store2<G>(a.last + at, carry, n);
   rec_cluster_leave(C, late);
 }
 
 // Position p = 0, 1, ... counts rows from the end: t = T - 1 - p.
-template <class T, bool GATE, class G>
-__global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+template <class T, bool GATE, class G, bool EXACT>
+__device__ __forceinline__ float2 rec_backward_pass(const RecArgs<T>& a, unsigned C, unsigned char* tiles, RecShared& sh,
+                                                    int round0, bool& late) {
   constexpr int R = G::R, NA = GATE ? 5 : 4;
-  extern __shared__ __align__(16) unsigned char tiles[];
-  __shared__ RecShared sh;
-  pdl_entry();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const unsigned strip = blockIdx.x / C;
@@ -500,8 +557,7 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
   unsigned marks = 0;
   float2 carry = a.dlast ? rec_load2<G>(a.dlast + at, n) : make_float2(0.f, 0.f);
   const float2 first = a.h0 ? rec_load2<G>(a.h0 + at, n) : make_float2(0.f, 0.f);
-  bool late = false;
-  rec_cluster_init(sh, C);
+  if constexpr (!EXACT) rec_cluster_init(sh, C);
 
   for (int k = 0; k < rounds; ++k) {
     const int rows = (int)(a.T_ - (long long)k * step) - tile0 - warp * R;  // rows r < rows exist; t = rows - 1 - r
@@ -512,16 +568,23 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
     const unsigned drop = __shfl_sync(0xffffffffu, marks, k % 32);
     const unsigned char* base = tiles + (k % G::STAGES) * (NA * G::ARRAY) + warp * R * G::PITCH;
     float2 s[R], s1[R];  // sigmoid(f) and 1 - sigmoid(f)
-    constexpr bool KEEP = G::EDGE && !GATE;  // keep dh, whose place takes some working out, where registers allow
+    constexpr bool KEEP = G::EDGE && !GATE && !EXACT;  // keep dh, whose place takes some working out, where registers allow
     float2 kept[KEEP ? R : 1];
+    // Row r's map is c -> a (dh + c).  The sum (dh + c of the rows so far, from c = 0) is kept
+    // one row ahead of the product, as one fused operation a row; dropped, c is 0.
     RecMap m = {make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+    float2 sum;
+    auto past = [&](int r, float2 v, float2 ds) {  // dh_t + a_{t+1} v, row r - 1 being t + 1
+      const bool dropped = drop >> (r - 1) & 1;
+      if (EXACT) return dropped ? ds : fma2(s[r - 1], v, ds);
+      return fma2(dropped ? make_float2(0.f, 0.f) : s[r - 1], v, ds);
+    };
     auto row = [&](int r) {
       const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(dho, r, dhp, a.dht, a.T_ - 1 - r));
       if constexpr (KEEP) kept[r] = ds;
       sigmoid_both(rec_pair<T, G>(base, r, rec_offset<T, G>(fo, r, fp, a.ft, a.T_ - 1 - r)), s[r], s1[r]);
-      const float2 av = drop >> r & 1 ? make_float2(0.f, 0.f) : s[r];
-      // a c + a dh = a (c + dh), so the map's b is a (b + dh).
-      m = {mul2(m.a, av), mul2(av, add2(m.b, ds))};
+      sum = r ? past(r, sum, ds) : ds;
+      m = {mul2(m.a, s[r]), drop >> r & 1 ? make_float2(0.f, 0.f) : mul2(s[r], sum)};
     };
     if (rows >= R) {
 #pragma unroll
@@ -531,23 +594,23 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
       for (int r = 0; r < R; ++r)
         if (r < rows) row(r);
     }
-    float2 c = rec_exchange(m, carry, sh, C, rank, k, late, a);  // c_{t+1} of the warp's first row
+    if (drop) m.a = EXACT ? rec_drop() : make_float2(0.f, 0.f);
+    const float2 c = rec_exchange<EXACT>(m, carry, sh, C, rank, round0 + k, late, a);  // c_{t+1} of the warp's first row
     T *ox = dx, *of = df, *oi = di;
     dx -= step * a.dxt;
     df -= step * a.dft;
     if constexpr (GATE) di -= step * a.dit;
+    float2 gt;  // dL/dh_t
     auto write = [&](int r) {
       const int t = rows - 1 - r;
       const float2 ds = KEEP ? kept[KEEP ? r : 0]
                              : rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(dho, r, dhp, a.dht, a.T_ - 1 - r));
       const float2 xs = rec_pair<T, G>(base + 2 * G::ARRAY, r, rec_offset<T, G>(xo, r, xp, a.xt, a.T_ - 1 - r));
       float2 hs = t > 0 ? rec_pair<T, G>(base + 3 * G::ARRAY, r, rec_offset<T, G>(ho, r, hp, a.ht, a.T_ - 2 - r)) : first;
-      const bool dropped = drop >> r & 1;
-      if (dropped) hs = make_float2(0.f, 0.f);
-      const float2 gt = add2(ds, c);  // dL/dh_t
-      c = mul2(s[r], gt);
-      const float2 fg = mul2(c, s1[r]);
-      if (dropped) c = make_float2(0.f, 0.f);
+      if (drop >> r & 1) hs = make_float2(0.f, 0.f);
+      if (r == 0) gt = add2(ds, c);
+      else gt = past(r, gt, ds);
+      const float2 fg = mul2(mul2(s[r], gt), s1[r]);
       if constexpr (GATE) {
         float2 u, u1;
         sigmoid_both(rec_pair<T, G>(base + 4 * G::ARRAY, r, rec_offset<T, G>(go, r, gp, a.it, a.T_ - 1 - r)), u, u1);
@@ -572,7 +635,23 @@ __global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_con
         if (r < rows) write(r);
     }
   }
-  if (a.dh0 && rank == 0 && warp == 7) rec_store2<G>(a.dh0 + at, carry, n);
+  return carry;
+}
+
+template <class T, bool GATE, class G>
+__global__ void __launch_bounds__(G::NT, 2) rec_backward_kernel(const __grid_constant__ RecArgs<T> a, unsigned C) {
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ RecShared sh;
+  pdl_entry();
+  bool late = false;
+  float2 carry = rec_backward_pass<T, GATE, G, false>(a, C, tiles, sh, 0, late);
+  long long at;
+  const int n = rec_where<T, G>(a, C, at);
+  if (rec_again(a.starts, carry, n, C)) {
+    const unsigned C2 = rec_afresh(C);
+    carry = rec_backward_pass<T, GATE, G, true>(a, C2, tiles, sh, rec_rounds<T, G>(a, C2), late);
+  }
+  if (a.dh0 && blockIdx.x % C == 0 && threadIdx.x >= 7 * 32) rec_store2<G>(a.dh0 + at, carry, n);
   rec_cluster_leave(C, late);
 }
 
