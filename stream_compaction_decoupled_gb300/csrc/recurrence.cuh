@@ -108,6 +108,12 @@ template <class T, bool EDGE_, int STAGES_> struct RecGeom {
   static constexpr int CHUNKS = 64 / V;                      // copies of a row
   static constexpr int PITCH = CHUNKS * 16;                  // bytes of a row in shared memory
   static constexpr int ARRAY = L * PITCH;
+  // EDGE: all lanes load both their channels, at the row's offset of up to 16 bytes less a
+  // value.  The last of the 64 then ends past the row, and in the last row of all past the
+  // tiles (none of it belongs to a channel that exists): the allocation is that much longer.
+  static constexpr int SLACK = EDGE ? 16 : 0;
+  static constexpr int REACH = (EDGE ? 16 - (int)sizeof(T) : 0) + (EDGE ? 31 + APART + 1 : 64) * (int)sizeof(T);
+  static_assert(REACH <= PITCH + SLACK, "loads stay in the tiles and their slack");
   static constexpr int ROWS = NT / CHUNKS;                   // rows that the CTA copies at once
   static_assert(L == 2 * ROWS, "each thread copies two rows' chunks of each array");
 };
@@ -772,7 +778,7 @@ cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const Lau
   a.err = ctx.err;
   a.wait_ns = ctx.wait_ns;
   a.stalled = ctx.stalled_tile;
-  constexpr int smem = G::STAGES * NA * G::ARRAY;
+  constexpr int smem = G::STAGES * NA * G::ARRAY + G::SLACK;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // What is resident is a property of this kernel (each instance launches one) and the device.
