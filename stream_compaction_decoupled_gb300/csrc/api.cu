@@ -43,7 +43,7 @@ namespace {
 
 using gbs::LaunchCtx;
 
-constexpr int kMaxDevices = 64;
+using gbs::kMaxDevices;
 constexpr int kMaxLanes = 4096;
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;  // 1 s
 
@@ -90,6 +90,7 @@ int make_ctx(void* stream, LaunchCtx& ctx) {
     ctx.err.dev = g_err_ptr[dev];
     ctx.err.call = nullptr;
     ctx.num_sms = g_num_sms[dev];
+    ctx.device = dev;
   }
   ctx.stream = (cudaStream_t)stream;
   const unsigned long long w = g_wait_ns.load();

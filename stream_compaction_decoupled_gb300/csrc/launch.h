@@ -31,6 +31,9 @@ __device__ __forceinline__ void raise_err(const ErrSink& e, unsigned bits) {
 }
 #endif
 
+// Device ordinals that the library keeps state for.
+constexpr int kMaxDevices = 64;
+
 // Settings the C ABI attaches to every launch.
 struct LaunchCtx {
   cudaStream_t stream = nullptr;
@@ -40,6 +43,7 @@ struct LaunchCtx {
   cudaEvent_t ev_before = nullptr;     // optional events around the main kernel
   cudaEvent_t ev_after = nullptr;
   int num_sms = 0;
+  int device = 0;                      // its ordinal
 };
 
 // Scan along the middle axis of a row-major (B, R, C) array.

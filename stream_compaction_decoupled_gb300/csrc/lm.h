@@ -105,7 +105,7 @@ cudaError_t launch_pdl_cluster(void (*kernel)(P...), unsigned grid, unsigned blo
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 
-// How many clusters of the kernel the device can hold at once (0: the query failed).
+// How many clusters of the kernel the device can hold at once (-1: the query failed).
 template <class... P>
 int clusters_resident(void (*kernel)(P...), unsigned block, unsigned cluster, size_t smem) {
   cudaLaunchConfig_t cfg = {};
@@ -122,7 +122,7 @@ int clusters_resident(void (*kernel)(P...), unsigned block, unsigned cluster, si
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
-    return 0;
+    return -1;
   }
   return n;
 }

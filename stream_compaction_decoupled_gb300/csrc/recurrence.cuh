@@ -41,11 +41,11 @@
 // the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
 #pragma once
 
-#include <atomic>
 #include <cmath>
 
 #include "lm.cuh"
 #include "lm.h"
+#include "resident.h"
 
 namespace gbs {
 
@@ -782,14 +782,11 @@ cudaError_t rec_launch(K kernel, const RecurrenceJob& j, RecArgs<T> a, const Lau
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // What is resident is a property of this kernel (each instance launches one) and the device.
-  static std::atomic<int> known[kRecMaxCluster + 1];
+  static ResidentTable<kMaxDevices, kRecMaxCluster> resident;
   const unsigned C = rec_cluster(strips * j.B, (j.T + G::L - 1) / G::L, [&](unsigned c) {
-    int n = known[c].load(std::memory_order_relaxed);
-    if (n == 0) {
-      n = c == 1 ? 2 * ctx.num_sms : clusters_resident(kernel, G::NT, c, smem);
-      known[c].store(n > 0 ? n : -1, std::memory_order_relaxed);
-    }
-    return n;
+    return resident.get(ctx.device, c, [&](unsigned size) {
+      return size == 1 ? 2 * ctx.num_sms : clusters_resident(kernel, G::NT, size, smem);
+    });
   });
   profile_before(ctx);
   e = launch_pdl_cluster(kernel, (unsigned)(strips * j.B * C), G::NT, C, smem, ctx.stream, a, C);
