@@ -6,16 +6,18 @@
 //   lower index, with their log probabilities;
 //   gradient:  dx_j = dlogprob ([j = target] - p_j) - dentropy p_j (log p_j + entropy).
 //
-// Each row is read once.  In base 2, a thread keeps a reference M near the largest
-// x log2(e) so far and, relative to it, s = sum 2^d and t = sum 2^d d with
-// d = x log2(e) - M (one fused multiply-add).  M follows the maximum only when that has
-// grown by more than 8, which costs no accuracy and almost never happens after a thread's
-// first values; s and t are then multiplied by 2^(M - M'), t moved first.  At the end
-//   lse = ln 2 (M + log2 s),   entropy = ln 2 (log2 s - t / s),
-// which loses nothing to cancellation.  Values are held at a floor (-2^126, or fp16's
-// lowest), so that a masked logit (-inf) gives 2^d = 0 and a product of 0, not a NaN.
-// Rows for which this does not do (nothing above the floor, values near the top of the
-// range, a NaN) are read again by the careful form in lp_careful.
+// Each row is read once.  A thread keeps the largest value so far, M, and relative to it
+// s = sum e^z and t = sum e^z z with z = x - M; when M grows, s and t are moved to the new
+// one.  At the end
+//   lse = M + log s,   entropy = log s - t / s,   logprob = (x_target - M) - log s.
+// M is the true maximum: below it, a confident row's log s and t / s would both be large and
+// cancel, and lse would not be the least number that it can be, M, so that e^(x - lse) could
+// pass 1.  In 16-bit types the sums are kept in base 2 (LpAcc), one fused multiply-add to an
+// exponent in place of a difference and a product.
+// Values are held at a floor (-2^126; bf16 -2^20, fp16 its lowest), so that a masked logit
+// (-inf, or a number far below) gives e^z = 0 and a product of 0, not a NaN.  Rows for which
+// this does not do (nothing above the floor, values far from 0, a NaN) are read again by the
+// careful form in lp_careful.
 //
 // The alternatives are found in the same pass, as a compaction.  A value's key (the value
 // in the high half, the index reversed in the low half: unique, so ties are settled) is
@@ -69,7 +71,6 @@ constexpr int kLpMaxCluster = 8;
 // Natural-log differences from a maximum stop here: e^d has long been 0 in fp32, and
 // products with d stay finite, so that 0 times them is 0.
 constexpr float kLpFloor = -1000.f;
-constexpr float kLpSlack = 8.f;    // how far values may rise above the reference, in base 2
 
 __device__ __forceinline__ long long lp_target(const void* targets, int is64, long long row) {
   return is64 ? ((const long long*)targets)[row] : (long long)((const int*)targets)[row];
@@ -100,7 +101,7 @@ template <> struct LpType<float> {
   }
 };
 template <> struct LpType<__nv_bfloat16> {
-  static constexpr float kFloor = -8.507059173023462e37f;
+  static constexpr float kFloor = -1048576.f;  // -2^20
   static __device__ __forceinline__ unsigned max2(unsigned a, unsigned b) {
     unsigned d;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -109,7 +110,7 @@ template <> struct LpType<__nv_bfloat16> {
   static __device__ __forceinline__ float hold(Pack<__nv_bfloat16, 8>& p) {
     uint4 u;
     memcpy(&u, &p, 16);
-    constexpr unsigned f = 0xfe80fe80u;
+    constexpr unsigned f = 0xc980c980u;
     u = make_uint4(max2(u.x, f), max2(u.y, f), max2(u.z, f), max2(u.w, f));
     memcpy(&p, &u, 16);
     const unsigned m = max2(max2(u.x, u.y), max2(u.z, u.w));
@@ -137,22 +138,74 @@ template <> struct LpType<__half> {
   }
 };
 
-// Sums relative to a reference m, in base 2 (or, in lp_careful, natural units).
+// The largest value m, and relative to it r = sum e^z - 1 (of all values but one largest) and
+// t = sum e^z z: what the many small terms of a confident row add to is not lost beside the 1.
+// r = -1: no values.
 struct LpSums {
-  float m, s, t;
+  float m, r, t;
 };
-template <bool BASE2> __device__ __forceinline__ void lp_rebase(LpSums& a, float m) {
-  const float d = max_nan(a.m - m, kLpFloor), k = ex2(BASE2 ? d : d * kLog2e);
-  a.t = k * fmaf(a.s, d, a.t);
-  a.s *= k;
-  a.m = m;
+__device__ __forceinline__ LpSums lp_join(LpSums a, LpSums b) {
+  const LpSums hi = a.m < b.m ? b : a, lo = a.m < b.m ? a : b;
+  const float d = max_nan(lo.m - hi.m, kLpFloor), k = ex2(d * kLog2e), s = 1.f + lo.r;
+  return {hi.m, fmaf(k, s, hi.r), fmaf(k, fmaf(s, d, lo.t), hi.t)};
 }
-template <bool BASE2> __device__ __forceinline__ LpSums lp_join(LpSums a, LpSums b) {
-  const float m = max_nan(a.m, b.m);
-  lp_rebase<BASE2>(a, m);
-  lp_rebase<BASE2>(b, m);
-  return {m, a.s + b.s, a.t + b.t};
-}
+
+// A thread's sums while it goes along its values, in pairs, s the whole sum.  fp32: as above.
+template <class T> struct LpAcc {
+  static constexpr float kFar = 1e38f;  // differences of values up to here stay finite
+  float m = LpType<T>::kFloor;
+  float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+  __device__ __forceinline__ void rise(float best) {  // best > m
+    const float d = max_nan(m - best, kLpFloor), k = ex2(d * kLog2e);
+    move(d, k);
+    m = best;
+  }
+  __device__ __forceinline__ void move(float d, float k) {
+    const float2 k2 = make_float2(k, k);
+    t = mul2(k2, fma2(s, make_float2(d, d), t));
+    s = mul2(s, k2);
+  }
+  __device__ __forceinline__ void add(float2 v) {
+    const float2 z = add2(v, make_float2(-m, -m)), y = mul2(z, make_float2(kLog2e, kLog2e));
+    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+    s = add2(s, e);
+    t = fma2(e, z, t);
+  }
+  __device__ __forceinline__ LpSums sums() const { return {m, s.x + s.y - 1.f, t.x + t.y}; }
+};
+// 16 bits: relative to r = m log2(e) as rounded, in base 2, s = sum 2^d and t = sum 2^d d with
+// d = x log2(e) - r exact but for one rounding (half an instruction a value less: 4096 x 128000
+// bf16 with 8 alternatives 204.6 us, with differences first 213.6).  d is z log2(e) + f, f = m
+// log2(e) - r: known exactly and taken out at the end.  (Further than kFar from 0 it is no small fraction any
+// more; the floor, and so every thread's m, is little below that.)
+template <class T> struct LpAcc16 : LpAcc<float> {
+  static constexpr float kFar = 1e6f;
+  float r;
+  __device__ __forceinline__ LpAcc16() {
+    m = LpType<T>::kFloor;
+    r = m * kLog2e;
+  }
+  __device__ __forceinline__ void rise(float best) {
+    const float to = best * kLog2e, d = max_nan(r - to, kLpFloor);
+    move(d, ex2(d));
+    m = best;
+    r = to;
+  }
+  __device__ __forceinline__ void add(float2 v) {
+    const float2 d = fma2(v, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
+    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+    s = add2(s, e);
+    t = fma2(e, d, t);
+  }
+  __device__ __forceinline__ LpSums sums() const {
+    // 2^-f - 1 by its series: |f| is 2^-4 at most, and the next term under 2^-22.
+    const float f = fmaf(m, kLog2e, -r), x = kLn2 * f, k = -x * (1.f - x * (0.5f - x * (1.f / 6.f)));
+    const float s1 = s.x + s.y, t1 = fmaf(-f, s1, t.x + t.y);
+    return {m, fmaf(s1, k, s1 - 1.f), kLn2 * fmaf(t1, k, t1)};
+  }
+};
+template <> struct LpAcc<__nv_bfloat16> : LpAcc16<__nv_bfloat16> {};
+template <> struct LpAcc<__half> : LpAcc16<__half> {};
 
 struct LpShared {
   unsigned long long keys[kLpKeys];
@@ -168,37 +221,34 @@ struct LpShared {
 };
 
 // The CTA's sums from its threads', in a fixed order; ends with a barrier.
-template <bool BASE2> __device__ __forceinline__ void lp_reduce(LpSums v, LpShared& sh) {
+__device__ __forceinline__ void lp_reduce(LpSums v, LpShared& sh) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) {
     LpSums o;
     o.m = __shfl_xor_sync(0xffffffffu, v.m, d);
-    o.s = __shfl_xor_sync(0xffffffffu, v.s, d);
+    o.r = __shfl_xor_sync(0xffffffffu, v.r, d);
     o.t = __shfl_xor_sync(0xffffffffu, v.t, d);
-    v = lp_join<BASE2>(v, o);
+    v = lp_join(v, o);
   }
   if (threadIdx.x % 32 == 0) sh.warp[threadIdx.x / 32] = v;
   __syncthreads();
   if (threadIdx.x == 0) {
     LpSums r = sh.warp[0];
-    for (int w = 1; w < kLpThreads / 32; ++w) r = lp_join<BASE2>(r, sh.warp[w]);
+    for (int w = 1; w < kLpThreads / 32; ++w) r = lp_join(r, sh.warp[w]);
     sh.sums = r;
   }
   __syncthreads();
 }
 
-// The sums of a whole row value by value, in natural units with differences taken first:
-// for values near the ends of the range.  A row with nothing left ends with s = 0.
+// The sums of a whole row value by value: for values near the ends of the range.  A row with
+// nothing left ends with r = -1.
 template <class T> __device__ void lp_careful(const T* x, int V, LpShared& sh) {
-  LpSums v = {-FLT_MAX, 0.f, 0.f};
+  LpSums v = {-FLT_MAX, -1.f, 0.f};
   for (int j = threadIdx.x; j < V; j += kLpThreads) {
     const float q = widen(x[j]);
-    if (q > v.m) lp_rebase<false>(v, q);
-    const float d = max_nan(q - v.m, kLpFloor), e = ex2(d * kLog2e);
-    v.s += e;
-    v.t = fmaf(e, d, v.t);
+    v = lp_join(v, {q, q == -INFINITY ? -1.f : q - q, 0.f});  // q - q: 0, or a NaN
   }
-  lp_reduce<false>(v, sh);
+  lp_reduce(v, sh);
 }
 
 // Of 64 groups of threads (a fixed number of neighbours each) the K-th largest of the
@@ -387,8 +437,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
     if (tid == 0) sh.missed = INT_MAX;
     __syncthreads();
   };
-  float ref = kFloor * kLog2e;
-  float2 s2 = make_float2(0.f, 0.f), t2 = s2;
+  LpAcc<T> acc;
   float bar = -INFINITY;  // the threshold's value
   int stage = 0, tile = 1, next = 2;
   fetch(p0, 0);
@@ -420,24 +469,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
         const unsigned long long q = j < p1 ? lp_key(best <= kFloor ? -INFINITY : best, i) : 0;
         most = q > most ? q : most;
       }
-      const float top = best * kLog2e;
-      if (top > ref + kLpSlack) {
-        const float d = max_nan(ref - top, kLpFloor), k = ex2(d);
-        const float2 k2 = make_float2(k, k), d2 = make_float2(d, d);
-        t2 = mul2(k2, fma2(s2, d2, t2));
-        s2 = mul2(s2, k2);
-        ref = top;
-      }
-      const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-ref, -ref);
+      if (best > acc.m) acc.rise(best);
       float v[V];
       widen_pack(held, v);
 #pragma unroll
-      for (int c = 0; c < V; c += 2) {
-        const float2 d2 = fma2(make_float2(v[c], v[c + 1]), l2, r2);
-        const float2 e2 = make_float2(ex2(d2.x), ex2(d2.y));
-        s2 = add2(s2, e2);
-        t2 = fma2(e2, d2, t2);
-      }
+      for (int c = 0; c < V; c += 2) acc.add(make_float2(v[c], v[c + 1]));
     }
     if constexpr (TOP) {
       if (p == p0) {
@@ -474,7 +510,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
     }
     stage ^= 1;
   }
-  lp_reduce<true>({ref, s2.x + s2.y, t2.x + t2.y}, sh);
+  lp_reduce(acc.sums(), sh);
   if constexpr (TOP) settle(INT_MAX);
   if (C > 1) {
     cluster_sync();
@@ -483,7 +519,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
         LpSums r = sh.sums;
         for (unsigned q = 1; q < C; ++q) {
           const unsigned at = cluster_addr(&sh.sums, q);
-          r = lp_join<true>(r, {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
+          r = lp_join(r, {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
         }
         sh.sums = r;
       }
@@ -499,26 +535,19 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
     if (rank != 0) return;
   }
   LpSums r = sh.sums;
-  // Nothing above the floor, a reference near the top of the range, or a NaN: read the row
-  // again with care.  (The same for all threads.)
-  const bool careful = !(r.m > kFloor * kLog2e) || r.m > 1e38f || !(r.s < INFINITY);
-  if (careful) {
+  // Nothing above the floor, a maximum far from 0, or a NaN: read the row again with care.
+  // (The same for all threads.)
+  if (!(r.m > kFloor) || !(fabsf(r.m) < LpAcc<T>::kFar) || !(r.r < INFINITY)) {
     __syncthreads();
     lp_careful(x, a.V, sh);
     r = sh.sums;
   }
-  const float log_s = careful ? logf(r.s) : log2f(r.s);
-  const float lse = careful ? r.m + log_s : kLn2 * (r.m + log_s);
-  auto logprob = [&](float v) {
-    if (careful) return (v - r.m) - log_s;
-    // Far below, where products with log2(e) may overflow, the difference is as exact.
-    const float d = fmaf(v, kLog2e, -r.m);
-    return d > -1024.f ? kLn2 * (d - log_s) : v - lse;
-  };
-  const bool none = r.s == 0.f;  // all -inf
+  const float log_s = log1pf(r.r);
+  auto logprob = [&](float v) { return (v - r.m) - log_s; };
+  const bool none = r.r == -1.f;  // all -inf
   if (tid == 0) {
-    a.lse[row] = none ? -INFINITY : lse;
-    a.entropy[row] = none ? 0.f : careful ? log_s - r.t / r.s : kLn2 * (log_s - r.t / r.s);
+    a.lse[row] = none ? -INFINITY : r.m + log_s;
+    a.entropy[row] = none ? 0.f : log_s - r.t / (1.f + r.r);
     a.logprob[row] = target < 0 ? 0.f : none ? -INFINITY : logprob(xt);
   }
   if constexpr (TOP) {
