@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const __grid_con
 //   dx = -p (w + h (log p + entropy)),   p = exp(x - lse),   and w more at the target
 // (w = dlogprob, h = dentropy).  Values are held at a floor far below any lse but small
 // enough that its products stay finite, so that a masked logit gets 0; rows whose lse is
-// itself near the floor (or -inf, or NaN) take each difference with care instead.  Where
+// itself near the floor (or -inf, or NaN), or as far above 0, or whose h is that large, take
+// each difference with care instead.  Where
 // the rows of the two arrays start at different offsets from a 16-byte boundary V is 1.
 template <class T> struct LogprobGradArgs {
   const T* logits;
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_backward_kernel(const __gr
   }
   const bool none = lse == -INFINITY;  // a row with nothing left has no gradient
   const float w = target >= 0 && target < a.V && !none ? dl : 0.f, h = none ? 0.f : dh;
-  const bool careful = !(lse > (std::is_same<T, __half>::value ? -60000.f : -1e18f));
+  const bool careful = !(lse > (std::is_same<T, __half>::value ? -60000.f : -1e18f) && lse < 1e18f && fabsf(h) < 1e18f);
   const float2 l2 = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
   // w + h (d + entropy) = h d + c.
   const float2 h2 = make_float2(-h, -h), c2 = make_float2(-fmaf(h, entropy, w), -fmaf(h, entropy, w));
