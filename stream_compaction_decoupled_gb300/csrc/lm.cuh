@@ -13,6 +13,7 @@ namespace gbs {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2Low = (float)(0.6931471805599453 - (double)kLn2);  // ln 2 is the two's sum
 
 // ---- element types: all arithmetic is in fp32, each output is rounded once ----------
 
@@ -99,7 +100,11 @@ template <class T, int V> __device__ __forceinline__ Pack<T, V> narrow_pack(cons
   return r;
 }
 
-// ---- approximate functions (PTX instructions, a few units in the last place) ---------
+// ---- approximate functions (PTX instructions) -----------------------------------------
+// The instructions are off by a few units in the last place (ex2: 2.5 units of 2^-24 measured).
+// A function whose argument was rounded first is off by more: 2^(x log2(e)) by 0.7 |x log2(e)|
+// units of 2^-24 besides.
+
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
