@@ -144,6 +144,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
   return float2_of(d);
 }
+// e^d to 4 units of 2^-24, for finite d: 2^y, y = d log2(e) rounded, and what that rounding lost,
+// e^(d - y ln 2) = 1 + (d - y ln 2).
+__device__ __forceinline__ float2 exp_full(float2 d) {
+  const float2 y = mul2(d, make_float2(kLog2e, kLog2e)), e = make_float2(ex2(y.x), ex2(y.y));
+  const float2 lost = fma2(y, make_float2(-kLn2Low, -kLn2Low), fma2(y, make_float2(-kLn2, -kLn2), d));
+  return fma2(e, lost, e);
+}
+// 1/d to a unit of 2^-24 or so, for d of at least 1: the instruction's, and one Newton step.
+__device__ __forceinline__ float2 rcp_full(float2 d) {
+  const float2 r = make_float2(rcp(d.x), rcp(d.y));
+  return fma2(r, fma2(make_float2(-d.x, -d.y), r, make_float2(1.f, 1.f)), r);
+}
 // min / max that keep a NaN operand (fminf and fmaxf drop it).
 __device__ __forceinline__ float min_nan(float a, float b) {
   float y;

@@ -593,14 +593,12 @@ template <class T, int V> __device__ __forceinline__ void lp_grad_hold(Pack<T, V
   }
 }
 
-// e^d = 2^y, y = d log2(e).  y's rounding alone puts it off by up to 8, 15 and 31 units of 2^-24
-// at d = -10, -20 and -40.  A 16-bit output's own rounding (2^-9 or 2^-12) hides that; for fp32
-// e^(d - y ln 2) = 1 + (d - y ln 2) makes up for it.
+// e^d.  2^(d log2 e) with the product rounded once is off by up to 8, 15 and 31 units of 2^-24 at
+// d = -10, -20 and -40: a 16-bit output's own rounding (2^-9 or 2^-12) hides that, fp32's not.
 template <class T> __device__ __forceinline__ float2 lp_exp(float2 d) {
-  const float2 y = mul2(d, make_float2(kLog2e, kLog2e)), e = make_float2(ex2(y.x), ex2(y.y));
-  if constexpr (sizeof(T) == 2) return e;
-  const float2 lost = fma2(y, make_float2(-kLn2Low, -kLn2Low), fma2(y, make_float2(-kLn2, -kLn2), d));
-  return fma2(e, lost, e);
+  if constexpr (sizeof(T) == 4) return exp_full(d);
+  const float2 y = mul2(d, make_float2(kLog2e, kLog2e));
+  return make_float2(ex2(y.x), ex2(y.y));
 }
 
 // fp32: six CTAs an SM, 40 registers (4096 x 32000, 16384 x 4096, 8192 x 1000: 148, 97 and 24.7

@@ -49,28 +49,43 @@
 
 namespace gbs {
 
-// sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z), both to a few units in the last place at
-// either end: e = exp(-z), 1/(1+e) and e/(1+e).  The exponent stops at 2^125, where the
-// first is 0 to fp32 and the second still finite; a NaN stays a NaN.
-__device__ __forceinline__ void sigmoid_both(float z, float& s, float& c) {
-  const float e = ex2(min_nan(-z * kLog2e, 125.f));
-  s = rcp(1.f + e);
-  c = e * s;
-}
-__device__ __forceinline__ void sigmoid_both(float2 z, float2& s, float2& c) {
-  const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
-  const float2 e = make_float2(ex2(min_nan(x.x, 125.f)), ex2(min_nan(x.y, 125.f)));
-  const float2 d = add2(e, make_float2(1.f, 1.f));
-  s = make_float2(rcp(d.x), rcp(d.y));
-  c = mul2(e, s);
+// sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z) of two values, each accurate where it is small.
+// A NaN stays a NaN.
+//
+// fp32: e = e^-|z| to 4 units of 2^-24, 1/(1+e) with a step that makes up for the
+// instruction's error, and e/(1+e).
+//
+// 16-bit gates: e = 2^(-z log2 e) with the product rounded once, 1/(1+e) and e/(1+e), by the
+// instructions alone: up to 8 + 1.3 |z| units of 2^-24, where the gate itself was rounded to 8
+// or 11 bits, which moves either by |z| 2^-9 or |z| 2^-12.  The exponent stops at 2^125, where
+// e/(1+e) is still finite; 1/(1+e) ends there, at 2^-125 in place of 0.
+template <class T> __device__ __forceinline__ void sigmoid_both(float2 z, float2& s, float2& c) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 e = exp_full(make_float2(max_nan(-fabsf(z.x), -104.f), max_nan(-fabsf(z.y), -104.f)));
+    const float2 big = rcp_full(add2(e, make_float2(1.f, 1.f))), small = mul2(e, big);
+    s = make_float2(z.x < 0.f ? small.x : big.x, z.y < 0.f ? small.y : big.y);
+    c = make_float2(z.x < 0.f ? big.x : small.x, z.y < 0.f ? big.y : small.y);
+  } else {
+    const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
+    const float2 e = make_float2(ex2(min_nan(x.x, 125.f)), ex2(min_nan(x.y, 125.f)));
+    const float2 d = add2(e, make_float2(1.f, 1.f));
+    s = make_float2(rcp(d.x), rcp(d.y));
+    c = mul2(e, s);
+  }
 }
 
-// sigmoid(z) alone: exp(-z) may overflow to infinity, which gives 0.
-__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-z * kLog2e)); }
-__device__ __forceinline__ float2 sigmoid(float2 z) {
-  const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
-  const float2 d = add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
-  return make_float2(rcp(d.x), rcp(d.y));
+// sigmoid(z) alone.  16 bits: e may overflow to infinity, which gives 0.
+template <class T> __device__ __forceinline__ float2 sigmoid(float2 z) {
+  const float2 one = make_float2(1.f, 1.f);
+  if constexpr (sizeof(T) == 4) {
+    // e^88 is finite; beyond, the result is below the normal numbers and 0.
+    const float2 d = make_float2(max_nan(min_nan(-z.x, 88.f), -104.f), max_nan(min_nan(-z.y, 88.f), -104.f));
+    return rcp_full(add2(exp_full(d), one));
+  } else {
+    const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
+    const float2 d = add2(make_float2(ex2(x.x), ex2(x.y)), one);
+    return make_float2(rcp(d.x), rcp(d.y));
+  }
 }
 
 template <class T> struct RecArgs {
@@ -425,11 +440,11 @@ __device__ __forceinline__ float2 rec_forward_pass(const RecArgs<T>& a, unsigned
       const float2 xs = rec_pair<T, G>(base, r, rec_offset<T, G>(xo, r, xp, a.xt, r));
       const float2 fs = rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(fo, r, fp, a.ft, r));
       if constexpr (GATE) {
-        av[r] = sigmoid(fs);
-        bv[r] = mul2(sigmoid(rec_pair<T, G>(base + 2 * G::ARRAY, r, rec_offset<T, G>(go, r, gp, a.it, r))), xs);
+        av[r] = sigmoid<T>(fs);
+        bv[r] = mul2(sigmoid<T>(rec_pair<T, G>(base + 2 * G::ARRAY, r, rec_offset<T, G>(go, r, gp, a.it, r))), xs);
       } else {
         float2 u;
-        sigmoid_both(fs, av[r], u);
+        sigmoid_both<T>(fs, av[r], u);
         bv[r] = mul2(u, xs);
       }
     };
@@ -588,7 +603,7 @@ __device__ __forceinline__ float2 rec_backward_pass(const RecArgs<T>& a, unsigne
     auto row = [&](int r) {
       const float2 ds = rec_pair<T, G>(base + G::ARRAY, r, rec_offset<T, G>(dho, r, dhp, a.dht, a.T_ - 1 - r));
       if constexpr (KEEP) kept[r] = ds;
-      sigmoid_both(rec_pair<T, G>(base, r, rec_offset<T, G>(fo, r, fp, a.ft, a.T_ - 1 - r)), s[r], s1[r]);
+      sigmoid_both<T>(rec_pair<T, G>(base, r, rec_offset<T, G>(fo, r, fp, a.ft, a.T_ - 1 - r)), s[r], s1[r]);
       sum = r ? past(r, sum, ds) : ds;
       m = {mul2(m.a, s[r]), drop >> r & 1 ? make_float2(0.f, 0.f) : mul2(s[r], sum)};
     };
@@ -619,7 +634,7 @@ __device__ __forceinline__ float2 rec_backward_pass(const RecArgs<T>& a, unsigne
       const float2 fg = mul2(mul2(s[r], gt), s1[r]);
       if constexpr (GATE) {
         float2 u, u1;
-        sigmoid_both(rec_pair<T, G>(base + 4 * G::ARRAY, r, rec_offset<T, G>(go, r, gp, a.it, a.T_ - 1 - r)), u, u1);
+        sigmoid_both<T>(rec_pair<T, G>(base + 4 * G::ARRAY, r, rec_offset<T, G>(go, r, gp, a.it, a.T_ - 1 - r)), u, u1);
         const float2 ug = mul2(u, gt);
         rec_store<T, G>(ox, ug, n);
         rec_store<T, G>(of, mul2(fg, hs), n);
@@ -712,10 +727,10 @@ __global__ void __launch_bounds__(128) rec_step_kernel(const __grid_constant__ R
     if constexpr (GATE) widen_pack(pi, is);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      float s, u;
-      if constexpr (GATE) s = sigmoid(fs[c]), u = sigmoid(is[c]);
-      else sigmoid_both(fs[c], s, u);
-      out[c] = fmaf(s, out[c], u * xs[c]);
+      float2 s, u;
+      if constexpr (GATE) s = sigmoid<T>(make_float2(fs[c], is[c])), u.x = s.y;
+      else sigmoid_both<T>(make_float2(fs[c], fs[c]), s, u);
+      out[c] = fmaf(s.x, out[c], u.x * xs[c]);
     }
     if constexpr (V == 1) {
       st[0] = out[0];
