@@ -321,6 +321,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, temp=
     _dense(rstd, "rstd", (n,), torch.float32, index)
     if weight is not None:
         pcode = _param(weight, "weight", x.dtype, d, index)
+    if temp is not None and (temp.get_device() != index or not temp.is_contiguous()):
+        raise ValueError("temp must be a contiguous CUDA tensor on device %d" % index)
     return _run(_layer_norm_backward, x, stream, (code, pcode, dy2, x, x2, mean, rstd, weight, bias, temp))
 
 
