@@ -5,7 +5,7 @@ The functions marshal torch tensors into the ``gb_*`` entry points of the same n
 (declared at the end of include/gbscan.h, where the formulas are), as the rest of the
 binding does.  Inputs are fp32, bf16 or fp16 CUDA tensors with unit stride along their
 last dimension and any strides along the others (slices of a fused projection need no
-copy); states and statistics are fp32.  ``autograd`` wraps the same calls for training.
+copy; what layer norm copies, it says); states and statistics are fp32.  ``autograd`` wraps the same calls for training.
 
 A call runs on `stream`, or the current stream.  With an explicit stream its outputs are
 allocated there and its inputs are kept from reuse until the call's kernels have run, but
@@ -257,7 +257,8 @@ def _p(t):
 
 
 def _rows(t, what):
-    """A tensor as rows: 2-D as it is, other shapes as a (rows, cols) view."""
+    """A tensor as rows: 2-D as it is, other shapes as a (rows, cols) view, or None where the
+    leading dimensions do not merge into rows of one stride."""
     if t.dim() == 2:
         return t
     if t.dim() == 0:
@@ -265,7 +266,12 @@ def _rows(t, what):
     try:
         return t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
     except RuntimeError:
-        raise ValueError("%s must be 2-D, or have leading dimensions that merge into rows" % what) from None
+        return None
+
+
+def _laid_out(t, t2):
+    """The rows t2 of t, copied where t has none (on the stream that is current)."""
+    return t.contiguous().view(-1, t.shape[-1]) if t2 is None else t2
 
 
 def _param(p, what, dtype, d, index):
@@ -277,24 +283,29 @@ def _param(p, what, dtype, d, index):
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
     """Layer norm over the last dimension: (y, mean, rstd), mean and rstd fp32 with one
-    entry a row.  weight and bias: of x's type or fp32, or None."""
+    entry a row.  weight and bias: of x's type or fp32, or None.  x may have any leading
+    dimensions: where they do not merge into rows of one stride (x[:, 1:] of three
+    dimensions) it is copied first.  Those of `out` must merge."""
     x2 = _rows(x, "x")
-    code = pcode = _first(x2, "x", 2, "rows")
-    d, index = x2.shape[1], x2.get_device()
+    code = pcode = _first(x, "x", x.dim(), "rows")
+    d, index = x.shape[-1], x.get_device()
     if weight is not None:
         pcode = _param(weight, "weight", x.dtype, d, index)
     if bias is not None:
         pcode = _param(bias, "bias", x.dtype, d, index)
         if weight is not None and weight.dtype is not bias.dtype:
             raise TypeError("weight and bias must have the same type")
-    if d == 0 and x2.shape[0]:
+    if d == 0 and (x2 is None or x2.shape[0]):
         raise ValueError("x must have at least one column")
     if out is not None:
         _out(out, "out", x.shape, x.dtype, index)
+        if _rows(out, "out") is None:
+            raise ValueError("out must be 2-D, or have leading dimensions that merge into rows")
     return _run(_layer_norm, x, stream, (code, pcode, x, x2, weight, bias, eps, out))
 
 
 def _layer_norm(s, code, pcode, x, x2, weight, bias, eps, out):
+    x2 = _laid_out(x, x2)
     (n, d), dev = x2.shape, x2.device
     if out is None:
         out, y_stride = torch.empty(x.shape, dtype=x.dtype, device=dev), d
@@ -312,21 +323,26 @@ def _layer_norm(s, code, pcode, x, x2, weight, bias, eps, out):
 def layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, temp=None, stream=None):
     """Gradient of layer_norm() from its input and its mean and rstd: (dx, dweight,
     dbias), the last two of weight's type (None without a weight; dbias None too with
-    bias=False)."""
+    bias=False).  x and dy may have any leading dimensions, as layer_norm()'s x."""
     x2, dy2 = _rows(x, "x"), _rows(dy, "dy")
-    code = pcode = _first(x2, "x", 2, "rows")
-    (n, d), index = x2.shape, x2.get_device()
-    _rows_like(dy2, "dy", x2.shape, x.dtype, index)
+    code = pcode = _first(x, "x", x.dim(), "rows")
+    d, index = x.shape[-1], x.get_device()
+    n = x.numel() // d if x2 is None else x2.shape[0]
+    if dy2 is None:  # checked as rows that it does not have: by its own shape
+        _rows_like(dy, "dy", x.shape, x.dtype, index)
+    else:
+        _rows_like(dy2, "dy", torch.Size((n, d)), x.dtype, index)
     _dense(mean, "mean", (n,), torch.float32, index)
     _dense(rstd, "rstd", (n,), torch.float32, index)
     if weight is not None:
         pcode = _param(weight, "weight", x.dtype, d, index)
     if temp is not None and (temp.get_device() != index or not temp.is_contiguous()):
         raise ValueError("temp must be a contiguous CUDA tensor on device %d" % index)
-    return _run(_layer_norm_backward, x, stream, (code, pcode, dy2, x, x2, mean, rstd, weight, bias, temp))
+    return _run(_layer_norm_backward, x, stream, (code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp))
 
 
-def _layer_norm_backward(s, code, pcode, dy2, x, x2, mean, rstd, weight, bias, temp):
+def _layer_norm_backward(s, code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp):
+    x2, dy2 = _laid_out(x, x2), _laid_out(dy, dy2)
     (n, d), dev, lib = x2.shape, x2.device, load()
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dw = db = None
