@@ -6,7 +6,9 @@ gradient calls of lm.py joined, so that they can stand in a module's forward pas
     logprob, entropy = autograd.token_logprobs(logits, targets)
 
 All compute is in the library's kernels, forward and backward; gradients are
-deterministic, and cannot be differentiated again.  The backward calls run on the stream that torch's autograd makes current,
+deterministic, and cannot be differentiated again.  The gradients of a recurrence's inputs
+come from one pass together, and layer norm's dx always; its weight's and bias's only where
+they are asked for.  The backward calls run on the stream that torch's autograd makes current,
 which is the forward call's.
 """
 from __future__ import annotations
@@ -54,9 +56,10 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, mean, rstd = ctx.saved_tensors
         dy = dy if dy.is_contiguous() else dy.contiguous()
-        scale = weight if weight is not None or bias is None else torch.ones_like(bias)
-        dx, dw, db = lm.layer_norm_backward(dy, x, mean, rstd, scale, bias=bias is not None)
-        return dx, dw if weight is not None else None, db, None
+        _, dweight, dbias, _ = ctx.needs_input_grad  # frozen parameters cost no sums over rows
+        scale = weight if weight is not None or not dbias else torch.ones_like(bias)
+        dx, dw, db = lm.layer_norm_backward(dy, x, mean, rstd, scale, bias=dbias, dweight=dweight)
+        return dx, dw, db, None
 
 
 class _TokenLogprobs(torch.autograd.Function):

@@ -320,10 +320,11 @@ def _layer_norm(s, code, pcode, x, x2, weight, bias, eps, out):
     return out, mean, rstd
 
 
-def layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, temp=None, stream=None):
+def layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, temp=None, stream=None,
+                        dweight: bool = True):
     """Gradient of layer_norm() from its input and its mean and rstd: (dx, dweight,
-    dbias), the last two of weight's type (None without a weight; dbias None too with
-    bias=False).  x and dy may have any leading dimensions, as layer_norm()'s x."""
+    dbias), the last two of weight's type (None without a weight, and each None
+    where `bias` or `dweight` is False; without both there are no sums over rows).  x and dy may have any leading dimensions, as layer_norm()'s x."""
     x2, dy2 = _rows(x, "x"), _rows(dy, "dy")
     code = pcode = _first(x, "x", x.dim(), "rows")
     d, index = x.shape[-1], x.get_device()
@@ -338,19 +339,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, bias: bool = True, temp=
         pcode = _param(weight, "weight", x.dtype, d, index)
     if temp is not None and (temp.get_device() != index or not temp.is_contiguous()):
         raise ValueError("temp must be a contiguous CUDA tensor on device %d" % index)
-    return _run(_layer_norm_backward, x, stream, (code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp))
+    return _run(_layer_norm_backward, x, stream, (code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp, dweight))
 
 
-def _layer_norm_backward(s, code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp):
+def _layer_norm_backward(s, code, pcode, dy, dy2, x, x2, mean, rstd, weight, bias, temp, dweight):
     x2, dy2 = _laid_out(x, x2), _laid_out(dy, dy2)
     (n, d), dev, lib = x2.shape, x2.device, load()
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dw = db = None
     tb = 0
-    if weight is None:
+    if weight is None or not (dweight or bias):
         temp = None
     else:
-        dw = torch.empty((d,), dtype=weight.dtype, device=dev)
+        if dweight:
+            dw = torch.empty((d,), dtype=weight.dtype, device=dev)
         if bias:
             db = torch.empty((d,), dtype=weight.dtype, device=dev)
         if temp is None:

@@ -85,3 +85,30 @@ def test_refused_shapes():
             bad()
     assert gb.layer_norm(torch.zeros((0, 4, 32), device="cuda"))[0].shape == (0, 4, 32)
     assert gb.layer_norm(torch.zeros((2, 5, 32), device="cuda")[:, :0])[0].shape == (2, 0, 32)
+
+
+@pytest.mark.parametrize("dweight", [True, False])
+@pytest.mark.parametrize("dbias", [True, False])
+def test_only_the_gradients_that_are_asked_for(monkeypatch, dweight, dbias):
+    from stream_compaction_decoupled_gb300 import autograd, lm
+    g = torch.Generator().manual_seed(3)
+    x, w, b = (torch.randn(s, generator=g).cuda() for s in ((700, 96), (96,), (96,)))
+    c = torch.randn((700, 96), generator=g).cuda()
+    _, mean, rstd = gb.layer_norm(x, w, b)
+    want = gb.layer_norm_backward(c, x, mean, rstd, w)
+    got = gb.layer_norm_backward(c, x, mean, rstd, w, bias=dbias, dweight=dweight)
+    for p, q, on in zip(got, want, (True, dweight, dbias)):
+        assert torch.equal(p, q) if on else p is None
+    seen = []
+    whole = lm.layer_norm_backward
+    monkeypatch.setattr(lm, "layer_norm_backward", lambda *a, **k: seen.append(k) or whole(*a, **k))
+    leaves = [t.clone().requires_grad_(on) for t, on in ((x, True), (w, dweight), (b, dbias))]
+    (autograd.layer_norm(*leaves) * c).sum().backward()
+    assert seen == [{"bias": dbias, "dweight": dweight}]
+    for t, q, on in zip(leaves, want, (True, dweight, dbias)):
+        assert torch.equal(t.grad, q) if on else t.grad is None
+    # A bias alone.
+    leaves = [x.clone().requires_grad_(), b.clone().requires_grad_(dbias)]
+    (autograd.layer_norm(leaves[0], None, leaves[1]) * c).sum().backward()
+    assert torch.equal(leaves[1].grad, want[2]) if dbias else leaves[1].grad is None
+    assert torch.equal(leaves[0].grad, gb.layer_norm_backward(c, x, mean, rstd)[0])
