@@ -14,6 +14,10 @@
  *         large element types": tiles sized per element type; ScanPrefixes,
  *         SliceScan along `dims`, findall.
  *
+ * The library is linked with the shared CUDA runtime (libcudart.so of the toolkit it was
+ * built with, found by its path there): a process that has that library loaded, as one with
+ * PyTorch does, runs both on the same one.
+ *
  * Conventions shared by every call:
  *   - All data pointers (in, out, out_idx, counts, offsets, records, out_count,
  *     out_total, temp) are DEVICE pointers owned by the caller.  `init` and

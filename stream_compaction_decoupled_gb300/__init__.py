@@ -85,7 +85,13 @@ def load(path: str = LIB_PATH):
     if _lib is None:
         if not os.path.exists(path):
             raise RuntimeError("libgbscan.so is not built (%s); run __graft_entry__.build()" % path)
-        lib = ctypes.CDLL(path)
+        try:
+            lib = ctypes.CDLL(path)
+        except OSError:
+            # The library needs the shared CUDA runtime: where the toolkit's, which it was
+            # linked with, has gone, the one that torch brings and loads serves.
+            import torch  # noqa: F401
+            lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             f = getattr(lib, name)
             f.restype = res
