@@ -151,11 +151,6 @@ __device__ __forceinline__ float2 exp_full(float2 d) {
   const float2 lost = fma2(y, make_float2(-kLn2Low, -kLn2Low), fma2(y, make_float2(-kLn2, -kLn2), d));
   return fma2(e, lost, e);
 }
-// 1/d to a unit of 2^-24 or so, for d of at least 1: the instruction's, and one Newton step.
-__device__ __forceinline__ float2 rcp_full(float2 d) {
-  const float2 r = make_float2(rcp(d.x), rcp(d.y));
-  return fma2(r, fma2(make_float2(-d.x, -d.y), r, make_float2(1.f, 1.f)), r);
-}
 // min / max that keep a NaN operand (fminf and fmaxf drop it).
 __device__ __forceinline__ float min_nan(float a, float b) {
   float y;

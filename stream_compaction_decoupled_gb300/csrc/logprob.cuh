@@ -35,10 +35,12 @@
 // Rows start anywhere: packs of 16 bytes are laid over the row from the boundary below its
 // first value, and values outside the row or the slice count as masked.
 //
-// Measured (GB300, copy rate 6.8 TB/s): 4096 x 128000 bf16 160 us without alternatives (6.5
+// Measured (GB300, copy rate 6.8 TB/s): 4096 x 128000 bf16 158.5 us without alternatives (6.6
 // TB/s, HBM), 205 with 8 and 253 with 32 (5.1 and 4.1 TB/s, issue); 7 x 50021 fp32 with 20
 // alternatives 12.6 us, the latency of threshold, selection and merge; the gradient of 4096
-// x 32000 bf16 98.8 us (5.3 TB/s, half of it writes).
+// x 32000 bf16 97.8 us (5.4 TB/s, half of it writes).  Rows that rise along the vocabulary, whose
+// list overflows in every tile: 4096 x 32000 bf16 with 8 alternatives 911 us, where rows in no
+// order take 85.
 #pragma once
 
 #include <cfloat>

@@ -33,12 +33,14 @@
 // h_{t-1} as 0 in df_t.  0 times an infinity or a NaN does not drop it, though.  It makes a
 // NaN, and what is not finite then never leaves the state again, in any order of composition:
 // the state after the last row tells.  Where that is not finite and there are starts, the
-// strip is gone through a second time (EXACT), its maps dropping the state by selection.
+// strip is gone through a second time (EXACT), its maps dropping the state by selection (8 x
+// 2048 x 2048 bf16 gated with a NaN in every channel 108 us in place of 50.6, gradient 167 in
+// place of 85.8).
 //
-// Measured (GB300, copy rate 6.8 TB/s): 8 x 2048 x 2048 bf16 with i 49.8 us (5.4 TB/s), its
-// gradient 85.1 us (6.3 TB/s); 1 x 65536 x 2048 249 us (4.3 TB/s); gradient of 3 x 1537 x
-// 1001 fp32 without i 26.7 us (4.2 TB/s).  The gradient runs at the memory's rate; forward,
-// the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
+// Measured (GB300, copy rate 6.8 TB/s): 8 x 2048 x 2048 bf16 with i and starts 50.3 us (5.3
+// TB/s), its gradient 86.8 us (6.2 TB/s); 1 x 65536 x 2048 254.7 us (4.2 TB/s); gradient of 3 x
+// 1537 x 1001 fp32 without i 28.7 us (3.9 TB/s).  The gradient runs at the memory's rate;
+// forward, the latency of a round (wait, compose, exchange, replay) shows, more so in a cluster.
 #pragma once
 
 #include <cmath>
@@ -52,8 +54,10 @@ namespace gbs {
 // sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z) of two values, each accurate where it is small.
 // A NaN stays a NaN.
 //
-// fp32: e = e^-|z| to 4 units of 2^-24, 1/(1+e) with a step that makes up for the
-// instruction's error, and e/(1+e).
+// fp32: e = e^-|z| to 4 units of 2^-24, 1/(1+e) by the instruction, 2 units, and e/(1+e): within
+// 8 units from end to end, and 0 and 1 at the ends.
+// (8 x 2048 x 2048 gated 82.6 us, by the instructions alone 82.7; 1 x 16384 x 2048 107.3 and
+// 103.5.)
 //
 // 16-bit gates: e = 2^(-z log2 e) with the product rounded once, 1/(1+e) and e/(1+e), by the
 // instructions alone: up to 8 + 1.3 |z| units of 2^-24, where the gate itself was rounded to 8
@@ -62,7 +66,7 @@ namespace gbs {
 template <class T> __device__ __forceinline__ void sigmoid_both(float2 z, float2& s, float2& c) {
   if constexpr (sizeof(T) == 4) {
     const float2 e = exp_full(make_float2(max_nan(-fabsf(z.x), -104.f), max_nan(-fabsf(z.y), -104.f)));
-    const float2 big = rcp_full(add2(e, make_float2(1.f, 1.f))), small = mul2(e, big);
+    const float2 d = add2(e, make_float2(1.f, 1.f)), big = make_float2(rcp(d.x), rcp(d.y)), small = mul2(e, big);
     s = make_float2(z.x < 0.f ? small.x : big.x, z.y < 0.f ? small.y : big.y);
     c = make_float2(z.x < 0.f ? big.x : small.x, z.y < 0.f ? big.y : small.y);
   } else {
@@ -79,8 +83,9 @@ template <class T> __device__ __forceinline__ float2 sigmoid(float2 z) {
   const float2 one = make_float2(1.f, 1.f);
   if constexpr (sizeof(T) == 4) {
     // e^88 is finite; beyond, the result is below the normal numbers and 0.
-    const float2 d = make_float2(max_nan(min_nan(-z.x, 88.f), -104.f), max_nan(min_nan(-z.y, 88.f), -104.f));
-    return rcp_full(add2(exp_full(d), one));
+    const float2 x = make_float2(max_nan(min_nan(-z.x, 88.f), -104.f), max_nan(min_nan(-z.y, 88.f), -104.f));
+    const float2 d = add2(exp_full(x), one);
+    return make_float2(rcp(d.x), rcp(d.y));
   } else {
     const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
     const float2 d = add2(make_float2(ex2(x.x), ex2(x.y)), one);
@@ -155,8 +160,8 @@ __device__ __forceinline__ float4 rec_pack(RecMap m) { return make_float4(m.a.x,
 __device__ __forceinline__ RecMap rec_unpack(float4 q) { return {make_float2(q.x, q.y), make_float2(q.z, q.w)}; }
 
 // What threads exchange, in turn over the rounds.  Two slots would do for the CTAs' maps;
-// with four the round loop is faster (8 x 2048 x 2048 bf16 gated, gradient: 94.0 us with
-// two, 86.1 with four; 1 x 65536 x 2048: 263.8 and 248.8).
+// with four the round loop is faster (8 x 2048 x 2048 bf16 gated, gradient: 84.8 us with
+// two, 78.4 with four; 1 x 65536 x 2048: 268 and 253, gradient 405 and 364).
 constexpr int kRecSlots = 4;
 struct RecShared {
   float4 warp[2][8][32];                      // the map of each warp's rows
@@ -222,8 +227,8 @@ template <class T, class G> __device__ __forceinline__ unsigned rec_offset(const
 }
 
 // With four rows a warp the offsets are kept in 16 bits, row r at t + dir r; eight are as
-// soon worked out each time (1 x 16384 x 2001 gated, gradient: fp32 209 us worked out and
-// 197 kept, bf16 155 and 160).
+// soon worked out each time (1 x 16384 x 2001 gated, gradient, when this was chosen: fp32 209
+// us worked out and 197 kept, bf16 155 and 160).
 template <class T, class G> __device__ __forceinline__ unsigned rec_keep(const T* strip, long long st, int t, int dir) {
   unsigned kept = 0;
   if constexpr (G::EDGE && sizeof(T) == 4) {
@@ -770,10 +775,10 @@ template <class T> RecArgs<T> rec_args(const RecurrenceJob& j) {
 // CTAs per cluster.  The strips take as many waves as the clusters that are resident at once
 // leave; a wave lasts as long as its rounds (and one to fill the pipeline), and a round
 // longer the more CTAs exchange their maps.  The estimate's least is taken.  Measured, both
-// directions gated, 5 batch rows of 1500: 60 strips (bf16) 15.2 and 24.1 us in fours, 19.1
-// and 25.1 in fives, of which not all are resident; 155 strips 36.2 and 55.9 alone, 38.1 and
-// 53.7 in pairs, 33.7 and 47.9 in threes; 255 strips 37.1 and 57.9 alone, 45.1 and 66.8 in
-// pairs; 320 strips (fp32) 99.7 and 174 alone, 93.0 and 155 in pairs.
+// directions gated, 5 batch rows of 1500: 60 strips (bf16) 14.1 and 19.2 us in fours, 19.7
+// and 25.3 in fives, of which not all are resident; 155 strips 36.6 and 56.1 alone, 39.5 and
+// 54.5 in pairs, 35.0 and 48.9 in threes; 255 strips 37.6 and 58.5 alone, 46.4 and 67.8 in
+// pairs; 320 strips (fp32) 101 and 173 alone, 99.4 and 158 in pairs.
 template <class F> unsigned rec_cluster(long long strips, long long tiles, F&& resident) {
   unsigned best = 1;
   double least = 0;
