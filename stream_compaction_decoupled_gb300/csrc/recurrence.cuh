@@ -610,7 +610,10 @@ __device__ __forceinline__ float2 rec_backward_pass(const RecArgs<T>& a, unsigne
       if constexpr (KEEP) kept[r] = ds;
       sigmoid_both<T>(rec_pair<T, G>(base, r, rec_offset<T, G>(fo, r, fp, a.ft, a.T_ - 1 - r)), s[r], s1[r]);
       sum = r ? past(r, sum, ds) : ds;
-      m = {mul2(m.a, s[r]), drop >> r & 1 ? make_float2(0.f, 0.f) : mul2(s[r], sum)};
+      // Dropped by the last row too, what is not finite stays in the first pass's map, as above.
+      const bool dropped = drop >> r & 1;
+      const float2 zero = make_float2(0.f, 0.f);
+      m = {mul2(m.a, s[r]), EXACT && dropped ? zero : mul2(!EXACT && dropped ? zero : s[r], sum)};
     };
     if (rows >= R) {
 #pragma unroll

@@ -140,3 +140,38 @@ def test_what_is_not_finite_stays_to_the_end_of_its_document(size, dt, gate):
     nan[:, t - 1, ::2] = True
     assert torch.equal(torch.isnan(h), nan) and torch.equal(h[~nan], want[~nan])
     assert torch.isnan(last[:, ::2]).all() and torch.equal(last[:, 1::2], wlast[:, 1::2])
+
+
+@pytest.mark.parametrize("gate", [False, True], ids=["tied", "gated"])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("often", [0.05, 0.3, 0.7])
+@pytest.mark.parametrize("t,d", [(5, 8), (9, 16), (40, 40), (70, 72), (257, 260), (300, 303)])
+def test_every_token_and_every_placing_of_starts(t, d, often, dt, gate):
+    """Channel j has a NaN at token j (of x, then of dh): what follows it, or comes before it, to
+    the next start is not finite, and everything else is as without."""
+    b = 4
+    x, f, i, h0, dh, dlast = make(b, t, d, DT[dt], gate, t + d)
+    g = torch.Generator().manual_seed(d)
+    starts = (torch.rand((b, t), generator=g) < often).to(torch.uint8).cuda()
+    document = starts.long().cumsum(1)  # of each token
+    n = min(t, d)
+    token, at = torch.arange(t, device="cuda")[:, None], torch.arange(n, device="cuda")
+    same_document = document[:, :, None] == document[:, None, :n]  # (batch, token, channel's token)
+    want, wlast = gb.recurrence(x, f, i, h0=h0, starts=starts)
+    x2 = x.clone()
+    x2[:, at, at] = NAN
+    h, last = gb.recurrence(x2, f, i, h0=h0, starts=starts)
+    nan = torch.zeros_like(h, dtype=torch.bool)
+    nan[:, :, :n] = same_document & (token >= at)
+    assert torch.equal(torch.isnan(h), nan) and torch.equal(h[~nan], want[~nan])
+    assert torch.equal(torch.isnan(last), nan[:, -1]) and torch.equal(last[~nan[:, -1]], wlast[~nan[:, -1]])
+    wants = gb.recurrence_backward(dh, x, f, want, i, h0=h0, starts=starts, dlast=dlast)
+    dh2 = dh.clone()
+    dh2[:, at, at] = NAN
+    grads = gb.recurrence_backward(dh2, x, f, want, i, h0=h0, starts=starts, dlast=dlast)
+    nan[:, :, :n] = same_document & (token <= at)
+    for p, q in zip(grads[:3], wants):
+        if q is not None:
+            assert torch.equal(torch.isnan(p), nan) and torch.equal(p[~nan], q[~nan])
+    first = nan[:, 0] & (starts[:, 0] == 0)[:, None]
+    assert torch.equal(torch.isnan(grads[3]), first) and torch.equal(grads[3][~first], wants[3][~first])
