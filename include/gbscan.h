@@ -374,8 +374,9 @@ void gb_set_stalled_tile(int64_t tile);
 
 /* ---- Language-model operators ------------------------------------------------------
  *
- * The gated linear recurrence (a scan of affine maps over time), layer norm, and log
- * probabilities of given tokens, each with its gradient.  dtype is GB_F32, GB_BF16 or
+ * The gated linear recurrence (a scan of affine maps over time), layer norm, log
+ * probabilities of given tokens, a short causal convolution and the selective state space
+ * scan, each with its gradient, and the verification of drafted tokens.  dtype is GB_F32, GB_BF16 or
  * GB_F16; all arithmetic, states, statistics and sums are fp32, and each output of a
  * 16-bit type is rounded once, to nearest even.  Results do not vary from run to run.
  *
@@ -492,6 +493,135 @@ int gb_token_logprobs_backward(int dtype, int64_t rows, int64_t vocab, const voi
                                const void* targets, int target_dtype, const float* lse, const float* entropy,
                                const float* dlogprob, const float* dentropy, void* dlogits, int64_t dstride,
                                void* stream);
+
+/*
+ * Short causal convolution of each channel over time of a (batch, length, channels) array:
+ *   p_t = bias + sum_k w_k x_{t-taps+1+k},   y_t = p_t sigmoid(p_t), or p_t with silu = 0.
+ * Inputs before token 0 come from `state`, those before a document's start count as zero.
+ *   param_dtype   of w and bias (dtype or GB_F32)
+ *   taps          1 .. 8
+ *   strides       host array (batch, time) of x, y, or NULL: contiguous
+ *   w, bias       (channels, taps) and (channels), contiguous; bias may be NULL: 0
+ *   state         (batch, taps - 1, channels), contiguous, the newest input last, or NULL: zero
+ *   starts        as in gb_recurrence
+ *   last          (batch, taps - 1, channels), contiguous, or NULL: the state after the last
+ *                 token (zero before the last document's start)
+ * GB_ERR_UNSUPPORTED for more than 8 taps.
+ */
+int gb_causal_conv(int dtype, int param_dtype, int64_t batch, int64_t length, int64_t channels, int taps,
+                   const void* x, const int64_t* strides, const void* w, const void* bias, int silu,
+                   const void* state, const uint8_t* starts, void* y, void* last, void* stream);
+
+/*
+ * Its gradient.  dy is the gradient of y, dlast that of `last` (NULL: 0).
+ *   strides   host array (batch, time) of dy, x, dx, or NULL: contiguous
+ *   dw, db    like w and bias, or NULL: not computed
+ *   dstate    (batch, taps - 1, channels), contiguous, or NULL: the gradient of state
+ *   temp      scratch of gb_causal_conv_temp_bytes(...) bytes, 256-byte aligned, or NULL (see
+ *             the conventions); not used where dw and db are NULL
+ */
+int gb_causal_conv_backward(int dtype, int param_dtype, int64_t batch, int64_t length, int64_t channels, int taps,
+                            const void* dy, const void* x, const int64_t* strides, const void* w, const void* bias,
+                            int silu, const void* state, const uint8_t* starts, const void* dlast, void* dx, void* dw,
+                            void* db, void* dstate, void* temp, size_t temp_bytes, void* stream);
+size_t gb_causal_conv_temp_bytes(int64_t batch, int64_t length, int64_t channels, int taps);
+
+/*
+ * One token for each of `batch` rows: row b convolves x_b with the inputs in state s = slots[b]
+ * of the pool, which then drops its oldest and takes x_b.
+ *   strides   host array (row strides) of x, y, or NULL: contiguous
+ *   state     (pool, taps - 1, channels), contiguous, the newest input last, updated in place
+ *   slots     as in gb_recurrence_step
+ */
+int gb_causal_conv_step(int dtype, int param_dtype, int64_t batch, int64_t channels, int taps, const void* x,
+                        const int64_t* strides, const void* w, const void* bias, int silu, void* state, int64_t pool,
+                        const int32_t* slots, void* y, void* stream);
+
+/*
+ * Selective state space scan over time of a (batch, length, channels) array, with `states`
+ * (1 .. 128) states h a channel:
+ *   D_t = softplus(dt_t + dt_bias), or dt_t + dt_bias with softplus = 0,
+ *   h_t = exp(D_t a) h_{t-1} + D_t x_t b_t,   h_{-1} = h0, or 0,
+ *   y_t = (sum over states of c_t h_t + d x_t) z_t sigmoid(z_t), without the last factor
+ *   where z is NULL.
+ * b and c are (batch, length, groups, states); channel k uses group k / (channels / groups).
+ *   a             (channels, states) fp32, contiguous
+ *   d, dt_bias    (channels) fp32, or NULL: 0
+ *   strides       host array: (batch, time) of x, dt, z, y, then (batch, time, group) of b, c;
+ *                 or NULL: contiguous
+ *   h0            (batch, channels, states) fp32, contiguous, or NULL: zero
+ *   starts        as in gb_recurrence
+ *   last          (batch, channels, states) fp32, contiguous, or NULL: the state after the last
+ *                 token, unrounded
+ *   kept          (batch, ceil(length / 16), channels, states) fp32, contiguous, or NULL: the
+ *                 state before every 16th token, which the gradient needs
+ *   temp          scratch of gb_selective_scan_temp_bytes(..., 0) bytes (0: none is needed),
+ *                 256-byte aligned, or NULL (see the conventions)
+ * exp(D_t a) is off by (4 + 2 |D_t a|) 2^-24 relative (its argument's rounding).
+ * GB_ERR_RANGE for more than 128 states.
+ */
+int gb_selective_scan(int dtype, int64_t batch, int64_t length, int64_t channels, int64_t states, int64_t groups,
+                      const void* x, const void* dt, const float* a, const void* b, const void* c, const float* d,
+                      const void* z, const float* dt_bias, int softplus, const int64_t* strides, const float* h0,
+                      const uint8_t* starts, void* y, float* last, float* kept, void* temp, size_t temp_bytes,
+                      void* stream);
+size_t gb_selective_scan_temp_bytes(int64_t batch, int64_t length, int64_t channels, int64_t states, int64_t groups,
+                                    int backward);
+
+/*
+ * Its gradient, from the inputs and what the forward call kept.
+ *   strides   host array: (batch, time) of dy, x, dt, z, dx, ddt, dz, then (batch, time, group)
+ *             of b, c, db, dc; or NULL: contiguous
+ *   dlast     (batch, channels, states) fp32, contiguous, or NULL: 0
+ *   dx, ddt, dz, db, dc   like x, dt, z, b, c; dz is required with z and ignored without
+ *   da        (channels, states) fp32; dd, ddt_bias (channels) fp32 or NULL: not written
+ *   dh0       (batch, channels, states) fp32, contiguous, or NULL: the gradient of h0
+ *   temp      scratch of gb_selective_scan_temp_bytes(..., 1) bytes, 256-byte aligned, or NULL
+ */
+int gb_selective_scan_backward(int dtype, int64_t batch, int64_t length, int64_t channels, int64_t states,
+                               int64_t groups, const void* dy, const void* x, const void* dt, const float* a,
+                               const void* b, const void* c, const float* d, const void* z, const float* dt_bias,
+                               int softplus, const int64_t* strides, const float* kept, const uint8_t* starts,
+                               const float* dlast, void* dx, void* ddt, float* da, void* db, void* dc, float* dd,
+                               void* dz, float* ddt_bias, float* dh0, void* temp, size_t temp_bytes, void* stream);
+
+/*
+ * One token for each of `batch` rows: row b moves state s = slots[b] of the pool on.
+ *   strides   host array: row strides of x, dt, z, y, then (row, group) of b, c; or NULL:
+ *             contiguous
+ *   state     (pool, channels, states) fp32, contiguous, updated in place
+ *   slots     as in gb_recurrence_step
+ */
+int gb_selective_scan_step(int dtype, int64_t batch, int64_t channels, int64_t states, int64_t groups, const void* x,
+                           const void* dt, const float* a, const void* b, const void* c, const float* d, const void* z,
+                           const float* dt_bias, int softplus, const int64_t* strides, float* state, int64_t pool,
+                           const int32_t* slots, void* y, void* stream);
+
+/*
+ * Verification of drafted tokens: row b has lengths[b] drafts d_i, which the target's
+ * probabilities p_i (the row after i drafts) accept or not, from given random numbers.
+ *   Draft i is accepted while accept_i q_i(d_i) < p_i(d_i), q_i the drafter's probabilities.  At
+ *   the first that is not, n, the token is drawn from r_j = max(p_n(j) - q_n(j), 0); after all
+ *   of them from r = p_n, n = lengths[b].  Drawn: the smallest j with
+ *   r_0 + ... + r_j > sample (r_0 + ... + r_{vocab-1}), sums as in 64 bits.
+ *   dtype         of target and draft
+ *   tokens        (batch, drafts) of GB_I32 or GB_I64 (token_dtype), contiguous
+ *   target        (batch, drafts + 1, vocab) probabilities
+ *   draft         (batch, drafts, vocab), or NULL: the drafts are certain (q_i(d_i) = 1, and d_n
+ *                 is left out of the draw)
+ *   strides       host array (batch, draft) of target, draft, or NULL: contiguous
+ *   accept        (batch, drafts) fp32 and sample (batch) fp32, contiguous, in [0, 1)
+ *   lengths       (batch) int32, 0 .. drafts, or NULL: drafts everywhere
+ *   accepted      (batch) int32: n, how many drafts are accepted
+ *   out           (batch, drafts + 1) int32, contiguous: the n accepted drafts, the token drawn,
+ *                 and -1 behind it
+ * Probabilities need not sum to 1; negative ones and NaNs count as 0.  Where r is 0 everywhere
+ * the token is -1.  A length outside 0 .. drafts is taken as the nearest within, a draft outside
+ * the vocabulary is not accepted; both are reported as GB_ERR_RANGE by gb_device_error.
+ */
+int gb_verify_drafts(int dtype, int64_t batch, int64_t drafts, int64_t vocab, const void* tokens, int token_dtype,
+                     const void* target, const void* draft, const int64_t* strides, const float* accept,
+                     const float* sample, const int32_t* lengths, int32_t* accepted, int32_t* out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 """Device-wide prefix sums and stream compaction for the GB300 (sm_103a),
 with the language-model operators that are scans, selections and reductions beside them
-(``recurrence``, ``layer_norm``, ``token_logprobs`` and their gradients, in lm.py).
+(``recurrence``, ``layer_norm``, ``token_logprobs`` and their gradients, in lm.py;
+``causal_conv``, ``selective_scan``, their gradients, and ``verify_drafts``, in ssm.py).
 
 A thin binding over the C ABI of ``libgbscan.so`` (declared in include/gbscan.h):
 every function marshals torch tensors into device pointers, sizes and the current
@@ -65,6 +66,15 @@ SIGNATURES = {
     "gb_layer_norm_temp_bytes": (_sz, [_i64, _i64]),
     "gb_token_logprobs": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
     "gb_token_logprobs_backward": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "gb_causal_conv": (_i, [_i, _i, _i64, _i64, _i64, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp]),
+    "gb_causal_conv_backward": (_i, [_i, _i, _i64, _i64, _i64, _i, _vp, _vp, _vp, _vp, _vp, _i] + [_vp] * 8 + [_sz, _vp]),
+    "gb_causal_conv_temp_bytes": (_sz, [_i64, _i64, _i64, _i]),
+    "gb_causal_conv_step": (_i, [_i, _i, _i64, _i64, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64, _vp, _vp, _vp]),
+    "gb_selective_scan": (_i, [_i] + [_i64] * 5 + [_vp] * 8 + [_i] + [_vp] * 7 + [_sz, _vp]),
+    "gb_selective_scan_backward": (_i, [_i] + [_i64] * 5 + [_vp] * 9 + [_i] + [_vp] * 14 + [_sz, _vp]),
+    "gb_selective_scan_temp_bytes": (_sz, [_i64] * 5 + [_i]),
+    "gb_selective_scan_step": (_i, [_i] + [_i64] * 4 + [_vp] * 8 + [_i, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "gb_verify_drafts": (_i, [_i, _i64, _i64, _i64, _vp, _i] + [_vp] * 9),
 }
 
 _lib = None
@@ -390,16 +400,20 @@ def scan_segmented(x, flags, op: str = "add", inclusive: bool = True, init=None,
     return out
 
 
-# The language-model operators (lm.py) are looked up on first use: they import torch,
+# The language-model operators (lm.py, ssm.py) are looked up on first use: they import torch,
 # which this module itself does not.
-_LM = ("recurrence", "recurrence_backward", "recurrence_step", "layer_norm", "layer_norm_backward",
-       "token_logprobs", "token_logprobs_backward", "TokenLogprobs")
+_LM = {"lm": ("recurrence", "recurrence_backward", "recurrence_step", "layer_norm", "layer_norm_backward",
+              "token_logprobs", "token_logprobs_backward", "TokenLogprobs"),
+       "ssm": ("causal_conv", "causal_conv_backward", "causal_conv_step", "selective_scan", "selective_scan_backward",
+               "selective_scan_step", "SelectiveScanGrads", "verify_drafts", "Verified")}
 
 
 def __getattr__(name):
-    if name in _LM:
-        from . import lm
-        for n in _LM:
-            globals()[n] = getattr(lm, n)
-        return globals()[name]
+    for module, names in _LM.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,14 +1,16 @@
 """The language-model operators as differentiable torch functions: the forward and
-gradient calls of lm.py joined, so that they can stand in a module's forward pass.
+gradient calls of lm.py and ssm.py joined, so that they can stand in a module's forward pass.
 
     h, last = autograd.recurrence(x, f, i, h0, starts)
     y = autograd.layer_norm(x, weight, bias)
     logprob, entropy = autograd.token_logprobs(logits, targets)
+    y, last = autograd.causal_conv(x, weight, bias, state, starts)
+    y, last = autograd.selective_scan(x, dt, a, b, c, d, z, dt_bias, h0, starts)
 
 All compute is in the library's kernels, forward and backward; gradients are
 deterministic, and cannot be differentiated again.  The gradients of a recurrence's inputs
-come from one pass together, and layer norm's dx always; its weight's and bias's only where
-they are asked for.  The backward calls run on the stream that torch's autograd makes current,
+come from one pass together, as those of a selective scan, and layer norm's and the
+convolution's dx always; their weight's and bias's only where they are asked for.  The backward calls run on the stream that torch's autograd makes current,
 which is the forward call's.
 """
 from __future__ import annotations
@@ -16,7 +18,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import lm
+from . import lm, ssm
 
 
 def _unit(t):
@@ -81,6 +83,52 @@ class _TokenLogprobs(torch.autograd.Function):
         return lm.token_logprobs_backward(logits, targets, lse, entropy, dlogprob, dentropy), None
 
 
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, state, starts, silu):
+        y, last = ssm.causal_conv(x, weight, bias, state=state, starts=starts, silu=silu)
+        ctx.save_for_backward(x, weight, bias, state, starts)
+        ctx.silu = silu
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, weight, bias, state, starts = ctx.saved_tensors
+        if dy is None and dlast is None:
+            return (None,) * 6
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _unit(dy)
+        dlast = None if dlast is None else dlast.contiguous()
+        _, dw, db, _, _, _ = ctx.needs_input_grad  # frozen parameters cost no sums over tokens
+        dx, dweight, dbias, dstate = ssm.causal_conv_backward(dy, x, weight, bias, state=state, starts=starts, dlast=dlast,
+                                                              silu=ctx.silu, dparams=dw or db)
+        return dx, dweight, dbias, dstate, None, None
+
+
+class _SelectiveScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus):
+        y, last, kept = ssm.selective_scan(x, dt, a, b, c, d, z, dt_bias, h0=h0, starts=starts, softplus=softplus,
+                                           keep=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x, dt, a, b, c, d, z, dt_bias, h0, starts, kept)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dlast):
+        x, dt, a, b, c, d, z, dt_bias, h0, starts, kept = ctx.saved_tensors
+        if dy is None and dlast is None:
+            return (None,) * 11
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _unit(dy)
+        dlast = None if dlast is None else dlast.contiguous()
+        g = ssm.selective_scan_backward(dy, x, dt, a, b, c, kept, d, z, dt_bias, starts=starts, dlast=dlast,
+                                        softplus=ctx.softplus)
+        return g.dx, g.ddt, g.da, g.db, g.dc, g.dd, g.dz, g.ddt_bias, g.dh0 if h0 is not None else None, None, None
+
+
 def recurrence(x, f, i=None, h0=None, starts=None):
     """lm.recurrence(): (h, last), differentiable in x, f, i and h0."""
     return _Recurrence.apply(x, f, i, h0, starts)
@@ -94,3 +142,13 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
 def token_logprobs(logits, targets):
     """lm.token_logprobs()'s (logprob, entropy), differentiable in the logits."""
     return _TokenLogprobs.apply(logits, targets)
+
+
+def causal_conv(x, weight, bias=None, state=None, starts=None, silu: bool = True):
+    """ssm.causal_conv(): (y, last), differentiable in x, weight, bias and state."""
+    return _CausalConv.apply(x, weight, bias, state, starts, silu)
+
+
+def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts=None, softplus: bool = True):
+    """ssm.selective_scan(): (y, last), differentiable in x, dt, a, b, c, d, z, dt_bias and h0."""
+    return _SelectiveScan.apply(x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus)

@@ -1,0 +1,595 @@
+// causal_conv.cuh -- a short causal convolution of each channel over time, its gradient, and
+// its form for one token a call on a pool of states.
+//
+//   p_t = bias + sum_{j < taps} w_{taps-1-j} x_{t-j},   y_t = p_t sigmoid(p_t), or p_t,
+//
+// x before token 0 from the state (zero without), and x_{t-j} = 0 where a document starts in
+// (t - j, t].  The gradient, with q_t = dy_t act'(p_t):
+//   dx_t = sum_j w_{taps-1-j} q_{t+j} [no start in (t, t + j]],   dw_{taps-1-j} = sum_t q_t x_{t-j},
+//   dbias = sum_t q_t.
+//
+// Bound by memory: x in and y out (dy and x in, dx out), a few packed operations an element.
+// A warp takes 32 V neighbouring channels and a run of tokens; a lane's V channels lie side by
+// side where all rows allow vectors of them, or 32 apart, where single values of 32 lanes are
+// neighbours.  The window of inputs moves along in registers, so x is read once but for the
+// taps - 1 tokens before a run (the gradient: and after it).  How far the window reaches back
+// into its document is one number for the whole warp: `age`, the tokens since the start.
+#pragma once
+
+#include "lm.cuh"
+#include "lm.h"
+
+namespace gbs {
+
+template <class T> struct ConvArgs {
+  const T *x, *dy, *state, *dlast;
+  T *y, *dx, *last, *dstate;
+  const void *w, *bias;
+  const uint8_t* starts;
+  float* part;
+  long long xb, xt, yb, yt, dyb, dyt, dxb, dxt;
+  long long units;  // warps' worth of work
+  long long B, slots;
+  int T_, D, taps, silu, wide;
+  int groups, runs, length;
+};
+
+__device__ __forceinline__ float conv_param(const void* p, long long k, int wide, float*) {
+  return ((const float*)p)[k];
+}
+template <class T> __device__ __forceinline__ float conv_param(const void* p, long long k, int wide, T*) {
+  return wide ? ((const float*)p)[k] : widen(((const T*)p)[k]);
+}
+
+// A lane's V values of a row: side by side, or APART from one another with a count of those
+// that exist.
+template <class T, int V, bool EDGE> struct ConvLane {
+  static constexpr int APART = EDGE ? 32 : 1;
+  int first;  // the lane's first channel
+  int count;  // how many of the V exist
+
+  __device__ __forceinline__ ConvLane(int group, int lane, int D) {
+    first = group * 32 * V + (EDGE ? lane : lane * V);
+    const int left = D - first;
+    count = left <= 0 ? 0 : (left + APART - 1) / APART;
+    if (count > V) count = V;
+  }
+  struct Raw {
+    alignas(EDGE ? sizeof(T) : V * sizeof(T)) T v[V];
+  };
+  __device__ __forceinline__ Raw zero() const {
+    Raw r;
+#pragma unroll
+    for (int e = 0; e < V; ++e) r.v[e] = narrow<T>(0.f);
+    return r;
+  }
+  __device__ __forceinline__ Raw load(const T* row) const {
+    Raw r = zero();
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < count) r.v[e] = row[first + e * APART];
+    } else {
+      if (count) {
+        if constexpr (V * sizeof(T) == 16) {
+          const uint4 u = *(const uint4*)(row + first);
+          memcpy(&r, &u, 16);
+        } else if constexpr (V * sizeof(T) == 8) {
+          const uint2 u = *(const uint2*)(row + first);
+          memcpy(&r, &u, 8);
+        } else {
+          const unsigned u = *(const unsigned*)(row + first);
+          memcpy(&r, &u, 4);
+        }
+      }
+    }
+    return r;
+  }
+  __device__ __forceinline__ void store(T* row, const Raw& r) const {
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < count) row[first + e * APART] = r.v[e];
+    } else {
+      if (count) {
+        if constexpr (V * sizeof(T) == 16) {
+          uint4 u;
+          memcpy(&u, &r, 16);
+          *(uint4*)(row + first) = u;
+        } else if constexpr (V * sizeof(T) == 8) {
+          uint2 u;
+          memcpy(&u, &r, 8);
+          *(uint2*)(row + first) = u;
+        } else {
+          unsigned u;
+          memcpy(&u, &r, 4);
+          *(unsigned*)(row + first) = u;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void widen_to(const Raw& r, float2 (&f)[V / 2]) const {
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      if constexpr (sizeof(T) == 2) {
+        unsigned u;
+        memcpy(&u, &r.v[2 * e], 4);
+        f[e] = widen2<T>(u);
+      } else {
+        f[e] = make_float2(r.v[2 * e], r.v[2 * e + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ Raw narrowed(const float2 (&f)[V / 2]) const {
+    Raw r;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      if constexpr (sizeof(T) == 2) {
+        const unsigned u = narrow2<T>(f[e]);
+        memcpy(&r.v[2 * e], &u, 4);
+      } else {
+        r.v[2 * e] = f[e].x, r.v[2 * e + 1] = f[e].y;
+      }
+    }
+    return r;
+  }
+  // Tap or bias values of the lane's channels: p[channel * stride + k].
+  __device__ __forceinline__ void params(const void* p, int stride, int k, int wide, float2 (&f)[V / 2]) const {
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      v[e] = e < count ? conv_param(p, (long long)(first + e * APART) * stride + k, wide, (T*)nullptr) : 0.f;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
+  }
+};
+
+// The input `back` tokens before token 0 (back >= 1): from the state, or zero.
+template <class T, class L>
+__device__ __forceinline__ typename L::Raw conv_before(const ConvArgs<T>& a, const L& lane, long long b, int back) {
+  const int k = a.taps - 1 - back;
+  if (!a.state || k < 0) return lane.zero();
+  return lane.load(a.state + (b * (a.taps - 1) + k) * a.D);
+}
+
+constexpr int kConvOld = 1 << 20;  // an age past every window
+
+// The window before token t0 (newest last) and how old the document of token t0 - 1 is.
+template <class T, int W, class L, int H>
+__device__ __forceinline__ int conv_window(const ConvArgs<T>& a, const L& lane, long long b, int t0,
+                                           float2 (&hist)[W - 1][H]) {
+  int age = kConvOld;
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int t = t0 - (W - 1) + k;
+    const auto raw = t >= 0 ? lane.load(a.x + b * a.xb + (long long)t * a.xt) : conv_before(a, lane, b, -t);
+    lane.widen_to(raw, hist[k]);
+    if (a.starts && t >= 0) age = a.starts[b * a.T_ + t] ? 0 : age + 1;
+  }
+  return age;
+}
+
+template <class T, int W, int V, bool EDGE>
+__global__ void __launch_bounds__(128) conv_forward_kernel(const __grid_constant__ ConvArgs<T> a) {
+  pdl_entry();
+  using L = ConvLane<T, V, EDGE>;
+  constexpr int H = V / 2, U = 4;  // tokens whose loads are in flight together
+  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const int group = (int)(unit % a.groups);
+  const long long rest = unit / a.groups;
+  const int run = (int)(rest % a.runs);
+  const long long b = rest / a.runs;
+  const L lane(group, threadIdx.x & 31, a.D);
+  const int t0 = run * a.length, t1 = min(a.T_, t0 + a.length);
+  float2 w[W][H], bias[H], hist[W - 1][H];  // w[j]: the tap of x_{t-j}
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    if (j < a.taps) lane.params(a.w, a.taps, a.taps - 1 - j, a.wide, w[j]);
+    else
+#pragma unroll
+      for (int h = 0; h < H; ++h) w[j][h] = make_float2(0.f, 0.f);
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) bias[h] = make_float2(0.f, 0.f);
+  if (a.bias) lane.params(a.bias, 1, 0, a.wide, bias);
+  int age = conv_window<T, W>(a, lane, b, t0, hist);
+  const T* px = a.x + b * a.xb + (long long)t0 * a.xt;
+  T* py = a.y + b * a.yb + (long long)t0 * a.yt;
+  const uint8_t* ps = a.starts ? a.starts + b * a.T_ : nullptr;
+  for (int t = t0; t < t1; t += U) {
+    float2 xs[U][H];
+    typename L::Raw raw[U];
+    unsigned flag[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      raw[u] = t + u < t1 ? lane.load(px + u * a.xt) : lane.zero();
+      flag[u] = ps && t + u < t1 ? ps[t + u] : 0;
+    }
+    int live = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (t + u < t1) {
+        lane.widen_to(raw[u], xs[u]);
+        age = flag[u] ? 0 : age + 1;
+        const int reach = min(a.taps - 1, age);
+        float2 p[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) {
+          if (j <= reach) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
+          }
+        }
+        if (a.silu) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) p[h] = mul2(p[h], sigmoid<T>(p[h]));
+        }
+        lane.store(py + u * a.yt, lane.narrowed(p));
+        live = u + 1;
+      }
+    }
+    if (live == U) {
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int h = 0; h < H; ++h) hist[k][h] = k + U < W - 1 ? hist[k + U < W - 1 ? k + U : 0][h] : xs[k + U < W - 1 ? 0 : k + U - (W - 1)][h];
+    } else {  // the last tokens of a row: one at a time
+      for (int u = 0; u < live; ++u) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+          for (int h = 0; h < H; ++h) hist[k][h] = k + 1 < W - 1 ? hist[k + 1 < W - 1 ? k + 1 : 0][h] : xs[0][h];
+#pragma unroll
+        for (int k = 0; k + 1 < U; ++k)
+#pragma unroll
+          for (int h = 0; h < H; ++h) xs[k][h] = xs[k + 1][h];
+      }
+    }
+    px += U * a.xt;
+    py += U * a.yt;
+  }
+  if (a.last && t1 == a.T_) {  // the newest inputs, of the last document only
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const int back = W - 1 - k;  // 1: the newest
+      if (back <= a.taps - 1)
+        lane.store(a.last + (b * (a.taps - 1) + a.taps - 1 - back) * a.D, back - 1 <= age ? lane.narrowed(hist[k]) : lane.zero());
+    }
+  }
+}
+
+// A run's tokens t0 .. t1 - 1 are its own; it goes W - 1 further for what they take from the
+// tokens after them.  pend: dx of the newest W tokens, by their number modulo W.  With very many
+// batch rows a warp takes every slots-th of them, so that there are not as many partial sums.
+template <class T, int W, int V, bool EDGE>
+__global__ void __launch_bounds__(128) conv_backward_kernel(const __grid_constant__ ConvArgs<T> a) {
+  pdl_entry();
+  using L = ConvLane<T, V, EDGE>;
+  constexpr int H = V / 2;
+  const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const int group = (int)(unit % a.groups);
+  const long long rest = unit / a.groups;
+  const int run = (int)(rest % a.runs);
+  const L lane(group, threadIdx.x & 31, a.D);
+  const int t0 = run * a.length, t1 = min(a.T_, t0 + a.length);
+  const float2 zero = make_float2(0.f, 0.f);
+  float2 w[W][H], dw[W][H], bias[H], db[H], hist[W - 1][H], pend[W][H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) bias[h] = db[h] = zero;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int h = 0; h < H; ++h) w[j][h] = dw[j][h] = zero;
+    if (j < a.taps) lane.params(a.w, a.taps, a.taps - 1 - j, a.wide, w[j]);
+  }
+  if (a.bias) lane.params(a.bias, 1, 0, a.wide, bias);
+  const long long slot = rest / a.runs;
+  for (long long b = slot; b < a.B; b += a.slots) {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int h = 0; h < H; ++h) pend[j][h] = zero;
+    int age = conv_window<T, W>(a, lane, b, t0, hist);
+    const T* px = a.x + b * a.xb + (long long)t0 * a.xt;
+    const T* pg = a.dy + b * a.dyb + (long long)t0 * a.dyt;
+    const uint8_t* ps = a.starts ? a.starts + b * a.T_ : nullptr;
+    const int end = t1 + W - 1;
+    for (int t = t0; t < end; t += W) {
+      float2 xs[W][H];
+      typename L::Raw raw[W], graw[W];
+      unsigned flag[W];
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        const bool here = t + u < a.T_ && t + u < end;
+        raw[u] = here ? lane.load(px + u * a.xt) : lane.zero();
+        graw[u] = here ? lane.load(pg + u * a.dyt) : lane.zero();
+        flag[u] = ps && here ? ps[t + u] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < W; ++u) {
+        lane.widen_to(raw[u], xs[u]);
+        if (t + u < a.T_ && t + u < end) {
+          age = flag[u] ? 0 : age + 1;
+          const int reach = min(a.taps - 1, age);
+          float2 q[H];
+          lane.widen_to(graw[u], q);
+          if (a.silu) {
+            float2 p[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
+#pragma unroll
+            for (int j = 1; j < W; ++j) {
+              if (j <= reach) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {  // act' = s + p s (1 - s)
+              const float2 s = sigmoid<T>(p[h]);
+              const float2 c = fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+              q[h] = mul2(q[h], fma2(mul2(p[h], s), c, s));
+            }
+          }
+          const bool own = t + u < t1;
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            if (j <= reach) {
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                const float2 xv = u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h];
+                pend[(u - j + W) % W][h] = fma2(w[j][h], q[h], pend[(u - j + W) % W][h]);
+                if (own) dw[j][h] = fma2(q[h], xv, dw[j][h]);
+              }
+            }
+          }
+          if (own) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) db[h] = add2(db[h], q[h]);
+          }
+        }
+        // Token t + u - (W - 1) takes nothing more.
+        const int done = t + u - (W - 1);
+        constexpr int kNext = 1;
+        float2(&out)[H] = pend[(u + kNext) % W];
+        if (done < t1 && (done >= t0 || (run == 0 && done >= 1 - a.taps))) {
+          const int k = done - (a.T_ - (a.taps - 1));  // its place in the last state
+          if (a.dlast && k >= 0 && a.T_ - 1 - done <= age) {
+            float2 g[H];
+            lane.widen_to(lane.load(a.dlast + (b * (a.taps - 1) + k) * a.D), g);
+#pragma unroll
+            for (int h = 0; h < H; ++h) out[h] = add2(out[h], g[h]);
+          }
+          if (done >= 0) lane.store(a.dx + b * a.dxb + (long long)done * a.dxt, lane.narrowed(out));
+          else if (a.dstate) lane.store(a.dstate + (b * (a.taps - 1) + a.taps - 1 + done) * a.D, lane.narrowed(out));
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) out[h] = zero;
+      }
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int h = 0; h < H; ++h) hist[k][h] = xs[k + 1][h];
+      px += W * a.xt;
+      pg += W * a.dyt;
+    }
+  }
+  if (a.part) {  // (run, tap or bias, channel)
+    float* p = a.part + (slot * a.runs + run) * (a.taps + 1) * a.D;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+      if (j < a.taps || j == W) {
+        float* row = p + (long long)(j == W ? a.taps : a.taps - 1 - j) * a.D;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 v = j == W ? db[e / 2] : dw[j == W ? 0 : j][e / 2];
+          if (e < lane.count) row[lane.first + e * L::APART] = e % 2 ? v.y : v.x;
+        }
+      }
+    }
+  }
+}
+
+// Sums the runs' parts, in a fixed order: a block takes 32 values, its 16 warps every 16th run
+// and then one warp the 16 sums.
+template <class T> struct ConvFoldArgs {
+  const float* part;
+  void *dw, *db;
+  long long rows;  // of parts
+  int D, taps, wide;
+};
+template <class T>
+__global__ void __launch_bounds__(512) conv_fold_kernel(const __grid_constant__ ConvFoldArgs<T> a) {
+  pdl_entry();
+  __shared__ float sums[16][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long width = (long long)(a.taps + 1) * a.D, at = (long long)blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (at < width) {
+#pragma unroll 8
+    for (long long r = warp; r < a.rows; r += 16) s += a.part[r * width + at];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && at < width) {
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += sums[k][lane];
+    const int tap = (int)(at / a.D), ch = (int)(at % a.D);
+    void* out = tap < a.taps ? a.dw : a.db;
+    const long long k = tap < a.taps ? (long long)ch * a.taps + tap : ch;
+    if (out) {
+      if (a.wide) ((float*)out)[k] = s;
+      else ((T*)out)[k] = narrow<T>(s);
+    }
+  }
+}
+
+// ---- one token a call ------------------------------------------------------------------
+
+template <class T> struct ConvStepArgs {
+  const T* x;
+  T *state, *y;
+  const void *w, *bias;
+  const int32_t* slots;
+  long long sx, sy, pool, n;  // n: threads
+  int D, taps, silu, wide, packs;
+  ErrSink err;
+};
+
+template <class T, int V>
+__global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepArgs<T> a) {
+  pdl_entry();
+  const long long at = (long long)blockIdx.x * 128 + threadIdx.x;
+  if (at >= a.n) return;
+  const long long b = at / a.packs;
+  const int ch = (int)(at % a.packs) * V;
+  long long slot = a.slots ? (long long)a.slots[b] : b;
+  if (slot >= a.pool) {  // no such state: reported, and the row treated as padding
+    if (ch == 0) raise_err(a.err, ERRBIT_RANGE);
+    slot = -1;
+  }
+  float p[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) p[c] = 0.f;
+  if (slot >= 0) {
+    const Pack<T, V> px = ld_pack<T, V>(a.x + b * a.sx + ch);
+    T* st = a.state + slot * (a.taps - 1) * a.D + ch;
+    Pack<T, V> old[kConvMaxTaps - 1];
+#pragma unroll
+    for (int k = 0; k < kConvMaxTaps - 1; ++k)
+      if (k < a.taps - 1) old[k] = ld_pack<T, V>(st + (long long)k * a.D);
+    if (a.bias) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) p[c] = conv_param(a.bias, ch + c, a.wide, (T*)nullptr);
+    }
+#pragma unroll
+    for (int k = 0; k < kConvMaxTaps; ++k) {
+      if (k < a.taps) {
+        float v[V];
+        if (k == a.taps - 1) widen_pack(px, v);
+        else if (k < kConvMaxTaps - 1) widen_pack(old[k < kConvMaxTaps - 1 ? k : 0], v);
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+          p[c] = fmaf(conv_param(a.w, (long long)(ch + c) * a.taps + k, a.wide, (T*)nullptr), v[c], p[c]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kConvMaxTaps - 1; ++k) {
+      if (k + 1 < a.taps - 1) st_pack(st + (long long)k * a.D, old[k + 1 < kConvMaxTaps - 1 ? k + 1 : 0]);
+      else if (k == a.taps - 2) st_pack(st + (long long)k * a.D, px);
+    }
+    if (a.silu) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float2 s = sigmoid<T>(make_float2(p[c], p[c]));
+        p[c] *= s.x;
+      }
+    }
+  }
+  st_pack(a.y + b * a.sy + ch, narrow_pack<T, V>(p));
+}
+
+// ---- launches --------------------------------------------------------------------------
+
+// Whether vectors of V values can be read and written in every row of the array.
+template <class T> bool conv_rows(const SeqArray& s, int V, long long B, long long T_) {
+  if (!s.p) return true;
+  return (uintptr_t)s.p % (V * sizeof(T)) == 0 && (B <= 1 || s.sb % V == 0) && (T_ <= 1 || s.st % V == 0);
+}
+template <class T> bool conv_dense(const void* p, int V) { return (uintptr_t)p % (V * sizeof(T)) == 0; }
+
+template <class T> ConvArgs<T> conv_args(const CausalConvJob& j) {
+  ConvArgs<T> a = {};
+  a.x = (const T*)j.x.p, a.xb = j.x.sb, a.xt = j.x.st;
+  a.y = (T*)j.y.p, a.yb = j.y.sb, a.yt = j.y.st;
+  a.dy = (const T*)j.dy.p, a.dyb = j.dy.sb, a.dyt = j.dy.st;
+  a.dx = (T*)j.dx.p, a.dxb = j.dx.sb, a.dxt = j.dx.st;
+  a.w = j.w, a.bias = j.bias, a.wide = j.wide_params;
+  a.state = (const T*)j.state, a.last = (T*)j.last, a.dlast = (const T*)j.dlast, a.dstate = (T*)j.dstate;
+  a.starts = j.starts;
+  a.B = j.B, a.T_ = (int)j.T, a.D = (int)j.D, a.taps = j.taps, a.silu = j.silu;
+  return a;
+}
+
+template <class T, int W, int V, bool EDGE> cudaError_t conv_forward(const CausalConvJob& j, const LaunchCtx& ctx) {
+  ConvArgs<T> a = conv_args<T>(j);
+  a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
+  // Some 24 warps an SM, and runs of 16 tokens at least: each reads taps - 1 tokens again.
+  long long runs = (24ll * ctx.num_sms + a.groups * j.B - 1) / (a.groups * j.B);
+  long long length = (j.T + runs - 1) / runs;
+  length = length < 16 ? 16 : (length + 3) / 4 * 4;
+  a.length = (int)length;
+  a.runs = j.T ? (int)((j.T + length - 1) / length) : 1;
+  a.units = j.B * a.runs * a.groups;
+  profile_before(ctx);
+  const cudaError_t e =
+      launch_pdl(conv_forward_kernel<T, W, V, EDGE>, (unsigned)((a.units + 3) / 4), 128, 0, ctx.stream, a);
+  profile_after(ctx);
+  return e;
+}
+
+template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
+  ConvArgs<T> a = conv_args<T>(j);
+  a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
+  const ConvSplit s = conv_backward_split(j.B, j.T, j.D);
+  a.length = (int)s.length, a.runs = (int)s.runs, a.slots = s.slots;
+  a.units = s.slots * a.runs * a.groups;
+  a.part = j.dw || j.db ? (float*)j.temp : nullptr;
+  profile_before(ctx);
+  cudaError_t e =
+      launch_pdl(conv_backward_kernel<T, W, V, EDGE>, (unsigned)((a.units + 3) / 4), 128, 0, ctx.stream, a);
+  if (e == cudaSuccess && a.part) {
+    ConvFoldArgs<T> f = {};
+    f.part = a.part, f.dw = j.dw, f.db = j.db, f.rows = s.slots * s.runs;
+    f.D = a.D, f.taps = j.taps, f.wide = j.wide_params;
+    e = launch_pdl(conv_fold_kernel<T>, (unsigned)(((j.taps + 1) * j.D + 31) / 32), 512, 0, ctx.stream, f);
+  }
+  profile_after(ctx);
+  return e;
+}
+
+template <class T> cudaError_t launch_causal_conv(const CausalConvJob& j, const LaunchCtx& ctx) {
+  constexpr int V = 4;
+  const bool even = j.D % V == 0 && conv_rows<T>(j.x, V, j.B, j.T) && conv_rows<T>(j.y, V, j.B, j.T) &&
+                    conv_dense<T>(j.state, V) && conv_dense<T>(j.last, V);
+  if (j.taps <= 4) return even ? conv_forward<T, 4, V, false>(j, ctx) : conv_forward<T, 4, V, true>(j, ctx);
+  return even ? conv_forward<T, 8, V, false>(j, ctx) : conv_forward<T, 8, V, true>(j, ctx);
+}
+
+template <class T> cudaError_t launch_causal_conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
+  const int V = j.taps <= 4 ? 4 : 2;
+  const bool even = j.D % V == 0 && conv_rows<T>(j.x, V, j.B, j.T) && conv_rows<T>(j.dy, V, j.B, j.T) &&
+                    conv_rows<T>(j.dx, V, j.B, j.T) && conv_dense<T>(j.state, V) && conv_dense<T>(j.dlast, V) &&
+                    conv_dense<T>(j.dstate, V);
+  if (j.taps <= 4) return even ? conv_backward<T, 4, 4, false>(j, ctx) : conv_backward<T, 4, 4, true>(j, ctx);
+  return even ? conv_backward<T, 8, 2, false>(j, ctx) : conv_backward<T, 8, 2, true>(j, ctx);
+}
+
+template <class T, int V> cudaError_t conv_step(const CausalConvStepJob& j, const LaunchCtx& ctx) {
+  ConvStepArgs<T> a = {};
+  a.x = (const T*)j.x, a.sx = j.sx, a.y = (T*)j.y, a.sy = j.sy;
+  a.w = j.w, a.bias = j.bias, a.wide = j.wide_params;
+  a.state = (T*)j.state, a.pool = j.pool, a.slots = j.slots;
+  a.D = (int)j.D, a.taps = j.taps, a.silu = j.silu;
+  a.packs = (int)(j.D / V);
+  a.n = j.B * a.packs;
+  a.err = ctx.err;
+  profile_before(ctx);
+  const cudaError_t e = launch_pdl(conv_step_kernel<T, V>, (unsigned)((a.n + 127) / 128), 128, 0, ctx.stream, a);
+  profile_after(ctx);
+  return e;
+}
+
+template <class T> cudaError_t launch_causal_conv_step(const CausalConvStepJob& j, const LaunchCtx& ctx) {
+  constexpr int V = 16 / sizeof(T);
+  const bool wide = j.D % V == 0 && conv_dense<T>(j.x, V) && conv_dense<T>(j.y, V) && conv_dense<T>(j.state, V) &&
+                    (j.B <= 1 || (j.sx % V == 0 && j.sy % V == 0));
+  return wide ? conv_step<T, V>(j, ctx) : conv_step<T, 1>(j, ctx);
+}
+
+}  // namespace gbs

@@ -75,6 +75,141 @@ struct LogprobJob {
 };
 constexpr int kMaxTop = 32;
 
+// A short causal convolution of each channel over time:
+// y_t = act(bias + sum_k w_k x_{t-taps+1+k}), act silu or the identity.
+struct CausalConvJob {
+  long long B = 0, T = 0, D = 0;
+  int taps = 0, silu = 0, wide_params = 0;  // wide_params: w and bias (dw and db) are fp32
+  SeqArray x, y;
+  const void *w = nullptr, *bias = nullptr;  // (D, taps), (D) or null
+  const void* state = nullptr;               // (B, taps - 1, D) or null: zero
+  const uint8_t* starts = nullptr;           // (B, T) or null
+  void* last = nullptr;                      // (B, taps - 1, D) or null
+  // Backward.
+  SeqArray dy, dx;
+  const void* dlast = nullptr;               // (B, taps - 1, D) or null
+  void *dw = nullptr, *db = nullptr;         // like w, bias, or null
+  void* dstate = nullptr;                    // (B, taps - 1, D) or null
+  void* temp = nullptr;                      // with dw or db
+};
+constexpr int kConvMaxTaps = 8;
+// How the gradient splits its tokens: a warp takes a run of `length` tokens of every slots-th
+// batch row, and leaves a row of partial sums for the weights.
+struct ConvSplit {
+  long long slots, runs, length;
+};
+inline ConvSplit conv_backward_split(long long B, long long T, long long D) {
+  const long long want = (152 * 12) / ((D + 127) / 128) + 1;  // warps of 128 channels: 12 an SM
+  const long long per_row = (want + B - 1) / B;
+  long long length = (T + per_row - 1) / per_row;
+  length = length < 32 ? 32 : (length + 7) / 8 * 8;  // a run reads up to 14 tokens of its neighbours
+  const long long runs = (T + length - 1) / length;
+  return {B < 4 * want ? B : 4 * want, runs < 1 ? 1 : runs, length};
+}
+inline size_t conv_temp_bytes(long long B, long long T, long long D, int taps) {
+  const ConvSplit s = conv_backward_split(B, T, D);
+  return round_up((size_t)(s.slots * s.runs) * (taps + 1) * (size_t)D * sizeof(float), 256);
+}
+
+struct CausalConvStepJob {
+  long long B = 0, D = 0, pool = 0;
+  int taps = 0, silu = 0, wide_params = 0;
+  const void *x = nullptr, *w = nullptr, *bias = nullptr;
+  long long sx = 0, sy = 0;        // row strides
+  void* state = nullptr;           // (pool, taps - 1, D)
+  const int32_t* slots = nullptr;  // (B) or null: row b uses state b
+  void* y = nullptr;
+};
+
+// A (batch, time, group, state) array with unit state stride.
+struct GroupArray {
+  void* p = nullptr;
+  long long sb = 0, st = 0, sg = 0;
+};
+
+// h_t = exp(D_t A) h_{t-1} + D_t x_t B_t, y_t = (C_t . h_t + d x_t) silu(z_t),
+// D_t = softplus(dt_t + bias) or dt_t + bias: N states a channel, channels in G groups that
+// share B and C.
+struct SelectiveScanJob {
+  long long B = 0, T = 0, D = 0, N = 0, G = 0;
+  int softplus = 0;
+  SeqArray x, dt, z, y;                // z.p null: no gate
+  GroupArray b, c;
+  const float *a = nullptr;            // (D, N)
+  const float *d = nullptr, *bias = nullptr;  // (D) or null
+  const float* h0 = nullptr;           // (B, D, N) or null: zero
+  const uint8_t* starts = nullptr;     // (B, T) or null
+  float* last = nullptr;               // (B, D, N) or null
+  float* kept = nullptr;               // (B, ceil(T / 16), D, N) or null; the backward reads it
+  // Backward.
+  SeqArray dy, dx, ddt, dz;
+  GroupArray db, dc;
+  const float* dlast = nullptr;        // (B, D, N) or null
+  float *da = nullptr, *dd = nullptr, *dbias = nullptr;  // (D, N), (D), (D); the last two may be null
+  float* dh0 = nullptr;                // (B, D, N) or null
+  void* temp = nullptr;
+};
+constexpr int kSscTile = 16;      // tokens of a tile: a kept state precedes each
+constexpr int kSscChannels = 64;  // channels of a block
+constexpr int kSscMaxStates = 128;
+// The tokens of a batch row in parts of `tiles` tiles, which run side by side: as many as it
+// takes to fill the device, where the rows and channels alone do not.
+struct SscSplit {
+  long long parts, tiles;
+};
+inline SscSplit ssc_split(long long B, long long T, long long D, long long G, bool backward) {
+  const long long units = B * G * ((D / G + kSscChannels - 1) / kSscChannels);
+  const long long tiles = (T + kSscTile - 1) / kSscTile;
+  const long long want = (backward ? 2 : 4) * 152;
+  long long parts = units >= 152 ? 1 : want / units;
+  if (parts > tiles / 4) parts = tiles / 4;
+  if (parts < 1) parts = 1;
+  const long long each = (tiles + parts - 1) / parts;
+  return {tiles ? (tiles + each - 1) / each : 1, each};
+}
+inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, bool backward) {
+  const SscSplit s = ssc_split(B, T, D, G, backward);
+  size_t floats = (size_t)B * (s.parts - 1) * (D * N + D + 1);
+  if (backward) {
+    floats += (size_t)B * s.parts * D * (N + 2);
+    floats += 2 * (size_t)((D / G + kSscChannels - 1) / kSscChannels) * B * T * G * N;
+  }
+  return round_up(floats * sizeof(float), 256);
+}
+
+struct SelectiveScanStepJob {
+  long long B = 0, D = 0, N = 0, G = 0, pool = 0;
+  int softplus = 0;
+  const void *x = nullptr, *dt = nullptr, *z = nullptr, *b = nullptr, *c = nullptr;
+  long long sx = 0, sdt = 0, sz = 0, sy = 0, sb = 0, sbg = 0, sc = 0, scg = 0;  // row (and group) strides
+  const float *a = nullptr, *d = nullptr, *bias = nullptr;
+  float* state = nullptr;          // (pool, D, N)
+  const int32_t* slots = nullptr;  // (B) or null
+  void* y = nullptr;
+};
+
+constexpr int kVerifyMaxCluster = 8;
+
+// Verification of up to K drafted tokens for each of B requests over a vocabulary of V.
+struct VerifyJob {
+  long long B = 0, K = 0, V = 0;
+  const void* tokens = nullptr;    // (B, K) int32 or int64
+  int tokens64 = 0;
+  const void *target = nullptr, *draft = nullptr;  // (B, K + 1, V), (B, K, V) or null
+  long long tb = 0, tt = 0, qb = 0, qt = 0;
+  const float *accept = nullptr, *sample = nullptr;  // (B, K), (B)
+  const int32_t* lengths = nullptr;                  // (B) or null: K
+  int32_t *accepted = nullptr, *out = nullptr;       // (B), (B, K + 1)
+};
+
+template <class T> cudaError_t launch_causal_conv(const CausalConvJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_causal_conv_backward(const CausalConvJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_causal_conv_step(const CausalConvStepJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_selective_scan(const SelectiveScanJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_selective_scan_backward(const SelectiveScanJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_selective_scan_step(const SelectiveScanStepJob& job, const LaunchCtx& ctx);
+template <class T> cudaError_t launch_verify(const VerifyJob& job, const LaunchCtx& ctx);
+
 template <class T> cudaError_t launch_logprob(const LogprobJob& job, const LaunchCtx& ctx);
 template <class T> cudaError_t launch_logprob_backward(const LogprobJob& job, const LaunchCtx& ctx);
 template <class T, class P> cudaError_t launch_layer_norm(const LayerNormJob& job, const LaunchCtx& ctx);

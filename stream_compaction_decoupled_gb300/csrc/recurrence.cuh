@@ -51,48 +51,6 @@
 
 namespace gbs {
 
-// sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z) of two values, each accurate where it is small.
-// A NaN stays a NaN.
-//
-// fp32: e = e^-|z| to 4 units of 2^-24, 1/(1+e) by the instruction, 2 units, and e/(1+e): within
-// 8 units from end to end, and 0 and 1 at the ends.
-// (8 x 2048 x 2048 gated 82.6 us, by the instructions alone 82.7; 1 x 16384 x 2048 107.3 and
-// 103.5.)
-//
-// 16-bit gates: e = 2^(-z log2 e) with the product rounded once, 1/(1+e) and e/(1+e), by the
-// instructions alone: up to 8 + 1.3 |z| units of 2^-24, where the gate itself was rounded to 8
-// or 11 bits, which moves either by |z| 2^-9 or |z| 2^-12.  The exponent stops at 2^125, where
-// e/(1+e) is still finite; 1/(1+e) ends there, at 2^-125 in place of 0.
-template <class T> __device__ __forceinline__ void sigmoid_both(float2 z, float2& s, float2& c) {
-  if constexpr (sizeof(T) == 4) {
-    const float2 e = exp_full(make_float2(max_nan(-fabsf(z.x), -104.f), max_nan(-fabsf(z.y), -104.f)));
-    const float2 d = add2(e, make_float2(1.f, 1.f)), big = make_float2(rcp(d.x), rcp(d.y)), small = mul2(e, big);
-    s = make_float2(z.x < 0.f ? small.x : big.x, z.y < 0.f ? small.y : big.y);
-    c = make_float2(z.x < 0.f ? big.x : small.x, z.y < 0.f ? big.y : small.y);
-  } else {
-    const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
-    const float2 e = make_float2(ex2(min_nan(x.x, 125.f)), ex2(min_nan(x.y, 125.f)));
-    const float2 d = add2(e, make_float2(1.f, 1.f));
-    s = make_float2(rcp(d.x), rcp(d.y));
-    c = mul2(e, s);
-  }
-}
-
-// sigmoid(z) alone.  16 bits: e may overflow to infinity, which gives 0.
-template <class T> __device__ __forceinline__ float2 sigmoid(float2 z) {
-  const float2 one = make_float2(1.f, 1.f);
-  if constexpr (sizeof(T) == 4) {
-    // e^88 is finite; beyond, the result is below the normal numbers and 0.
-    const float2 x = make_float2(max_nan(min_nan(-z.x, 88.f), -104.f), max_nan(min_nan(-z.y, 88.f), -104.f));
-    const float2 d = add2(exp_full(x), one);
-    return make_float2(rcp(d.x), rcp(d.y));
-  } else {
-    const float2 x = mul2(z, make_float2(-kLog2e, -kLog2e));
-    const float2 d = add2(make_float2(ex2(x.x), ex2(x.y)), one);
-    return make_float2(rcp(d.x), rcp(d.y));
-  }
-}
-
 template <class T> struct RecArgs {
   const T *x, *f, *i, *h, *dh;  // backward reads h and dh
   T *y, *dx, *df, *di;          // forward writes y
