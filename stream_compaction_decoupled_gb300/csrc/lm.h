@@ -2,6 +2,8 @@
 // (lm_api.cu) and their kernel launchers.
 #pragma once
 
+#include <math.h>
+
 #include "launch.h"
 
 namespace gbs {
@@ -167,8 +169,39 @@ inline SscSplit ssc_split(long long B, long long T, long long D, long long G, bo
   const long long each = (tiles + parts - 1) / parts;
   return {tiles ? (tiles + each - 1) / each : 1, each};
 }
+// Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 /
+// lanes channels each; 4 blocks fit an SM.  Where the rows and channels give enough blocks, a row
+// is one chain (more parts cost a second pass over all parts but the last: 16 x 1024 x 2048 bf16,
+// gated, 256 blocks: 211 us, in 4 parts 252).  Else it is split until the device is full (8 x 2048
+// x 2048, 128 blocks: 313 us, in 4 parts 276; 4 x 2048 x 2048 315, in 9 parts 152), with 4 lanes
+// where 2 cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).  A part goes through
+// all before it first, so their number stays below the root of 8 times the tiles (1 x 32768 x 128:
+// 64 parts 113 us, 128 102, 256 129).
+struct SscForwardPlan {
+  SscSplit split;
+  int lanes;
+};
+inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, long long G) {
+  const long long tiles = (T + kSscTile - 1) / kSscTile;
+  const auto blocks = [&](int lanes) {
+    const long long width = 64 / lanes;
+    return (B * G * ((D / G + width - 1) / width) + 3) / 4;
+  };
+  int lanes = 2;
+  long long parts = 1;
+  if (blocks(2) < 220) {
+    long long most = (long long)sqrt(8.0 * (double)tiles);
+    if (most > tiles / 2) most = tiles / 2;
+    if (blocks(2) * most < 456) lanes = 4;
+    parts = 608 / blocks(lanes);
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+  }
+  const long long each = (tiles + parts - 1) / parts;
+  return {{tiles ? (tiles + each - 1) / each : 1, each}, lanes};
+}
 inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, bool backward) {
-  const SscSplit s = ssc_split(B, T, D, G, backward);
+  const SscSplit s = backward ? ssc_split(B, T, D, G, true) : ssc_forward_plan(B, T, D, G).split;
   size_t floats = (size_t)B * (s.parts - 1) * (D * N + D + 1);
   if (backward) {
     floats += (size_t)B * s.parts * D * (N + 2);

@@ -13,18 +13,27 @@
 //   dA = sum_t q_t D_t,  dz_t = dy_t (C_t . h_t + d x_t) silu'(z_t),  ddt_t = dD_t sigmoid(dt_t + bias).
 //
 // Bound by issue: an exponential and four fp32 operations for each state and token, against 8
-// bytes a token and channel (16 bits).  So all of it is in packed pairs of channels, and what is
-// done once a token and channel (softplus, gate, conversions) is kept apart from the states:
+// bytes a token and channel (16 bits).  Forward, a warp is on its own: 64 / LN channels of one
+// group, LN lanes a pair of channels and 16 / LN states of both a lane (more than 16 states in
+// blocks of 16), so that a token's B and C, the same for all channels, are read once for 32 / LN
+// states and tokens a lane.  (A 128-bit read of shared memory costs four passes even where all
+// lanes read the same; reading B and C for 4 states of 2 channels with each value twice took 24
+// passes a token and a quarter of the time.)  What is done once a token and channel (softplus,
+// gate, conversions) goes around the lanes of a pair, a token each.  Inputs come through a ring of
+// asynchronous copies, their start flags 32 tiles at a time.
 //
-//   a block of 128 threads takes 64 channels and tiles of 16 tokens, one after another;
+// The gradient: a block of 128 threads takes 64 channels and tiles of 16 tokens, in three phases:
 //   A  a lane takes two neighbouring channels, a warp 4 tokens: D, D x to shared memory;
-//   B  a warp takes 16 channels and all 16 tokens: a thread 2 channels (a packed pair) and 4
-//      states of each block of 16, 4 lanes a channel; its part of C . h to shared memory;
-//   C  as A: the four lanes' parts are summed, gate, y.
+//   B  a warp takes 16 channels and all 16 tokens: a thread 2 channels and 4 states of each block
+//      of 16, 4 lanes a channel; its part of the sums over states to shared memory;
+//   C  as A: the four lanes' parts are summed, then what is done once a token and channel.
 //
 // The tokens of a row are one chain.  Where the rows and channels are too few for the device,
 // they are split into parts: a first kernel finds what each part makes of a state of zero, and
 // with exp(A sum D) each part knows where it starts (the gradient: from the other end).
+//
+// Measured (GB300): 8 x 2048 x 2048, 16 states, bf16, gated, with starts and kept states 285 us;
+// 1 x 32768 x 2048 continued 511 us.
 #pragma once
 
 #include "lm.cuh"
@@ -50,6 +59,7 @@ template <class T> struct SscArgs {
   float *part_b, *part_c, *part_a;
   long long B;
   int T_, D, N, NP, G, DG, blocks, parts, part_tiles, tiles, softplus;
+  bool vec;     // (D, N) arrays can be read and written in 16-byte pieces
 };
 
 // Two neighbouring channels of a row, as they lie in memory.
@@ -139,10 +149,12 @@ __device__ __forceinline__ void ssc_store(float* p, int n, int N, int count, flo
     if (count > 1) p[N + n] = v.y;
   }
 }
-__device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) {  // exp of the product, a in units of log2 e
-  const float2 e = mul2(a, d);
-  return make_float2(ex2(e.x), ex2(e.y));
-}
+// exp of the product, a in units of log2 e.  In single operations: a packed product before the
+// exponential costs more than the instruction it saves (measured in a loop of nothing else, 32
+// states a thread, 3 warps a scheduler: 6.9 cycles a state and token with packed products and sums,
+// 5.2 with these and the sums single and only D x B packed, 5.9 with all of it single).
+__device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) { return make_float2(ex2(a.x * d.x), ex2(a.y * d.y)); }
+__device__ __forceinline__ float2 ssc_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
 // The thread's A in units of log2 e.
 template <class T>
 __device__ __forceinline__ void ssc_rates(const SscArgs<T>& a, const SscPlace<T>& at, int n0, float2 (&r)[4]) {
@@ -232,152 +244,449 @@ struct SscShared {
   }
 };
 
+// ---- forward ---------------------------------------------------------------------------
+
+// M = 16 / LN states of two channels a thread, LN lanes a pair of channels; a warp is on its own:
+// WIDTH channels, tiles of L tokens, of which a lane prepares and finishes R.  What a warp reads
+// comes by asynchronous copies into a ring of STAGES tiles of its own in shared memory.
+template <class T, bool EDGE_, int LN_> struct SscLane {
+  static constexpr bool EDGE = EDGE_;
+  static constexpr int LN = LN_, L = 8, R = L / LN, M = 16 / LN, WIDTH = 64 / LN;
+  static constexpr int STAGES = sizeof(T) == 2 ? 3 : 2;
+  static constexpr int ROW = WIDTH * (int)sizeof(T), ARRAY = L * ROW;  // bytes
+  static constexpr int VECTORS = L * 32 * (int)sizeof(T);               // B and C of 16 states, as they are
+  static constexpr int CHUNKS = ROW / 16;                               // 16-byte copies of a row
+  using P = SscPair<T, EDGE>;
+  using Raw = typename P::Raw;
+  static __host__ __device__ constexpr int stage_bytes(int NB) { return 3 * ARRAY + NB * VECTORS; }
+  // Bytes a warp: the ring, B and C widened, D and D x of each pair, and with more than 16 states
+  // those of each block.
+  static __host__ __device__ constexpr int warp_bytes(int NB) {
+    return STAGES * stage_bytes(NB) + NB * L * 32 * 4 + L * (32 / LN) * 16 + (NB > 1 ? NB * 2 * M * 32 * 4 : 0);
+  }
+};
+
+// Where a warp works.
+template <class T> struct SscWarp {
+  long long b;
+  int group, part, t0, t1;  // tokens of its part
+  int base, width;          // the warp's first channel, and how many it has
+  int ch, count;            // the lane's first channel, and how many of its two exist
+  bool idle;
+  __device__ __forceinline__ SscWarp(const SscArgs<T>& a, int LN, int parts) {
+    const int lane = threadIdx.x & 31, most = 64 / LN, blocks = (a.DG + most - 1) / most;
+    long long u = (long long)blockIdx.x * (kSscThreads / 32) + (threadIdx.x >> 5);
+    const int block = (int)(u % blocks);
+    u /= blocks;
+    group = (int)(u % a.G);
+    u /= a.G;
+    part = (int)(u % parts);
+    b = u / parts;
+    idle = b >= a.B;
+    t0 = part * a.part_tiles * kSscTile;
+    t1 = (int)min((long long)a.T_, (long long)t0 + (long long)a.part_tiles * kSscTile);
+    base = group * a.DG + block * most;
+    width = min(most, (group + 1) * a.DG - base);
+    ch = base + 2 * (lane / LN);
+    count = min(2, base + width - ch);
+    if (count <= 0) ch = base;  // what it loads is real, what it makes is not stored
+  }
+};
+
+// M values of two channels of a (D, N) array, in pairs of states; `other` where there are none.
+template <int M, bool VEC> __device__ __forceinline__ void ssc_load_states(const float* p, int n0, int N, int count, float2 (&v)[2][M / 2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int j = 0; j < M / 4; ++j) {
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int n = n0 + 4 * j;
+      const float* at = p + (long long)c * N + n;
+      if (VEC) {
+        if (c < count && n < N) q = *(const float4*)at;
+      } else if (c < count) {
+        if (n < N) q.x = at[0];
+        if (n + 1 < N) q.y = at[1];
+        if (n + 2 < N) q.z = at[2];
+        if (n + 3 < N) q.w = at[3];
+      }
+      v[c][2 * j] = make_float2(q.x, q.y);
+      v[c][2 * j + 1] = make_float2(q.z, q.w);
+    }
+  }
+}
+template <int M, bool VEC> __device__ __forceinline__ void ssc_store_states(float* p, int n0, int N, int count, const float2 (&v)[2][M / 2]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int j = 0; j < M / 4; ++j) {
+      const int n = n0 + 4 * j;
+      const float4 q = make_float4(v[c][2 * j].x, v[c][2 * j].y, v[c][2 * j + 1].x, v[c][2 * j + 1].y);
+      float* at = p + (long long)c * N + n;
+      if (VEC) {
+        if (c < count && n < N) *(float4*)at = q;
+      } else if (c < count) {
+        if (n < N) at[0] = q.x;
+        if (n + 1 < N) at[1] = q.y;
+        if (n + 2 < N) at[2] = q.z;
+        if (n + 3 < N) at[3] = q.w;
+      }
+    }
+  }
+}
+template <int M> __device__ __forceinline__ void ssc_load_any(bool vec, const float* p, int n0, int N, int count, float2 (&v)[2][M / 2]) {
+  if (vec) ssc_load_states<M, true>(p, n0, N, count, v);
+  else ssc_load_states<M, false>(p, n0, N, count, v);
+}
+template <int M> __device__ __forceinline__ void ssc_store_any(bool vec, float* p, int n0, int N, int count, const float2 (&v)[2][M / 2]) {
+  if (vec) ssc_store_states<M, true>(p, n0, N, count, v);
+  else ssc_store_states<M, false>(p, n0, N, count, v);
+}
+
 // ENDS: only the states that the part ends with, from a state of zero, and its sum of D.
-template <class T, bool EDGE, bool ONE, bool ENDS>
+template <class T, bool EDGE, bool ONE, bool ENDS, int LN>
 __global__ void __launch_bounds__(kSscThreads, 4) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
-  const int NP = ONE ? 16 : a.NP;
+  using S = SscLane<T, EDGE, LN>;
+  using P = typename S::P;
+  constexpr int L = S::L, R = S::R, M = S::M;
   extern __shared__ __align__(16) float2 ssc_shared[];
-  float4* dxs = (float4*)ssc_shared;
-  float2* part = ssc_shared + SscShared::kDx;
-  float2* bs = part + (ENDS ? 0 : SscShared::kPart);
-  float2* cs = bs + kSscTile * NP;
-  float2* hs = bs + kSscTile * NP * (ENDS ? 1 : 2);
-  float2* sums = hs + (ONE ? 0 : NP / 16 * 4 * kSscThreads);
-  using P = SscPair<T, EDGE>;
-  const SscPlace<T> at(a, 0, ENDS ? a.parts - 1 : a.parts);
-  const int NB = NP / 16;
+  const int NB = ONE ? 1 : a.NP / 16;
+  const int lane = threadIdx.x & 31, ln = lane % LN;
+  unsigned char* ring = (unsigned char*)ssc_shared + (threadIdx.x >> 5) * S::warp_bytes(NB);
+  const int stage_bytes = S::stage_bytes(NB);
+  float* vs = (float*)(ring + S::STAGES * stage_bytes);  // B (16) and C (16) of each block's tokens
+  float4* ds = (float4*)(vs + NB * L * 32);           // D and D x (token, pair)
+  float4* hs = ds + L * (32 / LN);                    // states by block, where there are several
+  const SscWarp<T> at(a, LN, ENDS ? a.parts - 1 : a.parts);
+  if (at.idle) return;
   const float2 zero = make_float2(0.f, 0.f);
+  const long long row = at.b * a.D + at.ch;  // of (B, D, N) arrays
 
-  float2 rate[4], h[4];
-  for (int k = 0; k < NB; ++k) {
-    ssc_rates(a, at, k * 16, rate);
+  float2 rate[2][M / 2], h[2][M / 2];
+  const auto rates = [&](int k) {
+    ssc_load_any<M>(a.vec, a.a + (long long)at.ch * a.N, k * 16 + ln * M, a.N, at.count, rate);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int n = ssc_state(k * 16, at.ln, s);
-      h[s] = zero;
-      if constexpr (!ENDS) {
-        if (a.h0) h[s] = ssc_load(a.h0 + (at.b * a.D + at.chb) * a.N, n, a.N, at.countb, 0.f);
-        h[s] = ssc_through(a, at, n, rate[s], h[s], 0, at.part, 1);
-      }
-      if constexpr (!ONE) hs[(k * 4 + s) * kSscThreads + threadIdx.x] = h[s];
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < M / 2; ++j) rate[c][j] = mul2(rate[c][j], make_float2(kLog2e, kLog2e));
+  };
+  const auto put_h = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < M / 2; ++j) hs[(k * M / 2 + j) * 32 + lane] = make_float4(h[0][j].x, h[0][j].y, h[1][j].x, h[1][j].y);
+  };
+  const auto get_h = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < M / 2; ++j) {
+      const float4 q = hs[(k * M / 2 + j) * 32 + lane];
+      h[0][j] = make_float2(q.x, q.y), h[1][j] = make_float2(q.z, q.w);
     }
+  };
+  for (int k = 0; k < NB; ++k) {
+    rates(k);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < M / 2; ++j) h[c][j] = zero;
+    if constexpr (!ENDS) {
+      if (a.h0) ssc_load_any<M>(a.vec, a.h0 + row * a.N, k * 16 + ln * M, a.N, at.count, h);
+      // Through the parts before this one in turn.
+      for (int p = 0; p < at.part; ++p) {
+        const long long pr = at.b * (a.parts - 1) + p;
+        float2 e[2][M / 2];
+        ssc_load_any<M>(a.vec, a.ends + (pr * a.D + at.ch) * a.N, k * 16 + ln * M, a.N, at.count, e);
+        const float* s = a.sums + pr * a.D + at.ch;
+        const float sum[2] = {at.count > 0 ? s[0] : 0.f, at.count > 1 ? s[1] : 0.f};
+        const bool dropped = a.drops[pr] != 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < M / 2; ++j)
+            h[c][j] = dropped ? e[c][j] : fma2(ssc_decay(rate[c][j], make_float2(sum[c], sum[c])), h[c][j], e[c][j]);
+      }
+    }
+    if constexpr (!ONE) put_h(k);
   }
   float2 bias = zero, skip = zero, sum = zero;
   if (a.bias) bias = make_float2(at.count > 0 ? a.bias[at.ch] : 0.f, at.count > 1 ? a.bias[at.ch + 1] : 0.f);
   if (!ENDS && a.d) skip = make_float2(at.count > 0 ? a.d[at.ch] : 0.f, at.count > 1 ? a.d[at.ch + 1] : 0.f);
 
-  const int own = at.warp * kSscRows;  // the warp's first token of a tile in phases A and C
-  const long long t00 = (long long)at.tile0 * kSscTile + own;
-  const T* px = a.x + at.b * a.xb + t00 * a.xt + at.ch;
-  const T* pdt = a.dt + at.b * a.dtb + t00 * a.dtt + at.ch;
-  const T* pz = a.z ? a.z + at.b * a.zb + t00 * a.zt + at.ch : nullptr;
-  const T* pb = a.b + at.b * a.bb + (t00 - own) * a.bt + at.group * a.bg;
-  const T* pc = ENDS ? nullptr : a.c + at.b * a.cb + (t00 - own) * a.ct + at.group * a.cg;
-  T* py = ENDS ? nullptr : a.y + at.b * a.yb + t00 * a.yt + at.ch;
-  unsigned dropped = 0;
+  // The lane's own tokens of a tile are those with (t % LN) = ln.
+  const T* px = a.x + at.b * a.xb;
+  const T* pdt = a.dt + at.b * a.dtb;
+  const bool gated = !ENDS && a.z;
+  const T* pz = gated ? a.z + at.b * a.zb : nullptr;
+  T* py = ENDS ? nullptr : a.y + at.b * a.yb + (long long)(at.t0 + ln) * a.yt + at.ch;
+  const int n = lane & 15;
+  const bool second = !ENDS && lane >= 16;
+  const T* pb = a.b + at.b * a.bb + at.group * a.bg;
+  const T* pc = ENDS ? pb : a.c + at.b * a.cb + at.group * a.cg;
+  const T* pv = second ? pc : pb;
+  const long long sv = second ? a.ct : a.bt;
+  const uint8_t* ps = a.starts ? a.starts + at.b * a.T_ : nullptr;
 
-  for (int tile = at.tile0; tile < at.tile1; ++tile) {
-    const int t0 = tile * kSscTile;
-    // A
-    typename P::Raw x[kSscRows], z[kSscRows];
-    typename P::Raw dt[kSscRows];
+  // Starts a tile's copies into the ring.  EDGE, where they cannot be in pieces of 16 bytes: loads
+  // the tile, for `put` to store behind the one that is worked on.  (No ordinary load goes among
+  // the copies: waiting for it would be waiting for them.)
+  constexpr int V = 16 / sizeof(T), PER = 32 / V;
+  const int own_row = lane / S::CHUNKS, own_c = lane % S::CHUNKS * V;   // the lane's pieces of x, dt, z
+  const int v_row = lane / PER, v_c = lane % PER * V;                   // and of B or C
+  const bool copies = lane < L * S::CHUNKS && own_c < at.width;
+  const T* qx = px + (long long)(at.t0 + own_row) * a.xt + at.base + own_c;
+  const T* qd = pdt + (long long)(at.t0 + own_row) * a.dtt + at.base + own_c;
+  const T* qz = gated ? pz + (long long)(at.t0 + own_row) * a.zt + at.base + own_c : nullptr;
+  const long long qs = v_c < 16 ? a.bt : a.ct;
+  const T* qv = (v_c < 16 ? pb : pc) + (long long)(at.t0 + v_row) * qs + v_c % 16;
+  typename S::Raw ex[EDGE ? R : 1], ed[EDGE ? R : 1], ez[EDGE ? R : 1];
+  T ev[EDGE && ONE ? L : 1];
+  const auto get = [&](int t, int stage) {
+    unsigned char* to_stage = ring + stage * stage_bytes;
+    if (t < at.t1) {
+      if constexpr (EDGE) {
 #pragma unroll
-    for (int i = 0; i < kSscRows; ++i) {
-      const int count = t0 + own + i < a.T_ ? at.count : 0;
-      x[i] = P::load(px + i * a.xt, count);
-      dt[i] = P::load(pdt + i * a.dtt, count);
-      if (!ENDS && pz) z[i] = P::load(pz + i * a.zt, count);
-    }
-    const unsigned starts = ssc_starts(a, at.b, t0, at.lane);
-    dropped |= starts;
-    ssc_vectors(a, pb, a.bt, t0, NP, bs);
-    if constexpr (!ENDS) ssc_vectors(a, pc, a.ct, t0, NP, cs);
-#pragma unroll
-    for (int i = 0; i < kSscRows; ++i) {
-      float2 d = ssc_step_size(a, add2(P::wide(dt[i]), bias));
-      if (t0 + own + i >= a.T_) d = zero;
-      const float2 u = mul2(d, P::wide(x[i]));
-      dxs[(own + i) * 32 + at.lane] = make_float4(d.x, d.y, u.x, u.y);
-      if constexpr (ENDS) sum = add2(sum, d);
-    }
-    __syncthreads();
-    // B
-    for (int k = 0; k < NB; ++k) {
-      if constexpr (!ONE) {
-        ssc_rates(a, at, k * 16, rate);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) h[s] = hs[(k * 4 + s) * kSscThreads + threadIdx.x];
-      }
-      if (!ENDS && a.kept) {
-        float* p = a.kept + ((at.b * a.tiles + tile) * a.D + at.chb) * a.N;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) ssc_store(p, ssc_state(k * 16, at.ln, s), a.N, at.countb, h[s]);
-      }
-#pragma unroll 4
-      for (int t = 0; t < kSscTile; ++t) {
-        const float4 q = dxs[t * 32 + at.pr];
-        const float2 d = make_float2(q.x, q.y), u = make_float2(q.z, q.w);
-        if (starts >> t & 1) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) h[s] = zero;
+        for (int r = 0; r < R; ++r) {
+          const long long row = min(t + ln + r * LN, a.T_ - 1);
+          ex[r] = P::load(px + row * a.xt + at.ch, at.count);
+          ed[r] = P::load(pdt + row * a.dtt + at.ch, at.count);
+          if (gated) ez[r] = P::load(pz + row * a.zt + at.ch, at.count);
         }
-        float2 acc = zero;
+        if constexpr (ONE) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 bv = *(const float4*)(bs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-          h[2 * j] = fma2(ssc_decay(rate[2 * j], d), h[2 * j], mul2(u, make_float2(bv.x, bv.y)));
-          h[2 * j + 1] = fma2(ssc_decay(rate[2 * j + 1], d), h[2 * j + 1], mul2(u, make_float2(bv.z, bv.w)));
-          if constexpr (!ENDS) {
-            const float4 cv = *(const float4*)(cs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-            acc = fma2(h[2 * j], make_float2(cv.x, cv.y), acc);
-            acc = fma2(h[2 * j + 1], make_float2(cv.z, cv.w), acc);
+          for (int i = 0; i < L; ++i) ev[i] = pv[(long long)min(t + i, a.T_ - 1) * sv + (n < a.N ? n : 0)];
+        }
+      } else {
+        // Rows behind the last are read as the last: that many rows back.
+        const bool whole = t + L <= a.T_;
+#pragma unroll
+        for (int q = 0; q < (L * S::CHUNKS + 31) / 32; ++q) {
+          constexpr int ROWS = 32 / S::CHUNKS;
+          const int i = q * ROWS + own_row;
+          const long long back = whole ? q * ROWS : (long long)min(t + i, a.T_ - 1) - (t + own_row);
+          if (copies) {
+            unsigned char* to = to_stage + i * S::ROW + own_c * sizeof(T);
+            cp_async16(to, qx + back * a.xt);
+            cp_async16(to + S::ARRAY, qd + back * a.dtt);
+            if (gated) cp_async16(to + 2 * S::ARRAY, qz + back * a.zt);
           }
         }
-        if constexpr (!ENDS) {
-          if (!ONE && k > 0) acc = add2(acc, part[(t * 32 + at.pr) * 4 + ssc_half(at.pr, at.ln >> 1) * 2 + (at.ln & 1)]);
-          ssc_put(part, t, at.pr, at.ln, acc);
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+          for (int q = 0; q < L * PER / 32; ++q) {
+            const int i = q * (32 / PER) + v_row;
+            const long long back = whole ? q * (32 / PER) : (long long)min(t + i, a.T_ - 1) - (t + v_row);
+            if (k * 16 + v_c % 16 < a.N && (!ENDS || v_c < 16))
+              cp_async16(to_stage + 3 * S::ARRAY + ((k * L + i) * 32 + v_c) * sizeof(T), qv + back * qs + k * 16);
+          }
+        }
+        qx += L * a.xt, qd += L * a.dtt, qv += L * qs;
+        if (gated) qz += L * a.zt;
+      }
+    }
+    cp_async_commit();
+  };
+  const auto put = [&](int stage) {
+    if constexpr (EDGE) {
+      unsigned char* to_stage = ring + stage * stage_bytes;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        typename S::Raw* to = (typename S::Raw*)(to_stage + (ln + r * LN) * S::ROW) + lane / LN;
+        to[0] = ex[r];
+        to[S::ARRAY / sizeof(typename S::Raw)] = ed[r];
+        to[2 * S::ARRAY / sizeof(typename S::Raw)] = ez[r];
+      }
+      if constexpr (ONE) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) ((T*)(to_stage + 3 * S::ARRAY))[i * 32 + lane] = n < a.N ? ev[i] : narrow<T>(0.f);
+      }
+    }
+  };
+  if constexpr (!EDGE) {  // states past the last stay zero
+    for (int k = lane; k < S::STAGES * stage_bytes / 16; k += 32) ((float4*)ring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncwarp();
+  }
+  const auto finish = [&](float2 x, float2 z, float2 y, bool gate, bool there) {
+    float2 v = fma2(skip, x, y);
+    if (gate) v = mul2(v, mul2(z, sigmoid<T>(z)));
+    P::store(py, there ? at.count : 0, v);
+    py += LN * a.yt;
+  };
+  // Each lane the starts of one of the next 32 tiles, a bit a token.
+  const auto flags = [&](int t) {
+    unsigned f = 0;
+    if (ps) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const int u = t + lane * L + i;
+        if (u < at.t1 && ps[u]) f |= 1u << i;
+      }
+    }
+    return f;
+  };
+
+  unsigned flag = 0, dropped = 0;
+#pragma unroll
+  for (int k = 0; k < S::STAGES - 1; ++k) {
+    get(at.t0 + k * L, k);
+    put(k);
+  }
+  int stage = 0;
+  for (int t = at.t0; t < at.t1; t += L) {
+    const int number = (t - at.t0) / L % 32;
+    if (number == 0) flag = flags(t);
+    const unsigned starts = __shfl_sync(0xffffffffu, flag, number);
+    dropped |= starts;
+    cp_async_wait<S::STAGES - 2>();
+    __syncwarp();  // the tile is there, and the one before it is done with
+    const int fill = stage == 0 ? S::STAGES - 1 : stage - 1;
+    get(t + (S::STAGES - 1) * L, fill);
+    const unsigned char* tile = ring + stage * stage_bytes;
+    const auto pair = [&](int array, int r) {
+      return P::wide(((const typename S::Raw*)(tile + array * S::ARRAY + (ln + r * LN) * S::ROW))[lane / LN]);
+    };
+    // B and C of the tile, widened.
+    if constexpr (EDGE && !ONE) {
+      for (int k = 0; k < NB; ++k) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const int s = k * 16 + n;
+          vs[(k * L + i) * 32 + lane] = s < a.N ? widen(pv[(long long)min(t + i, a.T_ - 1) * sv + s]) : 0.f;
         }
       }
+    } else {
+      for (int k = 0; k < NB; ++k) {
+#pragma unroll
+        for (int q = 0; q < L / V; ++q) {
+          const int c = k * L * 32 + (q * 32 + lane) * V;
+          float f[V];
+          widen_pack(ld_pack<T, V>((const T*)(tile + 3 * S::ARRAY) + c), f);
+#pragma unroll
+          for (int e = 0; e < V; e += 4) *(float4*)(vs + c + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+      }
+    }
+    float2 d[R], y[ONE ? 1 : R];  // of the lane's own tokens
+    const auto sizes = [&](auto soft) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        d[r] = add2(pair(1, r), bias);
+        if constexpr (decltype(soft)::value) d[r] = softplus2<T>(d[r]);
+      }
+    };
+    if (a.softplus) sizes(std::true_type());
+    else sizes(std::false_type());
+    const bool whole = t + L <= a.T_;
+    if (!whole) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (t + ln + r * LN >= a.T_) d[r] = zero;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float2 u = mul2(d[r], pair(0, r));
+      ds[(ln + r * LN) * (32 / LN) + lane / LN] = make_float4(d[r].x, d[r].y, u.x, u.y);
+      if constexpr (ENDS) sum = add2(sum, d[r]);
+      if constexpr (!ONE) y[r] = zero;
+    }
+    __syncwarp();
+
+    for (int k = 0; k < NB; ++k) {
       if constexpr (!ONE) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) hs[(k * 4 + s) * kSscThreads + threadIdx.x] = h[s];
+        rates(k);
+        get_h(k);
       }
-    }
-    __syncthreads();
-    // C
-    if constexpr (!ENDS) {
+      if (!ENDS && a.kept && t % kSscTile == 0)
+        ssc_store_any<M>(a.vec, a.kept + ((at.b * a.tiles + t / kSscTile) * a.D + at.ch) * a.N, k * 16 + ln * M, a.N, at.count, h);
+      // A whole tile without starts has no branch between its tokens, so that their instructions mix.
+      const auto tokens = [&](auto plain, auto with_gate) {
+        constexpr bool STARTS = !decltype(plain)::value, GATE = decltype(with_gate)::value;
+        float2 held[LN];  // the lane's part of the last LN tokens' sums
 #pragma unroll
-      for (int i = 0; i < kSscRows; ++i) {
-        float2 y = fma2(skip, P::wide(x[i]), ssc_get(part, own + i, at.lane));
-        if (pz) {
-          const float2 zv = P::wide(z[i]);
-          y = mul2(y, mul2(zv, sigmoid<T>(zv)));
+        for (int i = 0; i < L; ++i) {
+          const int r = i / LN, q = i % LN;
+          const float4 du = ds[i * (32 / LN) + lane / LN];
+          if (STARTS && (starts >> i & 1)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < M / 2; ++j) h[c][j] = zero;
+          }
+          const float4* pbv = (const float4*)(vs + (k * L + i) * 32 + ln * M);
+          const float2 d2[2] = {make_float2(du.x, du.x), make_float2(du.y, du.y)};
+          const float2 u2[2] = {make_float2(du.z, du.z), make_float2(du.w, du.w)};
+          float2 acc[2] = {zero, zero};
+#pragma unroll
+          for (int j = 0; j < M / 4; ++j) {
+            const float4 bv = pbv[j];
+            const float2 b2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
+            float2 c2[2];
+            if constexpr (!ENDS) {
+              const float4 cv = pbv[4 + j];
+              c2[0] = make_float2(cv.x, cv.y), c2[1] = make_float2(cv.z, cv.w);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                float2& hh = h[c][2 * j + m];
+                hh = ssc_fma(ssc_decay(rate[c][2 * j + m], d2[c]), hh, mul2(u2[c], b2[m]));
+                if constexpr (!ENDS) acc[c] = ssc_fma(hh, c2[m], acc[c]);
+              }
+            }
+          }
+          if constexpr (!ENDS) {
+            held[q] = make_float2(acc[0].x + acc[0].y, acc[1].x + acc[1].y);
+            if (q == LN - 1) {  // over the lanes: each ends with the sum of its own token
+#pragma unroll
+              for (int bit = 1; bit < LN; bit *= 2) {
+                const bool up = ln & bit;
+#pragma unroll
+                for (int p = 0; p < LN / (2 * bit); ++p) {
+                  const float2 send = up ? held[2 * p] : held[2 * p + 1], keep = up ? held[2 * p + 1] : held[2 * p];
+                  held[p] = add2(keep, make_float2(__shfl_xor_sync(0xffffffffu, send.x, bit), __shfl_xor_sync(0xffffffffu, send.y, bit)));
+                }
+              }
+              if constexpr (ONE) {
+                if constexpr (STARTS) finish(pair(0, r), gated ? pair(2, r) : zero, held[0], gated, t + ln + r * LN < a.T_);
+                else finish(pair(0, r), GATE ? pair(2, r) : zero, held[0], GATE, true);
+              } else {
+                y[r] = add2(y[r], held[0]);
+              }
+            }
+          }
         }
-        P::store(py + i * a.yt, t0 + own + i < a.T_ ? at.count : 0, y);
-      }
-      py += kSscTile * a.yt;
-      pc += kSscTile * a.ct;
-      if (pz) pz += kSscTile * a.zt;
+      };
+      if (starts || !whole) tokens(std::false_type(), std::false_type());
+      else if (gated) tokens(std::true_type(), std::true_type());
+      else tokens(std::true_type(), std::false_type());
+      if constexpr (!ONE) put_h(k);
     }
-    px += kSscTile * a.xt, pdt += kSscTile * a.dtt, pb += kSscTile * a.bt;
+    if constexpr (!ONE && !ENDS) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) finish(pair(0, r), gated ? pair(2, r) : zero, y[r], gated, t + ln + r * LN < a.T_);
+    }
+    put(fill);
+    stage = stage == S::STAGES - 1 ? 0 : stage + 1;
   }
 
   float* out = nullptr;
   if constexpr (ENDS) {
-    const long long row = at.b * (a.parts - 1) + at.part;
-    out = a.ends + (row * a.D + at.chb) * a.N;
-    ssc_write_sums(a, at, sum, dropped != 0, row, sums);
+    const long long pr = at.b * (a.parts - 1) + at.part;
+    out = a.ends + (pr * a.D + at.ch) * a.N;
+#pragma unroll
+    for (int bit = 1; bit < LN; bit *= 2)
+      sum = add2(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, bit), __shfl_xor_sync(0xffffffffu, sum.y, bit)));
+    if (ln == 0) {
+      if (at.count > 0) a.sums[pr * a.D + at.ch] = sum.x;
+      if (at.count > 1) a.sums[pr * a.D + at.ch + 1] = sum.y;
+    }
+    if (lane == 0 && at.ch == 0) a.drops[pr] = dropped ? 1.f : 0.f;
   } else {
-    if (a.last && at.part == a.parts - 1) out = a.last + (at.b * a.D + at.chb) * a.N;
+    if (a.last && at.part == a.parts - 1) out = a.last + row * a.N;
   }
   if (out) {
     for (int k = 0; k < NB; ++k) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float2 v = ONE ? h[s] : hs[(k * 4 + s) * kSscThreads + threadIdx.x];
-        ssc_store(out, ssc_state(k * 16, at.ln, s), a.N, at.countb, v);
-      }
+      if constexpr (!ONE) get_h(k);
+      ssc_store_any<M>(a.vec, out, k * 16 + ln * M, a.N, at.count, h);
     }
   }
 }
@@ -894,10 +1203,14 @@ __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ S
 
 // ---- launches --------------------------------------------------------------------------
 
-// Whether pairs of values can be read and written in every row of the array.
-template <class T> bool ssc_rows(const SeqArray& s, long long B, long long T_) {
+// Whether every row of the array starts on a boundary of V values.
+template <class T> bool ssc_rows(const SeqArray& s, int V, long long B, long long T_) {
   if (!s.p) return true;
-  return (uintptr_t)s.p % (2 * sizeof(T)) == 0 && (B <= 1 || s.sb % 2 == 0) && (T_ <= 1 || s.st % 2 == 0);
+  return (uintptr_t)s.p % (V * sizeof(T)) == 0 && (B <= 1 || s.sb % V == 0) && (T_ <= 1 || s.st % V == 0);
+}
+template <class T> bool ssc_rows(const GroupArray& s, int V, long long B, long long T_, long long G) {
+  return (uintptr_t)s.p % (V * sizeof(T)) == 0 && (B <= 1 || s.sb % V == 0) && (T_ <= 1 || s.st % V == 0) &&
+         (G <= 1 || s.sg % V == 0);
 }
 
 template <class T> SscArgs<T> ssc_args(const SelectiveScanJob& j, const SscSplit& split) {
@@ -918,6 +1231,8 @@ template <class T> SscArgs<T> ssc_args(const SelectiveScanJob& j, const SscSplit
   a.G = (int)j.G, a.DG = (int)(j.D / j.G), a.blocks = (a.DG + kSscChannels - 1) / kSscChannels;
   a.tiles = (int)((j.T + kSscTile - 1) / kSscTile);
   a.parts = (int)split.parts, a.part_tiles = (int)split.tiles, a.softplus = j.softplus;
+  a.vec = j.N % 4 == 0;
+  for (const void* q : {(const void*)j.a, (const void*)j.h0, (const void*)j.last, (const void*)j.kept}) a.vec = a.vec && (uintptr_t)q % 16 == 0;
   float* p = (float*)j.temp;
   a.ends = p;
   a.sums = a.ends + j.B * (split.parts - 1) * j.D * j.N;
@@ -934,16 +1249,17 @@ template <class K, class A> cudaError_t ssc_launch(K kernel, long long grid, siz
   return launch_pdl(kernel, (unsigned)grid, kSscThreads, smem, ctx.stream, a);
 }
 
-template <class T, bool EDGE, bool ONE> cudaError_t ssc_forward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  const SscSplit split = ssc_split(j.B, j.T, j.D, j.G, false);
-  const SscArgs<T> a = ssc_args<T>(j, split);
-  const long long units = j.B * a.G * a.blocks;
+template <class T, bool EDGE, bool ONE, int LN> cudaError_t ssc_forward(const SelectiveScanJob& j, const SscForwardPlan& plan, const LaunchCtx& ctx) {
+  const SscArgs<T> a = ssc_args<T>(j, plan.split);
+  const long long units = j.B * a.G * ((a.DG + 64 / LN - 1) / (64 / LN));
+  const auto grid = [&](long long parts) { return (units * parts + kSscThreads / 32 - 1) / (kSscThreads / 32); };
+  using S = SscLane<T, EDGE, LN>;
+  const int NB = ONE ? 1 : a.NP / 16;
+  const size_t smem = (size_t)(kSscThreads / 32) * S::warp_bytes(NB);
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
-  if (split.parts > 1)
-    e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, true>, units * (split.parts - 1), SscShared::forward(a.NP, true), a, ctx);
-  if (e == cudaSuccess)
-    e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, false>, units * split.parts, SscShared::forward(a.NP, false), a, ctx);
+  if (plan.split.parts > 1) e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, true, LN>, grid(plan.split.parts - 1), smem, a, ctx);
+  if (e == cudaSuccess) e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, false, LN>, grid(plan.split.parts), smem, a, ctx);
   profile_after(ctx);
   return e;
 }
@@ -975,16 +1291,21 @@ template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const Selective
   return e;
 }
 
+template <class T, bool EDGE> cudaError_t ssc_forward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
+  const SscForwardPlan plan = ssc_forward_plan(j.B, j.T, j.D, j.G);
+  if (j.N > 16) return ssc_forward<T, EDGE, false, 4>(j, plan, ctx);
+  return plan.lanes == 2 ? ssc_forward<T, EDGE, true, 2>(j, plan, ctx) : ssc_forward<T, EDGE, true, 4>(j, plan, ctx);
+}
 template <class T> cudaError_t launch_selective_scan(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  bool even = (j.D / j.G) % 2 == 0;
-  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.y}) even = even && ssc_rows<T>(*s, j.B, j.T);
-  if (j.N <= 16) return even ? ssc_forward<T, false, true>(j, ctx) : ssc_forward<T, true, true>(j, ctx);
-  return even ? ssc_forward<T, false, false>(j, ctx) : ssc_forward<T, true, false>(j, ctx);
+  constexpr int V = 16 / sizeof(T);
+  bool even = (j.D / j.G) % V == 0 && j.N % V == 0 && ssc_rows<T>(j.b, V, j.B, j.T, j.G) && ssc_rows<T>(j.c, V, j.B, j.T, j.G);
+  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.y}) even = even && ssc_rows<T>(*s, V, j.B, j.T);
+  return even ? ssc_forward_any<T, false>(j, ctx) : ssc_forward_any<T, true>(j, ctx);
 }
 
 template <class T> cudaError_t launch_selective_scan_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
   bool even = (j.D / j.G) % 2 == 0;
-  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.dy, &j.dx, &j.ddt, &j.dz}) even = even && ssc_rows<T>(*s, j.B, j.T);
+  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.dy, &j.dx, &j.ddt, &j.dz}) even = even && ssc_rows<T>(*s, 2, j.B, j.T);
   if (j.N <= 16) return even ? ssc_backward<T, false, true>(j, ctx) : ssc_backward<T, true, true>(j, ctx);
   return even ? ssc_backward<T, false, false>(j, ctx) : ssc_backward<T, true, false>(j, ctx);
 }
