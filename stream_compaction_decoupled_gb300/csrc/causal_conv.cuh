@@ -13,7 +13,10 @@
 // side where all rows allow vectors of them, or 32 apart, where single values of 32 lanes are
 // neighbours.  The window of inputs moves along in registers, so x is read once but for the
 // taps - 1 tokens before a run (the gradient: and after it).  How far the window reaches back
-// into its document is one number for the whole warp: `age`, the tokens since the start.
+// into its document is one number for the whole warp: `age`, the tokens since the start.  What a
+// warp reads comes by asynchronous copies into a ring of its own in shared memory (registers alone
+// held too few bytes in flight: 8 x 2048 x 2048 bf16 49 us), or, where rows are not on 16-byte
+// boundaries, by loads a group of tokens ahead.
 #pragma once
 
 #include "lm.cuh"
@@ -169,11 +172,123 @@ __device__ __forceinline__ int conv_window(const ConvArgs<T>& a, const L& lane, 
   return age;
 }
 
+// Start flags of a run's tokens, 128 at a time (an ordinary load among asynchronous copies waits
+// for them): bit k of get(t) is token t + k's, for t that go up by the same divisor of 32 from the
+// first.
+struct ConvFlags {
+  const uint8_t* p;
+  int from, end;
+  unsigned bits[4] = {0, 0, 0, 0};
+  __device__ __forceinline__ ConvFlags(const uint8_t* p_, int t0, int t1) : p(p_), from(t0), end(t1) {
+    if (p) read();
+  }
+  __device__ __forceinline__ void read() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = from + 32 * k + (int)(threadIdx.x & 31);
+      bits[k] = __ballot_sync(0xffffffffu, t < end && p[t] != 0);
+    }
+  }
+  __device__ __forceinline__ unsigned get(int t) {
+    if (!p) return 0;
+    if (t - from >= 128) {
+      from += 128;
+      read();
+    }
+    const int k = (t - from) >> 5;
+    const unsigned lo = k & 1 ? bits[1] : bits[0], hi = k & 1 ? bits[3] : bits[2];
+    return (k & 2 ? hi : lo) >> ((t - from) & 31);
+  }
+};
+
+// Where a warp's rows come through: STAGES groups of U rows of each of ARRAYS arrays, copied
+// STAGES - 1 groups ahead; EDGE: one group, in registers.
+template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
+  using L = ConvLane<T, V, EDGE>;
+  static constexpr int STAGES = 4, ROW = 32 * V * (int)sizeof(T), STAGE = ARRAYS * U * ROW;
+  static constexpr int CHUNKS = ROW / 16, ROWS = 32 / CHUNKS;  // 16-byte copies of a row, rows a copy of all lanes
+  static constexpr int BYTES = EDGE ? 0 : STAGES * STAGE;      // a warp
+  static_assert(EDGE || (ROWS >= 1 && U % ROWS == 0), "whole rows");
+  const L& lane;
+  unsigned char* ring;
+  const T* p[ARRAYS];      // the next group's first row (the lane's part of it)
+  long long stride[ARRAYS];
+  int next, stop, stage = 0, own_row = 0;
+  bool copies = false;
+  typename L::Raw raw[EDGE ? ARRAYS : 1][EDGE ? U : 1];
+
+  // Rows `first` .. stop - 1; p: row 0 of each array.
+  __device__ __forceinline__ ConvRing(const L& lane_, unsigned char* ring_, const T* const (&rows)[ARRAYS],
+                                      const long long (&strides)[ARRAYS], int group, int D, int first, int stop_)
+      : lane(lane_), ring(ring_), next(first), stop(stop_) {
+    const int l = threadIdx.x & 31;
+    if constexpr (!EDGE) own_row = l / CHUNKS, copies = group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)) < D;
+#pragma unroll
+    for (int k = 0; k < ARRAYS; ++k) {
+      stride[k] = strides[k];
+      p[k] = rows[k] + (long long)(first + own_row) * strides[k] +
+             (EDGE ? 0 : group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)));
+    }
+    if constexpr (EDGE) {
+      fill();
+    } else {
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) fill();  // groups 0 .. STAGES - 2; the last place is empty
+    }
+  }
+  // Asks for the next group.
+  __device__ __forceinline__ void fill() {
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[k][u] = next + u < stop ? lane.load(p[k] + u * stride[k]) : lane.zero();
+        p[k] += U * stride[k];
+      }
+    } else {
+      unsigned char* to = ring + stage * STAGE + own_row * ROW + (threadIdx.x & 31) % CHUNKS * 16;
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k) {
+#pragma unroll
+        for (int u = 0; u < U; u += ROWS)
+          if (copies && next + u + own_row < stop) cp_async16(to + (k * U + u) * ROW, p[k] + u * stride[k]);
+        p[k] += U * stride[k];
+      }
+      cp_async_commit();
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    }
+    next += U;
+  }
+  // The group that was asked for first, widened; asks for another.  Rows from `stop` on are undefined.
+  __device__ __forceinline__ void take(float2 (&f)[ARRAYS][U][V / 2]) {
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u) lane.widen_to(raw[k][u], f[k][u]);
+      fill();  // under way while these are worked on
+    } else {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();  // the group is there, and the one before it, which is filled again, read by all
+      // `stage` is filled next: the group read here is the one after it in the ring.
+      const int at = stage == STAGES - 1 ? 0 : stage + 1;
+      const unsigned char* from = ring + at * STAGE + (threadIdx.x & 31) * V * (int)sizeof(T);
+      fill();
+#pragma unroll
+      for (int k = 0; k < ARRAYS; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u) lane.widen_to(*(const typename L::Raw*)(from + (k * U + u) * ROW), f[k][u]);
+    }
+  }
+};
+
+template <class T, int W> constexpr int kConvGroup = W == 4 && sizeof(T) == 2 ? 8 : 4;  // tokens of a group
+
 template <class T, int W, int V, bool EDGE>
-__global__ void __launch_bounds__(128) conv_forward_kernel(const __grid_constant__ ConvArgs<T> a) {
+__global__ void __launch_bounds__(128, W == 4 && !EDGE ? 4 : 3) conv_forward_kernel(const __grid_constant__ ConvArgs<T> a) {
   pdl_entry();
   using L = ConvLane<T, V, EDGE>;
-  constexpr int H = V / 2, U = 4;  // tokens whose loads are in flight together
+  constexpr int H = V / 2, U = kConvGroup<T, W>;  // tokens whose loads are in flight together
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= a.units) return;
   const int group = (int)(unit % a.groups);
@@ -194,50 +309,52 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(const __grid_constant
   for (int h = 0; h < H; ++h) bias[h] = make_float2(0.f, 0.f);
   if (a.bias) lane.params(a.bias, 1, 0, a.wide, bias);
   int age = conv_window<T, W>(a, lane, b, t0, hist);
-  const T* px = a.x + b * a.xb + (long long)t0 * a.xt;
   T* py = a.y + b * a.yb + (long long)t0 * a.yt;
-  const uint8_t* ps = a.starts ? a.starts + b * a.T_ : nullptr;
+  ConvFlags flags(a.starts ? a.starts + b * a.T_ : nullptr, t0, t1);
+  using Ring = ConvRing<T, V, U, 1, EDGE>;
+  extern __shared__ __align__(16) unsigned char conv_shared[];
+  Ring ring(lane, conv_shared + (threadIdx.x >> 5) * Ring::BYTES, {a.x + b * a.xb}, {a.xt}, group, a.D, t0, t1);
   for (int t = t0; t < t1; t += U) {
-    float2 xs[U][H];
-    typename L::Raw raw[U];
-    unsigned flag[U];
+    float2 in[1][U][H], (&xs)[U][H] = in[0];
+    ring.take(in);
+    const unsigned flag = flags.get(t) & ((1u << U) - 1);
+    const auto token = [&](int u, int reach) {
+      float2 p[H];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      raw[u] = t + u < t1 ? lane.load(px + u * a.xt) : lane.zero();
-      flag[u] = ps && t + u < t1 ? ps[t + u] : 0;
-    }
-    int live = 0;
+      for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u < t1) {
-        lane.widen_to(raw[u], xs[u]);
-        age = flag[u] ? 0 : age + 1;
-        const int reach = min(a.taps - 1, age);
-        float2 p[H];
+      for (int j = 1; j < W; ++j) {
+        if (j <= reach) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
-#pragma unroll
-        for (int j = 1; j < W; ++j) {
-          if (j <= reach) {
-#pragma unroll
-            for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
-          }
+          for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
         }
-        if (a.silu) {
+      }
+      if (a.silu) {
 #pragma unroll
-          for (int h = 0; h < H; ++h) p[h] = mul2(p[h], sigmoid<T>(p[h]));
+        for (int h = 0; h < H; ++h) p[h] = mul2(p[h], sigmoid<T>(p[h]));
+      }
+      lane.store(py + u * a.yt, lane.narrowed(p));
+    };
+    if (flag == 0 && age >= W - 1 && a.taps == W && t + U <= t1) {  // the whole window, four times
+#pragma unroll
+      for (int u = 0; u < U; ++u) token(u, W - 1);
+      age += U;
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u < t1) {
+          age = flag >> u & 1 ? 0 : age + 1;
+          token(u, min(a.taps - 1, age));
         }
-        lane.store(py + u * a.yt, lane.narrowed(p));
-        live = u + 1;
       }
     }
-    if (live == U) {
+    if (t + U <= t1) {
 #pragma unroll
       for (int k = 0; k < W - 1; ++k)
 #pragma unroll
         for (int h = 0; h < H; ++h) hist[k][h] = k + U < W - 1 ? hist[k + U < W - 1 ? k + U : 0][h] : xs[k + U < W - 1 ? 0 : k + U - (W - 1)][h];
     } else {  // the last tokens of a row: one at a time
-      for (int u = 0; u < live; ++u) {
+      for (int u = 0; u < t1 - t; ++u) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
@@ -248,7 +365,6 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(const __grid_constant
           for (int h = 0; h < H; ++h) xs[k][h] = xs[k + 1][h];
       }
     }
-    px += U * a.xt;
     py += U * a.yt;
   }
   if (a.last && t1 == a.T_) {  // the newest inputs, of the last document only
@@ -265,7 +381,7 @@ __global__ void __launch_bounds__(128) conv_forward_kernel(const __grid_constant
 // tokens after them.  pend: dx of the newest W tokens, by their number modulo W.  With very many
 // batch rows a warp takes every slots-th of them, so that there are not as many partial sums.
 template <class T, int W, int V, bool EDGE>
-__global__ void __launch_bounds__(128) conv_backward_kernel(const __grid_constant__ ConvArgs<T> a) {
+__global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_kernel(const __grid_constant__ ConvArgs<T> a) {
   pdl_entry();
   using L = ConvLane<T, V, EDGE>;
   constexpr int H = V / 2;
@@ -294,88 +410,100 @@ __global__ void __launch_bounds__(128) conv_backward_kernel(const __grid_constan
 #pragma unroll
       for (int h = 0; h < H; ++h) pend[j][h] = zero;
     int age = conv_window<T, W>(a, lane, b, t0, hist);
-    const T* px = a.x + b * a.xb + (long long)t0 * a.xt;
-    const T* pg = a.dy + b * a.dyb + (long long)t0 * a.dyt;
-    const uint8_t* ps = a.starts ? a.starts + b * a.T_ : nullptr;
-    const int end = t1 + W - 1;
+    T* po = a.dx + b * a.dxb + (long long)(t0 - (W - 1)) * a.dxt;  // of the token that takes nothing more
+    const int end = t1 + W - 1, stop = min(a.T_, end);  // tokens from `stop` on give nothing
+    ConvFlags flags(a.starts ? a.starts + b * a.T_ : nullptr, t0, stop);
+    using Ring = ConvRing<T, V, W, 2, EDGE>;
+    extern __shared__ __align__(16) unsigned char conv_shared[];
+    if constexpr (!EDGE) {  // the ring's last copies of the row before
+      cp_async_wait<0>();
+      __syncwarp();
+    }
+    Ring ring(lane, conv_shared + (threadIdx.x >> 5) * Ring::BYTES, {a.x + b * a.xb, a.dy + b * a.dyb}, {a.xt, a.dyt}, group,
+              a.D, t0, stop);
     for (int t = t0; t < end; t += W) {
-      float2 xs[W][H];
-      typename L::Raw raw[W], graw[W];
-      unsigned flag[W];
+      float2 in[2][W][H], (&xs)[W][H] = in[0], (&gs)[W][H] = in[1];
+      ring.take(in);
+      const unsigned flag = flags.get(t) & ((1u << W) - 1);
+      const auto token = [&](int u, int reach, bool own) {
+        float2 q[H];
+        if (a.silu) {
+          float2 p[H];
 #pragma unroll
-      for (int u = 0; u < W; ++u) {
-        const bool here = t + u < a.T_ && t + u < end;
-        raw[u] = here ? lane.load(px + u * a.xt) : lane.zero();
-        graw[u] = here ? lane.load(pg + u * a.dyt) : lane.zero();
-        flag[u] = ps && here ? ps[t + u] : 0;
-      }
+          for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
 #pragma unroll
-      for (int u = 0; u < W; ++u) {
-        lane.widen_to(raw[u], xs[u]);
-        if (t + u < a.T_ && t + u < end) {
-          age = flag[u] ? 0 : age + 1;
-          const int reach = min(a.taps - 1, age);
-          float2 q[H];
-          lane.widen_to(graw[u], q);
-          if (a.silu) {
-            float2 p[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) p[h] = fma2(w[0][h], xs[u][h], bias[h]);
-#pragma unroll
-            for (int j = 1; j < W; ++j) {
-              if (j <= reach) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < H; ++h) {  // act' = s + p s (1 - s)
-              const float2 s = sigmoid<T>(p[h]);
-              const float2 c = fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
-              q[h] = mul2(q[h], fma2(mul2(p[h], s), c, s));
-            }
-          }
-          const bool own = t + u < t1;
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
+          for (int j = 1; j < W; ++j) {
             if (j <= reach) {
 #pragma unroll
-              for (int h = 0; h < H; ++h) {
-                const float2 xv = u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h];
-                pend[(u - j + W) % W][h] = fma2(w[j][h], q[h], pend[(u - j + W) % W][h]);
-                if (own) dw[j][h] = fma2(q[h], xv, dw[j][h]);
-              }
+              for (int h = 0; h < H; ++h) p[h] = fma2(w[j][h], u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h], p[h]);
             }
           }
-          if (own) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) db[h] = add2(db[h], q[h]);
+          for (int h = 0; h < H; ++h) {  // act' = s + p s (1 - s)
+            const float2 s = sigmoid<T>(p[h]);
+            const float2 c = fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+            q[h] = mul2(gs[u][h], fma2(mul2(p[h], s), c, s));
           }
-        }
-        // Token t + u - (W - 1) takes nothing more.
-        const int done = t + u - (W - 1);
-        constexpr int kNext = 1;
-        float2(&out)[H] = pend[(u + kNext) % W];
-        if (done < t1 && (done >= t0 || (run == 0 && done >= 1 - a.taps))) {
-          const int k = done - (a.T_ - (a.taps - 1));  // its place in the last state
-          if (a.dlast && k >= 0 && a.T_ - 1 - done <= age) {
-            float2 g[H];
-            lane.widen_to(lane.load(a.dlast + (b * (a.taps - 1) + k) * a.D), g);
+        } else {
 #pragma unroll
-            for (int h = 0; h < H; ++h) out[h] = add2(out[h], g[h]);
-          }
-          if (done >= 0) lane.store(a.dx + b * a.dxb + (long long)done * a.dxt, lane.narrowed(out));
-          else if (a.dstate) lane.store(a.dstate + (b * (a.taps - 1) + a.taps - 1 + done) * a.D, lane.narrowed(out));
+          for (int h = 0; h < H; ++h) q[h] = gs[u][h];
         }
 #pragma unroll
-        for (int h = 0; h < H; ++h) out[h] = zero;
+        for (int j = 0; j < W; ++j) {
+          if (j <= reach) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const float2 xv = u >= j ? xs[u >= j ? u - j : 0][h] : hist[u >= j ? 0 : W - 1 + u - j][h];
+              pend[(u - j + W) % W][h] = fma2(w[j][h], q[h], pend[(u - j + W) % W][h]);
+              if (own) dw[j][h] = fma2(q[h], xv, dw[j][h]);
+            }
+          }
+        }
+        if (own) {
+#pragma unroll
+          for (int h = 0; h < H; ++h) db[h] = add2(db[h], q[h]);
+        }
+      };
+      // Token t + u - (W - 1) takes nothing more after token t + u.
+      if (flag == 0 && age >= W - 1 && a.taps == W && t + W <= t1 && t >= t0 + W - 1) {
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+          token(u, W - 1, true);
+          float2(&out)[H] = pend[(u + 1) % W];
+          lane.store(po + u * a.dxt, lane.narrowed(out));
+#pragma unroll
+          for (int h = 0; h < H; ++h) out[h] = zero;
+        }
+        age += W;
+      } else {
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+          if (t + u < stop) {
+            age = flag >> u & 1 ? 0 : age + 1;
+            token(u, min(a.taps - 1, age), t + u < t1);
+          }
+          const int done = t + u - (W - 1);
+          float2(&out)[H] = pend[(u + 1) % W];
+          if (done < t1 && (done >= t0 || (run == 0 && done >= 1 - a.taps))) {
+            const int k = done - (a.T_ - (a.taps - 1));  // its place in the last state
+            if (a.dlast && k >= 0 && a.T_ - 1 - done <= age) {
+              float2 g[H];
+              lane.widen_to(lane.load(a.dlast + (b * (a.taps - 1) + k) * a.D), g);
+#pragma unroll
+              for (int h = 0; h < H; ++h) out[h] = add2(out[h], g[h]);
+            }
+            if (done >= 0) lane.store(po + u * a.dxt, lane.narrowed(out));
+            else if (a.dstate) lane.store(a.dstate + (b * (a.taps - 1) + a.taps - 1 + done) * a.D, lane.narrowed(out));
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) out[h] = zero;
+        }
       }
 #pragma unroll
       for (int k = 0; k < W - 1; ++k)
 #pragma unroll
         for (int h = 0; h < H; ++h) hist[k][h] = xs[k + 1][h];
-      px += W * a.xt;
-      pg += W * a.dyt;
+      po += W * a.dxt;
     }
   }
   if (a.part) {  // (run, tap or bias, channel)
@@ -516,19 +644,26 @@ template <class T> ConvArgs<T> conv_args(const CausalConvJob& j) {
   return a;
 }
 
+template <class K, class T> cudaError_t conv_launch(K kernel, const ConvArgs<T>& a, int smem, const LaunchCtx& ctx) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, (unsigned)((a.units + 3) / 4), 128, (size_t)smem, ctx.stream, a);
+}
+
 template <class T, int W, int V, bool EDGE> cudaError_t conv_forward(const CausalConvJob& j, const LaunchCtx& ctx) {
   ConvArgs<T> a = conv_args<T>(j);
   a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
-  // Some 24 warps an SM, and runs of 16 tokens at least: each reads taps - 1 tokens again.
-  long long runs = (24ll * ctx.num_sms + a.groups * j.B - 1) / (a.groups * j.B);
+  // As many warps as fit an SM, and runs of 16 tokens at least: each reads taps - 1 tokens again.
+  long long runs = (W == 4 && !EDGE ? 16ll : 12ll) * ctx.num_sms / (a.groups * j.B);
+  if (runs < 1) runs = 1;
   long long length = (j.T + runs - 1) / runs;
-  length = length < 16 ? 16 : (length + 3) / 4 * 4;
+  length = length < 16 ? 16 : (length + 7) / 8 * 8;
   a.length = (int)length;
   a.runs = j.T ? (int)((j.T + length - 1) / length) : 1;
   a.units = j.B * a.runs * a.groups;
   profile_before(ctx);
   const cudaError_t e =
-      launch_pdl(conv_forward_kernel<T, W, V, EDGE>, (unsigned)((a.units + 3) / 4), 128, 0, ctx.stream, a);
+      conv_launch(conv_forward_kernel<T, W, V, EDGE>, a, 4 * ConvRing<T, V, kConvGroup<T, W>, 1, EDGE>::BYTES, ctx);
   profile_after(ctx);
   return e;
 }
@@ -542,7 +677,7 @@ template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const Caus
   a.part = j.dw || j.db ? (float*)j.temp : nullptr;
   profile_before(ctx);
   cudaError_t e =
-      launch_pdl(conv_backward_kernel<T, W, V, EDGE>, (unsigned)((a.units + 3) / 4), 128, 0, ctx.stream, a);
+      conv_launch(conv_backward_kernel<T, W, V, EDGE>, a, 4 * ConvRing<T, V, W, 2, EDGE>::BYTES, ctx);
   if (e == cudaSuccess && a.part) {
     ConvFoldArgs<T> f = {};
     f.part = a.part, f.dw = j.dw, f.db = j.db, f.rows = s.slots * s.runs;
@@ -553,17 +688,19 @@ template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const Caus
   return e;
 }
 
+// Rows that are copied start on 16-byte boundaries; the others are read and written V values at once.
 template <class T> cudaError_t launch_causal_conv(const CausalConvJob& j, const LaunchCtx& ctx) {
-  constexpr int V = 4;
-  const bool even = j.D % V == 0 && conv_rows<T>(j.x, V, j.B, j.T) && conv_rows<T>(j.y, V, j.B, j.T) &&
+  constexpr int V = 4, C = 16 / sizeof(T);
+  const bool even = j.D % C == 0 && conv_rows<T>(j.x, C, j.B, j.T) && conv_rows<T>(j.y, V, j.B, j.T) &&
                     conv_dense<T>(j.state, V) && conv_dense<T>(j.last, V);
   if (j.taps <= 4) return even ? conv_forward<T, 4, V, false>(j, ctx) : conv_forward<T, 4, V, true>(j, ctx);
   return even ? conv_forward<T, 8, V, false>(j, ctx) : conv_forward<T, 8, V, true>(j, ctx);
 }
 
 template <class T> cudaError_t launch_causal_conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
+  constexpr int C = 16 / sizeof(T);
   const int V = j.taps <= 4 ? 4 : 2;
-  const bool even = j.D % V == 0 && conv_rows<T>(j.x, V, j.B, j.T) && conv_rows<T>(j.dy, V, j.B, j.T) &&
+  const bool even = j.D % C == 0 && conv_rows<T>(j.x, C, j.B, j.T) && conv_rows<T>(j.dy, C, j.B, j.T) &&
                     conv_rows<T>(j.dx, V, j.B, j.T) && conv_dense<T>(j.state, V) && conv_dense<T>(j.dlast, V) &&
                     conv_dense<T>(j.dstate, V);
   if (j.taps <= 4) return even ? conv_backward<T, 4, 4, false>(j, ctx) : conv_backward<T, 4, 4, true>(j, ctx);

@@ -14,7 +14,8 @@
 //
 // Bound by memory: one or two rows of V.  A request's row is cut among the CTAs of a cluster and
 // their warps.  One pass finds the warps' sums; the CTAs exchange theirs through the cluster, and
-// the one warp within whose slice the draw falls reads it again, some thousand values.
+// the one within whose slice the draw falls reads that warp's part of it again, all threads together:
+// a thread a few values, a scan over the threads.
 #pragma once
 
 #include "lm.cuh"
@@ -22,7 +23,7 @@
 
 namespace gbs {
 
-constexpr int kVerifyWarps = 16;
+constexpr int kVerifyWarps = 8, kVerifyThreads = 32 * kVerifyWarps;
 
 template <class T> struct VerifyArgs {
   const T *target, *draft;
@@ -57,38 +58,63 @@ __device__ __forceinline__ float verify_rest(float p, float q, float& lost) {
 
 // The rows that a request's draw is made from.
 template <class T> struct VerifyRow {
-  const T *p, *q;    // q null: nothing is taken off
+  const T *p, *q;     // q: what is taken off (without a drafter's probabilities: not read)
   long long without;  // the token that is left out, or -1
-  template <int V> __device__ __forceinline__ void load(long long at, long long end, float (&pv)[V], float (&qv)[V]) const {
-    if (at < end) {
-      widen_pack(ld_pack<T, V>(p + at), pv);
-      if (q) widen_pack(ld_pack<T, V>(q + at), qv);
+};
+// What a lane reads at once of p (and q): U packs of V values, `step` apart.
+template <class T, int V, int U, bool Q> struct VerifyPiece {
+  Pack<T, V> p[U], q[U];
+  // Packs past `left` values from `at` are read as the pack at `at`, which exists.
+  __device__ __forceinline__ void load(const VerifyRow<T>& r, long long at, int step, long long left) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long k = at + (u * step < left ? u * step : 0);
+      p[u] = ld_pack<T, V>(r.p + k);
+      if constexpr (Q) q[u] = ld_pack<T, V>(r.q + k);
     }
+  }
+  // What is left of pack u, and what the differences' roundings lost.  out: the place in the pack
+  // of the token that is left out.
+  __device__ __forceinline__ void rest(int u, bool there, long long out, float (&d)[V], float (&lost)[V]) const {
+    float pv[V], qv[V];
+    widen_pack(p[u], pv);
+    if constexpr (Q) widen_pack(q[u], qv);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      if (at >= end) pv[e] = 0.f;
-      if (at >= end || !q) qv[e] = 0.f;
-      if (at + e == without) pv[e] = 0.f;
-      qv[e] = fmaxf(qv[e], 0.f);
+      if (!there || (!Q && e == out)) pv[e] = 0.f;
+      if constexpr (Q) {
+        d[e] = verify_rest(pv[e], fmaxf(qv[e], 0.f), lost[e]);
+      } else {
+        d[e] = pv[e] > 0.f ? pv[e] : 0.f;
+        lost[e] = 0.f;
+      }
     }
   }
 };
 
-template <class T, int V> __device__ double verify_sum(const VerifyRow<T>& r, long long s0, long long s1, int lane) {
-  constexpr int U = 4;
+template <class T, int V, bool Q> __device__ double verify_sum(const VerifyRow<T>& r, long long s0, long long s1, int lane) {
+  constexpr int U = V == 1 ? 16 : 4;
   VerifySum sum;
-  for (long long at = s0 + lane * V; at < s1; at += 32 * V * U) {
-    float p[U][V], q[U][V];
+  // A lane past the end of the slice reads its last pack, and counts it as nothing.
+  for (long long from = s0; from < s1; from += 32 * V * U) {
+    const long long left = s1 - from;
+    const int own = lane * V;
+    VerifyPiece<T, V, U, Q> piece;
+    const auto add = [&](auto whole) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) r.load(at + u * 32 * V, s1, p[u], q[u]);
+      for (int u = 0; u < U; ++u) {
+        float d[V], lost[V];
+        piece.rest(u, decltype(whole)::value || own + u * 32 * V < left, r.without - (from + own + u * 32 * V), d, lost);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float lost;
-        const float d = verify_rest(p[u][e], q[u][e], lost);
-        sum.add(d, lost);
+        for (int e = 0; e < V; ++e) sum.add(d[e], lost[e]);
       }
+    };
+    if (left >= 32 * V * U) {
+      piece.load(r, from + own, 32 * V, left);
+      add(std::true_type());
+    } else {
+      piece.load(r, own < left ? from + own : s1 - V, 32 * V, left - own);
+      add(std::false_type());
     }
   }
   double s = sum.value();
@@ -97,80 +123,109 @@ template <class T, int V> __device__ double verify_sum(const VerifyRow<T>& r, lo
   return s;
 }
 
-// The first j of the slice with before + r_s0 + ... + r_j > limit; the last with r_j > 0 where
-// rounding leaves none; -1 where no r_j is.
-template <class T, int V>
-__device__ long long verify_pick(const VerifyRow<T>& r, long long s0, long long s1, int lane, double before, double limit) {
-  long long last = -1;
-  for (long long from = s0; from < s1; from += 32 * V) {
-    const long long at = from + lane * V;
-    float p[V], q[V], d[V], lost[V];
-    r.load(at, s1, p, q);
-    double own = 0;
+struct VerifyShared {
+  double warp_sum[kVerifyWarps], cta_sum;
+  double before, limit;           // of the draw: the sum before the slice, what has to be exceeded
+  long long from, to;             // the slice; from < 0: not in this CTA
+  int accepted;
+  unsigned first;                 // the first thread past the limit
+  unsigned long long last;        // 1 + the last index with something left
+  long long pick;
+};
+
+// The first j of the slice with before + r_from + ... + r_j > limit; the last with r_j > 0 where
+// rounding leaves none; -1 where no r_j is.  All threads.
+template <class T, int V, bool Q> __device__ long long verify_pick(const VerifyRow<T>& r, VerifyShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double before = sh.before;
+  constexpr int P = V == 1 ? 4 : 1, E = P * V;  // neighbouring packs, and their values
+  for (long long from = sh.from; from < sh.to; from += kVerifyThreads * E) {
+    const long long at = from + threadIdx.x * E;
+    VerifyPiece<T, V, P, Q> piece;
+    piece.load(r, at < sh.to ? at : sh.from, V, sh.to - at);
+    float d[E], lost[E];
+#pragma unroll
+    for (int u = 0; u < P; ++u) {
+      float du[V], lu[V];
+      piece.rest(u, at + u * V < sh.to, r.without - (at + u * V), du, lu);
+#pragma unroll
+      for (int e = 0; e < V; ++e) d[u * V + e] = du[e], lost[u * V + e] = lu[e];
+    }
+    VerifySum sum;
     long long positive = -1;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      d[e] = verify_rest(p[e], q[e], lost[e]);
-      own += (double)d[e] + (double)lost[e];
+    for (int e = 0; e < E; ++e) {
+      sum.add(d[e], lost[e]);
       if (d[e] > 0.f) positive = at + e;
     }
+    const double own = sum.value();
     double upto = own;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
       const double below = __shfl_up_sync(0xffffffffu, upto, k);
       if (lane >= k) upto += below;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > limit && positive >= 0);
-    if (past) {
-      const int first = __ffs(past) - 1;
-      long long j = -1;
-      if (lane == first) {
-        double s = before + (upto - own);
+    if (lane == 31) sh.warp_sum[warp] = upto;
+    if (threadIdx.x == 0) sh.first = kVerifyThreads;
+    __syncthreads();
+    double base = before;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          s += (double)d[e] + (double)lost[e];
-          if (j < 0 && d[e] > 0.f && s > limit) j = at + e;
-        }
-        if (j < 0) j = positive;
-      }
-      return __shfl_sync(0xffffffffu, j, first);
+    for (int w = 0; w < kVerifyWarps; ++w) {
+      if (w < warp) base += sh.warp_sum[w];
+      before += sh.warp_sum[w];
     }
-    const unsigned some = __ballot_sync(0xffffffffu, positive >= 0);
-    if (some) last = __shfl_sync(0xffffffffu, positive, 31 - __clz(some));
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    const bool past = positive >= 0 && base + upto > sh.limit;
+    if (past) atomicMin(&sh.first, threadIdx.x);
+    if (positive >= 0) atomicMax(&sh.last, (unsigned long long)positive + 1);
+    __syncthreads();
+    const unsigned first = sh.first;
+    if (first < kVerifyThreads) {
+      if (threadIdx.x == first) {
+        double s = base + (upto - own);
+        long long j = -1;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          s += (double)d[e] + (double)lost[e];
+          if (j < 0 && d[e] > 0.f && s > sh.limit) j = at + e;
+        }
+        sh.pick = j < 0 ? positive : j;
+      }
+      __syncthreads();
+      return sh.pick;
+    }
   }
-  return last;
+  return (long long)sh.last - 1;
 }
 
 template <class T, int V>
-__global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const __grid_constant__ VerifyArgs<T> a, unsigned C) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs<T> a, unsigned C) {
   pdl_entry();
-  __shared__ double warp_sum[kVerifyWarps];
-  __shared__ double cta_sum;
-  __shared__ int drafts_accepted;
+  __shared__ VerifyShared sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned rank = C > 1 ? cluster_rank() : 0;
   const long long b = blockIdx.x / C;
 
-  // How many drafts are accepted (each CTA finds out for itself).
+  // How many drafts are accepted (each CTA finds out for itself).  What is read for it is asked for
+  // at once: the draft, then its probabilities.
   int length = a.lengths ? a.lengths[b] : a.K;
-  const bool wrong = length < 0 || length > a.K;
-  length = max(0, min(length, a.K));
+  float sample = 0.f;
   if (warp == 0) {
-    bool bad = wrong;
-    int n = length;
-    for (int from = 0; from < length; from += 32) {
+    sample = a.sample[b];
+    bool bad = false;
+    int n = a.K;
+    for (int from = 0; from < a.K; from += 32) {
       const int i = from + lane;
-      bool ok = true;
-      if (i < length) {
+      bool ok = i >= a.K;
+      if (i < a.K) {
         const long long at = b * a.K + i;
+        const float u = a.accept[at];
         const long long tok = a.tokens64 ? ((const long long*)a.tokens)[at] : ((const int*)a.tokens)[at];
-        ok = tok >= 0 && tok < a.V;
-        bad |= !ok;
-        if (ok) {
+        const bool real = tok >= 0 && tok < a.V;
+        bad |= !real && i < length;
+        if (real) {
           const float p = widen(a.target[b * a.tb + i * a.tt + tok]);
           const float q = a.draft ? fmaxf(widen(a.draft[b * a.qb + i * a.qt + tok]), 0.f) : 1.f;
-          ok = (double)a.accept[at] * (double)q < (double)p;
+          ok = (double)u * (double)q < (double)p;
         }
       }
       const unsigned no = __ballot_sync(0xffffffffu, !ok);
@@ -178,12 +233,16 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const __grid_
         n = from + __ffs(no) - 1;
         break;
       }
+      if (from + 32 >= length) break;
     }
+    bad |= length < 0 || length > a.K;
+    length = max(0, min(length, a.K));
     if (rank == 0 && bad) raise_err(a.err, ERRBIT_RANGE);
-    if (lane == 0) drafts_accepted = n;
+    if (lane == 0) sh.accepted = min(n, length);
   }
+  length = max(0, min(length, a.K));
   __syncthreads();
-  const int n = drafts_accepted;
+  const int n = sh.accepted;
   VerifyRow<T> row = {a.target + b * a.tb + n * a.tt, nullptr, -1};
   if (n < length) {
     if (a.draft) {
@@ -195,62 +254,60 @@ __global__ void __launch_bounds__(kVerifyWarps * 32) verify_kernel(const __grid_
   }
 
   const long long s0 = (long long)(rank * kVerifyWarps + warp) * a.slice, s1 = min(a.V, s0 + a.slice);
-  const double own = s0 < s1 ? verify_sum<T, V>(row, s0, s1, lane) : 0.0;
-  if (lane == 0) warp_sum[warp] = own;
+  double own = 0;
+  if (s0 < s1) own = row.q ? verify_sum<T, V, true>(row, s0, s1, lane) : verify_sum<T, V, false>(row, s0, s1, lane);
+  if (lane == 0) sh.warp_sum[warp] = own;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0;
+  // The sum of the lanes up to this one, of values of the first 8.
+  const auto scan8 = [&](double v) {
 #pragma unroll
-    for (int w = 0; w < kVerifyWarps; ++w) s += warp_sum[w];
-    cta_sum = s;
+    for (int k = 1; k < 8; k <<= 1) {
+      const double below = __shfl_up_sync(0xffffffffu, v, k);
+      if (lane >= k) v += below;
+    }
+    return v;
+  };
+  static_assert(kVerifyWarps == 8 && kVerifyMaxCluster <= 8, "sums over 8 lanes");
+  double slice = 0, slices = 0;
+  if (warp == 0) {
+    slice = lane < kVerifyWarps ? sh.warp_sum[lane] : 0.0;
+    slices = scan8(slice);
+    if (lane == kVerifyWarps - 1) sh.cta_sum = slices;
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
 
-  if (warp == 0) {
-    double total = 0, before = 0;
-    unsigned owner = C, positive = C;
-    double sums[kVerifyMaxCluster];
-    for (unsigned c = 0; c < C; ++c) {
-      const double s = C > 1 ? from_u64<double>(ld_cluster_u64(cluster_addr(&cta_sum, c))) : cta_sum;
-      sums[c] = s;
-      total += s;
-      if (s > 0) positive = c;
+  if (warp == 0) {  // where the draw falls: each CTA finds the same
+    double mine = 0;
+    if (lane < (int)C) mine = C > 1 ? from_u64<double>(ld_cluster_u64(cluster_addr(&sh.cta_sum, lane))) : sh.cta_sum;
+    const double upto = scan8(mine), limit = (double)sample * __shfl_sync(0xffffffffu, upto, C - 1);
+    // Of those with something left, the first past the limit, or the last.
+    const auto choose = [&](bool some, bool past) {
+      const unsigned all = __ballot_sync(0xffffffffu, some), over = __ballot_sync(0xffffffffu, some && past);
+      return over ? __ffs(over) - 1 : all ? 31 - __clz(all) : -1;
+    };
+    const int owner = choose(mine > 0, upto > limit);
+    const double before = __shfl_sync(0xffffffffu, upto - mine, owner < 0 ? 0 : owner);
+    const int k = choose(slice > 0, before + slices > limit);
+    const double skipped = __shfl_sync(0xffffffffu, slices - slice, k < 0 ? 0 : k);
+    if (lane == 0) {
+      const bool here = owner >= 0 && rank == (unsigned)owner && k >= 0;
+      sh.from = here ? (long long)(rank * kVerifyWarps + k) * a.slice : -1;
+      sh.to = min(a.V, sh.from + a.slice);
+      sh.before = before + skipped;
+      sh.limit = limit;
+      sh.last = 0;
+      if (owner < 0 && rank == 0) a.out[b * (a.K + 1) + n] = -1;
     }
-    const double limit = (double)a.sample[b] * total;
-    double upto = 0;
-    for (unsigned c = 0; c < C; ++c) {
-      const double next = upto + sums[c];
-      if (owner == C && sums[c] > 0 && next > limit) owner = c, before = upto;
-      if (owner == C && c == positive) before = upto;
-      upto = next;
-    }
-    if (owner == C) owner = positive;
-    if (rank == (owner == C ? 0 : owner)) {
-      long long j = -1;
-      if (owner < C) {
-        int w = -1, some = -1;
-        double s = before, at = before, at_some = before;
-        for (int k = 0; k < kVerifyWarps; ++k) {
-          const double next = s + warp_sum[k];
-          if (w < 0 && warp_sum[k] > 0) {
-            some = k, at_some = s;
-            if (next > limit) w = k, at = s;
-          }
-          s = next;
-        }
-        if (w < 0) w = some, at = at_some;
-        if (w >= 0) {
-          const long long f = (long long)(rank * kVerifyWarps + w) * a.slice;
-          j = verify_pick<T, V>(row, f, min(a.V, f + a.slice), lane, at, limit);
-        }
-      }
-      if (lane == 0) a.out[b * (a.K + 1) + n] = (int32_t)j;
-    }
+  }
+  __syncthreads();
+  if (sh.from >= 0) {
+    const long long j = row.q ? verify_pick<T, V, true>(row, sh) : verify_pick<T, V, false>(row, sh);
+    if (threadIdx.x == 0) a.out[b * (a.K + 1) + n] = (int32_t)j;
   }
   if (rank == 0) {
     if (threadIdx.x == 0) a.accepted[b] = n;
-    for (int i = threadIdx.x; i <= a.K; i += kVerifyWarps * 32) {
+    for (int i = threadIdx.x; i <= a.K; i += kVerifyThreads) {
       const long long at = b * a.K + i;
       if (i < n) a.out[b * (a.K + 1) + i] = a.tokens64 ? (int32_t)((const long long*)a.tokens)[at] : ((const int32_t*)a.tokens)[at];
       else if (i > n) a.out[b * (a.K + 1) + i] = -1;
@@ -266,14 +323,14 @@ template <class T, int V> cudaError_t verify_launch(const VerifyJob& j, const La
   a.tokens = j.tokens, a.tokens64 = j.tokens64, a.accept = j.accept, a.sample = j.sample, a.lengths = j.lengths;
   a.accepted = j.accepted, a.out = j.out, a.V = j.V, a.K = (int)j.K;
   a.err = ctx.err;
-  // CTAs of a request: while there are fewer than two an SM and a warp has more than 512 values.
+  // CTAs of a request: as many as all fit at once, 4 an SM, while a warp has more than 512 values.
   unsigned C = 1;
-  while (C < kVerifyMaxCluster && j.B * C < 2 * ctx.num_sms && j.V > (long long)C * kVerifyWarps * 512) C *= 2;
+  while (C < kVerifyMaxCluster && 2 * j.B * C <= 4 * ctx.num_sms && j.V > (long long)C * kVerifyWarps * 512) C *= 2;
   const long long step = 32 * V, warps = (long long)C * kVerifyWarps;
   a.slice = ((j.V + warps - 1) / warps + step - 1) / step * step;
   profile_before(ctx);
   const cudaError_t e =
-      launch_pdl_cluster(verify_kernel<T, V>, (unsigned)(j.B * C), kVerifyWarps * 32, C, 0, ctx.stream, a, C);
+      launch_pdl_cluster(verify_kernel<T, V>, (unsigned)(j.B * C), kVerifyThreads, C, 0, ctx.stream, a, C);
   profile_after(ctx);
   return e;
 }

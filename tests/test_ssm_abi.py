@@ -95,7 +95,7 @@ def test_selective_scan_backward(lib):
     assert call(d=0) == gb.OK
     need = lib.gb_selective_scan_temp_bytes
     assert need(0, 4, 8, 16, 1, 1) == need(2, 4, 8, 0, 1, 1) == need(2, 4, 8, 16, 3, 1) == need(2, 4, 8, 129, 1, 0) == 0
-    assert need(8, 2048, 2048, 16, 1, 0) == 0 < need(1, 2048, 64, 16, 1, 0) < need(1, 2048, 64, 16, 1, 1)
+    assert need(64, 2048, 2048, 16, 1, 0) == 0 < need(1, 2048, 64, 16, 1, 0) < need(1, 2048, 64, 16, 1, 1)
 
 
 def test_selective_scan_step(lib):
