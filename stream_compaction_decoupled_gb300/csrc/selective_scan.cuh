@@ -42,7 +42,6 @@
 namespace gbs {
 
 constexpr int kSscThreads = 128;
-constexpr int kSscRows = kSscTile / 4;  // tokens of a warp in phases A and C
 
 template <class T> struct SscArgs {
   const T *x, *dt, *z, *b, *c, *dy;
@@ -98,151 +97,15 @@ template <class T, bool EDGE> struct SscPair {
   }
 };
 
-// Where a block works, and which channels and states a thread has.
-template <class T> struct SscPlace {
-  long long b;         // batch row
-  int group, block;    // of channels, and the block of 64 within it
-  int part;            // of the tokens
-  int tile0, tile1;    // its tiles
-  int lane, warp;
-  int ch;              // phases A and C: the lane's first channel, and how many of its two exist
-  int count;
-  int pr, ln;          // phase B: the thread's pair of channels within the block, its place among 4 lanes
-  int chb, countb;
-  __device__ __forceinline__ SscPlace(const SscArgs<T>& a, int first_part, int parts) {
-    long long u = blockIdx.x;
-    block = (int)(u % a.blocks);
-    u /= a.blocks;
-    group = (int)(u % a.G);
-    u /= a.G;
-    part = first_part + (int)(u % parts);
-    b = u / parts;
-    tile0 = part * a.part_tiles;
-    tile1 = min(a.tiles, tile0 + a.part_tiles);
-    lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int left = min(kSscChannels, a.DG - block * kSscChannels), base = group * a.DG + block * kSscChannels;
-    ch = base + 2 * lane;
-    count = min(2, left - 2 * lane);
-    pr = warp * 8 + (lane >> 2);
-    ln = lane & 3;
-    chb = base + 2 * pr;
-    countb = min(2, left - 2 * pr);
-  }
-};
-
-// State s (0 .. 3) of a thread in the block of 16 from n0: the lanes' pairs lie side by side.
-__device__ __forceinline__ int ssc_state(int n0, int ln, int s) { return n0 + (s >> 1) * 8 + ln * 2 + (s & 1); }
-
-// Values (channel, state) of a (D, N) array for the thread's pair of channels; `other` where
-// there are none.
-__device__ __forceinline__ float2 ssc_load(const float* p, int n, int N, int count, float other) {
-  float2 v = make_float2(other, other);
-  if (n < N) {
-    if (count > 0) v.x = p[n];
-    if (count > 1) v.y = p[N + n];
-  }
-  return v;
-}
-__device__ __forceinline__ void ssc_store(float* p, int n, int N, int count, float2 v) {
-  if (n < N) {
-    if (count > 0) p[n] = v.x;
-    if (count > 1) p[N + n] = v.y;
-  }
-}
 // exp of the product, a in units of log2 e.  In single operations: a packed product before the
 // exponential costs more than the instruction it saves (measured in a loop of nothing else, 32
 // states a thread, 3 warps a scheduler: 6.9 cycles a state and token with packed products and sums,
 // 5.2 with these and the sums single and only D x B packed, 5.9 with all of it single).
 __device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) { return make_float2(ex2(a.x * d.x), ex2(a.y * d.y)); }
 __device__ __forceinline__ float2 ssc_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
-// The thread's A in units of log2 e.
-template <class T>
-__device__ __forceinline__ void ssc_rates(const SscArgs<T>& a, const SscPlace<T>& at, int n0, float2 (&r)[4]) {
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const float2 v = ssc_load(a.a + (long long)at.chb * a.N, ssc_state(n0, at.ln, s), a.N, at.countb, 0.f);
-    r[s] = mul2(v, make_float2(kLog2e, kLog2e));
-  }
-}
-// Bit t: token t of the tile starts a document.
-template <class T> __device__ __forceinline__ unsigned ssc_starts(const SscArgs<T>& a, long long b, int t0, int lane) {
-  if (!a.starts) return 0;
-  const bool s = lane < kSscTile && t0 + lane < a.T_ && a.starts[b * a.T_ + t0 + lane] != 0;
-  return __ballot_sync(0xffffffffu, s);
-}
-// A tile's values of B or C, each twice, to shared memory (tokens, NP), zero where there are none.
-template <class T>
-__device__ __forceinline__ void ssc_vectors(const SscArgs<T>& a, const T* p, long long stride, int t0, int NP, float2* out) {
-  const int total = kSscTile * NP;
-  for (int k = threadIdx.x; k < total; k += kSscThreads) {
-    const int t = k / NP, n = k % NP;
-    const float v = n < a.N && t0 + t < a.T_ ? widen(p[t * stride + n]) : 0.f;
-    out[k] = make_float2(v, v);
-  }
-}
 template <class T> __device__ __forceinline__ float2 ssc_step_size(const SscArgs<T>& a, float2 v) {
   return a.softplus ? softplus2<T>(v) : v;
 }
-// The two 16-byte halves of a pair's four parts, placed so that neither the writes (4 lanes
-// of 8 bytes a pair) nor the reads (a lane a pair) meet in a bank.
-__device__ __forceinline__ int ssc_half(int pair, int half) { return half ^ ((pair >> 2) & 1); }
-__device__ __forceinline__ void ssc_put(float2* part, int t, int pair, int ln, float2 v) {
-  part[(t * 32 + pair) * 4 + ssc_half(pair, ln >> 1) * 2 + (ln & 1)] = v;
-}
-__device__ __forceinline__ float2 ssc_get(const float2* part, int t, int pair) {
-  const float4* p = (const float4*)(part + (t * 32 + pair) * 4);
-  const float4 lo = p[ssc_half(pair, 0)], hi = p[ssc_half(pair, 1)];
-  return add2(add2(make_float2(lo.x, lo.y), make_float2(lo.z, lo.w)), add2(make_float2(hi.x, hi.y), make_float2(hi.z, hi.w)));
-}
-
-// The state before a part: what comes in, through each part before it in turn (`first` to
-// `last`, either way).
-template <class T>
-__device__ __forceinline__ float2 ssc_through(const SscArgs<T>& a, const SscPlace<T>& at, int n, float2 rate, float2 h,
-                                              int first, int count, int step) {
-  int p = first;
-#pragma unroll 4
-  for (int k = 0; k < count; ++k, p += step) {
-    const long long row = at.b * (a.parts - 1) + p;
-    const float2 e = ssc_load(a.ends + (row * a.D + at.chb) * a.N, n, a.N, at.countb, 0.f);
-    const float* s = a.sums + row * a.D + at.chb;
-    const float2 sum = make_float2(at.countb > 0 ? s[0] : 0.f, at.countb > 1 ? s[1] : 0.f);
-    h = a.drops[row] != 0.f ? e : fma2(ssc_decay(rate, sum), h, e);
-  }
-  return h;
-}
-
-// The part's sum of D: each thread's own over its tokens, summed over the warps.
-template <class T>
-__device__ __forceinline__ void ssc_write_sums(const SscArgs<T>& a, const SscPlace<T>& at, float2 sum, bool dropped, long long row,
-                                               float2* scratch) {
-  scratch[at.warp * 32 + at.lane] = sum;
-  __syncthreads();
-  if (at.warp == 0) {
-    const float2 s = add2(add2(scratch[at.lane], scratch[32 + at.lane]), add2(scratch[64 + at.lane], scratch[96 + at.lane]));
-    float* p = a.sums + row * a.D + at.ch;
-    if (at.count > 0) p[0] = s.x;
-    if (at.count > 1) p[1] = s.y;
-    if (at.lane == 0 && at.block == 0 && at.group == 0) a.drops[row] = dropped ? 1.f : 0.f;
-  }
-}
-
-// Shared memory, in float2: D and D x of the tile (2), [e (1)], the parts of sums over states (4
-// for each of SUMS), B and C, and with more than 16 states what a thread keeps of each block.
-struct SscShared {
-  static constexpr int kDx = kSscTile * 32 * 2, kE = kSscTile * 32, kPart = kSscTile * 32 * 4;
-  static constexpr int kSave = 3 * 4 * kSscThreads, kRed = kSscTile * 4 * 32 / 2;
-  static size_t forward(int NP, bool ends) {
-    return 8 * ((size_t)kDx + (ends ? 0 : kPart) + kSscTile * NP * (ends ? 1 : 2) + (NP > 16 ? NP / 16 * 4 * kSscThreads : 0)) +
-           (ends ? 8 * 128 : 0);
-  }
-  static size_t carry(int NP) {
-    return 8 * ((size_t)kDx + kE + kSscTile * NP + (NP > 16 ? NP / 16 * 4 * kSscThreads : 0) + 128);
-  }
-  static size_t backward(int NP) {
-    return 8 * ((size_t)kDx + kE + 3 * kPart + kSave + kRed + kSscTile * NP * 2 + (NP > 16 ? 2 * (NP / 16) * 4 * kSscThreads : 0));
-  }
-};
 
 // ---- forward ---------------------------------------------------------------------------
 
@@ -691,100 +554,7 @@ __global__ void __launch_bounds__(kSscThreads, 4) ssc_forward_kernel(const __gri
   }
 }
 
-// What each part but the first passes back of a carry of zero, and its sum of D: only C, e and
-// the decays are needed.
-template <class T, bool EDGE, bool ONE>
-__global__ void __launch_bounds__(kSscThreads, 4) ssc_carry_kernel(const __grid_constant__ SscArgs<T> a) {
-  pdl_entry();
-  const int NP = ONE ? 16 : a.NP;
-  extern __shared__ __align__(16) float2 ssc_shared[];
-  float2* ds = ssc_shared;
-  float2* es = ssc_shared + SscShared::kDx;
-  float2* cs = es + SscShared::kE;
-  float2* gs = cs + kSscTile * NP;
-  float2* sums = gs + (ONE ? 0 : NP / 16 * 4 * kSscThreads);
-  using P = SscPair<T, EDGE>;
-  const SscPlace<T> at(a, 1, a.parts - 1);
-  const int NB = NP / 16;
-  const float2 zero = make_float2(0.f, 0.f);
-  float2 rate[4], g[4];
-  if constexpr (ONE) ssc_rates(a, at, 0, rate);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) g[s] = zero;
-  if constexpr (!ONE) {
-    for (int k = 0; k < NB * 4; ++k) gs[k * kSscThreads + threadIdx.x] = zero;
-  }
-  float2 bias = zero, sum = zero;
-  if (a.bias) bias = make_float2(at.count > 0 ? a.bias[at.ch] : 0.f, at.count > 1 ? a.bias[at.ch + 1] : 0.f);
-  const int own = at.warp * kSscRows;
-  unsigned dropped = 0;
-  for (int tile = at.tile1 - 1; tile >= at.tile0; --tile) {
-    const int t0 = tile * kSscTile;
-    const long long tr = (long long)t0 + own;
-    const T* pdt = a.dt + at.b * a.dtb + tr * a.dtt + at.ch;
-    const T* pdy = a.dy + at.b * a.dyb + tr * a.dyt + at.ch;
-    const T* pz = a.z ? a.z + at.b * a.zb + tr * a.zt + at.ch : nullptr;
-    typename P::Raw dt[kSscRows], dy[kSscRows], z[kSscRows];
-#pragma unroll
-    for (int i = 0; i < kSscRows; ++i) {
-      const int count = t0 + own + i < a.T_ ? at.count : 0;
-      dt[i] = P::load(pdt + i * a.dtt, count);
-      dy[i] = P::load(pdy + i * a.dyt, count);
-      if (pz) z[i] = P::load(pz + i * a.zt, count);
-    }
-    const unsigned starts = ssc_starts(a, at.b, t0, at.lane);
-    dropped |= starts;
-    ssc_vectors(a, a.c + at.b * a.cb + (long long)t0 * a.ct + at.group * a.cg, a.ct, t0, NP, cs);
-#pragma unroll
-    for (int i = 0; i < kSscRows; ++i) {
-      float2 d = ssc_step_size(a, add2(P::wide(dt[i]), bias)), e = P::wide(dy[i]);
-      if (t0 + own + i >= a.T_) d = zero;
-      if (pz) {
-        const float2 zv = P::wide(z[i]);
-        e = mul2(e, mul2(zv, sigmoid<T>(zv)));
-      }
-      ds[(own + i) * 32 + at.lane] = d;
-      es[(own + i) * 32 + at.lane] = e;
-      sum = add2(sum, d);
-    }
-    __syncthreads();
-    for (int k = 0; k < NB; ++k) {
-      if constexpr (!ONE) {
-        ssc_rates(a, at, k * 16, rate);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) g[s] = gs[(k * 4 + s) * kSscThreads + threadIdx.x];
-      }
-#pragma unroll 4
-      for (int t = kSscTile - 1; t >= 0; --t) {
-        const float2 d = ds[t * 32 + at.pr], e = es[t * 32 + at.pr];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 cv = *(const float4*)(cs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-          g[2 * j] = mul2(ssc_decay(rate[2 * j], d), fma2(e, make_float2(cv.x, cv.y), g[2 * j]));
-          g[2 * j + 1] = mul2(ssc_decay(rate[2 * j + 1], d), fma2(e, make_float2(cv.z, cv.w), g[2 * j + 1]));
-        }
-        if (starts >> t & 1) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) g[s] = zero;
-        }
-      }
-      if constexpr (!ONE) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) gs[(k * 4 + s) * kSscThreads + threadIdx.x] = g[s];
-      }
-    }
-    __syncthreads();
-  }
-  const long long row = at.b * (a.parts - 1) + at.part - 1;
-  ssc_write_sums(a, at, sum, dropped != 0, row, sums);
-  for (int k = 0; k < NB; ++k) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const float2 v = ONE ? g[s] : gs[(k * 4 + s) * kSscThreads + threadIdx.x];
-      ssc_store(a.ends + (row * a.D + at.chb) * a.N, ssc_state(k * 16, at.ln, s), a.N, at.countb, v);
-    }
-  }
-}
+// ---- gradient --------------------------------------------------------------------------
 
 // One step of a sum over lanes that differ in bit `bit`: a lane keeps the half of its values
 // that the bit names and adds its neighbour's.
@@ -797,275 +567,497 @@ template <int M> __device__ __forceinline__ void ssc_exchange(float (&v)[M], int
   }
 }
 
-// The gradient: tiles from the last to the first.  Phase B of a tile goes forward from the kept
-// state, leaving the states before tokens 4, 8 and 12 in shared memory, and then takes its four
-// quarters from the last to the first: forward again with decays and states in registers, then
-// backward.
-template <class T, bool EDGE, bool ONE>
-__global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
-  pdl_entry();
-  const int NP = ONE ? 16 : a.NP;
-  extern __shared__ __align__(16) float2 ssc_shared[];
-  float4* dxs = (float4*)ssc_shared;
-  float2* es = ssc_shared + SscShared::kDx;
-  float2* part = es + SscShared::kE;  // of B . g, q . A, C . h
-  float2* save = part + 3 * SscShared::kPart;
-  float* red = (float*)(save + SscShared::kSave);
-  float2* bs = (float2*)red + SscShared::kRed;
-  float2* cs = bs + kSscTile * NP;
-  float2* gs = cs + kSscTile * NP;
+// A block takes 64 channels of a group, a warp 16 of them: 4 lanes a pair of channels, 4 states of
+// both a lane.  A tile's 16 tokens go to the lanes of a pair in turn (t % 4 = ln).  In shared
+// memory, for each warp: a ring of two tiles as they lie in memory; D and D x, e, of the tile;
+// the lanes' parts of three sums over states for 4 tokens; states before tokens 4, 8 and 12; the
+// warp's sums of dB and dC; with more than 16 states what a lane keeps of each block.  For the
+// block: two tiles of B and C as they are, one widened.
+template <class T, bool EDGE_> struct SscBack {
+  static constexpr bool EDGE = EDGE_;
+  static constexpr int L = kSscTile, R = L / 4, M = 4, STAGES = 2;
+  static constexpr int ROW = 16 * (int)sizeof(T), ARRAY = L * ROW, KEPT = 16 * 16 * 4, STAGE = 4 * ARRAY + KEPT;
+  static constexpr int CHUNKS = ROW / 16;
+  static constexpr int DU = L * 8 * 16, E = L * 8 * 8, SUMS = 3 * 4 * 8 * 4 * 8, SAVE = 3 * 8 * 32 * 4, RED = L * 32 * 4;
+  static constexpr int VECTORS = L * 32 * (int)sizeof(T);
   using P = SscPair<T, EDGE>;
-  const SscPlace<T> at(a, 0, a.parts);
-  const int NB = NP / 16;
-  const float2 zero = make_float2(0.f, 0.f);
-  float2* das = gs + NB * 4 * kSscThreads;
+  using Raw = typename P::Raw;
+  static __host__ __device__ constexpr int warp_bytes(int NB, bool carry) {
+    return STAGES * STAGE + DU + E + (carry ? 0 : SUMS + SAVE + RED) + (NB > 1 ? NB * 2 * 8 * 32 * 4 : 0);
+  }
+  static __host__ __device__ constexpr int bytes(int NB, bool carry) {
+    return 4 * warp_bytes(NB, carry) + STAGES * VECTORS + NB * L * 32 * 4;
+  }
+};
 
-  float2 rate[4], g[4], da[4];
-  for (int k = 0; k < NB; ++k) {
-    ssc_rates(a, at, k * 16, rate);
+// Place of lane ln's part of token i's sums for a pair, so that neither the writes (all lanes one
+// token) nor the reads (a lane its own token's four parts, 16 bytes at a time) meet in a bank.
+__device__ __forceinline__ int ssc_sum_half(int i, int pair, int half) {
+  const int px = pair ^ (2 * i);
+  return ((i * 8 + px) * 2 + (half ^ (px >> 2 & 1))) * 2;
+}
+
+// CARRY: only what each part but the first passes back of a carry of zero, and its sum of D.
+//
+// Tiles go from the last to the first.  A: the lane's own tokens' D, D x, e.  B: forward from the
+// kept state, leaving the states before tokens 4, 8 and 12; then the four quarters from the last to
+// the first: forward again with decays and states in registers, then backward.  C, after each
+// quarter: the lane's own token, from the sums over states.  The sums over channels for dB and
+// dC: over the pair in the thread, over the warp by exchanges, over the block in shared memory,
+// and over the blocks by a second kernel.
+template <class T, bool EDGE, bool ONE, bool CARRY>
+__global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
+  pdl_entry();
+  using S = SscBack<T, EDGE>;
+  using P = typename S::P;
+  using Raw = typename S::Raw;
+  constexpr int L = S::L, R = S::R, M = S::M;
+  extern __shared__ __align__(16) float2 ssc_shared[];
+  const int NB = ONE ? 1 : a.NP / 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ln = lane & 3, pr = lane >> 2;
+  unsigned char* ring = (unsigned char*)ssc_shared + warp * S::warp_bytes(NB, CARRY);
+  float4* du = (float4*)(ring + S::STAGES * S::STAGE);  // D and D x (token, pair)
+  float2* es = (float2*)(du + L * 8);                   // (token, pair)
+  float2* sums = es + L * 8;                            // of B . g, q . A, C . h (which, token of 4, pair, lane)
+  float4* save = (float4*)(sums + (CARRY ? 0 : 3 * 4 * 8 * 4));
+  float* red = (float*)save + (CARRY ? 0 : 3 * 8 * 32);  // dB and dC over the warp (token, 32)
+  float4* keep = (float4*)(red + (CARRY ? 0 : L * 32));  // g and dA by block, where there are several
+  unsigned char* vring = (unsigned char*)ssc_shared + 4 * S::warp_bytes(NB, CARRY);
+  float* vs = (float*)(vring + S::STAGES * S::VECTORS);  // B (16) and C (16) (block, token)
+  const float2 zero = make_float2(0.f, 0.f);
+
+  // Where the block works.
+  long long unit = blockIdx.x;
+  const int block = (int)(unit % a.blocks);
+  unit /= a.blocks;
+  const int group = (int)(unit % a.G);
+  unit /= a.G;
+  const int parts = CARRY ? a.parts - 1 : a.parts, part = (int)(unit % parts) + (CARRY ? 1 : 0);
+  const long long b = unit / parts;
+  const int tile0 = part * a.part_tiles, tile1 = min(a.tiles, tile0 + a.part_tiles);
+  const int first = group * a.DG + block * kSscChannels, width = min(16, (group + 1) * a.DG - first - 16 * warp);
+  const int base = width > 0 ? first + 16 * warp : first;  // a warp without channels reads real ones and stores nothing
+  const int count = min(2, width - 2 * pr), ch = count > 0 ? base + 2 * pr : base;
+  const long long row = b * a.D + ch;
+
+  float2 rate[2][2], g[2][2], da[2][2];  // (channel, pair of states)
+  const auto rates = [&](int k) {
+    ssc_load_any<M>(a.vec, a.a + (long long)ch * a.N, k * 16 + ln * M, a.N, count, rate);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int n = ssc_state(k * 16, at.ln, s);
-      g[s] = da[s] = zero;
-      if (a.dlast) g[s] = ssc_load(a.dlast + (at.b * a.D + at.chb) * a.N, n, a.N, at.countb, 0.f);
-      g[s] = ssc_through(a, at, n, rate[s], g[s], a.parts - 2, a.parts - 1 - at.part, -1);
-      if constexpr (!ONE) {
-        gs[(k * 4 + s) * kSscThreads + threadIdx.x] = g[s];
-        das[(k * 4 + s) * kSscThreads + threadIdx.x] = zero;
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) rate[c][j] = mul2(rate[c][j], make_float2(kLog2e, kLog2e));
+  };
+  const auto put = [&](int at, const float2 (&v)[2][2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) keep[(at * 2 + c) * 32 + lane] = make_float4(v[c][0].x, v[c][0].y, v[c][1].x, v[c][1].y);
+  };
+  const auto get = [&](int at, float2 (&v)[2][2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float4 q = keep[(at * 2 + c) * 32 + lane];
+      v[c][0] = make_float2(q.x, q.y), v[c][1] = make_float2(q.z, q.w);
+    }
+  };
+  for (int k = 0; k < NB; ++k) {
+    rates(k);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) g[c][j] = da[c][j] = zero;
+    if constexpr (!CARRY) {
+      if (a.dlast) ssc_load_any<M>(a.vec, a.dlast + row * a.N, k * 16 + ln * M, a.N, count, g);
+      // Through the parts behind this one in turn.
+      for (int p = a.parts - 2; p >= part; --p) {
+        const long long q = b * (a.parts - 1) + p;
+        float2 e[2][2];
+        ssc_load_any<M>(a.vec, a.ends + (q * a.D + ch) * a.N, k * 16 + ln * M, a.N, count, e);
+        const float* sp = a.sums + q * a.D + ch;
+        const float sum[2] = {count > 0 ? sp[0] : 0.f, count > 1 ? sp[1] : 0.f};
+        const bool dropped = a.drops[q] != 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            g[c][j] = dropped ? e[c][j] : fma2(ssc_decay(rate[c][j], make_float2(sum[c], sum[c])), g[c][j], e[c][j]);
       }
     }
+    if constexpr (!ONE) {
+      put(2 * k, g);
+      put(2 * k + 1, da);
+    }
   }
-  float2 bias = zero, skip = zero, dskip = zero, dbias = zero;
-  if (a.bias) bias = make_float2(at.count > 0 ? a.bias[at.ch] : 0.f, at.count > 1 ? a.bias[at.ch + 1] : 0.f);
-  if (a.d) skip = make_float2(at.count > 0 ? a.d[at.ch] : 0.f, at.count > 1 ? a.d[at.ch + 1] : 0.f);
-  const int own = at.warp * kSscRows;
+  float2 bias = zero, skip = zero, dskip = zero, dbias = zero, sum_d = zero;
+  if (a.bias) bias = make_float2(count > 0 ? a.bias[ch] : 0.f, count > 1 ? a.bias[ch + 1] : 0.f);
+  if (!CARRY && a.d) skip = make_float2(count > 0 ? a.d[ch] : 0.f, count > 1 ? a.d[ch + 1] : 0.f);
   const bool gated = a.z != nullptr;
+  const T* px = a.x + b * a.xb;
+  const T* pdt = a.dt + b * a.dtb;
+  const T* pdy = a.dy + b * a.dyb;
+  const T* pz = gated ? a.z + b * a.zb : nullptr;
+  const T* pb = a.b + b * a.bb + group * a.bg;
+  const T* pc = a.c + b * a.cb + group * a.cg;
+  const uint8_t* ps = a.starts ? a.starts + b * a.T_ : nullptr;
 
-  for (int tile = at.tile1 - 1; tile >= at.tile0; --tile) {
-    const int t0 = tile * kSscTile;
-    const long long tr = (long long)t0 + own;
-    const T* px = a.x + at.b * a.xb + tr * a.xt + at.ch;
-    const T* pdt = a.dt + at.b * a.dtb + tr * a.dtt + at.ch;
-    const T* pdy = a.dy + at.b * a.dyb + tr * a.dyt + at.ch;
-    const T* pz = gated ? a.z + at.b * a.zb + tr * a.zt + at.ch : nullptr;
-    const unsigned starts = ssc_starts(a, at.b, t0, at.lane);
-    // A
-    {
-      typename P::Raw x[kSscRows], dt[kSscRows], dy[kSscRows], z[kSscRows];
+  // Each lane the starts of one of the next 32 tiles, a bit a token.
+  const auto flags = [&](int tile) {
+    unsigned f = 0;
+    const int t = (tile - lane) * L;
+    if (ps && tile - lane >= tile0) {
 #pragma unroll
-      for (int i = 0; i < kSscRows; ++i) {
-        const int count = t0 + own + i < a.T_ ? at.count : 0;
-        x[i] = P::load(px + i * a.xt, count);
-        dt[i] = P::load(pdt + i * a.dtt, count);
-        dy[i] = P::load(pdy + i * a.dyt, count);
-        if (gated) z[i] = P::load(pz + i * a.zt, count);
-      }
-      ssc_vectors(a, a.b + at.b * a.bb + (long long)t0 * a.bt + at.group * a.bg, a.bt, t0, NP, bs);
-      ssc_vectors(a, a.c + at.b * a.cb + (long long)t0 * a.ct + at.group * a.cg, a.ct, t0, NP, cs);
+      for (int i = 0; i < L; ++i)
+        if (t + i < a.T_ && ps[t + i]) f |= 1u << i;
+    }
+    return f;
+  };
+  // Starts a tile's copies into the ring (EDGE: loads it at once).
+  constexpr int V = 16 / sizeof(T), PER = 32 / V;
+  const auto fetch = [&](int tile, int stage) {
+    unsigned char* to = ring + stage * S::STAGE;
+    if (tile >= tile0) {
+      const int t = tile * L;
+      if constexpr (EDGE) {
 #pragma unroll
-      for (int i = 0; i < kSscRows; ++i) {
-        float2 d = ssc_step_size(a, add2(P::wide(dt[i]), bias)), e = P::wide(dy[i]);
-        if (t0 + own + i >= a.T_) d = zero;
-        const float2 u = mul2(d, P::wide(x[i]));
-        if (gated) {
-          const float2 zv = P::wide(z[i]);
-          e = mul2(e, mul2(zv, sigmoid<T>(zv)));
+        for (int r = 0; r < R; ++r) {
+          const long long u = min(t + 4 * r + ln, a.T_ - 1);
+          Raw* at = (Raw*)(to + (4 * r + ln) * S::ROW) + pr;
+          if (!CARRY) at[0] = P::load(px + u * a.xt + ch, count);
+          at[S::ARRAY / sizeof(Raw)] = P::load(pdt + u * a.dtt + ch, count);
+          at[2 * S::ARRAY / sizeof(Raw)] = P::load(pdy + u * a.dyt + ch, count);
+          if (gated) at[3 * S::ARRAY / sizeof(Raw)] = P::load(pz + u * a.zt + ch, count);
         }
-        dxs[(own + i) * 32 + at.lane] = make_float4(d.x, d.y, u.x, u.y);
-        es[(own + i) * 32 + at.lane] = e;
+      } else {
+#pragma unroll
+        for (int q = 0; q < L * S::CHUNKS / 32; ++q) {
+          const int k = q * 32 + lane, i = k / S::CHUNKS, c = k % S::CHUNKS * V;
+          if (c < width) {
+            const long long u = min(t + i, a.T_ - 1);
+            unsigned char* at = to + i * S::ROW + c * sizeof(T);
+            if (!CARRY) cp_async16(at, px + u * a.xt + base + c);
+            cp_async16(at + S::ARRAY, pdt + u * a.dtt + base + c);
+            cp_async16(at + 2 * S::ARRAY, pdy + u * a.dyt + base + c);
+            if (gated) cp_async16(at + 3 * S::ARRAY, pz + u * a.zt + base + c);
+          }
+        }
+        if constexpr (ONE) {
+          if (!CARRY && ln * M < a.N) {  // the lane's own states
+            const float* from = a.kept + ((b * a.tiles + tile) * a.D + ch) * a.N + ln * M;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              if (c < count) cp_async16(to + 4 * S::ARRAY + (c * 32 + lane) * 16, from + c * a.N);
+          }
+          // The warp's tokens of B and C.
+          const int i = warp * 4 + lane / PER, c = lane % PER * V;
+#pragma unroll
+          for (int q = 0; q < 4 * PER / 32 || q == 0; ++q) {
+            const int ii = i + q * (32 / PER);
+            const long long u = min(t + ii, a.T_ - 1);
+            if (lane < 4 * PER && c % 16 < a.N && (!CARRY || c >= 16))
+              cp_async16(vring + stage * S::VECTORS + (ii * 32 + c) * sizeof(T), c < 16 ? pb + u * a.bt + c : pc + u * a.ct + c - 16);
+          }
+        }
       }
+    }
+    cp_async_commit();
+  };
+  if constexpr (!EDGE) {  // states past the last stay zero
+    for (int k = lane; k < S::STAGES * S::STAGE / 16; k += 32) ((float4*)ring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = threadIdx.x; k < S::STAGES * S::VECTORS / 16; k += kSscThreads) ((float4*)vring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+  }
+
+  unsigned flag = 0, dropped = 0;
+  int stage = 0;
+  fetch(tile1 - 1, 0);
+  for (int tile = tile1 - 1; tile >= tile0; --tile) {
+    const int t0 = tile * L, number = (tile1 - 1 - tile) % 32;
+    if (number == 0) flag = flags(tile);
+    const unsigned starts = __shfl_sync(0xffffffffu, flag, number);
+    dropped |= starts;
+    cp_async_wait<0>();
+    __syncwarp();
+    const unsigned char* raw = ring + stage * S::STAGE;
+    const auto pair = [&](int array, int t) { return P::wide(((const Raw*)(raw + array * S::ARRAY + t * S::ROW))[pr]); };
+    // A
+    if (EDGE || !ONE) {
+      for (int k = threadIdx.x; k < NB * L * 32; k += kSscThreads) {
+        const int n = k % 16, second = k / 16 % 2, i = k / 32 % L, n0 = k / (32 * L) * 16 + n;
+        const long long u = min(t0 + i, a.T_ - 1);
+        vs[k] = n0 < a.N ? widen(second ? pc[u * a.ct + n0] : pb[u * a.bt + n0]) : 0.f;
+      }
+    } else {
+      const int c = threadIdx.x * 4;
+      const T* from = (const T*)(vring + stage * S::VECTORS) + (warp * 4 * 32 + lane * 4);
+      *(float4*)(vs + c) = make_float4(widen(from[0]), widen(from[1]), widen(from[2]), widen(from[3]));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = 4 * r + ln;
+      float2 d = ssc_step_size(a, add2(pair(1, t), bias)), e = pair(2, t);
+      if (gated) {
+        const float2 z = pair(3, t);
+        e = mul2(e, mul2(z, sigmoid<T>(z)));
+      }
+      if (t0 + t >= a.T_) d = e = zero;
+      const float2 u = CARRY ? zero : mul2(d, pair(0, t));
+      du[t * 8 + pr] = make_float4(d.x, d.y, u.x, u.y);
+      es[t * 8 + pr] = e;
+      if constexpr (CARRY) sum_d = add2(sum_d, d);
     }
     __syncthreads();
-    // B
+    // The other stage has been read: its copies go on behind B.  (EDGE's loads are waited for here.)
+    stage ^= 1;
+    fetch(tile - 1, stage);
+
+    float2 acc[3][ONE ? 1 : R];  // more than 16 states: the own tokens' sums over the blocks
+    if constexpr (!ONE && !CARRY) {
+#pragma unroll
+      for (int w = 0; w < 3; ++w)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[w][r] = zero;
+    }
+    // C, of own token r.
+    const auto finish = [&](int r, float2 along, float2 through, float2 y) {
+      const int t = 4 * r + ln, n = t0 + t < a.T_ ? count : 0;
+      const long long u = t0 + t;
+      const float2 x = pair(0, t), e = es[t * 8 + pr];
+      const float4 q = du[t * 8 + pr];
+      through = mul2(through, make_float2(kLn2, kLn2));
+      float2 dd = fma2(x, along, through);
+      if (a.softplus) dd = mul2(dd, sigmoid<T>(add2(pair(1, t), bias)));
+      P::store(a.dx + b * a.dxb + u * a.dxt + ch, n, fma2(skip, e, mul2(make_float2(q.x, q.y), along)));
+      P::store(a.ddt + b * a.ddtb + u * a.ddtt + ch, n, dd);
+      if (n > 0) {
+        dskip = fma2(e, x, dskip);
+        dbias = add2(dbias, dd);
+      }
+      if (gated) {
+        const float2 z = pair(3, t), s = sigmoid<T>(z);
+        const float2 slope = fma2(mul2(z, s), fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
+        P::store(a.dz + b * a.dzb + u * a.dzt + ch, n, mul2(mul2(pair(2, t), fma2(skip, x, y)), slope));
+      }
+    };
+
     for (int k = 0; k < NB; ++k) {
       if constexpr (!ONE) {
-        ssc_rates(a, at, k * 16, rate);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          g[s] = gs[(k * 4 + s) * kSscThreads + threadIdx.x];
-          da[s] = das[(k * 4 + s) * kSscThreads + threadIdx.x];
-        }
+        rates(k);
+        get(2 * k, g);
+        get(2 * k + 1, da);
       }
-      const float* kept = a.kept + ((at.b * a.tiles + tile) * a.D + at.chb) * a.N;
-      float2 h[4];
+      const float* vk = vs + k * L * 32 + ln * M;
+      if constexpr (CARRY) {
+        const auto tokens = [&](auto plain) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) h[s] = ssc_load(kept, ssc_state(k * 16, at.ln, s), a.N, at.countb, 0.f);
-#pragma unroll 4
-      for (int t = 0; t < 12; ++t) {
-        const float4 q = dxs[t * 32 + at.pr];
-        const float2 d = make_float2(q.x, q.y), u = make_float2(q.z, q.w);
-        if (starts >> t & 1) {
+          for (int t = L - 1; t >= 0; --t) {
+            const float4 q = du[t * 8 + pr], cv = *(const float4*)(vk + t * 32 + 16);
+            const float2 e = es[t * 8 + pr];
+            const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
 #pragma unroll
-          for (int s = 0; s < 4; ++s) h[s] = zero;
-        }
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 bv = *(const float4*)(bs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-          h[2 * j] = fma2(ssc_decay(rate[2 * j], d), h[2 * j], mul2(u, make_float2(bv.x, bv.y)));
-          h[2 * j + 1] = fma2(ssc_decay(rate[2 * j + 1], d), h[2 * j + 1], mul2(u, make_float2(bv.z, bv.w)));
-        }
-        if ((t & 3) == 3) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) save[((t >> 2) * 4 + s) * kSscThreads + threadIdx.x] = h[s];
-        }
-      }
-      for (int quarter = 3; quarter >= 0; --quarter) {
-        float2 before[4][4], decay[4][4];  // of a token: the state that the one before it left, its decay
-        if (quarter == 0) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) h[s] = ssc_load(kept, ssc_state(k * 16, at.ln, s), a.N, at.countb, 0.f);
-        } else {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) h[s] = save[((quarter - 1) * 4 + s) * kSscThreads + threadIdx.x];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = quarter * 4 + i;
-          const float4 q = dxs[t * 32 + at.pr];
-          const float2 d = make_float2(q.x, q.y), u = make_float2(q.z, q.w);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) before[i][s] = h[s];
-          if (starts >> t & 1) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) h[s] = zero;
+              for (int j = 0; j < 2; ++j) {
+                const float dd = c ? q.y : q.x, ee = c ? e.y : e.x;
+                g[c][j] = mul2(ssc_decay(rate[c][j], make_float2(dd, dd)), ssc_fma(make_float2(ee, ee), c2[j], g[c][j]));
+                if (!decltype(plain)::value && (starts >> t & 1)) g[c][j] = zero;
+              }
           }
+        };
+        if (starts) tokens(std::false_type());
+        else tokens(std::true_type());
+      } else {
+        float2 h[2][2];
+        const auto first_state = [&]() {
+          if constexpr (ONE && !EDGE) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 bv = *(const float4*)(bs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
+            for (int c = 0; c < 2; ++c) {
+              const float4 q = *(const float4*)(raw + 4 * S::ARRAY + (c * 32 + lane) * 16);
+              h[c][0] = make_float2(q.x, q.y), h[c][1] = make_float2(q.z, q.w);
+            }
+          } else {
+            ssc_load_any<M>(a.vec, a.kept + ((b * a.tiles + tile) * a.D + ch) * a.N, k * 16 + ln * M, a.N, count, h);
+          }
+        };
+        const auto tokens = [&](auto plain) {
+          constexpr bool STARTS = !decltype(plain)::value;
+          first_state();
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const int s = 2 * j + m;
-              decay[i][s] = ssc_decay(rate[s], d);
-              h[s] = fma2(decay[i][s], h[s], mul2(u, m ? make_float2(bv.z, bv.w) : make_float2(bv.x, bv.y)));
+          for (int t = 0; t < 12; ++t) {
+            const float4 q = du[t * 8 + pr], bv = *(const float4*)(vk + t * 32);
+            const float2 b2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float dd = c ? q.y : q.x, uu = c ? q.w : q.z;
+                if (STARTS && (starts >> t & 1)) h[c][j] = zero;
+                h[c][j] = ssc_fma(ssc_decay(rate[c][j], make_float2(dd, dd)), h[c][j], mul2(make_float2(uu, uu), b2[j]));
+              }
+            if ((t & 3) == 3) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) save[((t >> 2) * 2 + c) * 32 + lane] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
             }
           }
-        }
+#pragma unroll 1
+          for (int r = R - 1; r >= 0; --r) {
+            float2 before[4][2][2], decay[4][2][2];  // of a token: the state that the one before it left, its decay
+            float4 q4[4];
+            float2 b2[4][2];
+            if (r == 0) {
+              first_state();
+            } else {
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          const int t = quarter * 4 + i;
-          const float4 q = dxs[t * 32 + at.pr];
-          const float2 d = make_float2(q.x, q.y), u = make_float2(q.z, q.w), e = es[t * 32 + at.pr];
-          const bool start = starts >> t & 1;
-          float2 along = zero, through = zero, y = zero;
-          float v[8];  // dB and dC of the four states, summed over the pair
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 bv = *(const float4*)(bs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-            const float4 cv = *(const float4*)(cs + t * NP + ssc_state(k * 16, at.ln, 2 * j));
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const int s = 2 * j + m;
-              const float2 bb = m ? make_float2(bv.z, bv.w) : make_float2(bv.x, bv.y);
-              const float2 cc = m ? make_float2(cv.z, cv.w) : make_float2(cv.x, cv.y);
-              const float2 now = i == 3 ? h[s] : before[i == 3 ? 0 : i + 1][s];  // h_t
-              g[s] = fma2(e, cc, g[s]);
-              v[s] = fmaf(g[s].x, u.x, g[s].y * u.y);
-              v[4 + s] = fmaf(e.x, now.x, e.y * now.y);
-              along = fma2(g[s], bb, along);
-              if (gated) y = fma2(now, cc, y);
-              if (start) {
-                g[s] = zero;
-              } else {
-                g[s] = mul2(decay[i][s], g[s]);
-                const float2 qv = mul2(g[s], before[i][s]);
-                through = fma2(qv, rate[s], through);
-                da[s] = fma2(qv, d, da[s]);
+              for (int c = 0; c < 2; ++c) {
+                const float4 q = save[((r - 1) * 2 + c) * 32 + lane];
+                h[c][0] = make_float2(q.x, q.y), h[c][1] = make_float2(q.z, q.w);
               }
             }
-          }
-          if (!ONE && k > 0) {
-            const int place = (t * 32 + at.pr) * 4 + ssc_half(at.pr, at.ln >> 1) * 2 + (at.ln & 1);
-            along = add2(along, part[place]);
-            through = add2(through, part[SscShared::kPart + place]);
-            y = add2(y, part[2 * SscShared::kPart + place]);
-          }
-          ssc_put(part, t, at.pr, at.ln, along);
-          ssc_put(part + SscShared::kPart, t, at.pr, at.ln, through);
-          if (gated) ssc_put(part + 2 * SscShared::kPart, t, at.pr, at.ln, y);
-          // Over the 8 pairs of the warp: the lane keeps value 4 bit2 + 2 bit3 + bit4 of its lane number.
-          ssc_exchange(v, at.lane, 4);
-          float v4[4] = {v[0], v[1], v[2], v[3]};
-          ssc_exchange(v4, at.lane, 8);
-          float v2[2] = {v4[0], v4[1]};
-          ssc_exchange(v2, at.lane, 16);
-          red[(t * 4 + at.warp) * 32 + at.lane] = v2[0];
-        }
-      }
-      __syncthreads();
-      // The block's sums for B and C: 16 tokens of 32 values, over the four warps.
-      {
-        const int which = (at.lane >> 2 & 1) * 4 + (at.lane >> 3 & 1) * 2 + (at.lane >> 4 & 1);
-        const int n = ssc_state(k * 16, at.ln, which & 3);
-        float* out = which < 4 ? a.part_b : a.part_c;
 #pragma unroll
-        for (int i = 0; i < kSscRows; ++i) {
-          const int t = own + i;
-          const float* r = red + t * 128 + at.lane;
-          const float s = (r[0] + r[32]) + (r[64] + r[96]);
+            for (int i = 0; i < 4; ++i) {
+              const int t = 4 * r + i;
+              q4[i] = du[t * 8 + pr];
+              const float4 bv = *(const float4*)(vk + t * 32);
+              b2[i][0] = make_float2(bv.x, bv.y), b2[i][1] = make_float2(bv.z, bv.w);
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float dd = c ? q4[i].y : q4[i].x, uu = c ? q4[i].w : q4[i].z;
+                  before[i][c][j] = h[c][j];
+                  if (STARTS && (starts >> t & 1)) h[c][j] = zero;
+                  decay[i][c][j] = ssc_decay(rate[c][j], make_float2(dd, dd));
+                  h[c][j] = ssc_fma(decay[i][c][j], h[c][j], mul2(make_float2(uu, uu), b2[i][j]));
+                }
+            }
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+              const int t = 4 * r + i;
+              const float4 cv = *(const float4*)(vk + t * 32 + 16);
+              const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)}, e = es[t * 8 + pr];
+              const bool start = STARTS && (starts >> t & 1);
+              float2 along[2] = {zero, zero}, through[2] = {zero, zero}, y[2] = {zero, zero};
+              float2 vb[2], vc[2];  // dB and dC of the four states, over the pair
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float dd = c ? q4[i].y : q4[i].x, uu = c ? q4[i].w : q4[i].z, ee = c ? e.y : e.x;
+                const float2 u2 = make_float2(uu, uu), e2 = make_float2(ee, ee), d2 = make_float2(dd, dd);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 now = i == 3 ? h[c][j] : before[i == 3 ? 0 : i + 1][c][j];  // h_t
+                  float2& gg = g[c][j];
+                  gg = ssc_fma(e2, c2[j], gg);
+                  vb[j] = c ? ssc_fma(gg, u2, vb[j]) : mul2(gg, u2);
+                  vc[j] = c ? ssc_fma(now, e2, vc[j]) : mul2(now, e2);
+                  along[c] = ssc_fma(gg, b2[i][j], along[c]);
+                  if (gated) y[c] = ssc_fma(now, c2[j], y[c]);
+                  if (start) {
+                    gg = zero;
+                  } else {
+                    gg = mul2(decay[i][c][j], gg);
+                    const float2 q = mul2(gg, before[i][c][j]);
+                    through[c] = ssc_fma(q, rate[c][j], through[c]);
+                    da[c][j] = ssc_fma(q, d2, da[c][j]);
+                  }
+                }
+              }
+              float2* part = sums + ssc_sum_half(i, pr, ln >> 1) + (ln & 1);
+              part[0] = make_float2(along[0].x + along[0].y, along[1].x + along[1].y);
+              part[128] = make_float2(through[0].x + through[0].y, through[1].x + through[1].y);
+              if (gated) part[256] = make_float2(y[0].x + y[0].y, y[1].x + y[1].y);
+              // Over the 8 pairs of the warp: a lane keeps value 4 bit2 + 2 bit3 + bit4 of its lane number.
+              float v[8] = {vb[0].x, vb[0].y, vb[1].x, vb[1].y, vc[0].x, vc[0].y, vc[1].x, vc[1].y};
+              ssc_exchange(v, lane, 4);
+              float v4[4] = {v[0], v[1], v[2], v[3]};
+              ssc_exchange(v4, lane, 8);
+              float v2[2] = {v4[0], v4[1]};
+              ssc_exchange(v2, lane, 16);
+              red[t * 32 + lane] = v2[0];
+            }
+            __syncwarp();
+            float2 own[3];  // of token 4 r + ln, over the states
+#pragma unroll
+            for (int w = 0; w < 3; ++w) {
+              const float4 lo = *(const float4*)(sums + w * 128 + ssc_sum_half(ln, pr, 0));
+              const float4 hi = *(const float4*)(sums + w * 128 + ssc_sum_half(ln, pr, 1));
+              own[w] = add2(add2(make_float2(lo.x, lo.y), make_float2(lo.z, lo.w)), add2(make_float2(hi.x, hi.y), make_float2(hi.z, hi.w)));
+            }
+            if constexpr (ONE) {
+              finish(r, own[0], own[1], own[2]);
+            } else {
+#pragma unroll
+              for (int w = 0; w < 3; ++w)
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                  if (q == r) acc[w][q] = add2(acc[w][q], own[w]);
+            }
+            __syncwarp();
+          }
+        };
+        if (starts) tokens(std::false_type());
+        else tokens(std::true_type());
+        __syncthreads();
+        // The block's sums for B and C: 16 tokens of 32 values, over the four warps.
+        const int which = (lane >> 2 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 4 & 1);
+        const int n = k * 16 + ln * M + (which & 3);
+        float* out = which < 4 ? a.part_b : a.part_c;
+        const float* all = (const float*)((const unsigned char*)red - warp * S::warp_bytes(NB, CARRY));
+        const int step = S::warp_bytes(NB, CARRY) / 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = warp * 4 + i;
+          const float* r = all + t * 32 + lane;
+          const float s = (r[0] + r[step]) + (r[2 * step] + r[3 * step]);
           if (n < a.N && t0 + t < a.T_)
-            out[(((at.block * a.B + at.b) * a.T_ + t0 + t) * a.G + at.group) * a.N + n] = s;
+            out[(((block * a.B + b) * a.T_ + t0 + t) * a.G + group) * a.N + n] = s;
         }
+        if (!ONE && k + 1 < NB) __syncthreads();  // before the sums are written again
       }
       if constexpr (!ONE) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          gs[(k * 4 + s) * kSscThreads + threadIdx.x] = g[s];
-          das[(k * 4 + s) * kSscThreads + threadIdx.x] = da[s];
-        }
-        if (k + 1 < NB) __syncthreads();  // before the sums are written again
+        put(2 * k, g);
+        put(2 * k + 1, da);
       }
     }
-    // C
+    if constexpr (!ONE && !CARRY) {
 #pragma unroll
-    for (int i = 0; i < kSscRows; ++i) {
-      const int count = t0 + own + i < a.T_ ? at.count : 0;
-      const float2 x = P::wide(P::load(px + i * a.xt, count));
-      const float4 q = dxs[(own + i) * 32 + at.lane];
-      const float2 d = make_float2(q.x, q.y), e = es[(own + i) * 32 + at.lane];
-      const float2 along = ssc_get(part, own + i, at.lane);
-      const float2 through = mul2(ssc_get(part + SscShared::kPart, own + i, at.lane), make_float2(kLn2, kLn2));
-      const float2 dx = fma2(skip, e, mul2(d, along));
-      float2 dd = fma2(x, along, through);
-      if (a.softplus) dd = mul2(dd, sigmoid<T>(add2(P::wide(P::load(pdt + i * a.dtt, count)), bias)));
-      if (!count) dd = zero;
-      dskip = fma2(e, x, dskip);
-      dbias = add2(dbias, dd);
-      const long long t = t0 + own + i;
-      P::store(a.dx + at.b * a.dxb + t * a.dxt + at.ch, count, dx);
-      P::store(a.ddt + at.b * a.ddtb + t * a.ddtt + at.ch, count, dd);
-      if (gated) {
-        const float2 z = P::wide(P::load(pz + i * a.zt, count)), s = sigmoid<T>(z);
-        const float2 y = fma2(skip, x, ssc_get(part + 2 * SscShared::kPart, own + i, at.lane));
-        const float2 slope = fma2(mul2(z, s), fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
-        const float2 dy = P::wide(P::load(pdy + i * a.dyt, count));
-        P::store(a.dz + at.b * a.dzb + t * a.dzt + at.ch, count, mul2(mul2(dy, y), slope));
-      }
+      for (int r = 0; r < R; ++r) finish(r, acc[0][r], acc[1][r], acc[2][r]);
     }
+    if constexpr (CARRY) __syncthreads();  // before B and C are widened again
   }
 
-  // The sums over the part's tokens.
-  const long long row = at.b * a.parts + at.part;
-  float* pa = a.part_a + row * a.D * (a.N + 2);
-  for (int k = 0; k < NB; ++k) {
+  // The sums over the part's tokens: over the lanes of a pair.
+  const auto over_lanes = [&](float2 v) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int n = ssc_state(k * 16, at.ln, s);
-      const float2 v = ONE ? da[s] : das[(k * 4 + s) * kSscThreads + threadIdx.x];
-      const float2 c = ONE ? g[s] : gs[(k * 4 + s) * kSscThreads + threadIdx.x];
-      ssc_store(pa + (long long)at.chb * a.N, n, a.N, at.countb, v);
-      if (a.dh0 && at.part == 0) ssc_store(a.dh0 + (at.b * a.D + at.chb) * a.N, n, a.N, at.countb, c);
+    for (int bit = 1; bit < 4; bit *= 2) v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, bit), __shfl_xor_sync(0xffffffffu, v.y, bit)));
+    return v;
+  };
+  if constexpr (CARRY) {
+    const long long q = b * (a.parts - 1) + part - 1;
+    const float2 sum = over_lanes(sum_d);
+    if (ln == 0) {
+      if (count > 0) a.sums[q * a.D + ch] = sum.x;
+      if (count > 1) a.sums[q * a.D + ch + 1] = sum.y;
     }
-  }
-  __syncthreads();
-  part[at.warp * 32 + at.lane] = dskip;
-  part[128 + at.warp * 32 + at.lane] = dbias;
-  __syncthreads();
-  if (at.warp < 2) {
-    const float2* p = part + at.warp * 128 + at.lane;
-    const float2 s = add2(add2(p[0], p[32]), add2(p[64], p[96]));
-    float* out = pa + (long long)a.D * a.N + at.warp * a.D + at.ch;
-    if (at.count > 0) out[0] = s.x;
-    if (at.count > 1) out[1] = s.y;
+    if (threadIdx.x == 0 && block == 0 && group == 0) a.drops[q] = dropped ? 1.f : 0.f;
+    for (int k = 0; k < NB; ++k) {
+      if constexpr (!ONE) get(2 * k, g);
+      ssc_store_any<M>(a.vec, a.ends + (q * a.D + ch) * a.N, k * 16 + ln * M, a.N, count, g);
+    }
+  } else {
+    float* pa = a.part_a + (b * a.parts + part) * a.D * (a.N + 2);
+    for (int k = 0; k < NB; ++k) {
+      if constexpr (!ONE) {
+        get(2 * k, g);
+        get(2 * k + 1, da);
+      }
+      ssc_store_any<M>(false, pa + (long long)ch * a.N, k * 16 + ln * M, a.N, count, da);
+      if (a.dh0 && part == 0) ssc_store_any<M>(a.vec, a.dh0 + row * a.N, k * 16 + ln * M, a.N, count, g);
+    }
+    dskip = over_lanes(dskip), dbias = over_lanes(dbias);
+    if (ln < 2) {
+      const float2 v = ln ? dbias : dskip;
+      float* out = pa + (long long)a.D * a.N + ln * a.D + ch;
+      if (count > 0) out[0] = v.x;
+      if (count > 1) out[1] = v.y;
+    }
   }
 }
 
@@ -1232,7 +1224,7 @@ template <class T> SscArgs<T> ssc_args(const SelectiveScanJob& j, const SscSplit
   a.tiles = (int)((j.T + kSscTile - 1) / kSscTile);
   a.parts = (int)split.parts, a.part_tiles = (int)split.tiles, a.softplus = j.softplus;
   a.vec = j.N % 4 == 0;
-  for (const void* q : {(const void*)j.a, (const void*)j.h0, (const void*)j.last, (const void*)j.kept}) a.vec = a.vec && (uintptr_t)q % 16 == 0;
+  for (const void* q : {(const void*)j.a, (const void*)j.h0, (const void*)j.last, (const void*)j.kept, (const void*)j.dlast, (const void*)j.dh0}) a.vec = a.vec && (uintptr_t)q % 16 == 0;
   float* p = (float*)j.temp;
   a.ends = p;
   a.sums = a.ends + j.B * (split.parts - 1) * j.D * j.N;
@@ -1270,10 +1262,11 @@ template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const Selective
   const long long units = j.B * a.G * a.blocks;
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
+  using S = SscBack<T, EDGE>;
   if (split.parts > 1)
-    e = ssc_launch(ssc_carry_kernel<T, EDGE, ONE>, units * (split.parts - 1), SscShared::carry(a.NP), a, ctx);
+    e = ssc_launch(ssc_backward_kernel<T, EDGE, ONE, true>, units * (split.parts - 1), S::bytes(a.NP / 16, true), a, ctx);
   if (e == cudaSuccess)
-    e = ssc_launch(ssc_backward_kernel<T, EDGE, ONE>, units * split.parts, SscShared::backward(a.NP), a, ctx);
+    e = ssc_launch(ssc_backward_kernel<T, EDGE, ONE, false>, units * split.parts, S::bytes(a.NP / 16, false), a, ctx);
   if (e == cudaSuccess) {
     SscFoldArgs<T> f = {};
     f.part_a = a.part_a, f.part_b = a.part_b, f.part_c = a.part_c;
@@ -1304,8 +1297,11 @@ template <class T> cudaError_t launch_selective_scan(const SelectiveScanJob& j, 
 }
 
 template <class T> cudaError_t launch_selective_scan_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  bool even = (j.D / j.G) % 2 == 0;
-  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.dy, &j.dx, &j.ddt, &j.dz}) even = even && ssc_rows<T>(*s, 2, j.B, j.T);
+  constexpr int V = 16 / sizeof(T);
+  bool even = (j.D / j.G) % V == 0 && j.N % V == 0 && (uintptr_t)j.kept % 16 == 0 && ssc_rows<T>(j.b, V, j.B, j.T, j.G) &&
+              ssc_rows<T>(j.c, V, j.B, j.T, j.G);
+  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.dy}) even = even && ssc_rows<T>(*s, V, j.B, j.T);
+  for (const SeqArray* s : {&j.dx, &j.ddt, &j.dz}) even = even && ssc_rows<T>(*s, 2, j.B, j.T);
   if (j.N <= 16) return even ? ssc_backward<T, false, true>(j, ctx) : ssc_backward<T, true, true>(j, ctx);
   return even ? ssc_backward<T, false, false>(j, ctx) : ssc_backward<T, true, false>(j, ctx);
 }
