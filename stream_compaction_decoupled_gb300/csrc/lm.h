@@ -154,29 +154,40 @@ struct SelectiveScanJob {
 constexpr int kSscTile = 16;      // tokens of a tile: a kept state precedes each
 constexpr int kSscChannels = 64;  // channels of a block
 constexpr int kSscMaxStates = 128;
-// The tokens of a batch row in parts of `tiles` tiles, which run side by side: as many as it
-// takes to fill the device, where the rows and channels alone do not.
+// How the tokens of a batch row are split: parts of `tiles` tiles each, which run side by side.
 struct SscSplit {
   long long parts, tiles;
 };
-inline SscSplit ssc_split(long long B, long long T, long long D, long long G, bool backward) {
-  const long long units = B * G * ((D / G + kSscChannels - 1) / kSscChannels);
-  const long long tiles = (T + kSscTile - 1) / kSscTile;
-  const long long want = (backward ? 2 : 4) * 152;
-  long long parts = units >= 152 ? 1 : want / units;
-  if (parts > tiles / 4) parts = tiles / 4;
+// At most so many parts: a part goes through all before it first, so that many make it longer than
+// they make the tokens of one shorter (forward, 1 x 32768 x 128 bf16: 64 parts 113 us, 128 102, 256
+// 129; the bound is 128).
+inline long long ssc_most_parts(long long tiles) {
+  const long long root = (long long)sqrt(8.0 * (double)tiles);
+  return root < tiles / 2 ? root : tiles / 2;
+}
+inline SscSplit ssc_parts(long long tiles, long long parts) {
+  const long long most = ssc_most_parts(tiles);
+  if (parts > most) parts = most;
   if (parts < 1) parts = 1;
   const long long each = (tiles + parts - 1) / parts;
   return {tiles ? (tiles + each - 1) / each : 1, each};
 }
+// The gradient: a block takes 64 channels.  Few blocks are split until the
+// device is full once; many four times over, since those that are left at the end then are short (8
+// x 2048 x 2048 bf16, 256 blocks: 885 us, in 3 parts 863, in 7 804; 1 x 8192 x 2048, 32 blocks: in
+// 14 parts 421 us, in 28 433).
+// per_sm: how many blocks fit an SM.  More of them give more parts: the scratch is sized for 3.
+inline SscSplit ssc_backward_split(long long B, long long T, long long D, long long G, int per_sm) {
+  const long long units = B * G * ((D / G + kSscChannels - 1) / kSscChannels);
+  return ssc_parts((T + kSscTile - 1) / kSscTile, (units < 128 ? 1 : 4) * per_sm * 152 / units);
+}
+
 // Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 /
 // lanes channels each; 4 blocks fit an SM.  Where the rows and channels give enough blocks, a row
 // is one chain (more parts cost a second pass over all parts but the last: 16 x 1024 x 2048 bf16,
 // gated, 256 blocks: 211 us, in 4 parts 252).  Else it is split until the device is full (8 x 2048
 // x 2048, 128 blocks: 313 us, in 4 parts 276; 4 x 2048 x 2048 315, in 9 parts 152), with 4 lanes
-// where 2 cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).  A part goes through
-// all before it first, so their number stays below the root of 8 times the tiles (1 x 32768 x 128:
-// 64 parts 113 us, 128 102, 256 129).
+// where 2 cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).
 struct SscForwardPlan {
   SscSplit split;
   int lanes;
@@ -190,18 +201,13 @@ inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, lo
   int lanes = 2;
   long long parts = 1;
   if (blocks(2) < 220) {
-    long long most = (long long)sqrt(8.0 * (double)tiles);
-    if (most > tiles / 2) most = tiles / 2;
-    if (blocks(2) * most < 456) lanes = 4;
+    if (blocks(2) * ssc_most_parts(tiles) < 456) lanes = 4;
     parts = 608 / blocks(lanes);
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
   }
-  const long long each = (tiles + parts - 1) / parts;
-  return {{tiles ? (tiles + each - 1) / each : 1, each}, lanes};
+  return {ssc_parts(tiles, parts), lanes};
 }
 inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, bool backward) {
-  const SscSplit s = backward ? ssc_split(B, T, D, G, true) : ssc_forward_plan(B, T, D, G).split;
+  const SscSplit s = backward ? ssc_backward_split(B, T, D, G, 3) : ssc_forward_plan(B, T, D, G).split;
   size_t floats = (size_t)B * (s.parts - 1) * (D * N + D + 1);
   if (backward) {
     floats += (size_t)B * s.parts * D * (N + 2);

@@ -606,7 +606,7 @@ __device__ __forceinline__ int ssc_sum_half(int i, int pair, int half) {
 // dC: over the pair in the thread, over the warp by exchanges, over the block in shared memory,
 // and over the blocks by a second kernel.
 template <class T, bool EDGE, bool ONE, bool CARRY>
-__global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
+__global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
   using S = SscBack<T, EDGE>;
   using P = typename S::P;
@@ -710,8 +710,12 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
     }
     return f;
   };
-  // Starts a tile's copies into the ring (EDGE: loads it at once).
+  // Starts a tile's copies into the ring.  EDGE, where they cannot be in pieces of 16 bytes: loads
+  // the tile, for `land` to store behind the one that is worked on.
   constexpr int V = 16 / sizeof(T), PER = 32 / V;
+  Raw ex[EDGE ? R : 1], ed[EDGE ? R : 1], ey[EDGE ? R : 1], ez[EDGE ? R : 1];
+  T ev[EDGE && ONE ? 4 : 1];
+  float2 ek[2][2];
   const auto fetch = [&](int tile, int stage) {
     unsigned char* to = ring + stage * S::STAGE;
     if (tile >= tile0) {
@@ -720,11 +724,19 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const long long u = min(t + 4 * r + ln, a.T_ - 1);
-          Raw* at = (Raw*)(to + (4 * r + ln) * S::ROW) + pr;
-          if (!CARRY) at[0] = P::load(px + u * a.xt + ch, count);
-          at[S::ARRAY / sizeof(Raw)] = P::load(pdt + u * a.dtt + ch, count);
-          at[2 * S::ARRAY / sizeof(Raw)] = P::load(pdy + u * a.dyt + ch, count);
-          if (gated) at[3 * S::ARRAY / sizeof(Raw)] = P::load(pz + u * a.zt + ch, count);
+          if (!CARRY) ex[r] = P::load(px + u * a.xt + ch, count);
+          ed[r] = P::load(pdt + u * a.dtt + ch, count);
+          ey[r] = P::load(pdy + u * a.dyt + ch, count);
+          if (gated) ez[r] = P::load(pz + u * a.zt + ch, count);
+        }
+        if constexpr (ONE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long u = min(t + 4 * warp + i, a.T_ - 1);
+            const int n = lane % 16 < a.N ? lane % 16 : 0;
+            ev[i] = lane < 16 ? pb[u * a.bt + n] : pc[u * a.ct + n];
+          }
+          if constexpr (!CARRY) ssc_load_any<M>(a.vec, a.kept + ((b * a.tiles + tile) * a.D + ch) * a.N, ln * M, a.N, count, ek);
         }
       } else {
 #pragma unroll
@@ -760,6 +772,29 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
     }
     cp_async_commit();
   };
+  const auto land = [&](int stage) {
+    if constexpr (EDGE) {
+      unsigned char* to = ring + stage * S::STAGE;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        Raw* at = (Raw*)(to + (4 * r + ln) * S::ROW) + pr;
+        at[0] = ex[r];
+        at[S::ARRAY / sizeof(Raw)] = ed[r];
+        at[2 * S::ARRAY / sizeof(Raw)] = ey[r];
+        at[3 * S::ARRAY / sizeof(Raw)] = ez[r];
+      }
+      if constexpr (ONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          ((T*)(vring + stage * S::VECTORS))[(4 * warp + i) * 32 + lane] = lane % 16 < a.N ? ev[i] : narrow<T>(0.f);
+        if constexpr (!CARRY) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *(float4*)(to + 4 * S::ARRAY + (c * 32 + lane) * 16) = make_float4(ek[c][0].x, ek[c][0].y, ek[c][1].x, ek[c][1].y);
+        }
+      }
+    }
+  };
   if constexpr (!EDGE) {  // states past the last stay zero
     for (int k = lane; k < S::STAGES * S::STAGE / 16; k += 32) ((float4*)ring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = threadIdx.x; k < S::STAGES * S::VECTORS / 16; k += kSscThreads) ((float4*)vring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -769,6 +804,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
   unsigned flag = 0, dropped = 0;
   int stage = 0;
   fetch(tile1 - 1, 0);
+  land(0);
   for (int tile = tile1 - 1; tile >= tile0; --tile) {
     const int t0 = tile * L, number = (tile1 - 1 - tile) % 32;
     if (number == 0) flag = flags(tile);
@@ -777,9 +813,10 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
     cp_async_wait<0>();
     __syncwarp();
     const unsigned char* raw = ring + stage * S::STAGE;
+    const bool whole = t0 + L <= a.T_;
     const auto pair = [&](int array, int t) { return P::wide(((const Raw*)(raw + array * S::ARRAY + t * S::ROW))[pr]); };
     // A
-    if (EDGE || !ONE) {
+    if constexpr (!ONE) {
       for (int k = threadIdx.x; k < NB * L * 32; k += kSscThreads) {
         const int n = k % 16, second = k / 16 % 2, i = k / 32 % L, n0 = k / (32 * L) * 16 + n;
         const long long u = min(t0 + i, a.T_ - 1);
@@ -798,14 +835,14 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
         const float2 z = pair(3, t);
         e = mul2(e, mul2(z, sigmoid<T>(z)));
       }
-      if (t0 + t >= a.T_) d = e = zero;
+      if (!whole && t0 + t >= a.T_) d = e = zero;
       const float2 u = CARRY ? zero : mul2(d, pair(0, t));
       du[t * 8 + pr] = make_float4(d.x, d.y, u.x, u.y);
       es[t * 8 + pr] = e;
       if constexpr (CARRY) sum_d = add2(sum_d, d);
     }
     __syncthreads();
-    // The other stage has been read: its copies go on behind B.  (EDGE's loads are waited for here.)
+    // The other stage has been read: its copies go on behind B.
     stage ^= 1;
     fetch(tile - 1, stage);
 
@@ -818,7 +855,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
     }
     // C, of own token r.
     const auto finish = [&](int r, float2 along, float2 through, float2 y) {
-      const int t = 4 * r + ln, n = t0 + t < a.T_ ? count : 0;
+      const int t = 4 * r + ln, n = whole || t0 + t < a.T_ ? count : 0;
       const long long u = t0 + t;
       const float2 x = pair(0, t), e = es[t * 8 + pr];
       const float4 q = du[t * 8 + pr];
@@ -827,10 +864,9 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
       if (a.softplus) dd = mul2(dd, sigmoid<T>(add2(pair(1, t), bias)));
       P::store(a.dx + b * a.dxb + u * a.dxt + ch, n, fma2(skip, e, mul2(make_float2(q.x, q.y), along)));
       P::store(a.ddt + b * a.ddtb + u * a.ddtt + ch, n, dd);
-      if (n > 0) {
-        dskip = fma2(e, x, dskip);
-        dbias = add2(dbias, dd);
-      }
+      if (!whole && n <= 0) dd = zero;  // (e is 0 there)
+      dskip = fma2(e, x, dskip);
+      dbias = add2(dbias, dd);
       if (gated) {
         const float2 z = pair(3, t), s = sigmoid<T>(z);
         const float2 slope = fma2(mul2(z, s), fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
@@ -867,7 +903,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
       } else {
         float2 h[2][2];
         const auto first_state = [&]() {
-          if constexpr (ONE && !EDGE) {
+          if constexpr (ONE) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float4 q = *(const float4*)(raw + 4 * S::ARRAY + (c * 32 + lane) * 16);
@@ -1018,9 +1054,10 @@ __global__ void __launch_bounds__(kSscThreads, ONE ? 3 : 2) ssc_backward_kernel(
     }
     if constexpr (!ONE && !CARRY) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) finish(r, acc[0][r], acc[1][r], acc[2][r]);
+      for (int r = R - 1; r >= 0; --r) finish(r, acc[0][r], acc[1][r], acc[2][r]);
     }
     if constexpr (CARRY) __syncthreads();  // before B and C are widened again
+    land(stage);
   }
 
   // The sums over the part's tokens: over the lanes of a pair.
@@ -1257,7 +1294,8 @@ template <class T, bool EDGE, bool ONE, int LN> cudaError_t ssc_forward(const Se
 }
 
 template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  const SscSplit split = ssc_split(j.B, j.T, j.D, j.G, true);
+  // What the kernel's registers and (fp32, more states) shared memory allow.
+  const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.G, EDGE || !ONE || sizeof(T) == 4 ? 2 : 3);
   const SscArgs<T> a = ssc_args<T>(j, split);
   const long long units = j.B * a.G * a.blocks;
   profile_before(ctx);
