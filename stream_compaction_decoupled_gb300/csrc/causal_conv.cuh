@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_ke
             }
           }
 #pragma unroll
-          for (int h = 0; h < H; ++h) {  // act' = s + p s (1 - s)
-            const float2 s = sigmoid<T>(p[h]);
+          for (int h = 0; h < H; ++h) {  // act' = s + p s (1 - s); dw and db may be fp32
+            const float2 s = sigmoid<float>(p[h]);
             const float2 c = fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
             q[h] = mul2(gs[u][h], fma2(mul2(p[h], s), c, s));
           }

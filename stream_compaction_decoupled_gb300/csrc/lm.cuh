@@ -205,33 +205,17 @@ template <class T> __device__ __forceinline__ float2 sigmoid(float2 z) {
   }
 }
 
-// log(1 + e) / e on [0, 1]: polynomials of least relative error (exchange algorithm in 64 bits), off
-// by 2.6 units of 2^-24 in fp32 arithmetic (degree 9), or by 24, which 16-bit inputs' own rounding
-// hides (degree 6).
-template <class T> __device__ __forceinline__ float2 log1p_over2(float2 e) {
-  constexpr float c9[] = {1.f, -0.499999017f, 0.333299637f, -0.249541342f, 0.196759388f, -0.153055921f,
-                          0.106036551f, -0.0569595359f, 0.0198514629f, -0.00324402517f};
-  constexpr float c6[] = {0.999998748f, -0.499869645f, 0.331094503f, -0.235038608f, 0.149223879f,
-                          -0.066401802f, 0.0141410241f};
-  constexpr int N = sizeof(T) == 4 ? 9 : 6;
-  float2 p = sizeof(T) == 4 ? make_float2(c9[9], c9[9]) : make_float2(c6[6], c6[6]);
+// log(1 + e^v) = max(v, 0) + log(1 + e^-|v|) of two values, relatively accurate where it is small:
+// log(1 + e) / e on [0, 1] is a polynomial of least relative error (exchange algorithm in 64 bits; off by
+// 2.6 units of 2^-24 in fp32 arithmetic).
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  constexpr float c[] = {1.f, -0.499999017f, 0.333299637f, -0.249541342f, 0.196759388f, -0.153055921f,
+                         0.106036551f, -0.0569595359f, 0.0198514629f, -0.00324402517f};
+  const float2 e = exp_full(make_float2(fmaxf(-fabsf(v.x), -104.f), fmaxf(-fabsf(v.y), -104.f)));
+  float2 p = make_float2(c[9], c[9]);
 #pragma unroll
-  for (int k = N - 1; k >= 0; --k) {
-    const float c = sizeof(T) == 4 ? c9[k] : c6[k];
-    p = fma2(p, e, make_float2(c, c));
-  }
-  return p;
-}
-
-// log(1 + e^v) = max(v, 0) + log(1 + e^-|v|) of two values, relatively accurate where it is small.
-template <class T> __device__ __forceinline__ float2 softplus2(float2 v) {
-  float2 e;
-  if constexpr (sizeof(T) == 4) {
-    e = exp_full(make_float2(fmaxf(-fabsf(v.x), -104.f), fmaxf(-fabsf(v.y), -104.f)));
-  } else {
-    e = make_float2(ex2(-kLog2e * fabsf(v.x)), ex2(-kLog2e * fabsf(v.y)));
-  }
-  return fma2(e, log1p_over2<T>(e), make_float2(max_nan(v.x, 0.f), max_nan(v.y, 0.f)));
+  for (int k = 8; k >= 0; --k) p = fma2(p, e, make_float2(c[k], c[k]));
+  return fma2(e, p, make_float2(max_nan(v.x, 0.f), max_nan(v.y, 0.f)));
 }
 
 // ---- asynchronous copies of 16 bytes, tracked by the issuing thread ------------------

@@ -101,8 +101,9 @@ struct ConvSplit {
   long long slots, runs, length;
 };
 inline ConvSplit conv_backward_split(long long B, long long T, long long D) {
-  const long long want = (152 * 12) / ((D + 127) / 128) + 1;  // warps of 128 channels: 12 an SM
-  const long long per_row = (want + B - 1) / B;
+  long long want = (152 * 12) / ((D + 127) / 128);  // warps of 128 channels, 12 an SM: all run at once
+  if (want < 1) want = 1;
+  const long long per_row = want / B > 1 ? want / B : 1;
   long long length = (T + per_row - 1) / per_row;
   length = length < 32 ? 32 : (length + 7) / 8 * 8;  // a run reads up to 14 tokens of its neighbours
   const long long runs = (T + length - 1) / length;

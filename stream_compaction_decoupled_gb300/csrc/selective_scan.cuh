@@ -103,8 +103,10 @@ template <class T, bool EDGE> struct SscPair {
 // 5.2 with these and the sums single and only D x B packed, 5.9 with all of it single).
 __device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) { return make_float2(ex2(a.x * d.x), ex2(a.y * d.y)); }
 __device__ __forceinline__ float2 ssc_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+// D and e go into fp32 results (states, dA, dd, dbias) whatever the inputs' type, so that their
+// functions are the fp32 ones; what only 16-bit outputs see (y, dz) is as exact as their type.
 template <class T> __device__ __forceinline__ float2 ssc_step_size(const SscArgs<T>& a, float2 v) {
-  return a.softplus ? softplus2<T>(v) : v;
+  return a.softplus ? softplus2(v) : v;
 }
 
 // ---- forward ---------------------------------------------------------------------------
@@ -208,7 +210,7 @@ template <int M> __device__ __forceinline__ void ssc_store_any(bool vec, float* 
 
 // ENDS: only the states that the part ends with, from a state of zero, and its sum of D.
 template <class T, bool EDGE, bool ONE, bool ENDS, int LN>
-__global__ void __launch_bounds__(kSscThreads, 4) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
+__global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
   using S = SscLane<T, EDGE, LN>;
   using P = typename S::P;
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kSscThreads, 4) ssc_forward_kernel(const __gri
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         d[r] = add2(pair(1, r), bias);
-        if constexpr (decltype(soft)::value) d[r] = softplus2<T>(d[r]);
+        if constexpr (decltype(soft)::value) d[r] = softplus2(d[r]);
       }
     };
     if (a.softplus) sizes(std::true_type());
@@ -833,7 +835,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
       float2 d = ssc_step_size(a, add2(pair(1, t), bias)), e = pair(2, t);
       if (gated) {
         const float2 z = pair(3, t);
-        e = mul2(e, mul2(z, sigmoid<T>(z)));
+        e = mul2(e, mul2(z, sigmoid<float>(z)));
       }
       if (!whole && t0 + t >= a.T_) d = e = zero;
       const float2 u = CARRY ? zero : mul2(d, pair(0, t));
@@ -861,7 +863,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
       const float4 q = du[t * 8 + pr];
       through = mul2(through, make_float2(kLn2, kLn2));
       float2 dd = fma2(x, along, through);
-      if (a.softplus) dd = mul2(dd, sigmoid<T>(add2(pair(1, t), bias)));
+      if (a.softplus) dd = mul2(dd, sigmoid<float>(add2(pair(1, t), bias)));
       P::store(a.dx + b * a.dxb + u * a.dxt + ch, n, fma2(skip, e, mul2(make_float2(q.x, q.y), along)));
       P::store(a.ddt + b * a.ddtb + u * a.ddtt + ch, n, dd);
       if (!whole && n <= 0) dd = zero;  // (e is 0 there)
@@ -1159,7 +1161,7 @@ __global__ void __launch_bounds__(256) ssc_fold_kernel(const __grid_constant__ S
 template <class T> struct SscStepArgs {
   const T *x, *dt, *z, *b, *c;
   T* y;
-  long long sx, sdt, sz, sy, sb, sbg, sc, scg, pool, n;  // n: channels of all rows
+  long long sx, sdt, sz, sy, sb, sbg, sc, scg, pool, B, n;  // n: channels of all groups of rows
   const float *a, *d, *bias;
   float* state;
   const int32_t* slots;
@@ -1167,66 +1169,112 @@ template <class T> struct SscStepArgs {
   ErrSink err;
 };
 
-// Four lanes a channel, four neighbouring states a lane (VEC: as one 16-byte access).
-template <class T, bool VEC>
+// Four lanes a channel, four neighbouring states of each 16 a lane (VEC: as one access of 16
+// bytes, and B and C as one of four values); ROWS rows, which share the channel's A.
+template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ SscStepArgs<T> a) {
   pdl_entry();
   const long long at = ((long long)blockIdx.x * 128 + threadIdx.x) >> 2;
   const int ln = threadIdx.x & 3;
   const bool live = at < a.n;
-  const long long b = live ? at / a.D : 0;
   const int ch = live ? (int)(at % a.D) : 0, group = ch / a.DG;
-  long long slot = a.slots ? (long long)a.slots[b] : b;
-  if (slot >= a.pool) {  // no such state: reported, and the row treated as padding
-    if (live && ch == 0 && ln == 0) raise_err(a.err, ERRBIT_RANGE);
-    slot = -1;
+  const long long b0 = live ? at / a.D * ROWS : 0;
+  const int rows = live ? (int)min((long long)ROWS, a.B - b0) : 0;
+  long long slot[ROWS];
+  T rx[ROWS], rdt[ROWS], rz[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    slot[r] = -1;
+    if (r < rows) {
+      const long long b = b0 + r;
+      slot[r] = a.slots ? (long long)a.slots[b] : b;
+      rx[r] = a.x[b * a.sx + ch];
+      rdt[r] = a.dt[b * a.sdt + ch];
+      if (a.z) rz[r] = a.z[b * a.sz + ch];
+    }
   }
-  float y = 0.f;
-  if (live && slot >= 0) {
-    const float x = widen(a.x[b * a.sx + ch]);
-    const float v = widen(a.dt[b * a.sdt + ch]) + (a.bias ? a.bias[ch] : 0.f);
-    const float step = a.softplus ? softplus2<T>(make_float2(v, v)).x : v;
-    const T *pb = a.b + b * a.sb + group * a.sbg, *pc = a.c + b * a.sc + group * a.scg;
-    float* ps = a.state + (slot * a.D + ch) * a.N;
-    const float* pa = a.a + (long long)ch * a.N;
-    for (int n0 = ln * 4; n0 < a.N; n0 += 16) {
-      float h[4], r[4];
-      if constexpr (VEC) {
-        const float4 q = *(const float4*)(ps + n0), w = *(const float4*)(pa + n0);
-        h[0] = q.x, h[1] = q.y, h[2] = q.z, h[3] = q.w;
-        r[0] = w.x, r[1] = w.y, r[2] = w.z, r[3] = w.w;
-      } else {
+  const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.d ? a.d[ch] : 0.f;
+  const float* pa = a.a + (long long)ch * a.N;
+  float y[ROWS], step[ROWS], x[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (slot[r] >= a.pool) {  // no such state: reported, and the row treated as padding
+      if (ch == 0 && ln == 0) raise_err(a.err, ERRBIT_RANGE);
+      slot[r] = -1;
+    }
+    x[r] = step[r] = y[r] = 0.f;
+    if (slot[r] >= 0) {
+      x[r] = widen(rx[r]);
+      const float v = widen(rdt[r]) + bias;
+      step[r] = a.softplus ? softplus2(make_float2(v, v)).x : v;
+    }
+  }
+  for (int n0 = ln * 4; n0 < a.N; n0 += 16) {
+    float w[4], h[ROWS][4];
+    T vb[ROWS][4], vc[ROWS][4];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (slot[r] >= 0) {
+        const float* ps = a.state + (slot[r] * a.D + ch) * a.N + n0;
+        const T *pb = a.b + (b0 + r) * a.sb + group * a.sbg + n0, *pc = a.c + (b0 + r) * a.sc + group * a.scg + n0;
+        if constexpr (VEC) {
+          const float4 q = *(const float4*)ps;
+          h[r][0] = q.x, h[r][1] = q.y, h[r][2] = q.z, h[r][3] = q.w;
+          using Four = std::conditional_t<sizeof(T) == 4, float4, uint2>;
+          const Four fb = *(const Four*)pb, fc = *(const Four*)pc;
+          memcpy(vb[r], &fb, sizeof(fb));
+          memcpy(vc[r], &fc, sizeof(fc));
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (n0 + s < a.N) h[r][s] = ps[s], vb[r][s] = pb[s], vc[r][s] = pc[s];
+          }
+        }
+      }
+    }
+    if constexpr (VEC) {
+      const float4 q = *(const float4*)(pa + n0);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) w[s] = n0 + s < a.N ? pa[n0 + s] : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (slot[r] >= 0) {
+        float* ps = a.state + (slot[r] * a.D + ch) * a.N + n0;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          h[s] = n0 + s < a.N ? ps[n0 + s] : 0.f;
-          r[s] = n0 + s < a.N ? pa[n0 + s] : 0.f;
+          if (VEC || n0 + s < a.N) {
+            h[r][s] = fmaf(ex2(step[r] * (w[s] * kLog2e)), h[r][s], step[r] * x[r] * widen(vb[r][s]));
+            y[r] = fmaf(h[r][s], widen(vc[r][s]), y[r]);
+          }
         }
-      }
+        if constexpr (VEC) {
+          *(float4*)ps = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+        } else {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (VEC || n0 + s < a.N) {
-          h[s] = fmaf(ex2(step * (r[s] * kLog2e)), h[s], step * x * widen(pb[n0 + s]));
-          y = fmaf(h[s], widen(pc[n0 + s]), y);
+          for (int s = 0; s < 4; ++s)
+            if (n0 + s < a.N) ps[s] = h[r][s];
         }
-      }
-      if constexpr (VEC) {
-        *(float4*)(ps + n0) = make_float4(h[0], h[1], h[2], h[3]);
-      } else {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (n0 + s < a.N) ps[n0 + s] = h[s];
       }
     }
-    if (ln == 0 && a.d) y = fmaf(a.d[ch], x, y);
   }
-  y += __shfl_xor_sync(0xffffffffu, y, 1);
-  y += __shfl_xor_sync(0xffffffffu, y, 2);
-  if (live && ln == 0) {
-    if (slot >= 0 && a.z) {
-      const float z = widen(a.z[b * a.sz + ch]);
-      y *= z * sigmoid<T>(make_float2(z, z)).x;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    y[r] += __shfl_xor_sync(0xffffffffu, y[r], 1);
+    y[r] += __shfl_xor_sync(0xffffffffu, y[r], 2);
+    if (r < rows && ln == r % 4) {
+      float v = 0.f;
+      if (slot[r] >= 0) {
+        v = fmaf(skip, x[r], y[r]);
+        if (a.z) {
+          const float z = widen(rz[r]);
+          v *= z * sigmoid<T>(make_float2(z, z)).x;
+        }
+      }
+      a.y[(b0 + r) * a.sy + ch] = narrow<T>(v);
     }
-    a.y[b * a.sy + ch] = narrow<T>(y);
   }
 }
 
@@ -1351,13 +1399,23 @@ template <class T> cudaError_t launch_selective_scan_step(const SelectiveScanSte
   a.sx = j.sx, a.sdt = j.sdt, a.sz = j.sz, a.sy = j.sy, a.sb = j.sb, a.sbg = j.sbg, a.sc = j.sc, a.scg = j.scg;
   a.a = j.a, a.d = j.d, a.bias = j.bias, a.state = j.state, a.slots = j.slots, a.pool = j.pool;
   a.D = (int)j.D, a.N = (int)j.N, a.DG = (int)(j.D / j.G), a.softplus = j.softplus;
-  a.n = j.B * j.D;
+  a.B = j.B;
   a.err = ctx.err;
-  const bool vec = j.N % 4 == 0 && (uintptr_t)j.state % 16 == 0 && (uintptr_t)j.a % 16 == 0;
+  const auto four = [&](const void* p, long long row, long long group) {  // four values at once
+    return (uintptr_t)p % (4 * sizeof(T)) == 0 && (j.B <= 1 || row % 4 == 0) && (j.G <= 1 || group % 4 == 0);
+  };
+  const bool vec = j.N % 4 == 0 && (uintptr_t)j.state % 16 == 0 && (uintptr_t)j.a % 16 == 0 && four(j.b, j.sb, j.sbg) &&
+                   four(j.c, j.sc, j.scg);
+  // Four rows a thread keep more loads in flight, where there are threads enough all the same.
+  const bool many = j.B * j.D >= 256ll * ctx.num_sms;
+  a.n = (many ? (j.B + 3) / 4 : j.B) * j.D;
   const unsigned grid = (unsigned)((a.n + 31) / 32);
   profile_before(ctx);
-  const cudaError_t e = vec ? launch_pdl(ssc_step_kernel<T, true>, grid, 128, 0, ctx.stream, a)
-                            : launch_pdl(ssc_step_kernel<T, false>, grid, 128, 0, ctx.stream, a);
+  cudaError_t e;
+  if (many) e = vec ? launch_pdl(ssc_step_kernel<T, true, 4>, grid, 128, 0, ctx.stream, a)
+                    : launch_pdl(ssc_step_kernel<T, false, 4>, grid, 128, 0, ctx.stream, a);
+  else e = vec ? launch_pdl(ssc_step_kernel<T, true, 1>, grid, 128, 0, ctx.stream, a)
+               : launch_pdl(ssc_step_kernel<T, false, 1>, grid, 128, 0, ctx.stream, a);
   profile_after(ctx);
   return e;
 }

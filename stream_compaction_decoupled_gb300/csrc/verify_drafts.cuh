@@ -14,8 +14,8 @@
 //
 // Bound by memory: one or two rows of V.  A request's row is cut among the CTAs of a cluster and
 // their warps.  One pass finds the warps' sums; the CTAs exchange theirs through the cluster, and
-// the one within whose slice the draw falls reads that warp's part of it again, all threads together:
-// a thread a few values, a scan over the threads.
+// the one within whose slice the draw falls reads that warp's slice again: its warps an eighth each,
+// and one warp the eighth.
 #pragma once
 
 #include "lm.cuh"
@@ -92,8 +92,9 @@ template <class T, int V, int U, bool Q> struct VerifyPiece {
   }
 };
 
+// (lane 0's)
 template <class T, int V, bool Q> __device__ double verify_sum(const VerifyRow<T>& r, long long s0, long long s1, int lane) {
-  constexpr int U = V == 1 ? 16 : 4;
+  constexpr int U = V == 1 ? 12 : 16 / V;
   VerifySum sum;
   // A lane past the end of the slice reads its last pack, and counts it as nothing.
   for (long long from = s0; from < s1; from += 32 * V * U) {
@@ -117,47 +118,59 @@ template <class T, int V, bool Q> __device__ double verify_sum(const VerifyRow<T
       add(std::false_type());
     }
   }
-  double s = sum.value();
 #pragma unroll
-  for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  return s;
+  for (int k = 16; k; k >>= 1) sum.add(__shfl_xor_sync(0xffffffffu, sum.hi, k), __shfl_xor_sync(0xffffffffu, sum.lo, k));
+  return sum.value();
 }
 
 struct VerifyShared {
   double warp_sum[kVerifyWarps], cta_sum;
-  double before, limit;           // of the draw: the sum before the slice, what has to be exceeded
-  long long from, to;             // the slice; from < 0: not in this CTA
+  double before, limit;  // of the draw: the sum before the slice, what has to be exceeded
+  long long from, to;    // the slice; from < 0: not in this CTA
   int accepted;
-  unsigned first;                 // the first thread past the limit
-  unsigned long long last;        // 1 + the last index with something left
-  long long pick;
 };
 
-// The first j of the slice with before + r_from + ... + r_j > limit; the last with r_j > 0 where
-// rounding leaves none; -1 where no r_j is.  All threads.
-template <class T, int V, bool Q> __device__ long long verify_pick(const VerifyRow<T>& r, VerifyShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double before = sh.before;
-  constexpr int P = V == 1 ? 4 : 1, E = P * V;  // neighbouring packs, and their values
-  for (long long from = sh.from; from < sh.to; from += kVerifyThreads * E) {
-    const long long at = from + threadIdx.x * E;
+static_assert(kVerifyWarps == 8 && kVerifyMaxCluster <= 8, "sums over 8 lanes");
+// The sum of the lanes up to this one, of values of the first 8.
+__device__ __forceinline__ double verify_scan8(double v, int lane) {
+#pragma unroll
+  for (int k = 1; k < 8; k <<= 1) {
+    const double below = __shfl_up_sync(0xffffffffu, v, k);
+    if (lane >= k) v += below;
+  }
+  return v;
+}
+// Of the lanes with something left, the first past the limit, or the last; -1: there is none.
+__device__ __forceinline__ int verify_choose(bool some, bool past) {
+  const unsigned all = __ballot_sync(0xffffffffu, some), over = __ballot_sync(0xffffffffu, some && past);
+  return over ? __ffs(over) - 1 : all ? 31 - __clz(all) : -1;
+}
+
+// The first j in [from, to) with before + r_from + ... + r_j > limit; the last with r_j > 0 where
+// rounding leaves none; -1 where no r_j is.  One warp, 8 neighbouring values a lane at a time.
+template <class T, int V, bool Q>
+__device__ long long verify_pick(const VerifyRow<T>& r, long long from, long long to, double before, double limit, int lane) {
+  constexpr int E = 8, P = E / V;
+  long long last = -1;
+  for (; from < to; from += 32 * E) {
+    const long long at = from + lane * E;
     VerifyPiece<T, V, P, Q> piece;
-    piece.load(r, at < sh.to ? at : sh.from, V, sh.to - at);
-    float d[E], lost[E];
+    piece.load(r, at < to ? at : from, V, to - at);
+    const auto values = [&](auto&& each) {  // each(index, what is left, what its rounding lost), in order
 #pragma unroll
-    for (int u = 0; u < P; ++u) {
-      float du[V], lu[V];
-      piece.rest(u, at + u * V < sh.to, r.without - (at + u * V), du, lu);
+      for (int u = 0; u < P; ++u) {
+        float d[V], lost[V];
+        piece.rest(u, at + u * V < to, r.without - (at + u * V), d, lost);
 #pragma unroll
-      for (int e = 0; e < V; ++e) d[u * V + e] = du[e], lost[u * V + e] = lu[e];
-    }
+        for (int e = 0; e < V; ++e) each(u * V + e, d[e], lost[e]);
+      }
+    };
     VerifySum sum;
-    long long positive = -1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      sum.add(d[e], lost[e]);
-      if (d[e] > 0.f) positive = at + e;
-    }
+    int positive = -1;
+    values([&](int e, float d, float lost) {
+      sum.add(d, lost);
+      if (d > 0.f) positive = e;
+    });
     const double own = sum.value();
     double upto = own;
 #pragma unroll
@@ -165,36 +178,25 @@ template <class T, int V, bool Q> __device__ long long verify_pick(const VerifyR
       const double below = __shfl_up_sync(0xffffffffu, upto, k);
       if (lane >= k) upto += below;
     }
-    if (lane == 31) sh.warp_sum[warp] = upto;
-    if (threadIdx.x == 0) sh.first = kVerifyThreads;
-    __syncthreads();
-    double base = before;
-#pragma unroll
-    for (int w = 0; w < kVerifyWarps; ++w) {
-      if (w < warp) base += sh.warp_sum[w];
-      before += sh.warp_sum[w];
-    }
-    const bool past = positive >= 0 && base + upto > sh.limit;
-    if (past) atomicMin(&sh.first, threadIdx.x);
-    if (positive >= 0) atomicMax(&sh.last, (unsigned long long)positive + 1);
-    __syncthreads();
-    const unsigned first = sh.first;
-    if (first < kVerifyThreads) {
-      if (threadIdx.x == first) {
-        double s = base + (upto - own);
-        long long j = -1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          s += (double)d[e] + (double)lost[e];
-          if (j < 0 && d[e] > 0.f && s > sh.limit) j = at + e;
-        }
-        sh.pick = j < 0 ? positive : j;
+    const unsigned past = __ballot_sync(0xffffffffu, positive >= 0 && before + upto > limit);
+    if (past) {
+      const int first = __ffs(past) - 1;
+      int j = -1;
+      if (lane == first) {
+        double s = before + (upto - own);
+        values([&](int e, float d, float lost) {
+          s += (double)d + (double)lost;
+          if (j < 0 && d > 0.f && s > limit) j = e;
+        });
+        if (j < 0) j = positive;
       }
-      __syncthreads();
-      return sh.pick;
+      return from + first * E + __shfl_sync(0xffffffffu, j, first);
     }
+    const unsigned some = __ballot_sync(0xffffffffu, positive >= 0);
+    if (some) last = from + (31 - __clz(some)) * E + __shfl_sync(0xffffffffu, positive, 31 - __clz(some));
+    before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  return (long long)sh.last - 1;
+  return last;
 }
 
 template <class T, int V>
@@ -258,20 +260,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   if (s0 < s1) own = row.q ? verify_sum<T, V, true>(row, s0, s1, lane) : verify_sum<T, V, false>(row, s0, s1, lane);
   if (lane == 0) sh.warp_sum[warp] = own;
   __syncthreads();
-  // The sum of the lanes up to this one, of values of the first 8.
-  const auto scan8 = [&](double v) {
-#pragma unroll
-    for (int k = 1; k < 8; k <<= 1) {
-      const double below = __shfl_up_sync(0xffffffffu, v, k);
-      if (lane >= k) v += below;
-    }
-    return v;
-  };
-  static_assert(kVerifyWarps == 8 && kVerifyMaxCluster <= 8, "sums over 8 lanes");
   double slice = 0, slices = 0;
   if (warp == 0) {
     slice = lane < kVerifyWarps ? sh.warp_sum[lane] : 0.0;
-    slices = scan8(slice);
+    slices = verify_scan8(slice, lane);
     if (lane == kVerifyWarps - 1) sh.cta_sum = slices;
   }
   if (C > 1) cluster_sync();
@@ -280,15 +272,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
   if (warp == 0) {  // where the draw falls: each CTA finds the same
     double mine = 0;
     if (lane < (int)C) mine = C > 1 ? from_u64<double>(ld_cluster_u64(cluster_addr(&sh.cta_sum, lane))) : sh.cta_sum;
-    const double upto = scan8(mine), limit = (double)sample * __shfl_sync(0xffffffffu, upto, C - 1);
-    // Of those with something left, the first past the limit, or the last.
-    const auto choose = [&](bool some, bool past) {
-      const unsigned all = __ballot_sync(0xffffffffu, some), over = __ballot_sync(0xffffffffu, some && past);
-      return over ? __ffs(over) - 1 : all ? 31 - __clz(all) : -1;
-    };
-    const int owner = choose(mine > 0, upto > limit);
+    const double upto = verify_scan8(mine, lane), limit = (double)sample * __shfl_sync(0xffffffffu, upto, C - 1);
+    const int owner = verify_choose(mine > 0, upto > limit);
     const double before = __shfl_sync(0xffffffffu, upto - mine, owner < 0 ? 0 : owner);
-    const int k = choose(slice > 0, before + slices > limit);
+    const int k = verify_choose(slice > 0, before + slices > limit);
     const double skipped = __shfl_sync(0xffffffffu, slices - slice, k < 0 ? 0 : k);
     if (lane == 0) {
       const bool here = owner >= 0 && rank == (unsigned)owner && k >= 0;
@@ -296,14 +283,31 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const __grid_
       sh.to = min(a.V, sh.from + a.slice);
       sh.before = before + skipped;
       sh.limit = limit;
-      sh.last = 0;
       if (owner < 0 && rank == 0) a.out[b * (a.K + 1) + n] = -1;
     }
   }
   __syncthreads();
+  // The warps share that slice once more, and one of them picks the value.
   if (sh.from >= 0) {
-    const long long j = row.q ? verify_pick<T, V, true>(row, sh) : verify_pick<T, V, false>(row, sh);
-    if (threadIdx.x == 0) a.out[b * (a.K + 1) + n] = (int32_t)j;
+    const long long sub = ((sh.to - sh.from + kVerifyWarps - 1) / kVerifyWarps + V - 1) / V * V;
+    const long long f = sh.from + warp * sub, g = min(sh.to, f + sub);
+    double part = 0;
+    if (f < g) part = row.q ? verify_sum<T, V, true>(row, f, g, lane) : verify_sum<T, V, false>(row, f, g, lane);
+    __syncthreads();  // the sums of the slices have been read
+    if (lane == 0) sh.warp_sum[warp] = part;
+    __syncthreads();
+    if (warp == 0) {
+      const double mine = lane < kVerifyWarps ? sh.warp_sum[lane] : 0.0, upto = verify_scan8(mine, lane);
+      const int k = verify_choose(mine > 0, sh.before + upto > sh.limit);
+      const double before = sh.before + __shfl_sync(0xffffffffu, upto - mine, k < 0 ? 0 : k);
+      long long j = -1;
+      if (k >= 0) {
+        const long long from = sh.from + k * sub, to = min(sh.to, from + sub);
+        j = row.q ? verify_pick<T, V, true>(row, from, to, before, sh.limit, lane)
+                  : verify_pick<T, V, false>(row, from, to, before, sh.limit, lane);
+      }
+      if (lane == 0) a.out[b * (a.K + 1) + n] = (int32_t)j;
+    }
   }
   if (rank == 0) {
     if (threadIdx.x == 0) a.accepted[b] = n;

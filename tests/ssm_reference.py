@@ -4,9 +4,9 @@ with the sizes that bound a 32-bit evaluation's error.
 u = 2^-24 is fp32's unit roundoff.  What the kernels' functions are off by, relative:
   sigmoid(p)      (12 + 2 |p|) u: an exponential of a rounded product (2.5 + 1.3 |p|), 1 + e, the
                   reciprocal, and the rounding of its use
-  D = softplus(v) (34 + 2 |v|) u: an exponential of a rounded product, the polynomial for 16-bit
-                  types (24), and three roundings; v = dt + bias itself is rounded, which moves D
-                  by |v| u at most (softplus' <= 1 and D >= |v| for v >= 0, D' / D <= 1 for v < 0)
+  D = softplus(v) (12 + |v|) u: the exponential (4), the polynomial (3) and three roundings; v = dt +
+                  bias itself is rounded, which moves D by |v| u at most (softplus' <= 1 and D >=
+                  |v| for v >= 0, D' / D <= 1 for v < 0)
   exp(D A)        (4 + 2 |D A|) u + |D A| times D's
 First-order bounds of everything else follow from these; they are doubled at the end for the
 second order and for the parts in which long rows are worked on (a part's decay is the exponential
@@ -108,7 +108,7 @@ def _step_sizes(dt, dt_bias, softplus):
     v = dt if dt_bias is None else dt + dt_bias
     if not softplus:
         return v, v, U * torch.ones_like(v)
-    return v, torch.nn.functional.softplus(v, threshold=200.0), (34 + 3 * v.abs()) * U
+    return v, torch.nn.functional.softplus(v, threshold=200.0), (12 + v.abs()) * U
 
 
 def scan(x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus=True, states=None):
