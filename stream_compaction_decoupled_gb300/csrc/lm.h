@@ -173,14 +173,14 @@ inline SscSplit ssc_parts(long long tiles, long long parts) {
   const long long each = (tiles + parts - 1) / parts;
   return {tiles ? (tiles + each - 1) / each : 1, each};
 }
-// The gradient: a block takes 64 channels.  Few blocks are split until the
-// device is full once; many four times over, since those that are left at the end then are short (8
-// x 2048 x 2048 bf16, 256 blocks: 885 us, in 3 parts 863, in 7 804; 1 x 8192 x 2048, 32 blocks: in
-// 14 parts 421 us, in 28 433).
-// per_sm: how many blocks fit an SM.  More of them give more parts: the scratch is sized for 3.
-inline SscSplit ssc_backward_split(long long B, long long T, long long D, long long G, int per_sm) {
+// The gradient: a block takes 64 channels, two blocks fit an SM.  Where the rows and channels give
+// enough blocks, a row is one chain (8 x 2048 x 2048 bf16, 256 blocks: 819 us, in 4 parts 898); some
+// are split four times over the device, since what is left at the end is then short (128 blocks: 608
+// us, in 2 parts 511, in 9 462), few until it is full (1 x 8192 x 2048, 32 blocks: in 9 parts 472 us, in
+// 14 501).
+inline SscSplit ssc_backward_split(long long B, long long T, long long D, long long G) {
   const long long units = B * G * ((D / G + kSscChannels - 1) / kSscChannels);
-  return ssc_parts((T + kSscTile - 1) / kSscTile, (units < 128 ? 1 : 4) * per_sm * 152 / units);
+  return ssc_parts((T + kSscTile - 1) / kSscTile, units >= 220 ? 1 : (units < 128 ? 1 : 4) * 304 / units);
 }
 
 // Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 /
@@ -208,7 +208,7 @@ inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, lo
   return {ssc_parts(tiles, parts), lanes};
 }
 inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, bool backward) {
-  const SscSplit s = backward ? ssc_backward_split(B, T, D, G, 3) : ssc_forward_plan(B, T, D, G).split;
+  const SscSplit s = backward ? ssc_backward_split(B, T, D, G) : ssc_forward_plan(B, T, D, G).split;
   size_t floats = (size_t)B * (s.parts - 1) * (D * N + D + 1);
   if (backward) {
     floats += (size_t)B * s.parts * D * (N + 2);

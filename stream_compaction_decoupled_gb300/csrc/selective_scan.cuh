@@ -101,7 +101,15 @@ template <class T, bool EDGE> struct SscPair {
 // exponential costs more than the instruction it saves (measured in a loop of nothing else, 32
 // states a thread, 3 warps a scheduler: 6.9 cycles a state and token with packed products and sums,
 // 5.2 with these and the sums single and only D x B packed, 5.9 with all of it single).
-__device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) { return make_float2(ex2(a.x * d.x), ex2(a.y * d.y)); }
+//
+// The instruction's result is low by 0.3 to 0.45 units of 2^-24 on average for arguments of -0.001 to
+// -0.3 (measured), which in a chain of decays adds up over as many tokens as the state lasts.  2^-25
+// added to the argument leaves 0.02 to 0.1 (0.26 high below -0.001); of 0 it is 1 all the same.
+// 8 x 2048 x 2048 bf16, error against 64 bits: last state 4.0e-7 without it, dA 1.2e-6.
+constexpr float kSscCentre = 0x1p-25f;
+__device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) {
+  return make_float2(ex2(fmaf(a.x, d.x, kSscCentre)), ex2(fmaf(a.y, d.y, kSscCentre)));
+}
 __device__ __forceinline__ float2 ssc_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
 // D and e go into fp32 results (states, dA, dd, dbias) whatever the inputs' type, so that their
 // functions are the fp32 ones; what only 16-bit outputs see (y, dz) is as exact as their type.
@@ -608,7 +616,7 @@ __device__ __forceinline__ int ssc_sum_half(int i, int pair, int half) {
 // dC: over the pair in the thread, over the warp by exchanges, over the block in shared memory,
 // and over the blocks by a second kernel.
 template <class T, bool EDGE, bool ONE, bool CARRY>
-__global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
+__global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
   using S = SscBack<T, EDGE>;
   using P = typename S::P;
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
   const int count = min(2, width - 2 * pr), ch = count > 0 ? base + 2 * pr : base;
   const long long row = b * a.D + ch;
 
-  float2 rate[2][2], g[2][2], da[2][2];  // (channel, pair of states)
+  float2 rate[2][2], g[2][2], da[2][2], da_few[2][2];  // (channel, pair of states)
   const auto rates = [&](int k) {
     ssc_load_any<M>(a.vec, a.a + (long long)ch * a.N, k * 16 + ln * M, a.N, count, rate);
 #pragma unroll
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) g[c][j] = da[c][j] = zero;
+      for (int j = 0; j < 2; ++j) g[c][j] = da[c][j] = da_few[c][j] = zero;
     if constexpr (!CARRY) {
       if (a.dlast) ssc_load_any<M>(a.vec, a.dlast + row * a.N, k * 16 + ln * M, a.N, count, g);
       // Through the parts behind this one in turn.
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
       put(2 * k + 1, da);
     }
   }
-  float2 bias = zero, skip = zero, dskip = zero, dbias = zero, sum_d = zero;
+  float2 bias = zero, skip = zero, dskip = zero, dbias = zero, dskip_few = zero, dbias_few = zero, sum_d = zero;
   if (a.bias) bias = make_float2(count > 0 ? a.bias[ch] : 0.f, count > 1 ? a.bias[ch + 1] : 0.f);
   if (!CARRY && a.d) skip = make_float2(count > 0 ? a.d[ch] : 0.f, count > 1 ? a.d[ch + 1] : 0.f);
   const bool gated = a.z != nullptr;
@@ -867,8 +875,8 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
       P::store(a.dx + b * a.dxb + u * a.dxt + ch, n, fma2(skip, e, mul2(make_float2(q.x, q.y), along)));
       P::store(a.ddt + b * a.ddtb + u * a.ddtt + ch, n, dd);
       if (!whole && n <= 0) dd = zero;  // (e is 0 there)
-      dskip = fma2(e, x, dskip);
-      dbias = add2(dbias, dd);
+      dskip_few = fma2(e, x, dskip_few);
+      dbias_few = add2(dbias_few, dd);
       if (gated) {
         const float2 z = pair(3, t), s = sigmoid<T>(z);
         const float2 slope = fma2(mul2(z, s), fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
@@ -993,7 +1001,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
                     gg = mul2(decay[i][c][j], gg);
                     const float2 q = mul2(gg, before[i][c][j]);
                     through[c] = ssc_fma(q, rate[c][j], through[c]);
-                    da[c][j] = ssc_fma(q, d2, da[c][j]);
+                    da_few[c][j] = ssc_fma(q, d2, da_few[c][j]);
                   }
                 }
               }
@@ -1032,6 +1040,14 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
         };
         if (starts) tokens(std::false_type());
         else tokens(std::true_type());
+        // Sums over the part's tokens go over four tiles, then over as many as there are: a chain of all
+        // of them would be off by more.
+        if (!ONE || (tile & 3) == 0 || tile == tile0) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) da[c][j] = add2(da[c][j], da_few[c][j]), da_few[c][j] = zero;
+        }
         __syncthreads();
         // The block's sums for B and C: 16 tokens of 32 values, over the four warps.
         const int which = (lane >> 2 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 4 & 1);
@@ -1057,6 +1073,10 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !EDGE ? 3 : 2) ssc_backwar
     if constexpr (!ONE && !CARRY) {
 #pragma unroll
       for (int r = R - 1; r >= 0; --r) finish(r, acc[0][r], acc[1][r], acc[2][r]);
+    }
+    if (!CARRY && ((tile & 3) == 0 || tile == tile0)) {
+      dskip = add2(dskip, dskip_few), dbias = add2(dbias, dbias_few);
+      dskip_few = dbias_few = zero;
     }
     if constexpr (CARRY) __syncthreads();  // before B and C are widened again
     land(stage);
@@ -1246,7 +1266,7 @@ __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ S
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           if (VEC || n0 + s < a.N) {
-            h[r][s] = fmaf(ex2(step[r] * (w[s] * kLog2e)), h[r][s], step[r] * x[r] * widen(vb[r][s]));
+            h[r][s] = fmaf(ex2(fmaf(step[r], w[s] * kLog2e, kSscCentre)), h[r][s], step[r] * x[r] * widen(vb[r][s]));
             y[r] = fmaf(h[r][s], widen(vc[r][s]), y[r]);
           }
         }
@@ -1342,8 +1362,7 @@ template <class T, bool EDGE, bool ONE, int LN> cudaError_t ssc_forward(const Se
 }
 
 template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  // What the kernel's registers and (fp32, more states) shared memory allow.
-  const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.G, EDGE || !ONE || sizeof(T) == 4 ? 2 : 3);
+  const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.G);
   const SscArgs<T> a = ssc_args<T>(j, split);
   const long long units = j.B * a.G * a.blocks;
   profile_before(ctx);
