@@ -162,9 +162,10 @@ struct SscSplit {
 // At most so many parts: a part goes through all before it first, so that many make it longer than
 // they make the tokens of one shorter (forward, 1 x 32768 x 128 bf16: 64 parts 113 us, 128 102, 256
 // 129; the bound is 128).
+// Rows below 8 tiles are not worth a second launch.
 inline long long ssc_most_parts(long long tiles) {
   const long long root = (long long)sqrt(8.0 * (double)tiles);
-  return root < tiles / 2 ? root : tiles / 2;
+  return tiles < 8 ? 1 : root < tiles / 2 ? root : tiles / 2;
 }
 inline SscSplit ssc_parts(long long tiles, long long parts) {
   const long long most = ssc_most_parts(tiles);
@@ -187,7 +188,9 @@ inline SscSplit ssc_backward_split(long long B, long long T, long long D, long l
 // lanes channels each; 4 blocks fit an SM.  Where the rows and channels give enough blocks, a row
 // is one chain (more parts cost a second pass over all parts but the last: 16 x 1024 x 2048 bf16,
 // gated, 256 blocks: 211 us, in 4 parts 252).  Else it is split until the device is full (8 x 2048
-// x 2048, 128 blocks: 313 us, in 4 parts 276; 4 x 2048 x 2048 315, in 9 parts 152), with 4 lanes
+// x 2048, 128 blocks: 313 us, in 4 parts 276), or twice over by an even number of parts (in 8 256, in 9
+// 270; 4 x 2048 x 2048 315, in 9 parts 152, in 16 150; 1 x 32768 x 2048, 16 blocks, once: in 32 596, in
+// 38 510), with 4 lanes
 // where 2 cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).
 struct SscForwardPlan {
   SscSplit split;
@@ -204,6 +207,11 @@ inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, lo
   if (blocks(2) < 220) {
     if (blocks(2) * ssc_most_parts(tiles) < 456) lanes = 4;
     parts = 608 / blocks(lanes);
+    if (blocks(2) >= 64) {
+      const long long twice = 1216 / blocks(2);
+      for (parts = twice; tiles % parts != 0 && 4 * parts > 3 * twice;) --parts;
+      if (tiles % parts != 0) parts = twice;
+    }
   }
   return {ssc_parts(tiles, parts), lanes};
 }

@@ -448,14 +448,10 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
     if (a.softplus) sizes(std::true_type());
     else sizes(std::false_type());
     const bool whole = t + L <= a.T_;
-    if (!whole) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (t + ln + r * LN >= a.T_) d[r] = zero;
-    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float2 u = mul2(d[r], pair(0, r));
+      float2 u = mul2(d[r], pair(0, r));
+      if (!whole && t + ln + r * LN >= a.T_) d[r] = u = zero;  // no token: the state stays
       ds[(ln + r * LN) * (32 / LN) + lane / LN] = make_float4(d[r].x, d[r].y, u.x, u.y);
       if constexpr (ENDS) sum = add2(sum, d[r]);
       if constexpr (!ONE) y[r] = zero;
@@ -845,8 +841,8 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
         const float2 z = pair(3, t);
         e = mul2(e, mul2(z, sigmoid<float>(z)));
       }
-      if (!whole && t0 + t >= a.T_) d = e = zero;
-      const float2 u = CARRY ? zero : mul2(d, pair(0, t));
+      float2 u = CARRY ? zero : mul2(d, pair(0, t));
+      if (!whole && t0 + t >= a.T_) d = e = u = zero;
       du[t * 8 + pr] = make_float4(d.x, d.y, u.x, u.y);
       es[t * 8 + pr] = e;
       if constexpr (CARRY) sum_d = add2(sum_d, d);
@@ -1341,8 +1337,10 @@ template <class T> SscArgs<T> ssc_args(const SelectiveScanJob& j, const SscSplit
 }
 
 template <class K, class A> cudaError_t ssc_launch(K kernel, long long grid, size_t smem, const A& a, const LaunchCtx& ctx) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(kernel, (unsigned)grid, kSscThreads, smem, ctx.stream, a);
 }
 

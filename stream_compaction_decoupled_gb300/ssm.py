@@ -10,6 +10,7 @@ or the current stream.  ``autograd`` wraps the convolution and the scan for trai
 """
 from __future__ import annotations
 
+import functools
 import struct
 from collections import namedtuple
 
@@ -22,7 +23,7 @@ SelectiveScanGrads = namedtuple("SelectiveScanGrads", "dx ddt da db dc dd dz ddt
 Verified = namedtuple("Verified", "accepted tokens")
 
 _KEPT = 16  # tokens from one kept state to the next
-_pack = {n: struct.Struct("%dq" % n).pack for n in (4, 6, 8, 14, 26)}
+_pack = {n: struct.Struct("%dq" % n).pack for n in (2, 4, 6, 8, 14, 26)}
 
 
 # ------------------------------------------------------------ causal convolution ------
@@ -64,8 +65,8 @@ def causal_conv(x, weight, bias=None, state=None, starts=None, silu: bool = True
 def _causal_conv(s, code, pcode, taps, x, weight, bias, state, starts, silu, out):
     b, t, d = x.shape
     if out is None:
-        out = torch.empty((b, t, d), dtype=x.dtype, device=x.device)
-    last = torch.empty((b, taps - 1, d), dtype=x.dtype, device=x.device)
+        out = x.new_empty((b, t, d))
+    last = x.new_empty((b, taps - 1, d))
     sx, sy = x.stride(), out.stride()
     rc = load().gb_causal_conv(code, pcode, b, t, d, taps, x.data_ptr(), _pack[4](sx[0], sx[1], sy[0], sy[1]),
                                weight.data_ptr(), _p(bias), 1 if silu else 0, _p(state), _p(starts), out.data_ptr(),
@@ -99,7 +100,7 @@ def causal_conv_backward(dy, x, weight, bias=None, state=None, starts=None, dlas
 def _causal_conv_backward(s, code, pcode, taps, dy, x, weight, bias, state, starts, dlast, silu, dparams, out, temp):
     (b, t, d), dev, lib = x.shape, x.device, load()
     if out is None:
-        out = torch.empty((b, t, d), dtype=x.dtype, device=dev)
+        out = x.new_empty((b, t, d))
     dw = db = dstate = None
     tb = 0
     if dparams:
@@ -138,8 +139,8 @@ def causal_conv_step(x, state, weight, bias=None, slots=None, silu: bool = True,
 def _causal_conv_step(s, code, pcode, taps, x, state, weight, bias, slots, silu, out):
     b, d = x.shape
     if out is None:
-        out = torch.empty((b, d), dtype=x.dtype, device=x.device)
-    rc = load().gb_causal_conv_step(code, pcode, b, d, taps, x.data_ptr(), struct.pack("2q", x.stride(0), out.stride(0)),
+        out = x.new_empty((b, d))
+    rc = load().gb_causal_conv_step(code, pcode, b, d, taps, x.data_ptr(), _pack[2](x.stride()[0], out.stride()[0]),
                                     weight.data_ptr(), _p(bias), 1 if silu else 0, state.data_ptr(), state.shape[0],
                                     _p(slots), out.data_ptr(), s)
     if rc:
@@ -168,22 +169,21 @@ def _temp(temp, need, dev):
 
 # ------------------------------------------------------------ selective scan ------
 
-def _vectors(m, what, lead, dtype, index):
-    """b or c as (..., groups, states): a tensor without the groups' dimension has one group."""
-    if m.dim() == len(lead) + 1:
-        m = m.unsqueeze(-2)
+def _check_vectors(m, what, lead, dtype, index):
+    """Raises what is wrong with b or c, if anything is (a single state has any stride)."""
     if m.dim() != len(lead) + 2:
         raise ValueError("%s must be (%s, groups, states), or without groups" % (what, "batch, length" if len(lead) == 2
                                                                                else "batch"))
     _rows_like(m, what, lead + m.shape[-2:], dtype, index)
-    return m
 
 
 def _ssm(x, dt, a, b, c, d, z, dt_bias):
-    """Checks what the forms of the scan share; b and c with their groups."""
-    shape, lead, width, dtype, index = x.shape, x.shape[:-1], x.shape[-1], x.dtype, x.get_device()
-    _rows_like(dt, "dt", shape, dtype, index)
-    if z is not None:
+    """Checks what the forms of the scan share; b and c with their groups' dimension."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    width = shape[-1]
+    if dt.dtype is not dtype or dt.shape != shape or dt.get_device() != index or dt.stride()[-1] != 1:
+        _rows_like(dt, "dt", shape, dtype, index)
+    if z is not None and (z.dtype is not dtype or z.shape != shape or z.get_device() != index or z.stride()[-1] != 1):
         _rows_like(z, "z", shape, dtype, index)
     if a.dim() != 2:
         raise ValueError("a must be (channels, states)")
@@ -191,16 +191,29 @@ def _ssm(x, dt, a, b, c, d, z, dt_bias):
     if not 1 <= states <= 128:
         raise ValueError("a must have between 1 and 128 states, not %d" % states)
     _dense(a, "a", (width, states), torch.float32, index)
-    b, c = _vectors(b, "b", lead, dtype, index), _vectors(c, "c", lead, dtype, index)
-    if b.shape[-1] != states or c.shape != b.shape:
+    if b.dim() == len(shape):
+        b = b.unsqueeze(-2)
+    if c.dim() == len(shape):
+        c = c.unsqueeze(-2)
+    vectors = b.shape
+    if b.dtype is not dtype or vectors[:-2] != shape[:-1] or b.get_device() != index or b.stride()[-1] != 1:
+        _check_vectors(b, "b", shape[:-1], dtype, index)
+    if c.dtype is not dtype or c.shape != vectors or c.get_device() != index or c.stride()[-1] != 1:
+        _check_vectors(c, "c", shape[:-1], dtype, index)
+    if vectors[-1] != states or c.shape != vectors:
         raise ValueError("b and c must have %d states and the same groups" % states)
-    if b.shape[-2] < 1 or width % b.shape[-2]:
-        raise ValueError("%d channels do not divide into %d groups" % (width, b.shape[-2]))
+    if vectors[-2] < 1 or width % vectors[-2]:
+        raise ValueError("%d channels do not divide into %d groups" % (width, vectors[-2]))
     if d is not None:
         _dense(d, "d", (width,), torch.float32, index)
     if dt_bias is not None:
         _dense(dt_bias, "dt_bias", (width,), torch.float32, index)
     return b, c
+
+
+@functools.lru_cache(maxsize=512)
+def _scan_scratch(rows, t, width, states, groups, backward):
+    return load().gb_selective_scan_temp_bytes(rows, t, width, states, groups, backward)
 
 
 def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts=None, softplus: bool = True,
@@ -230,17 +243,17 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts
 
 def _selective_scan(s, code, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, keep, out, temp):
     (rows, t, width), dev, lib = x.shape, x.device, load()
-    groups, states = b.shape[2], a.shape[1]
+    _, _, groups, states = b.shape
     if out is None:
-        out = torch.empty((rows, t, width), dtype=x.dtype, device=dev)
-    last = torch.empty((rows, width, states), dtype=torch.float32, device=dev)
-    kept = torch.empty((rows, -(-t // _KEPT), width, states), dtype=torch.float32, device=dev) if keep else None
-    temp, tb = _temp(temp, lib.gb_selective_scan_temp_bytes(rows, t, width, states, groups, 0), dev)
-    sz = (0, 0) if z is None else z.stride()
+        out = x.new_empty((rows, t, width))
+    last = a.new_empty((rows, width, states))
+    kept = a.new_empty((rows, -(-t // _KEPT), width, states)) if keep else None
+    temp, tb = _temp(temp, _scan_scratch(rows, t, width, states, groups, 0), dev)
+    sx, sd, sz, sy, sb, sc = x.stride(), dt.stride(), (0, 0) if z is None else z.stride(), out.stride(), b.stride(), c.stride()
     rc = lib.gb_selective_scan(
         code, rows, t, width, states, groups, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(),
         _p(d), _p(z), _p(dt_bias), 1 if softplus else 0,
-        _pack[14](*x.stride()[:2], *dt.stride()[:2], *sz[:2], *out.stride()[:2], *b.stride()[:3], *c.stride()[:3]),
+        _pack[14](sx[0], sx[1], sd[0], sd[1], sz[0], sz[1], sy[0], sy[1], sb[0], sb[1], sb[2], sc[0], sc[1], sc[2]),
         _p(h0), _p(starts), out.data_ptr(), last.data_ptr(), _p(kept), _p(temp), tb, s)
     if rc:
         _check(rc, "gb_selective_scan")
@@ -279,17 +292,17 @@ def _selective_scan_backward(s, code, flat, dy, x, dt, a, b, c, kept, d, z, dt_b
     (rows, t, width), dtype, dev, lib = x.shape, x.dtype, x.device, load()
     groups, states = b.shape[2], a.shape[1]
     if dx is None:
-        dx = torch.empty((rows, t, width), dtype=dtype, device=dev)
-        ddt = torch.empty((rows, t, width), dtype=dtype, device=dev)
+        dx = x.new_empty((rows, t, width))
+        ddt = x.new_empty((rows, t, width))
         if z is not None:
-            dz = torch.empty((rows, t, width), dtype=dtype, device=dev)
-    db = torch.empty((rows, t, groups, states), dtype=dtype, device=dev)
-    dc = torch.empty((rows, t, groups, states), dtype=dtype, device=dev)
-    da = torch.empty((width, states), dtype=torch.float32, device=dev)
-    dd = None if d is None else torch.empty((width,), dtype=torch.float32, device=dev)
-    dbias = None if dt_bias is None else torch.empty((width,), dtype=torch.float32, device=dev)
-    dh0 = torch.empty((rows, width, states), dtype=torch.float32, device=dev)
-    temp, tb = _temp(temp, lib.gb_selective_scan_temp_bytes(rows, t, width, states, groups, 1), dev)
+            dz = x.new_empty((rows, t, width))
+    db = x.new_empty((rows, t, groups, states))
+    dc = x.new_empty((rows, t, groups, states))
+    da = a.new_empty((width, states))
+    dd = None if d is None else a.new_empty((width,))
+    dbias = None if dt_bias is None else a.new_empty((width,))
+    dh0 = a.new_empty((rows, width, states))
+    temp, tb = _temp(temp, _scan_scratch(rows, t, width, states, groups, 1), dev)
     sz, sdz = ((0, 0), (0, 0)) if z is None else (z.stride()[:2], dz.stride()[:2])
     rc = lib.gb_selective_scan_backward(
         code, rows, t, width, states, groups, dy.data_ptr(), x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(),
@@ -325,12 +338,12 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slo
 def _selective_scan_step(s, code, x, dt, a, b, c, state, d, z, dt_bias, slots, softplus, out):
     rows, width = x.shape
     if out is None:
-        out = torch.empty((rows, width), dtype=x.dtype, device=x.device)
+        out = x.new_empty((rows, width))
     sb, sc = b.stride(), c.stride()
     rc = load().gb_selective_scan_step(
         code, rows, width, a.shape[1], b.shape[1], x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(),
         _p(d), _p(z), _p(dt_bias), 1 if softplus else 0,
-        _pack[8](x.stride(0), dt.stride(0), 0 if z is None else z.stride(0), out.stride(0), sb[0], sb[1], sc[0], sc[1]),
+        _pack[8](x.stride()[0], dt.stride()[0], 0 if z is None else z.stride()[0], out.stride()[0], sb[0], sb[1], sc[0], sc[1]),
         state.data_ptr(), state.shape[0], _p(slots), out.data_ptr(), s)
     if rc:
         _check(rc, "gb_selective_scan_step")
@@ -368,8 +381,8 @@ def verify_drafts(drafts, target, draft, accept, sample, lengths=None, stream=No
 
 def _verify_drafts(s, code, drafts, target, draft, accept, sample, lengths):
     n, k, v = target.shape
-    accepted = torch.empty((n,), dtype=torch.int32, device=target.device)
-    tokens = torch.empty((n, k), dtype=torch.int32, device=target.device)
+    accepted = sample.new_empty((n,), dtype=torch.int32)
+    tokens = sample.new_empty((n, k), dtype=torch.int32)
     st, sd = target.stride(), (0, 0) if draft is None else draft.stride()
     rc = load().gb_verify_drafts(code, n, k - 1, v, drafts.data_ptr(), I64 if drafts.dtype is torch.int64 else I32,
                                  target.data_ptr(), _p(draft), _pack[4](st[0], st[1], sd[0], sd[1]), accept.data_ptr(),

@@ -142,6 +142,17 @@ def test_a_start_drops_infinities_and_nans(t):
     assert torch.isfinite(g.dx[:, fine]).all() and torch.isfinite(g.db[:, fine]).all() and not g.dh0.any()
 
 
+@pytest.mark.parametrize("t", [1, 7, 21])
+def test_an_infinity_in_the_last_token_stays_one(t):
+    """Rows end inside a tile: what is behind the last token takes no part."""
+    q, more, dy, _ = inputs(1, t, 24, 16, 1, torch.float32, True, 13, p_start=0.0)
+    more["starts"] = None
+    q["x"][0, t - 1] = float("inf")
+    q["b"][0, t - 1] = 1.0
+    _, last, _ = gb.selective_scan(**q, **more)
+    assert torch.isinf(last).all()
+
+
 def test_in_pieces_and_token_by_token():
     """A row in pieces and one token a call: the same as at once, up to the roundings that the
     bounds of both allow."""
