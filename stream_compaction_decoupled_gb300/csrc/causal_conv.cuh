@@ -677,7 +677,8 @@ template <class T, int W, int V, bool EDGE> cudaError_t conv_forward(const Causa
 template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
   ConvArgs<T> a = conv_args<T>(j);
   a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
-  const ConvSplit s = conv_backward_split(j.B, j.T, j.D);
+  // What fits by registers; with more than 4 taps a warp has 64 channels.
+  const ConvSplit s = conv_backward_split(j.B, j.T, j.D, W == 4 ? EDGE ? 8 : 12 : 4);
   a.length = (int)s.length, a.runs = (int)s.runs, a.slots = s.slots;
   a.units = s.slots * a.runs * a.groups;
   a.part = j.dw || j.db ? (float*)j.temp : nullptr;

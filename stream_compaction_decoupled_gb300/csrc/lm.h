@@ -100,8 +100,9 @@ constexpr int kConvMaxTaps = 8;
 struct ConvSplit {
   long long slots, runs, length;
 };
-inline ConvSplit conv_backward_split(long long B, long long T, long long D) {
-  long long want = (152 * 12) / ((D + 127) / 128);  // warps of 128 channels, 12 an SM: all run at once
+// warps: how many run on an SM at once.  More of them give more runs: the scratch is sized for 12.
+inline ConvSplit conv_backward_split(long long B, long long T, long long D, int warps) {
+  long long want = 152 * warps / ((D + 127) / 128);  // of 128 channels
   if (want < 1) want = 1;
   const long long per_row = want / B > 1 ? want / B : 1;
   long long length = (T + per_row - 1) / per_row;
@@ -110,7 +111,7 @@ inline ConvSplit conv_backward_split(long long B, long long T, long long D) {
   return {B < 4 * want ? B : 4 * want, runs < 1 ? 1 : runs, length};
 }
 inline size_t conv_temp_bytes(long long B, long long T, long long D, int taps) {
-  const ConvSplit s = conv_backward_split(B, T, D);
+  const ConvSplit s = conv_backward_split(B, T, D, 12);
   return round_up((size_t)(s.slots * s.runs) * (taps + 1) * (size_t)D * sizeof(float), 256);
 }
 
