@@ -568,7 +568,8 @@ template <class T> struct ConvStepArgs {
   T *state, *y;
   const void *w, *bias;
   const int32_t* slots;
-  long long sx, sy, pool, n;  // n: threads
+  long long sx, sy, pool;
+  unsigned row_blocks;  // blocks of a row
   int D, taps, silu, wide, packs;
   ErrSink err;
 };
@@ -576,10 +577,10 @@ template <class T> struct ConvStepArgs {
 template <class T, int V>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepArgs<T> a) {
   pdl_entry();
-  const long long at = (long long)blockIdx.x * 128 + threadIdx.x;
-  if (at >= a.n) return;
-  const long long b = at / a.packs;
-  const int ch = (int)(at % a.packs) * V;
+  const long long b = blockIdx.x / a.row_blocks;
+  const int pack = (int)(blockIdx.x % a.row_blocks) * 128 + threadIdx.x;
+  if (pack >= a.packs) return;
+  const int ch = pack * V;
   long long slot = a.slots ? (long long)a.slots[b] : b;
   if (slot >= a.pool) {  // no such state: reported, and the row treated as padding
     if (ch == 0) raise_err(a.err, ERRBIT_RANGE);
@@ -721,10 +722,10 @@ template <class T, int V> cudaError_t conv_step(const CausalConvStepJob& j, cons
   a.state = (T*)j.state, a.pool = j.pool, a.slots = j.slots;
   a.D = (int)j.D, a.taps = j.taps, a.silu = j.silu;
   a.packs = (int)(j.D / V);
-  a.n = j.B * a.packs;
+  a.row_blocks = (unsigned)((a.packs + 127) / 128);
   a.err = ctx.err;
   profile_before(ctx);
-  const cudaError_t e = launch_pdl(conv_step_kernel<T, V>, (unsigned)((a.n + 127) / 128), 128, 0, ctx.stream, a);
+  const cudaError_t e = launch_pdl(conv_step_kernel<T, V>, (unsigned)(j.B * a.row_blocks), 128, 0, ctx.stream, a);
   profile_after(ctx);
   return e;
 }

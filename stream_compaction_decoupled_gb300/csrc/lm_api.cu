@@ -93,7 +93,7 @@ int check_ssc(int dtype, long long B, long long T, long long D, long long N, lon
   // single-token kernel's of 32 channels.
   const long double blocks = D == 0 ? 0 : (long double)B * G * ((D / G + 63) / 64);
   if (blocks + 65536 > (long double)kMaxGrid || 2 * ((long double)B * T * G * N / 256 + 1) + D * 5.0L > (long double)kMaxGrid ||
-      (long double)B * D / 32 + 1 > (long double)kMaxGrid)
+      (long double)B * ((D + 31) / 32) > (long double)kMaxGrid)
     return GB_ERR_RANGE;
   return GB_OK;
 }
@@ -369,7 +369,8 @@ int gb_causal_conv_step(int dtype, int param_dtype, int64_t batch, int64_t chann
   int rc = check_conv(dtype, param_dtype, batch, 1, channels, taps, silu);
   if (rc) return rc;
   if (pool < 0) return GB_ERR_INVALID;
-  if ((long double)pool * taps * channels > 9.0e17L || (long double)batch * channels > 128.0L * kMaxGrid)
+  // A block takes 128 channels of a row.
+  if ((long double)pool * taps * channels > 9.0e17L || (long double)batch * ((channels + 127) / 128) > (long double)kMaxGrid)
     return GB_ERR_RANGE;
   if (batch == 0 || channels == 0) return GB_OK;
   if (!x || !w || !y || (pool > 0 && taps > 1 && !state)) return GB_ERR_INVALID;

@@ -1177,7 +1177,8 @@ __global__ void __launch_bounds__(256) ssc_fold_kernel(const __grid_constant__ S
 template <class T> struct SscStepArgs {
   const T *x, *dt, *z, *b, *c;
   T* y;
-  long long sx, sdt, sz, sy, sb, sbg, sc, scg, pool, B, n;  // n: channels of all groups of rows
+  long long sx, sdt, sz, sy, sb, sbg, sc, scg, pool, B;
+  unsigned row_blocks;  // blocks of a group of rows
   const float *a, *d, *bias;
   float* state;
   const int32_t* slots;
@@ -1186,44 +1187,50 @@ template <class T> struct SscStepArgs {
 };
 
 // Four lanes a channel, four neighbouring states of each 16 a lane (VEC: as one access of 16
-// bytes, and B and C as one of four values); ROWS rows, which share the channel's A.
+// bytes, and B and C as one of four values).  ROWS = 4: four rows, which share the channel's A and
+// keep more loads in flight; what is done once a row and channel is done by one lane for each row.
+// 64 rows x 4096 channels x 16 states bf16: bound by issue and by the latency of its one pass.
 template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ SscStepArgs<T> a) {
+  static_assert(ROWS == 1 || ROWS == 4, "a row a lane, or one row");
   pdl_entry();
-  const long long at = ((long long)blockIdx.x * 128 + threadIdx.x) >> 2;
-  const int ln = threadIdx.x & 3;
-  const bool live = at < a.n;
-  const int ch = live ? (int)(at % a.D) : 0, group = ch / a.DG;
-  const long long b0 = live ? at / a.D * ROWS : 0;
+  const int lane = threadIdx.x & 31, ln = lane & 3;
+  // A block takes 32 channels of a group of rows.
+  const long long b0 = (long long)(blockIdx.x / a.row_blocks) * ROWS;
+  const int place = (int)(blockIdx.x % a.row_blocks) * 32 + (threadIdx.x >> 2);
+  const bool live = place < a.D;
+  const int ch = live ? place : 0, group = a.DG == a.D ? 0 : ch / a.DG;
   const int rows = live ? (int)min((long long)ROWS, a.B - b0) : 0;
   long long slot[ROWS];
-  T rx[ROWS], rdt[ROWS], rz[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     slot[r] = -1;
-    if (r < rows) {
-      const long long b = b0 + r;
-      slot[r] = a.slots ? (long long)a.slots[b] : b;
-      rx[r] = a.x[b * a.sx + ch];
-      rdt[r] = a.dt[b * a.sdt + ch];
-      if (a.z) rz[r] = a.z[b * a.sz + ch];
-    }
-  }
-  const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.d ? a.d[ch] : 0.f;
-  const float* pa = a.a + (long long)ch * a.N;
-  float y[ROWS], step[ROWS], x[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
+    if (r < rows) slot[r] = a.slots ? (long long)a.slots[b0 + r] : b0 + r;
     if (slot[r] >= a.pool) {  // no such state: reported, and the row treated as padding
       if (ch == 0 && ln == 0) raise_err(a.err, ERRBIT_RANGE);
       slot[r] = -1;
     }
-    x[r] = step[r] = y[r] = 0.f;
-    if (slot[r] >= 0) {
-      x[r] = widen(rx[r]);
-      const float v = widen(rdt[r]) + bias;
-      step[r] = a.softplus ? softplus2(make_float2(v, v)).x : v;
-    }
+  }
+  // The lane's own row (ROWS = 1: each lane the same).
+  const int own = ROWS == 1 ? 0 : ln;
+  const long long b = b0 + own;
+  float x = 0.f, step = 0.f, z = 0.f;
+  long long own_slot = slot[0];
+#pragma unroll
+  for (int r = 1; r < ROWS; ++r) own_slot = own == r ? slot[r] : own_slot;
+  if (own_slot >= 0) {
+    x = widen(a.x[b * a.sx + ch]);
+    const float v = widen(a.dt[b * a.sdt + ch]) + (a.bias ? a.bias[ch] : 0.f);
+    if (a.z) z = widen(a.z[b * a.sz + ch]);
+    step = a.softplus ? softplus2(make_float2(v, v)).x : v;
+  }
+  const float* pa = a.a + (long long)ch * a.N;
+  float y[ROWS], steps[ROWS], inputs[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    y[r] = 0.f;
+    steps[r] = ROWS == 1 ? step : __shfl_sync(0xffffffffu, step, (lane & ~3) | r);
+    inputs[r] = ROWS == 1 ? step * x : __shfl_sync(0xffffffffu, step * x, (lane & ~3) | r);
   }
   for (int n0 = ln * 4; n0 < a.N; n0 += 16) {
     float w[4], h[ROWS][4];
@@ -1256,13 +1263,15 @@ __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ S
       for (int s = 0; s < 4; ++s) w[s] = n0 + s < a.N ? pa[n0 + s] : 0.f;
     }
 #pragma unroll
+    for (int s = 0; s < 4; ++s) w[s] *= kLog2e;
+#pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (slot[r] >= 0) {
         float* ps = a.state + (slot[r] * a.D + ch) * a.N + n0;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           if (VEC || n0 + s < a.N) {
-            h[r][s] = fmaf(ex2(fmaf(step[r], w[s] * kLog2e, kSscCentre)), h[r][s], step[r] * x[r] * widen(vb[r][s]));
+            h[r][s] = fmaf(ex2(fmaf(steps[r], w[s], kSscCentre)), h[r][s], inputs[r] * widen(vb[r][s]));
             y[r] = fmaf(h[r][s], widen(vc[r][s]), y[r]);
           }
         }
@@ -1276,21 +1285,29 @@ __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ S
       }
     }
   }
+  // Over the four lanes: each ends with its own row's sum.
+  float sum;
+  if constexpr (ROWS == 1) {
+    sum = y[0] + __shfl_xor_sync(0xffffffffu, y[0], 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  } else {
+    float v[2];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    y[r] += __shfl_xor_sync(0xffffffffu, y[r], 1);
-    y[r] += __shfl_xor_sync(0xffffffffu, y[r], 2);
-    if (r < rows && ln == r % 4) {
-      float v = 0.f;
-      if (slot[r] >= 0) {
-        v = fmaf(skip, x[r], y[r]);
-        if (a.z) {
-          const float z = widen(rz[r]);
-          v *= z * sigmoid<T>(make_float2(z, z)).x;
-        }
-      }
-      a.y[(b0 + r) * a.sy + ch] = narrow<T>(v);
+    for (int q = 0; q < 2; ++q) {
+      const float send = ln & 1 ? y[2 * q] : y[2 * q + 1], keep = ln & 1 ? y[2 * q + 1] : y[2 * q];
+      v[q] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
     }
+    const float send = ln & 2 ? v[0] : v[1], keep = ln & 2 ? v[1] : v[0];
+    sum = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+  }
+  if (own < rows && (ROWS > 1 || ln == 0)) {
+    if (own_slot >= 0) {
+      if (a.d) sum = fmaf(a.d[ch], x, sum);
+      if (a.z) sum *= z * sigmoid<T>(make_float2(z, z)).x;
+    } else {
+      sum = 0.f;
+    }
+    a.y[b * a.sy + ch] = narrow<T>(sum);
   }
 }
 
@@ -1425,8 +1442,8 @@ template <class T> cudaError_t launch_selective_scan_step(const SelectiveScanSte
                    four(j.c, j.sc, j.scg);
   // Four rows a thread keep more loads in flight, where there are threads enough all the same.
   const bool many = j.B * j.D >= 256ll * ctx.num_sms;
-  a.n = (many ? (j.B + 3) / 4 : j.B) * j.D;
-  const unsigned grid = (unsigned)((a.n + 31) / 32);
+  a.row_blocks = (unsigned)((j.D + 31) / 32);
+  const unsigned grid = (unsigned)((many ? (j.B + 3) / 4 : j.B) * a.row_blocks);
   profile_before(ctx);
   cudaError_t e;
   if (many) e = vec ? launch_pdl(ssc_step_kernel<T, true, 4>, grid, 128, 0, ctx.stream, a)
