@@ -571,9 +571,24 @@ template <class T> struct ConvStepArgs {
   long long sx, sy, pool;
   unsigned row_blocks;  // blocks of a row
   int D, taps, silu, wide, packs;
+  bool four;  // 4 taps, which can be read at once
   ErrSink err;
 };
 
+// A channel's 4 taps.
+template <class T> __device__ __forceinline__ float4 conv_four(const void* p, int ch, int wide) {
+  if constexpr (sizeof(T) == 2) {
+    if (!wide) {
+      const uint2 u = ((const uint2*)p)[ch];
+      const float2 lo = widen2<T>(u.x), hi = widen2<T>(u.y);
+      return make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+  return ((const float4*)p)[ch];
+}
+
+// Bound by latency: the slot, then the state and the taps (64 x 4096, 4 taps bf16 9.4 us with cold
+// caches, 11.4 with the taps read one by one).
 template <class T, int V>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepArgs<T> a) {
   pdl_entry();
@@ -600,15 +615,27 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 #pragma unroll
       for (int c = 0; c < V; ++c) p[c] = conv_param(a.bias, ch + c, a.wide, (T*)nullptr);
     }
+    if (a.four) {
+      float v[4][V];
 #pragma unroll
-    for (int k = 0; k < kConvMaxTaps; ++k) {
-      if (k < a.taps) {
-        float v[V];
-        if (k == a.taps - 1) widen_pack(px, v);
-        else if (k < kConvMaxTaps - 1) widen_pack(old[k < kConvMaxTaps - 1 ? k : 0], v);
+      for (int k = 0; k < 3; ++k) widen_pack(old[k], v[k]);
+      widen_pack(px, v[3]);
 #pragma unroll
-        for (int c = 0; c < V; ++c)
-          p[c] = fmaf(conv_param(a.w, (long long)(ch + c) * a.taps + k, a.wide, (T*)nullptr), v[c], p[c]);
+      for (int c = 0; c < V; ++c) {
+        const float4 w = conv_four<T>(a.w, ch + c, a.wide);
+        p[c] = fmaf(w.w, v[3][c], fmaf(w.z, v[2][c], fmaf(w.y, v[1][c], fmaf(w.x, v[0][c], p[c]))));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kConvMaxTaps; ++k) {
+        if (k < a.taps) {
+          float v[V];
+          if (k == a.taps - 1) widen_pack(px, v);
+          else if (k < kConvMaxTaps - 1) widen_pack(old[k < kConvMaxTaps - 1 ? k : 0], v);
+#pragma unroll
+          for (int c = 0; c < V; ++c)
+            p[c] = fmaf(conv_param(a.w, (long long)(ch + c) * a.taps + k, a.wide, (T*)nullptr), v[c], p[c]);
+        }
       }
     }
 #pragma unroll
@@ -723,6 +750,7 @@ template <class T, int V> cudaError_t conv_step(const CausalConvStepJob& j, cons
   a.D = (int)j.D, a.taps = j.taps, a.silu = j.silu;
   a.packs = (int)(j.D / V);
   a.row_blocks = (unsigned)((a.packs + 127) / 128);
+  a.four = j.taps == 4 && (uintptr_t)j.w % (4 * (j.wide_params ? 4 : sizeof(T))) == 0;
   a.err = ctx.err;
   profile_before(ctx);
   const cudaError_t e = launch_pdl(conv_step_kernel<T, V>, (unsigned)(j.B * a.row_blocks), 128, 0, ctx.stream, a);
