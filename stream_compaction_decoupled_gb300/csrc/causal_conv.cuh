@@ -17,6 +17,10 @@
 // warp reads comes by asynchronous copies into a ring of its own in shared memory (registers alone
 // held too few bytes in flight: 8 x 2048 x 2048 bf16 49 us), or, where rows are not on 16-byte
 // boundaries, by loads a group of tokens ahead.
+//
+// Measured (GB300, cold caches): 8 x 2048 x 2048, 4 taps, bf16, with starts 33.9 us (0.58 of the copy rate),
+// its gradient 64.6 us (0.46): registers allow 16 and 12 warps an SM, and the chain from the
+// products through the gate leaves half the issue slots empty.
 #pragma once
 
 #include "lm.cuh"

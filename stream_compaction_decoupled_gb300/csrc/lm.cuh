@@ -1,7 +1,8 @@
-// lm.cuh -- device helpers of the language-model operators (recurrence, layer norm,
-// token log probabilities): 16-byte vectors of fp32 / bf16 / fp16 values widened to
-// fp32, the approximate exponential and reciprocal, asynchronous copies into shared
-// memory, thread-block clusters.
+// lm.cuh -- device helpers of the language-model operators (recurrence, layer norm, token
+// log probabilities, causal convolution, selective scan, verification of drafts): 16-byte
+// vectors of fp32 / bf16 / fp16 values widened to fp32, the approximate exponential and
+// reciprocal, sigmoid and softplus, asynchronous copies into shared memory, thread-block
+// clusters.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -189,10 +189,10 @@ inline SscSplit ssc_backward_split(long long B, long long T, long long D, long l
 // lanes channels each; 4 blocks fit an SM.  Where the rows and channels give enough blocks, a row
 // is one chain (more parts cost a second pass over all parts but the last: 16 x 1024 x 2048 bf16,
 // gated, 256 blocks: 211 us, in 4 parts 252).  Else it is split until the device is full (8 x 2048
-// x 2048, 128 blocks: 313 us, in 4 parts 276), or twice over by an even number of parts (in 8 256, in 9
-// 270; 4 x 2048 x 2048 315, in 9 parts 152, in 16 150; 1 x 32768 x 2048, 16 blocks, once: in 32 596, in
-// 38 510), with 4 lanes
-// where 2 cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).
+// x 2048, 128 blocks: 313 us, in 4 parts 276), or, from 64 blocks on, twice over, by parts of the
+// same length where there are some (in 8 256, in 9 270; 4 x 2048 x 2048 315, in 9 parts 152, in 16
+// 150); fewer blocks once (1 x 32768 x 2048, 16 blocks: in 32 596, in 38 510), with 4 lanes where 2
+// cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).
 struct SscForwardPlan {
   SscSplit split;
   int lanes;
