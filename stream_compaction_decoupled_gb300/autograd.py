@@ -10,8 +10,14 @@ gradient calls of lm.py and ssm.py joined, so that they can stand in a module's 
 All compute is in the library's kernels, forward and backward; gradients are
 deterministic, and cannot be differentiated again.  The gradients of a recurrence's inputs
 come from one pass together, as those of a selective scan, and layer norm's and the
-convolution's dx always; their weight's and bias's only where they are asked for.  The backward calls run on the stream that torch's autograd makes current,
-which is the forward call's.
+convolution's dx always; their weight's and bias's only where they are asked for.  The
+backward calls run on the stream that torch's autograd makes current, which is the forward
+call's.
+
+A forward and backward pass can be captured into a CUDA graph while no eager graph of the same
+leaves is alive (a loss that was kept is one): torch accumulates a leaf's gradient on the stream
+of the graph that used it first, and a capture that meets another stream is void, which
+loss.backward() does not survive.  Capture before the first eager pass, or delete its results.
 """
 from __future__ import annotations
 

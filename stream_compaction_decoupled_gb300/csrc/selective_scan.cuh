@@ -22,11 +22,12 @@
 // gate, conversions) goes around the lanes of a pair, a token each.  Inputs come through a ring of
 // asynchronous copies, their start flags 32 tiles at a time.
 //
-// The gradient: a block of 128 threads takes 64 channels and tiles of 16 tokens, in three phases:
-//   A  a lane takes two neighbouring channels, a warp 4 tokens: D, D x to shared memory;
-//   B  a warp takes 16 channels and all 16 tokens: a thread 2 channels and 4 states of each block
-//      of 16, 4 lanes a channel; its part of the sums over states to shared memory;
-//   C  as A: the four lanes' parts are summed, then what is done once a token and channel.
+// The gradient: a block of 4 warps takes 64 channels and tiles of 16 tokens, from the last to the
+// first; a warp 16 channels, 4 lanes a pair of channels and 4 states of both a lane.  A tile's states
+// are computed again from the one kept before it.  The warps meet twice a tile, for B and C and for
+// the sums over channels.  Issue and shared memory bound it about equally: of some 236 instructions
+// and 58 passes a token and warp, 8 passes bring D, D x, B and C forward and 6 C and e back, 12 and
+// 8 instructions are the lanes' parts of the sums over states, 7 and 28 the sums over channels.
 //
 // The tokens of a row are one chain.  Where the rows and channels are too few for the device,
 // they are split into parts: a first kernel finds what each part makes of a state of zero, and

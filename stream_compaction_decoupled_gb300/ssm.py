@@ -44,6 +44,12 @@ def _taps(weight, bias, dtype, d, index):
     return code, taps
 
 
+def _apart(out, x):
+    """Tokens need their neighbours' inputs, so nothing is computed in place."""
+    if out.data_ptr() == x.data_ptr() and x.numel():
+        raise ValueError("out must not be an input")
+
+
 def causal_conv(x, weight, bias=None, state=None, starts=None, silu: bool = True, out=None, stream=None):
     """Causal convolution of each channel over dim 1 of a (batch, length, channels) tensor,
     then silu (or, silu=False, as it is): y_t = silu(bias + sum_k weight[:, k] x_{t-taps+1+k}).
@@ -59,6 +65,7 @@ def causal_conv(x, weight, bias=None, state=None, starts=None, silu: bool = True
         starts = _starts(starts, (b, t), index)
     if out is not None:
         _out(out, "out", x.shape, dtype, index)
+        _apart(out, x)
     return _run(_causal_conv, x, stream, (code, pcode, taps, x, weight, bias, state, starts, silu, out))
 
 
@@ -92,6 +99,8 @@ def causal_conv_backward(dy, x, weight, bias=None, state=None, starts=None, dlas
         starts = _starts(starts, (b, t), index)
     if out is not None:
         _out(out, "out", x.shape, dtype, index)
+        _apart(out, x)
+        _apart(out, dy)
     _scratch(temp, index)
     return _run(_causal_conv_backward, x, stream,
                 (code, pcode, taps, dy, x, weight, bias, state, starts, dlast, silu, dparams, out, temp))
@@ -267,7 +276,7 @@ def selective_scan_backward(dy, x, dt, a, b, c, kept, d=None, z=None, dt_bias=No
     ddt_bias, dh0): None for what the call had no input for, dh0 always, da, dd, ddt_bias and dh0
     fp32.  `out` gives the tensors for (dx, ddt, dz) or, without z, (dx, ddt)."""
     code = _first(x, "x", 3, "(batch, length, channels)")
-    flat = b.dim() == 3
+    flat, flat_c = b.dim() == 3, c.dim() == 3
     b, c = _ssm(x, dt, a, b, c, d, z, dt_bias)
     (rows, t, width), dtype, index = x.shape, x.dtype, x.get_device()
     _rows_like(dy, "dy", x.shape, dtype, index)
@@ -284,11 +293,11 @@ def selective_scan_backward(dy, x, dt, a, b, c, kept, d=None, z=None, dt_bias=No
                 _out(v, what, x.shape, dtype, index)
     _scratch(temp, index)
     return _run(_selective_scan_backward, x, stream,
-                (code, flat, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt, dz, temp))
+                (code, flat, flat_c, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt, dz, temp))
 
 
-def _selective_scan_backward(s, code, flat, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt,
-                             dz, temp):
+def _selective_scan_backward(s, code, flat, flat_c, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx,
+                             ddt, dz, temp):
     (rows, t, width), dtype, dev, lib = x.shape, x.dtype, x.device, load()
     groups, states = b.shape[2], a.shape[1]
     if dx is None:
@@ -314,7 +323,9 @@ def _selective_scan_backward(s, code, flat, dy, x, dt, a, b, c, kept, d, z, dt_b
     if rc:
         _check(rc, "gb_selective_scan_backward")
     if flat:
-        db, dc = db.squeeze(2), dc.squeeze(2)
+        db = db.squeeze(2)
+    if flat_c:
+        dc = dc.squeeze(2)
     return SelectiveScanGrads(dx, ddt, da, db, dc, dd, dz, dbias, dh0)
 
 

@@ -1,0 +1,162 @@
+"""GPU: calls of the state space operators at the edges of what they allow: offsets past 32 bits, two
+calls at once, a training step captured and replayed, outputs in place of inputs, one group
+with and without its dimension."""
+import pytest
+import torch
+
+import stream_compaction_decoupled_gb300 as gb
+from stream_compaction_decoupled_gb300 import autograd
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(shape, dtype=torch.float32, scale=1.0, shift=0.0, seed=0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.empty(shape, dtype=dtype, device="cuda").normal_(generator=g).mul_(scale).add_(shift))
+
+
+def close(got, want):
+    """Two roundings to bf16, each off by half a step (2^-8 relative), and states that two ways to
+    split the tokens leave a few units of 2^-24 apart: 16 of them, weighted, stay below 2^-12 of
+    the largest output."""
+    got, want = got.float(), want.float()
+    assert ((got - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -12 * want.abs().max()).all()
+
+
+def test_offsets_past_32_bits():
+    """A row of more than 2^31 values: its end as the same tokens give alone, from the state before."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    t, d, n, tail = (1 << 20) + 5000, 2048, 16, 4096
+    head = t - tail
+    x, dy = rand((1, t, d), torch.bfloat16, seed=1), rand((1, t, d), torch.bfloat16, seed=2)
+    w, bias = rand((d, 4), torch.bfloat16, 0.5), rand((d,), torch.bfloat16, 0.1)
+    end = slice(head, None)
+    y, last = gb.causal_conv(x, w, bias)
+    want, want_last = gb.causal_conv(x[:, end], w, bias, state=x[:, head - 3:head].contiguous())
+    assert torch.equal(y[:, end], want) and torch.equal(last, want_last)
+    dx = gb.causal_conv_backward(dy, x, w, bias)[0]
+    want = gb.causal_conv_backward(dy[:, end], x[:, end], w, bias, state=x[:, head - 3:head].contiguous())[0]
+    assert torch.equal(dx[:, end], want)
+    del y, dx
+
+    dt, a = rand((1, t, d), torch.bfloat16, 0.5, seed=3), -torch.exp(rand((d, n), scale=0.5, seed=4))
+    b, c, skip = rand((1, t, n), torch.bfloat16, seed=5), rand((1, t, n), torch.bfloat16, seed=6), rand((d,), seed=7)
+    y, last, kept = gb.selective_scan(x, dt, a, b, c, skip, keep=True)
+    assert kept.numel() > 1 << 31
+    h0 = gb.selective_scan(x[:, :head], dt[:, :head], a, b[:, :head], c[:, :head], skip)[1]
+    want, want_last, tail_kept = gb.selective_scan(x[:, end], dt[:, end], a, b[:, end], c[:, end], skip, h0=h0, keep=True)
+    close(y[:, end], want)
+    assert ((last - want_last).abs() <= 2.0 ** -18 * want_last.abs().max()).all()
+    del y
+    g = gb.selective_scan_backward(dy, x, dt, a, b, c, kept, skip)
+    del kept
+    want = gb.selective_scan_backward(dy[:, end], x[:, end], dt[:, end], a, b[:, end], c[:, end], tail_kept, skip)
+    for k in ("dx", "ddt", "db", "dc"):
+        close(getattr(g, k)[:, end], getattr(want, k))
+
+
+def layer(size, dtype, seed):
+    b, t, d, n = size
+    leaves = [rand((b, t, d), dtype, seed=seed), rand((d, 4), dtype, 0.5, seed=seed + 1), rand((d,), dtype, 0.1, seed=seed + 2),
+              rand((b, t, d), dtype, 0.5, -1.0, seed=seed + 3), rand((d, n), scale=0.5, seed=seed + 4),
+              rand((b, t, n), dtype, seed=seed + 5), rand((b, t, n), dtype, seed=seed + 6), rand((d,), seed=seed + 7),
+              rand((b, t, d), dtype, seed=seed + 8), rand((d,), scale=0.3, seed=seed + 9)]
+    return [v.requires_grad_() for v in leaves]
+
+
+def train(leaves):
+    x, w, bias, dt, log_a, b, c, d, z, dt_bias = leaves
+    u, _ = autograd.causal_conv(x, w, bias)
+    y, last = autograd.selective_scan(u, dt, -torch.exp(log_a), b, c, d, z, dt_bias)
+    loss = y.float().square().mean() + last.mean()
+    return (loss.detach(), *torch.autograd.grad(loss, leaves))
+
+
+@pytest.mark.parametrize("size", [(2, 100, 96, 16), (1, 1500, 72, 8)])
+def test_a_training_step_in_a_graph(size):
+    """Captured, replayed with other inputs and again with the first.  (No eager graph of the leaves is
+    alive: torch would run their end of the backward pass on that graph's stream.)"""
+    leaves, other = layer(size, torch.bfloat16, 10), layer(size, torch.bfloat16, 50)
+    want = train(leaves)
+    with torch.no_grad():
+        keep = [v.clone() for v in leaves]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = train(leaves)
+    graph.replay()
+    for u, v in zip(got, want):
+        assert torch.equal(u, v)
+    with torch.no_grad():
+        for v, w in zip(leaves, other):
+            v.copy_(w)
+    graph.replay()
+    for u, v in zip(got, train(other)):
+        assert torch.equal(u, v)
+    with torch.no_grad():
+        for v, w in zip(leaves, keep):
+            v.copy_(w)
+    graph.replay()
+    for u, v in zip(got, want):
+        assert torch.equal(u, v)
+
+
+def test_two_training_steps_at_once():
+    """On two streams, over and over: each as alone."""
+    size = (2, 900, 160, 16)
+    many = [layer(size, torch.bfloat16, 10), layer(size, torch.bfloat16, 90)]
+    want = [train(v) for v in many]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(train(many[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for run in got[k]:
+            for u, v in zip(run, want[k]):
+                assert torch.equal(u, v)
+
+
+def test_nothing_of_the_convolution_in_place():
+    x, w = rand((2, 40, 64)), rand((64, 4))
+    with pytest.raises(ValueError):
+        gb.causal_conv(x, w, out=x)
+    dy = rand((2, 40, 64), seed=1)
+    for out in (x, dy):
+        with pytest.raises(ValueError):
+            gb.causal_conv_backward(dy, x, w, out=out)
+
+
+def test_one_group_with_its_dimension_beside_one_without():
+    size = (2, 40, 64, 16)
+    leaves = layer(size, torch.float32, 3)
+    want = train(leaves)
+    x, w, bias, dt, log_a, b, c, d, z, dt_bias = leaves
+    u, _ = autograd.causal_conv(x, w, bias)
+    y, last = autograd.selective_scan(u, dt, -torch.exp(log_a), b[:, :, None], c, d, z, dt_bias)
+    loss = y.square().mean() + last.mean()
+    for u, v in zip((loss, *torch.autograd.grad(loss, leaves)), want):
+        assert torch.equal(u, v)
+
+
+def test_a_gradient_of_broadcast_inputs():
+    """Inputs that all rows share get the sum of the rows' gradients (in 64 bits, rounded: each row's
+    is off by 2^-24 or so of the largest, the sum of 3 by less than 2^-20)."""
+    b, t, d, n = 3, 50, 64, 16
+    x, dt, z = rand((1, t, d), seed=1), rand((1, t, d), seed=2), rand((1, t, d), seed=3)
+    bm, cm = rand((1, t, n), seed=4), rand((1, t, n), seed=5)
+    a, h0, dy = -torch.exp(rand((d, n), scale=0.5, seed=6)), rand((b, d, n), seed=7), rand((b, t, d), seed=8)
+    shared = [v.requires_grad_() for v in (x, dt, z, bm, cm)]
+    e = [v.expand(b, -1, -1) for v in shared]
+    y, _ = autograd.selective_scan(e[0], e[1], a, e[3], e[4], None, e[2], h0=h0)
+    got = torch.autograd.grad(y, shared, dy)
+    full = [v.detach().expand(b, -1, -1).contiguous().requires_grad_() for v in shared]
+    y2, _ = autograd.selective_scan(full[0], full[1], a, full[3], full[4], None, full[2], h0=h0)
+    assert torch.equal(y, y2)
+    for u, v in zip(got, torch.autograd.grad(y2, full, dy)):
+        v = v.double().sum(0, keepdim=True)
+        assert ((u.double() - v).abs() <= 2.0 ** -20 * v.abs().max()).all()
