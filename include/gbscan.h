@@ -615,8 +615,8 @@ int gb_selective_scan_step(int dtype, int64_t batch, int64_t channels, int64_t s
  *   accepted      (batch) int32: n, how many drafts are accepted
  *   out           (batch, drafts + 1) int32, contiguous: the n accepted drafts, the token drawn,
  *                 and -1 behind it
- * Probabilities need not sum to 1; negative ones and NaNs count as 0.  Where r is 0 everywhere
- * the token is -1.  A length outside 0 .. drafts is taken as the nearest within, a draft outside
+ * Probabilities need not sum to 1; negative ones and NaNs count as 0 (with an infinite one it is
+ * not said which token is drawn).  Where r is 0 everywhere the token is -1.  A length outside 0 .. drafts is taken as the nearest within, a draft outside
  * the vocabulary is not accepted; both are reported as GB_ERR_RANGE by gb_device_error.
  */
 int gb_verify_drafts(int dtype, int64_t batch, int64_t drafts, int64_t vocab, const void* tokens, int token_dtype,

@@ -56,6 +56,80 @@ def test_offsets_past_32_bits():
         close(getattr(g, k)[:, end], getattr(want, k))
 
 
+def test_pools_past_32_bits():
+    """States whose places are past 2^31 values, by the forms for one token."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    d, n, small = 4096, 16, 6
+    pool = (1 << 31) // (d * n) + 10
+    high = [pool - 1, 3, pool - 7, -1, pool // 2 + 1, pool - 2]
+    slots = torch.tensor(high, dtype=torch.int32, device="cuda")
+    low = torch.tensor([0, 1, 2, -1, 4, 5], dtype=torch.int32, device="cuda")
+    x, dt, z = rand((small, d), torch.bfloat16, seed=1), rand((small, d), torch.bfloat16, seed=2), rand((small, d), torch.bfloat16, seed=3)
+    b, c = rand((small, n), torch.bfloat16, seed=4), rand((small, n), torch.bfloat16, seed=5)
+    a, start = -torch.exp(rand((d, n), scale=0.5, seed=6)), rand((small, d, n), seed=7)
+    states = torch.zeros((pool, d, n), device="cuda")
+    for k, s in enumerate(high):
+        if s >= 0:
+            states[s] = start[k]
+    want_states = start.clone()
+    want = gb.selective_scan_step(x, dt, a, b, c, want_states, z=z, slots=low)
+    got = gb.selective_scan_step(x, dt, a, b, c, states, z=z, slots=slots)
+    assert torch.equal(got, want)
+    for k, s in enumerate(high):
+        if s >= 0:
+            assert torch.equal(states[s], want_states[k])
+            states[s] = 0
+    assert not states.any()
+    del states
+    pool = (1 << 31) // (3 * d) + 10
+    high = [pool - 1, 3, pool - 7, -1, pool // 2 + 1, pool - 2]
+    slots = torch.tensor(high, dtype=torch.int32, device="cuda")
+    w, start = rand((d, 4), torch.bfloat16, 0.5), rand((small, 3, d), torch.bfloat16, seed=8)
+    windows = torch.zeros((pool, 3, d), dtype=torch.bfloat16, device="cuda")
+    for k, s in enumerate(high):
+        if s >= 0:
+            windows[s] = start[k]
+    want_windows = start.clone()
+    want = gb.causal_conv_step(x, want_windows, w, slots=low)
+    got = gb.causal_conv_step(x, windows, w, slots=slots)
+    assert torch.equal(got, want)
+    for k, s in enumerate(high):
+        if s >= 0:
+            assert torch.equal(windows[s], want_windows[k])
+
+
+@pytest.mark.parametrize("drafter", [True, False])
+def test_vocabularies_past_32_bits(drafter):
+    """More than 2^31 probabilities, rows at odd offsets."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    n, k, v = 4, 4, (1 << 27) + 3
+    g = torch.Generator("cuda").manual_seed(1)
+    target = torch.rand((n, k + 1, v), generator=g, device="cuda")
+    draft = torch.rand((n, k, v), generator=g, device="cuda") if drafter else None
+    drafts = torch.randint(0, v, (n, k), generator=g, device="cuda")
+    accept = torch.zeros((n, k), device="cuda")
+    accept[0, 1] = accept[1, 3] = accept[3, 2] = 0.999
+    for row, i in ((0, 1), (1, 3), (3, 2)):  # refused there
+        target[row, i, drafts[row, i]] = 0.0
+    sample = torch.tensor([0.999, 0.5, 0.25, 0.75], device="cuda")
+    got = gb.verify_drafts(drafts, target, draft, accept, sample)
+    assert got.accepted.tolist() == [1, 3, 4, 2]
+    for row, i in enumerate((1, 3, 4, 2)):
+        rest = target[row, i].double()
+        if i < k:
+            if drafter:
+                rest = (rest - draft[row, i].double()).clamp(min=0)
+            else:
+                rest[drafts[row, i]] = 0.0
+        sums = rest.cumsum(0)
+        token = int(got.tokens[row, i])
+        # Within what 64-bit sums of 2^27 values leave open: 2^27 roundings of 2^-53 of the total.
+        limit, slack = sample[row].double() * sums[-1], 2.0 ** -25 * sums[-1]
+        assert sums[token] > limit - slack and (token == 0 or sums[token - 1] <= limit + slack) and rest[token] > 0
+
+
 def layer(size, dtype, seed):
     b, t, d, n = size
     leaves = [rand((b, t, d), dtype, seed=seed), rand((d, 4), dtype, 0.5, seed=seed + 1), rand((d,), dtype, 0.1, seed=seed + 2),
