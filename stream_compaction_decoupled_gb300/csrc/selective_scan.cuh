@@ -64,8 +64,15 @@ template <class T> struct SscArgs {
   bool vec;     // (D, N) arrays can be read and written in 16-byte pieces
 };
 
+// How rows are read: by asynchronous copies of 16 bytes (WHOLE), of 4 (WORDS: any fp32 rows, and
+// 16-bit ones with even widths, strides and counts of states on 4-byte boundaries), or value by value
+// through registers (SINGLES, 16 bits only).  8 x 2048 tokens, 16 states, WORDS and SINGLES: 2046
+// channels bf16 295 and 547 us, the gradient 864 and 1235; 4 x 2048 x 2001 fp32 205 and 252, 552 and 589.
+enum SscMode { kSscWhole, kSscWords, kSscSingles };
+
 // Two neighbouring channels of a row, as they lie in memory.
-template <class T, bool EDGE> struct SscPair {
+template <class T, SscMode MODE> struct SscPair {
+  static constexpr bool EDGE = MODE == kSscSingles || (MODE == kSscWords && sizeof(T) == 4);  // not at once
   using Raw = std::conditional_t<sizeof(T) == 2, unsigned, float2>;
   static __device__ __forceinline__ Raw load(const T* p, int count) {
     Raw r;
@@ -125,14 +132,13 @@ template <class T> __device__ __forceinline__ float2 ssc_step_size(const SscArgs
 // M = 16 / LN states of two channels a thread, LN lanes a pair of channels; a warp is on its own:
 // WIDTH channels, tiles of L tokens, of which a lane prepares and finishes R.  What a warp reads
 // comes by asynchronous copies into a ring of STAGES tiles of its own in shared memory.
-template <class T, bool EDGE_, int LN_> struct SscLane {
-  static constexpr bool EDGE = EDGE_;
+template <class T, SscMode MODE, int LN_> struct SscLane {
   static constexpr int LN = LN_, L = 8, R = L / LN, M = 16 / LN, WIDTH = 64 / LN;
   static constexpr int STAGES = sizeof(T) == 2 ? 3 : 2;
   static constexpr int ROW = WIDTH * (int)sizeof(T), ARRAY = L * ROW;  // bytes
   static constexpr int VECTORS = L * 32 * (int)sizeof(T);               // B and C of 16 states, as they are
   static constexpr int CHUNKS = ROW / 16;                               // 16-byte copies of a row
-  using P = SscPair<T, EDGE>;
+  using P = SscPair<T, MODE>;
   using Raw = typename P::Raw;
   static __host__ __device__ constexpr int stage_bytes(int NB) { return 3 * ARRAY + NB * VECTORS; }
   // Bytes a warp: the ring, B and C widened, D and D x of each pair, and with more than 16 states
@@ -220,11 +226,12 @@ template <int M> __device__ __forceinline__ void ssc_store_any(bool vec, float* 
 }
 
 // ENDS: only the states that the part ends with, from a state of zero, and its sum of D.
-template <class T, bool EDGE, bool ONE, bool ENDS, int LN>
-__global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
+template <class T, SscMode MODE, bool ONE, bool ENDS, int LN>
+__global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && LN == 2) ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
-  using S = SscLane<T, EDGE, LN>;
+  using S = SscLane<T, MODE, LN>;
   using P = typename S::P;
+  constexpr bool SINGLES = MODE == kSscSingles;
   constexpr int L = S::L, R = S::R, M = S::M;
   extern __shared__ __align__(16) float2 ssc_shared[];
   const int NB = ONE ? 1 : a.NP / 16;
@@ -301,9 +308,9 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
   const long long sv = second ? a.ct : a.bt;
   const uint8_t* ps = a.starts ? a.starts + at.b * a.T_ : nullptr;
 
-  // Starts a tile's copies into the ring.  EDGE, where they cannot be in pieces of 16 bytes: loads
-  // the tile, for `put` to store behind the one that is worked on.  (No ordinary load goes among
-  // the copies: waiting for it would be waiting for them.)
+  // Starts a tile's copies into the ring.  SINGLES: loads the tile, for `put` to store behind the
+  // one that is worked on.  (No ordinary load goes among the copies: waiting for it would be waiting
+  // for them.)
   constexpr int V = 16 / sizeof(T), PER = 32 / V;
   const int own_row = lane / S::CHUNKS, own_c = lane % S::CHUNKS * V;   // the lane's pieces of x, dt, z
   const int v_row = lane / PER, v_c = lane % PER * V;                   // and of B or C
@@ -313,12 +320,12 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
   const T* qz = gated ? pz + (long long)(at.t0 + own_row) * a.zt + at.base + own_c : nullptr;
   const long long qs = v_c < 16 ? a.bt : a.ct;
   const T* qv = (v_c < 16 ? pb : pc) + (long long)(at.t0 + v_row) * qs + v_c % 16;
-  typename S::Raw ex[EDGE ? R : 1], ed[EDGE ? R : 1], ez[EDGE ? R : 1];
-  T ev[EDGE && ONE ? L : 1];
+  typename S::Raw ex[SINGLES ? R : 1], ed[SINGLES ? R : 1], ez[SINGLES ? R : 1];
+  T ev[SINGLES && ONE ? L : 1];
   const auto get = [&](int t, int stage) {
     unsigned char* to_stage = ring + stage * stage_bytes;
     if (t < at.t1) {
-      if constexpr (EDGE) {
+      if constexpr (SINGLES) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const long long row = min(t + ln + r * LN, a.T_ - 1);
@@ -329,6 +336,31 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
         if constexpr (ONE) {
 #pragma unroll
           for (int i = 0; i < L; ++i) ev[i] = pv[(long long)min(t + i, a.T_ - 1) * sv + (n < a.N ? n : 0)];
+        }
+      } else if constexpr (MODE == kSscWords) {
+        constexpr int VW = 4 / sizeof(T), ROW_WORDS = 32 / VW, WORDS = S::ROW / 4;  // words of B and C, of x
+        const int x_c = lane % WORDS * VW;
+#pragma unroll
+        for (int q = 0; q < L * WORDS / 32; ++q) {
+          const int i = q * (32 / WORDS) + lane / WORDS;
+          const long long row = min(t + i, a.T_ - 1);
+          if (x_c < at.width) {
+            unsigned char* to = to_stage + i * S::ROW + x_c * sizeof(T);
+            cp_async4(to, px + row * a.xt + at.base + x_c);
+            cp_async4(to + S::ARRAY, pdt + row * a.dtt + at.base + x_c);
+            if (gated) cp_async4(to + 2 * S::ARRAY, pz + row * a.zt + at.base + x_c);
+          }
+        }
+        const int w_c = lane % ROW_WORDS * VW;
+        const T* from = (w_c < 16 ? pb : pc) + w_c % 16;
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+          for (int q = 0; q < L / VW; ++q) {
+            const int i = q * VW + lane / ROW_WORDS;
+            if (k * 16 + w_c % 16 < a.N && (!ENDS || w_c < 16))
+              cp_async4(to_stage + 3 * S::ARRAY + ((k * L + i) * 32 + w_c) * sizeof(T),
+                        from + (long long)min(t + i, a.T_ - 1) * (w_c < 16 ? a.bt : a.ct) + k * 16);
+          }
         }
       } else {
         // Rows behind the last are read as the last: that many rows back.
@@ -361,7 +393,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
     cp_async_commit();
   };
   const auto put = [&](int stage) {
-    if constexpr (EDGE) {
+    if constexpr (SINGLES) {
       unsigned char* to_stage = ring + stage * stage_bytes;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -376,7 +408,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
       }
     }
   };
-  if constexpr (!EDGE) {  // states past the last stay zero
+  if constexpr (!SINGLES) {  // states past the last, and channels, stay zero
     for (int k = lane; k < S::STAGES * stage_bytes / 16; k += 32) ((float4*)ring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
   }
@@ -420,7 +452,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(EDGE && LN == 2) ? 4 : 3
       return P::wide(((const typename S::Raw*)(tile + array * S::ARRAY + (ln + r * LN) * S::ROW))[lane / LN]);
     };
     // B and C of the tile, widened.
-    if constexpr (EDGE && !ONE) {
+    if constexpr (SINGLES && !ONE) {
       for (int k = 0; k < NB; ++k) {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
@@ -582,14 +614,13 @@ template <int M> __device__ __forceinline__ void ssc_exchange(float (&v)[M], int
 // the lanes' parts of three sums over states for 4 tokens; states before tokens 4, 8 and 12; the
 // warp's sums of dB and dC; with more than 16 states what a lane keeps of each block.  For the
 // block: two tiles of B and C as they are, one widened.
-template <class T, bool EDGE_> struct SscBack {
-  static constexpr bool EDGE = EDGE_;
+template <class T, SscMode MODE> struct SscBack {
   static constexpr int L = kSscTile, R = L / 4, M = 4, STAGES = 2;
   static constexpr int ROW = 16 * (int)sizeof(T), ARRAY = L * ROW, KEPT = 16 * 16 * 4, STAGE = 4 * ARRAY + KEPT;
   static constexpr int CHUNKS = ROW / 16;
   static constexpr int DU = L * 8 * 16, E = L * 8 * 8, SUMS = 3 * 4 * 8 * 4 * 8, SAVE = 3 * 8 * 32 * 4, RED = L * 32 * 4;
   static constexpr int VECTORS = L * 32 * (int)sizeof(T);
-  using P = SscPair<T, EDGE>;
+  using P = SscPair<T, MODE>;
   using Raw = typename P::Raw;
   static __host__ __device__ constexpr int warp_bytes(int NB, bool carry) {
     return STAGES * STAGE + DU + E + (carry ? 0 : SUMS + SAVE + RED) + (NB > 1 ? NB * 2 * 8 * 32 * 4 : 0);
@@ -614,11 +645,12 @@ __device__ __forceinline__ int ssc_sum_half(int i, int pair, int half) {
 // quarter: the lane's own token, from the sums over states.  The sums over channels for dB and
 // dC: over the pair in the thread, over the warp by exchanges, over the block in shared memory,
 // and over the blocks by a second kernel.
-template <class T, bool EDGE, bool ONE, bool CARRY>
+template <class T, SscMode MODE, bool ONE, bool CARRY>
 __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
-  using S = SscBack<T, EDGE>;
+  using S = SscBack<T, MODE>;
   using P = typename S::P;
+  constexpr bool SINGLES = MODE == kSscSingles;
   using Raw = typename S::Raw;
   constexpr int L = S::L, R = S::R, M = S::M;
   extern __shared__ __align__(16) float2 ssc_shared[];
@@ -719,17 +751,17 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
     }
     return f;
   };
-  // Starts a tile's copies into the ring.  EDGE, where they cannot be in pieces of 16 bytes: loads
-  // the tile, for `land` to store behind the one that is worked on.
+  // Starts a tile's copies into the ring.  SINGLES: loads the tile, for `land` to store behind the
+  // one that is worked on.
   constexpr int V = 16 / sizeof(T), PER = 32 / V;
-  Raw ex[EDGE ? R : 1], ed[EDGE ? R : 1], ey[EDGE ? R : 1], ez[EDGE ? R : 1];
-  T ev[EDGE && ONE ? 4 : 1];
+  Raw ex[SINGLES ? R : 1], ed[SINGLES ? R : 1], ey[SINGLES ? R : 1], ez[SINGLES ? R : 1];
+  T ev[SINGLES && ONE ? 4 : 1];
   float2 ek[2][2];
   const auto fetch = [&](int tile, int stage) {
     unsigned char* to = ring + stage * S::STAGE;
     if (tile >= tile0) {
       const int t = tile * L;
-      if constexpr (EDGE) {
+      if constexpr (SINGLES) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const long long u = min(t + 4 * r + ln, a.T_ - 1);
@@ -746,6 +778,45 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
             ev[i] = lane < 16 ? pb[u * a.bt + n] : pc[u * a.ct + n];
           }
           if constexpr (!CARRY) ssc_load_any<M>(a.vec, a.kept + ((b * a.tiles + tile) * a.D + ch) * a.N, ln * M, a.N, count, ek);
+        }
+      } else if constexpr (MODE == kSscWords) {
+        constexpr int VW = 4 / sizeof(T), ROW_WORDS = 32 / VW, WORDS = S::ROW / 4;  // words of B and C, of x
+        const int x_c = lane % WORDS * VW;
+#pragma unroll
+        for (int q = 0; q < L * WORDS / 32; ++q) {
+          const int i = q * (32 / WORDS) + lane / WORDS;
+          if (x_c < width) {
+            const long long u = min(t + i, a.T_ - 1);
+            unsigned char* at = to + i * S::ROW + x_c * sizeof(T);
+            if (!CARRY) cp_async4(at, px + u * a.xt + base + x_c);
+            cp_async4(at + S::ARRAY, pdt + u * a.dtt + base + x_c);
+            cp_async4(at + 2 * S::ARRAY, pdy + u * a.dyt + base + x_c);
+            if (gated) cp_async4(at + 3 * S::ARRAY, pz + u * a.zt + base + x_c);
+          }
+        }
+        if constexpr (ONE) {
+          if constexpr (!CARRY) {  // the lane's own states
+            const float* from = a.kept + ((b * a.tiles + tile) * a.D + ch) * a.N + ln * M;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              unsigned char* at = to + 4 * S::ARRAY + (c * 32 + lane) * 16;
+              if (a.vec) {
+                if (c < count && ln * M < a.N) cp_async16(at, from + c * a.N);
+              } else {
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                  if (c < count && ln * M + m < a.N) cp_async4(at + 4 * m, from + c * a.N + m);
+              }
+            }
+          }
+          const int c = lane % ROW_WORDS * VW;
+#pragma unroll
+          for (int q = 0; q < 4 / VW; ++q) {
+            const int i = warp * 4 + q * VW + lane / ROW_WORDS;
+            const long long u = min(t + i, a.T_ - 1);
+            if (c % 16 < a.N && (!CARRY || c >= 16))
+              cp_async4(vring + stage * S::VECTORS + (i * 32 + c) * sizeof(T), c < 16 ? pb + u * a.bt + c : pc + u * a.ct + c - 16);
+          }
         }
       } else {
 #pragma unroll
@@ -782,7 +853,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
     cp_async_commit();
   };
   const auto land = [&](int stage) {
-    if constexpr (EDGE) {
+    if constexpr (SINGLES) {
       unsigned char* to = ring + stage * S::STAGE;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -804,7 +875,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
       }
     }
   };
-  if constexpr (!EDGE) {  // states past the last stay zero
+  if constexpr (!SINGLES) {  // states past the last, and channels, stay zero
     for (int k = lane; k < S::STAGES * S::STAGE / 16; k += 32) ((float4*)ring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = threadIdx.x; k < S::STAGES * S::VECTORS / 16; k += kSscThreads) ((float4*)vring)[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
@@ -1364,32 +1435,32 @@ template <class K, class A> cudaError_t ssc_launch(K kernel, long long grid, siz
   return launch_pdl(kernel, (unsigned)grid, kSscThreads, smem, ctx.stream, a);
 }
 
-template <class T, bool EDGE, bool ONE, int LN> cudaError_t ssc_forward(const SelectiveScanJob& j, const SscForwardPlan& plan, const LaunchCtx& ctx) {
+template <class T, SscMode MODE, bool ONE, int LN> cudaError_t ssc_forward(const SelectiveScanJob& j, const SscForwardPlan& plan, const LaunchCtx& ctx) {
   const SscArgs<T> a = ssc_args<T>(j, plan.split);
   const long long units = j.B * a.G * ((a.DG + 64 / LN - 1) / (64 / LN));
   const auto grid = [&](long long parts) { return (units * parts + kSscThreads / 32 - 1) / (kSscThreads / 32); };
-  using S = SscLane<T, EDGE, LN>;
+  using S = SscLane<T, MODE, LN>;
   const int NB = ONE ? 1 : a.NP / 16;
   const size_t smem = (size_t)(kSscThreads / 32) * S::warp_bytes(NB);
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
-  if (plan.split.parts > 1) e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, true, LN>, grid(plan.split.parts - 1), smem, a, ctx);
-  if (e == cudaSuccess) e = ssc_launch(ssc_forward_kernel<T, EDGE, ONE, false, LN>, grid(plan.split.parts), smem, a, ctx);
+  if (plan.split.parts > 1) e = ssc_launch(ssc_forward_kernel<T, MODE, ONE, true, LN>, grid(plan.split.parts - 1), smem, a, ctx);
+  if (e == cudaSuccess) e = ssc_launch(ssc_forward_kernel<T, MODE, ONE, false, LN>, grid(plan.split.parts), smem, a, ctx);
   profile_after(ctx);
   return e;
 }
 
-template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
+template <class T, SscMode MODE, bool ONE> cudaError_t ssc_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
   const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.G);
   const SscArgs<T> a = ssc_args<T>(j, split);
   const long long units = j.B * a.G * a.blocks;
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
-  using S = SscBack<T, EDGE>;
+  using S = SscBack<T, MODE>;
   if (split.parts > 1)
-    e = ssc_launch(ssc_backward_kernel<T, EDGE, ONE, true>, units * (split.parts - 1), S::bytes(a.NP / 16, true), a, ctx);
+    e = ssc_launch(ssc_backward_kernel<T, MODE, ONE, true>, units * (split.parts - 1), S::bytes(a.NP / 16, true), a, ctx);
   if (e == cudaSuccess)
-    e = ssc_launch(ssc_backward_kernel<T, EDGE, ONE, false>, units * split.parts, S::bytes(a.NP / 16, false), a, ctx);
+    e = ssc_launch(ssc_backward_kernel<T, MODE, ONE, false>, units * split.parts, S::bytes(a.NP / 16, false), a, ctx);
   if (e == cudaSuccess) {
     SscFoldArgs<T> f = {};
     f.part_a = a.part_a, f.part_b = a.part_b, f.part_c = a.part_c;
@@ -1407,26 +1478,38 @@ template <class T, bool EDGE, bool ONE> cudaError_t ssc_backward(const Selective
   return e;
 }
 
-template <class T, bool EDGE> cudaError_t ssc_forward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
+template <class T, SscMode MODE> cudaError_t ssc_forward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
   const SscForwardPlan plan = ssc_forward_plan(j.B, j.T, j.D, j.G);
-  if (j.N > 16) return ssc_forward<T, EDGE, false, 4>(j, plan, ctx);
-  return plan.lanes == 2 ? ssc_forward<T, EDGE, true, 2>(j, plan, ctx) : ssc_forward<T, EDGE, true, 4>(j, plan, ctx);
+  if (j.N > 16) return ssc_forward<T, MODE, false, 4>(j, plan, ctx);
+  return plan.lanes == 2 ? ssc_forward<T, MODE, true, 2>(j, plan, ctx) : ssc_forward<T, MODE, true, 4>(j, plan, ctx);
+}
+// Whether what is read starts in pieces of V values; written: of a pair.
+template <class T> bool ssc_pieces(const SelectiveScanJob& j, int V, std::initializer_list<const SeqArray*> read,
+                                   std::initializer_list<const SeqArray*> written) {
+  bool even = (j.D / j.G) % V == 0 && j.N % V == 0 && ssc_rows<T>(j.b, V, j.B, j.T, j.G) && ssc_rows<T>(j.c, V, j.B, j.T, j.G);
+  for (const SeqArray* s : read) even = even && ssc_rows<T>(*s, V, j.B, j.T);
+  for (const SeqArray* s : written) even = even && ssc_rows<T>(*s, 2, j.B, j.T);
+  return even;
 }
 template <class T> cudaError_t launch_selective_scan(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  constexpr int V = 16 / sizeof(T);
-  bool even = (j.D / j.G) % V == 0 && j.N % V == 0 && ssc_rows<T>(j.b, V, j.B, j.T, j.G) && ssc_rows<T>(j.c, V, j.B, j.T, j.G);
-  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.y}) even = even && ssc_rows<T>(*s, V, j.B, j.T);
-  return even ? ssc_forward_any<T, false>(j, ctx) : ssc_forward_any<T, true>(j, ctx);
+  const auto pieces = [&](int V) { return ssc_pieces<T>(j, V, {&j.x, &j.dt, &j.z}, {&j.y}); };
+  if (pieces(16 / sizeof(T))) return ssc_forward_any<T, kSscWhole>(j, ctx);
+  if constexpr (sizeof(T) == 2) {
+    if (!pieces(2)) return ssc_forward_any<T, kSscSingles>(j, ctx);
+  }
+  return ssc_forward_any<T, kSscWords>(j, ctx);
 }
 
+template <class T, SscMode MODE> cudaError_t ssc_backward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
+  return j.N <= 16 ? ssc_backward<T, MODE, true>(j, ctx) : ssc_backward<T, MODE, false>(j, ctx);
+}
 template <class T> cudaError_t launch_selective_scan_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  constexpr int V = 16 / sizeof(T);
-  bool even = (j.D / j.G) % V == 0 && j.N % V == 0 && (uintptr_t)j.kept % 16 == 0 && ssc_rows<T>(j.b, V, j.B, j.T, j.G) &&
-              ssc_rows<T>(j.c, V, j.B, j.T, j.G);
-  for (const SeqArray* s : {&j.x, &j.dt, &j.z, &j.dy}) even = even && ssc_rows<T>(*s, V, j.B, j.T);
-  for (const SeqArray* s : {&j.dx, &j.ddt, &j.dz}) even = even && ssc_rows<T>(*s, 2, j.B, j.T);
-  if (j.N <= 16) return even ? ssc_backward<T, false, true>(j, ctx) : ssc_backward<T, true, true>(j, ctx);
-  return even ? ssc_backward<T, false, false>(j, ctx) : ssc_backward<T, true, false>(j, ctx);
+  const auto pieces = [&](int V) { return ssc_pieces<T>(j, V, {&j.x, &j.dt, &j.z, &j.dy}, {&j.dx, &j.ddt, &j.dz}); };
+  if (pieces(16 / sizeof(T)) && (uintptr_t)j.kept % 16 == 0) return ssc_backward_any<T, kSscWhole>(j, ctx);
+  if constexpr (sizeof(T) == 2) {
+    if (!pieces(2)) return ssc_backward_any<T, kSscSingles>(j, ctx);
+  }
+  return ssc_backward_any<T, kSscWords>(j, ctx);
 }
 
 template <class T> cudaError_t launch_selective_scan_step(const SelectiveScanStepJob& j, const LaunchCtx& ctx) {
