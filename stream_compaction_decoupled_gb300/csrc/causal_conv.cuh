@@ -473,16 +473,20 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_ke
         }
       };
       // Token t + u - (W - 1) takes nothing more after token t + u.
-      if (flag == 0 && age >= W - 1 && a.taps == W && t + W <= t1 && t >= t0 + W - 1) {
+      const auto inside = [&](int reach) {
 #pragma unroll
         for (int u = 0; u < W; ++u) {
-          token(u, W - 1, true);
+          token(u, reach, true);
           float2(&out)[H] = pend[(u + 1) % W];
           lane.store(po + u * a.dxt, lane.narrowed(out));
 #pragma unroll
           for (int h = 0; h < H; ++h) out[h] = zero;
         }
         age += W;
+      };
+      if (flag == 0 && age >= W - 1 && t + W <= t1 && t >= t0 + W - 1) {
+        if (a.taps == W) inside(W - 1);
+        else inside(a.taps - 1);
       } else {
 #pragma unroll
         for (int u = 0; u < W; ++u) {
