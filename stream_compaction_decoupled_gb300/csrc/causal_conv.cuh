@@ -48,21 +48,23 @@ template <class T> __device__ __forceinline__ float conv_param(const void* p, lo
   return wide ? ((const float*)p)[k] : widen(((const T*)p)[k]);
 }
 
-// A lane's V values of a row: side by side, or APART from one another with a count of those
-// that exist.
-template <class T, int V, bool EDGE> struct ConvLane {
-  static constexpr int APART = EDGE ? 32 : 1;
+// A lane's V values of a row: P side by side, then P of 32 P channels on.  P = V: one access.
+// P = 2, 16 bits: words, where rows cannot be read in larger pieces.  P = 1: single values.
+template <class T, int V, int P> struct ConvLane {
+  static constexpr int GROUPS = V / P;
+  using Word = std::conditional_t<P * sizeof(T) == 2, unsigned short,
+                                  std::conditional_t<P * sizeof(T) == 4, unsigned, std::conditional_t<P * sizeof(T) == 8, uint2, uint4>>>;
   int first;  // the lane's first channel
-  int count;  // how many of the V exist
+  int count;  // how many of the V exist: a multiple of P
 
   __device__ __forceinline__ ConvLane(int group, int lane, int D) {
-    first = group * 32 * V + (EDGE ? lane : lane * V);
+    first = group * 32 * V + lane * P;
     const int left = D - first;
-    count = left <= 0 ? 0 : (left + APART - 1) / APART;
-    if (count > V) count = V;
+    count = left <= 0 ? 0 : P * min(GROUPS, (left + 32 * P - 1) / (32 * P));
   }
+  static __device__ __forceinline__ constexpr int place(int e) { return e / P * 32 * P + e % P; }  // from the first
   struct Raw {
-    alignas(EDGE ? sizeof(T) : V * sizeof(T)) T v[V];
+    alignas(sizeof(Word)) T v[V];
   };
   __device__ __forceinline__ Raw zero() const {
     Raw r;
@@ -72,46 +74,22 @@ template <class T, int V, bool EDGE> struct ConvLane {
   }
   __device__ __forceinline__ Raw load(const T* row) const {
     Raw r = zero();
-    if constexpr (EDGE) {
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < count) r.v[e] = row[first + e * APART];
-    } else {
-      if (count) {
-        if constexpr (V * sizeof(T) == 16) {
-          const uint4 u = *(const uint4*)(row + first);
-          memcpy(&r, &u, 16);
-        } else if constexpr (V * sizeof(T) == 8) {
-          const uint2 u = *(const uint2*)(row + first);
-          memcpy(&r, &u, 8);
-        } else {
-          const unsigned u = *(const unsigned*)(row + first);
-          memcpy(&r, &u, 4);
-        }
+    for (int g = 0; g < GROUPS; ++g) {
+      if (g * P < count) {
+        const Word u = *(const Word*)(row + first + g * 32 * P);
+        memcpy(r.v + g * P, &u, sizeof(u));
       }
     }
     return r;
   }
   __device__ __forceinline__ void store(T* row, const Raw& r) const {
-    if constexpr (EDGE) {
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (e < count) row[first + e * APART] = r.v[e];
-    } else {
-      if (count) {
-        if constexpr (V * sizeof(T) == 16) {
-          uint4 u;
-          memcpy(&u, &r, 16);
-          *(uint4*)(row + first) = u;
-        } else if constexpr (V * sizeof(T) == 8) {
-          uint2 u;
-          memcpy(&u, &r, 8);
-          *(uint2*)(row + first) = u;
-        } else {
-          unsigned u;
-          memcpy(&u, &r, 4);
-          *(unsigned*)(row + first) = u;
-        }
+    for (int g = 0; g < GROUPS; ++g) {
+      if (g * P < count) {
+        Word u;
+        memcpy(&u, r.v + g * P, sizeof(u));
+        *(Word*)(row + first + g * 32 * P) = u;
       }
     }
   }
@@ -145,7 +123,7 @@ template <class T, int V, bool EDGE> struct ConvLane {
     float v[V];
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      v[e] = e < count ? conv_param(p, (long long)(first + e * APART) * stride + k, wide, (T*)nullptr) : 0.f;
+      v[e] = e < count ? conv_param(p, (long long)(first + place(e)) * stride + k, wide, (T*)nullptr) : 0.f;
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
   }
@@ -206,34 +184,37 @@ struct ConvFlags {
 };
 
 // Where a warp's rows come through: STAGES groups of U rows of each of ARRAYS arrays, copied
-// STAGES - 1 groups ahead; EDGE: one group, in registers.
-template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
-  using L = ConvLane<T, V, EDGE>;
+// STAGES - 1 groups ahead, in pieces of 16 bytes, or each lane its own words (8 x 2048 x 2046 bf16
+// 38.9 us, value by value 41.0; the gradient 67.6 and 86.0).  Single values: one group, in registers
+// (fp32 rows are not copied in words: 8 x 2048 x 2047 59.4 us either way, the gradient 94.2 and 98.3).
+template <class T, int V, int U, int ARRAYS, int P> struct ConvRing {
+  using L = ConvLane<T, V, P>;
+  static constexpr bool WHOLE = P == V, SINGLES = P == 1;
   static constexpr int STAGES = 4, ROW = 32 * V * (int)sizeof(T), STAGE = ARRAYS * U * ROW;
   static constexpr int CHUNKS = ROW / 16, ROWS = 32 / CHUNKS;  // 16-byte copies of a row, rows a copy of all lanes
-  static constexpr int BYTES = EDGE ? 0 : STAGES * STAGE;      // a warp
-  static_assert(EDGE || (ROWS >= 1 && U % ROWS == 0), "whole rows");
+  static constexpr int BYTES = SINGLES ? 0 : STAGES * STAGE;   // a warp
+  static_assert(!WHOLE || (ROWS >= 1 && U % ROWS == 0), "whole rows");
   const L& lane;
   unsigned char* ring;
   const T* p[ARRAYS];      // the next group's first row (the lane's part of it)
   long long stride[ARRAYS];
   int next, stop, stage = 0, own_row = 0;
   bool copies = false;
-  typename L::Raw raw[EDGE ? ARRAYS : 1][EDGE ? U : 1];
+  typename L::Raw raw[SINGLES ? ARRAYS : 1][SINGLES ? U : 1];
 
   // Rows `first` .. stop - 1; p: row 0 of each array.
   __device__ __forceinline__ ConvRing(const L& lane_, unsigned char* ring_, const T* const (&rows)[ARRAYS],
                                       const long long (&strides)[ARRAYS], int group, int D, int first, int stop_)
       : lane(lane_), ring(ring_), next(first), stop(stop_) {
     const int l = threadIdx.x & 31;
-    if constexpr (!EDGE) own_row = l / CHUNKS, copies = group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)) < D;
+    if constexpr (WHOLE) own_row = l / CHUNKS, copies = group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)) < D;
 #pragma unroll
     for (int k = 0; k < ARRAYS; ++k) {
       stride[k] = strides[k];
       p[k] = rows[k] + (long long)(first + own_row) * strides[k] +
-             (EDGE ? 0 : group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)));
+             (WHOLE ? group * 32 * V + l % CHUNKS * (16 / (int)sizeof(T)) : 0);
     }
-    if constexpr (EDGE) {
+    if constexpr (SINGLES) {
       fill();
     } else {
 #pragma unroll
@@ -242,7 +223,7 @@ template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
   }
   // Asks for the next group.
   __device__ __forceinline__ void fill() {
-    if constexpr (EDGE) {
+    if constexpr (SINGLES) {
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k) {
 #pragma unroll
@@ -250,12 +231,24 @@ template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
         p[k] += U * stride[k];
       }
     } else {
-      unsigned char* to = ring + stage * STAGE + own_row * ROW + (threadIdx.x & 31) % CHUNKS * 16;
+      unsigned char* to = ring + stage * STAGE;
+      if constexpr (WHOLE) to += own_row * ROW + (threadIdx.x & 31) % CHUNKS * 16;
+      else to += (threadIdx.x & 31) * 4;
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k) {
+        if constexpr (WHOLE) {
 #pragma unroll
-        for (int u = 0; u < U; u += ROWS)
-          if (copies && next + u + own_row < stop) cp_async16(to + (k * U + u) * ROW, p[k] + u * stride[k]);
+          for (int u = 0; u < U; u += ROWS)
+            if (copies && next + u + own_row < stop) cp_async16(to + (k * U + u) * ROW, p[k] + u * stride[k]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const T* row = p[k] + u * stride[k] + lane.first;
+#pragma unroll
+            for (int g = 0; g < L::GROUPS; ++g)
+              if (g * P < lane.count && next + u < stop) cp_async4(to + (k * U + u) * ROW + g * 128, row + g * 32 * P);
+          }
+        }
         p[k] += U * stride[k];
       }
       cp_async_commit();
@@ -265,7 +258,7 @@ template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
   }
   // The group that was asked for first, widened; asks for another.  Rows from `stop` on are undefined.
   __device__ __forceinline__ void take(float2 (&f)[ARRAYS][U][V / 2]) {
-    if constexpr (EDGE) {
+    if constexpr (SINGLES) {
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k)
 #pragma unroll
@@ -276,26 +269,44 @@ template <class T, int V, int U, int ARRAYS, bool EDGE> struct ConvRing {
       __syncwarp();  // the group is there, and the one before it, which is filled again, read by all
       // `stage` is filled next: the group read here is the one after it in the ring.
       const int at = stage == STAGES - 1 ? 0 : stage + 1;
-      const unsigned char* from = ring + at * STAGE + (threadIdx.x & 31) * V * (int)sizeof(T);
+      const unsigned char* from = ring + at * STAGE + (threadIdx.x & 31) * (WHOLE ? V * (int)sizeof(T) : 4);
       fill();
 #pragma unroll
       for (int k = 0; k < ARRAYS; ++k)
 #pragma unroll
-        for (int u = 0; u < U; ++u) lane.widen_to(*(const typename L::Raw*)(from + (k * U + u) * ROW), f[k][u]);
+        for (int u = 0; u < U; ++u) {
+          if constexpr (WHOLE) {
+            lane.widen_to(*(const typename L::Raw*)(from + (k * U + u) * ROW), f[k][u]);
+          } else {
+            typename L::Raw own;
+#pragma unroll
+            for (int g = 0; g < L::GROUPS; ++g) {
+              const unsigned word = *(const unsigned*)(from + (k * U + u) * ROW + g * 128);
+              memcpy(own.v + g * P, &word, 4);
+            }
+            lane.widen_to(own, f[k][u]);
+          }
+        }
     }
   }
 };
 
 template <class T, int W> constexpr int kConvGroup = W == 4 && sizeof(T) == 2 ? 8 : 4;  // tokens of a group
 
+// Blocks of 4 warps an SM, by registers.
+template <int W> constexpr int conv_forward_blocks(int P) {
+  return P == 1 ? W == 4 ? 3 : 2 : W == 4 && P == 4 ? 4 : 3;
+}
+template <int W> constexpr int conv_backward_blocks(int P) { return W == 4 && P > 1 ? 3 : 2; }
+
 // Two single operations: beside the gate's exponentials they are quicker than a packed one (forward
 // 36.0 -> 33.9 us; the gradient has the same 65 us either way).
 __device__ __forceinline__ float2 conv_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
 
-template <class T, int W, int V, bool EDGE>
-__global__ void __launch_bounds__(128, W == 4 && !EDGE ? 4 : W == 8 && EDGE ? 2 : 3) conv_forward_kernel(const __grid_constant__ ConvArgs<T> a) {
+template <class T, int W, int V, int P>
+__global__ void __launch_bounds__(128, conv_forward_blocks<W>(P)) conv_forward_kernel(const __grid_constant__ ConvArgs<T> a) {
   pdl_entry();
-  using L = ConvLane<T, V, EDGE>;
+  using L = ConvLane<T, V, P>;
   constexpr int H = V / 2, U = kConvGroup<T, W>;  // tokens whose loads are in flight together
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= a.units) return;
@@ -319,7 +330,7 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 4 : W == 8 && EDGE ? 2 
   int age = conv_window<T, W>(a, lane, b, t0, hist);
   T* py = a.y + b * a.yb + (long long)t0 * a.yt;
   ConvFlags flags(a.starts ? a.starts + b * a.T_ : nullptr, t0, t1);
-  using Ring = ConvRing<T, V, U, 1, EDGE>;
+  using Ring = ConvRing<T, V, U, 1, P>;
   extern __shared__ __align__(16) unsigned char conv_shared[];
   Ring ring(lane, conv_shared + (threadIdx.x >> 5) * Ring::BYTES, {a.x + b * a.xb}, {a.xt}, group, a.D, t0, t1);
   for (int t = t0; t < t1; t += U) {
@@ -388,10 +399,10 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 4 : W == 8 && EDGE ? 2 
 // A run's tokens t0 .. t1 - 1 are its own; it goes W - 1 further for what they take from the
 // tokens after them.  pend: dx of the newest W tokens, by their number modulo W.  With very many
 // batch rows a warp takes every slots-th of them, so that there are not as many partial sums.
-template <class T, int W, int V, bool EDGE>
-__global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_kernel(const __grid_constant__ ConvArgs<T> a) {
+template <class T, int W, int V, int P>
+__global__ void __launch_bounds__(128, conv_backward_blocks<W>(P)) conv_backward_kernel(const __grid_constant__ ConvArgs<T> a) {
   pdl_entry();
-  using L = ConvLane<T, V, EDGE>;
+  using L = ConvLane<T, V, P>;
   constexpr int H = V / 2;
   const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= a.units) return;
@@ -421,9 +432,9 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_ke
     T* po = a.dx + b * a.dxb + (long long)(t0 - (W - 1)) * a.dxt;  // of the token that takes nothing more
     const int end = t1 + W - 1, stop = min(a.T_, end);  // tokens from `stop` on give nothing
     ConvFlags flags(a.starts ? a.starts + b * a.T_ : nullptr, t0, stop);
-    using Ring = ConvRing<T, V, W, 2, EDGE>;
+    using Ring = ConvRing<T, V, W, 2, P>;
     extern __shared__ __align__(16) unsigned char conv_shared[];
-    if constexpr (!EDGE) {  // the ring's last copies of the row before
+    if constexpr (!Ring::SINGLES) {  // the ring's last copies of the row before
       cp_async_wait<0>();
       __syncwarp();
     }
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(128, W == 4 && !EDGE ? 3 : 2) conv_backward_ke
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float2 v = j == W ? db[e / 2] : dw[j == W ? 0 : j][e / 2];
-          if (e < lane.count) row[lane.first + e * L::APART] = e % 2 ? v.y : v.x;
+          if (e < lane.count) row[lane.first + L::place(e)] = e % 2 ? v.y : v.x;
         }
       }
     }
@@ -692,11 +703,11 @@ template <class K, class T> cudaError_t conv_launch(K kernel, const ConvArgs<T>&
   return launch_pdl(kernel, (unsigned)((a.units + 3) / 4), 128, (size_t)smem, ctx.stream, a);
 }
 
-template <class T, int W, int V, bool EDGE> cudaError_t conv_forward(const CausalConvJob& j, const LaunchCtx& ctx) {
+template <class T, int W, int V, int P> cudaError_t conv_forward(const CausalConvJob& j, const LaunchCtx& ctx) {
   ConvArgs<T> a = conv_args<T>(j);
   a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
   // As many warps as fit an SM, and runs of 16 tokens at least: each reads taps - 1 tokens again.
-  long long runs = (W == 4 && !EDGE ? 16ll : 12ll) * ctx.num_sms / (a.groups * j.B);
+  long long runs = 4ll * conv_forward_blocks<W>(P) * ctx.num_sms / (a.groups * j.B);
   if (runs < 1) runs = 1;
   long long length = (j.T + runs - 1) / runs;
   length = length < 16 ? 16 : (length + 7) / 8 * 8;
@@ -705,22 +716,22 @@ template <class T, int W, int V, bool EDGE> cudaError_t conv_forward(const Causa
   a.units = j.B * a.runs * a.groups;
   profile_before(ctx);
   const cudaError_t e =
-      conv_launch(conv_forward_kernel<T, W, V, EDGE>, a, 4 * ConvRing<T, V, kConvGroup<T, W>, 1, EDGE>::BYTES, ctx);
+      conv_launch(conv_forward_kernel<T, W, V, P>, a, 4 * ConvRing<T, V, kConvGroup<T, W>, 1, P>::BYTES, ctx);
   profile_after(ctx);
   return e;
 }
 
-template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
+template <class T, int W, int V, int P> cudaError_t conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
   ConvArgs<T> a = conv_args<T>(j);
   a.groups = (int)((j.D + 32 * V - 1) / (32 * V));
   // What fits by registers; with more than 4 taps a warp has 64 channels.
-  const ConvSplit s = conv_backward_split(j.B, j.T, j.D, W == 4 ? EDGE ? 8 : 12 : 4);
+  const ConvSplit s = conv_backward_split(j.B, j.T, j.D, W == 4 ? 4 * conv_backward_blocks<W>(P) : 4);
   a.length = (int)s.length, a.runs = (int)s.runs, a.slots = s.slots;
   a.units = s.slots * a.runs * a.groups;
   a.part = j.dw || j.db ? (float*)j.temp : nullptr;
   profile_before(ctx);
   cudaError_t e =
-      conv_launch(conv_backward_kernel<T, W, V, EDGE>, a, 4 * ConvRing<T, V, W, 2, EDGE>::BYTES, ctx);
+      conv_launch(conv_backward_kernel<T, W, V, P>, a, 4 * ConvRing<T, V, W, 2, P>::BYTES, ctx);
   if (e == cudaSuccess && a.part) {
     ConvFoldArgs<T> f = {};
     f.part = a.part, f.dw = j.dw, f.db = j.db, f.rows = s.slots * s.runs;
@@ -731,23 +742,34 @@ template <class T, int W, int V, bool EDGE> cudaError_t conv_backward(const Caus
   return e;
 }
 
-// Rows that are copied start on 16-byte boundaries; the others are read and written V values at once.
+// Rows that are copied in pieces of 16 bytes start on such boundaries, words on theirs.
 template <class T> cudaError_t launch_causal_conv(const CausalConvJob& j, const LaunchCtx& ctx) {
   constexpr int V = 4, C = 16 / sizeof(T);
-  const bool even = j.D % C == 0 && conv_rows<T>(j.x, C, j.B, j.T) && conv_rows<T>(j.y, V, j.B, j.T) &&
-                    conv_dense<T>(j.state, V) && conv_dense<T>(j.last, V);
-  if (j.taps <= 4) return even ? conv_forward<T, 4, V, false>(j, ctx) : conv_forward<T, 4, V, true>(j, ctx);
-  return even ? conv_forward<T, 8, V, false>(j, ctx) : conv_forward<T, 8, V, true>(j, ctx);
+  const auto even = [&](int in, int out) {
+    return j.D % in == 0 && conv_rows<T>(j.x, in, j.B, j.T) && conv_rows<T>(j.y, out, j.B, j.T) &&
+           conv_dense<T>(j.state, out) && conv_dense<T>(j.last, out);
+  };
+  if (even(C, V)) return j.taps <= 4 ? conv_forward<T, 4, V, V>(j, ctx) : conv_forward<T, 8, V, V>(j, ctx);
+  if constexpr (sizeof(T) == 2) {
+    if (even(2, 2)) return j.taps <= 4 ? conv_forward<T, 4, V, 2>(j, ctx) : conv_forward<T, 8, V, 2>(j, ctx);
+  }
+  return j.taps <= 4 ? conv_forward<T, 4, V, 1>(j, ctx) : conv_forward<T, 8, V, 1>(j, ctx);
 }
 
+// (With more than 4 taps a lane has 2 channels.)
 template <class T> cudaError_t launch_causal_conv_backward(const CausalConvJob& j, const LaunchCtx& ctx) {
   constexpr int C = 16 / sizeof(T);
-  const int V = j.taps <= 4 ? 4 : 2;
-  const bool even = j.D % C == 0 && conv_rows<T>(j.x, C, j.B, j.T) && conv_rows<T>(j.dy, C, j.B, j.T) &&
-                    conv_rows<T>(j.dx, V, j.B, j.T) && conv_dense<T>(j.state, V) && conv_dense<T>(j.dlast, V) &&
-                    conv_dense<T>(j.dstate, V);
-  if (j.taps <= 4) return even ? conv_backward<T, 4, 4, false>(j, ctx) : conv_backward<T, 4, 4, true>(j, ctx);
-  return even ? conv_backward<T, 8, 2, false>(j, ctx) : conv_backward<T, 8, 2, true>(j, ctx);
+  const auto even = [&](int in, int out) {
+    return j.D % in == 0 && conv_rows<T>(j.x, in, j.B, j.T) && conv_rows<T>(j.dy, in, j.B, j.T) &&
+           conv_rows<T>(j.dx, out, j.B, j.T) && conv_dense<T>(j.state, out) && conv_dense<T>(j.dlast, out) &&
+           conv_dense<T>(j.dstate, out);
+  };
+  if (j.taps > 4) return even(C, 2) ? conv_backward<T, 8, 2, 2>(j, ctx) : conv_backward<T, 8, 2, 1>(j, ctx);
+  if (even(C, 4)) return conv_backward<T, 4, 4, 4>(j, ctx);
+  if constexpr (sizeof(T) == 2) {
+    if (even(2, 2)) return conv_backward<T, 4, 4, 2>(j, ctx);
+  }
+  return conv_backward<T, 4, 4, 1>(j, ctx);
 }
 
 template <class T, int V> cudaError_t conv_step(const CausalConvStepJob& j, const LaunchCtx& ctx) {
