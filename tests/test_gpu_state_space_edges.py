@@ -1,10 +1,12 @@
-"""GPU: calls of the state space operators at the edges of what they allow: offsets past 32 bits, two
-calls at once, a training step captured and replayed, outputs in place of inputs, one group
-with and without its dimension."""
+"""GPU: calls of the state space operators at the edges of what they allow: offsets past 32 bits,
+two calls at once, a training step captured and replayed, outputs in place of inputs, rows on
+4-byte boundaries, one group with and without its dimension."""
 import pytest
 import torch
 
 import stream_compaction_decoupled_gb300 as gb
+import test_gpu_causal_conv as conv
+import test_gpu_selective_scan as scan
 from stream_compaction_decoupled_gb300 import autograd
 
 pytestmark = pytest.mark.gpu
@@ -234,3 +236,19 @@ def test_a_gradient_of_broadcast_inputs():
     for u, v in zip(got, torch.autograd.grad(y2, full, dy)):
         v = v.double().sum(0, keepdim=True)
         assert ((u.double() - v).abs() <= 2.0 ** -20 * v.abs().max()).all()
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("size", [(2, 45, 46, 6, 1), (1, 150, 130, 18, 1), (2, 33, 60, 10, 3), (1, 700, 34, 14, 1),
+                                  (2, 20, 30, 44, 1), (1, 40, 2, 2, 1), (3, 18, 66, 16, 1)], ids=str)
+def test_scans_of_rows_on_4_byte_boundaries(size, dt):
+    scan.run(*size, scan.DT[dt], True, seed=sum(size))
+    scan.run(*size, scan.DT[dt], False, seed=sum(size), pad=2)
+
+
+@pytest.mark.parametrize("dt", list(conv.DT))
+@pytest.mark.parametrize("taps", [2, 3, 4, 6])
+@pytest.mark.parametrize("size", [(2, 70, 66), (1, 513, 130), (3, 40, 2046), (1, 30, 2)], ids=str)
+def test_convolutions_of_rows_on_4_byte_boundaries(size, taps, dt):
+    conv.run(*size, taps, conv.DT[dt], True, seed=sum(size) + taps)
+    conv.run(*size, taps, conv.DT[dt], False, seed=sum(size) + taps, pad=2)
