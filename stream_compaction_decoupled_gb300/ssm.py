@@ -179,16 +179,22 @@ def _temp(temp, need, dev):
 
 # ------------------------------------------------------------ selective scan ------
 
-def _check_vectors(m, what, lead, dtype, index):
-    """Raises what is wrong with b or c, if anything is (a single state has any stride)."""
-    if m.dim() != len(lead) + 2:
-        raise ValueError("%s must be (%s, groups, states), or without groups" % (what, "batch, length" if len(lead) == 2
-                                                                               else "batch"))
-    _rows_like(m, what, lead + m.shape[-2:], dtype, index)
+def _vectors(m, what, lead, states, dtype, index):
+    """Checks b or c, (*lead, groups, states) or (*lead, states): (groups, its strides but the last,
+    with a group's stride of 0 where it has no such dimension)."""
+    shape, strides, dims = m.shape, m.stride(), len(lead)
+    grouped = len(shape) == dims + 2
+    if not grouped and len(shape) != dims + 1:
+        raise ValueError("%s must be (%s, groups, states), or without groups" % (what, "batch, length" if dims == 2 else "batch"))
+    if m.dtype is not dtype or shape[:dims] != lead or m.get_device() != index or (strides[-1] != 1 and shape[-1] > 1):
+        _rows_like(m, what, lead + shape[dims:], dtype, index)
+    if shape[-1] != states:
+        raise ValueError("%s must have %d states, not %d" % (what, states, shape[-1]))
+    return (shape[-2], strides[:-1]) if grouped else (1, strides[:-1] + (0,))
 
 
 def _ssm(x, dt, a, b, c, d, z, dt_bias):
-    """Checks what the forms of the scan share; b and c with their groups' dimension."""
+    """Checks what the forms of the scan share: (groups, strides of b, strides of c)."""
     shape, dtype, index = x.shape, x.dtype, x.get_device()
     width = shape[-1]
     if dt.dtype is not dtype or dt.shape != shape or dt.get_device() != index or dt.stride()[-1] != 1:
@@ -201,24 +207,17 @@ def _ssm(x, dt, a, b, c, d, z, dt_bias):
     if not 1 <= states <= 128:
         raise ValueError("a must have between 1 and 128 states, not %d" % states)
     _dense(a, "a", (width, states), torch.float32, index)
-    if b.dim() == len(shape):
-        b = b.unsqueeze(-2)
-    if c.dim() == len(shape):
-        c = c.unsqueeze(-2)
-    vectors = b.shape
-    if b.dtype is not dtype or vectors[:-2] != shape[:-1] or b.get_device() != index or b.stride()[-1] != 1:
-        _check_vectors(b, "b", shape[:-1], dtype, index)
-    if c.dtype is not dtype or c.shape != vectors or c.get_device() != index or c.stride()[-1] != 1:
-        _check_vectors(c, "c", shape[:-1], dtype, index)
-    if vectors[-1] != states or c.shape != vectors:
-        raise ValueError("b and c must have %d states and the same groups" % states)
-    if vectors[-2] < 1 or width % vectors[-2]:
-        raise ValueError("%d channels do not divide into %d groups" % (width, vectors[-2]))
+    groups, sb = _vectors(b, "b", shape[:-1], states, dtype, index)
+    also, sc = _vectors(c, "c", shape[:-1], states, dtype, index)
+    if groups != also:
+        raise ValueError("b and c must have the same groups")
+    if groups < 1 or width % groups:
+        raise ValueError("%d channels do not divide into %d groups" % (width, groups))
     if d is not None:
         _dense(d, "d", (width,), torch.float32, index)
     if dt_bias is not None:
         _dense(dt_bias, "dt_bias", (width,), torch.float32, index)
-    return b, c
+    return groups, sb, sc
 
 
 @functools.lru_cache(maxsize=512)
@@ -239,7 +238,7 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts
     Returns (y, last, kept): last the state after the last token, kept (with keep=True; else
     None) what selective_scan_backward() needs: the state before every 16th token, fp32."""
     code = _first(x, "x", 3, "(batch, length, channels)")
-    b, c = _ssm(x, dt, a, b, c, d, z, dt_bias)
+    vectors = _ssm(x, dt, a, b, c, d, z, dt_bias)
     (rows, t, width), index = x.shape, x.get_device()
     if h0 is not None:
         _dense(h0, "h0", (rows, width, a.shape[1]), torch.float32, index)
@@ -248,18 +247,18 @@ def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts
     if out is not None:
         _out(out, "out", x.shape, x.dtype, index)
     _scratch(temp, index)
-    return _run(_selective_scan, x, stream, (code, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, keep, out, temp))
+    return _run(_selective_scan, x, stream, (code, vectors, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, keep, out, temp))
 
 
-def _selective_scan(s, code, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, keep, out, temp):
+def _selective_scan(s, code, vectors, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, keep, out, temp):
     (rows, t, width), dev, lib = x.shape, x.device, load()
-    _, _, groups, states = b.shape
+    (groups, sb, sc), states = vectors, a.shape[1]
     if out is None:
         out = _empty((rows, t, width), dtype=x.dtype, device=x.device)
     last = _empty((rows, width, states), dtype=torch.float32, device=x.device)
     kept = _empty((rows, -(-t // _KEPT), width, states), dtype=torch.float32, device=x.device) if keep else None
     temp, tb = _temp(temp, _scan_scratch(rows, t, width, states, groups, 0), dev)
-    sx, sd, sz, sy, sb, sc = x.stride(), dt.stride(), (0, 0) if z is None else z.stride(), out.stride(), b.stride(), c.stride()
+    sx, sd, sz, sy = x.stride(), dt.stride(), (0, 0) if z is None else z.stride(), out.stride()
     rc = lib.gb_selective_scan(
         code, rows, t, width, states, groups, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(),
         _p(d), _p(z), _p(dt_bias), 1 if softplus else 0,
@@ -277,8 +276,7 @@ def selective_scan_backward(dy, x, dt, a, b, c, kept, d=None, z=None, dt_bias=No
     ddt_bias, dh0): None for what the call had no input for, dh0 always, da, dd, ddt_bias and dh0
     fp32.  `out` gives the tensors for (dx, ddt, dz) or, without z, (dx, ddt)."""
     code = _first(x, "x", 3, "(batch, length, channels)")
-    flat, flat_c = b.dim() == 3, c.dim() == 3
-    b, c = _ssm(x, dt, a, b, c, d, z, dt_bias)
+    vectors = _ssm(x, dt, a, b, c, d, z, dt_bias)
     (rows, t, width), dtype, index = x.shape, x.dtype, x.get_device()
     _rows_like(dy, "dy", x.shape, dtype, index)
     _dense(kept, "kept", (rows, -(-t // _KEPT), width, a.shape[1]), torch.float32, index)
@@ -294,20 +292,20 @@ def selective_scan_backward(dy, x, dt, a, b, c, kept, d=None, z=None, dt_bias=No
                 _out(v, what, x.shape, dtype, index)
     _scratch(temp, index)
     return _run(_selective_scan_backward, x, stream,
-                (code, flat, flat_c, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt, dz, temp))
+                (code, vectors, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt, dz, temp))
 
 
-def _selective_scan_backward(s, code, flat, flat_c, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx,
-                             ddt, dz, temp):
+def _selective_scan_backward(s, code, vectors, dy, x, dt, a, b, c, kept, d, z, dt_bias, starts, dlast, softplus, dx, ddt,
+                             dz, temp):
     (rows, t, width), dtype, dev, lib = x.shape, x.dtype, x.device, load()
-    groups, states = b.shape[2], a.shape[1]
+    (groups, sb, sc), states = vectors, a.shape[1]
     if dx is None:
         dx = _empty((rows, t, width), dtype=x.dtype, device=x.device)
         ddt = _empty((rows, t, width), dtype=x.dtype, device=x.device)
         if z is not None:
             dz = _empty((rows, t, width), dtype=x.dtype, device=x.device)
-    db = _empty((rows, t, groups, states), dtype=x.dtype, device=x.device)
-    dc = _empty((rows, t, groups, states), dtype=x.dtype, device=x.device)
+    db = _empty(b.shape, dtype=x.dtype, device=x.device)
+    dc = _empty(c.shape, dtype=x.dtype, device=x.device)
     da = _empty((width, states), dtype=torch.float32, device=x.device)
     dd = None if d is None else _empty((width,), dtype=torch.float32, device=x.device)
     dbias = None if dt_bias is None else _empty((width,), dtype=torch.float32, device=x.device)
@@ -318,15 +316,11 @@ def _selective_scan_backward(s, code, flat, flat_c, dy, x, dt, a, b, c, kept, d,
         code, rows, t, width, states, groups, dy.data_ptr(), x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(),
         c.data_ptr(), _p(d), _p(z), _p(dt_bias), 1 if softplus else 0,
         _pack[26](*dy.stride()[:2], *x.stride()[:2], *dt.stride()[:2], *sz, *dx.stride()[:2], *ddt.stride()[:2], *sdz,
-                  *b.stride()[:3], *c.stride()[:3], *db.stride()[:3], *dc.stride()[:3]),
+                  *sb, *sc, t * groups * states, groups * states, states, t * groups * states, groups * states, states),
         kept.data_ptr(), _p(starts), _p(dlast), dx.data_ptr(), ddt.data_ptr(), da.data_ptr(), db.data_ptr(),
         dc.data_ptr(), _p(dd), _p(dz), _p(dbias), dh0.data_ptr(), _p(temp), tb, s)
     if rc:
         _check(rc, "gb_selective_scan_backward")
-    if flat:
-        db = db.squeeze(2)
-    if flat_c:
-        dc = dc.squeeze(2)
     return SelectiveScanGrads(dx, ddt, da, db, dc, dd, dz, dbias, dh0)
 
 
@@ -336,7 +330,7 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slo
     (pool, channels, states)), which is updated in place.  b, c (batch, groups, states) or (batch,
     states); slots as in recurrence_step().  Returns y."""
     code = _first(x, "x", 2, "(batch, channels)")
-    b, c = _ssm(x, dt, a, b, c, d, z, dt_bias)
+    vectors = _ssm(x, dt, a, b, c, d, z, dt_bias)
     (rows, width), index = x.shape, x.get_device()
     if state.dim() != 3:
         raise ValueError("state must be (pool, channels, states)")
@@ -344,16 +338,16 @@ def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, slo
     _slots(slots, rows, state, index)
     if out is not None:
         _out(out, "out", x.shape, x.dtype, index)
-    return _run(_selective_scan_step, x, stream, (code, x, dt, a, b, c, state, d, z, dt_bias, slots, softplus, out))
+    return _run(_selective_scan_step, x, stream, (code, vectors, x, dt, a, b, c, state, d, z, dt_bias, slots, softplus, out))
 
 
-def _selective_scan_step(s, code, x, dt, a, b, c, state, d, z, dt_bias, slots, softplus, out):
+def _selective_scan_step(s, code, vectors, x, dt, a, b, c, state, d, z, dt_bias, slots, softplus, out):
     rows, width = x.shape
     if out is None:
         out = _empty((rows, width), dtype=x.dtype, device=x.device)
-    sb, sc = b.stride(), c.stride()
+    groups, sb, sc = vectors
     rc = load().gb_selective_scan_step(
-        code, rows, width, a.shape[1], b.shape[1], x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(),
+        code, rows, width, a.shape[1], groups, x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(),
         _p(d), _p(z), _p(dt_bias), 1 if softplus else 0,
         _pack[8](x.stride()[0], dt.stride()[0], 0 if z is None else z.stride()[0], out.stride()[0], sb[0], sb[1], sc[0], sc[1]),
         state.data_ptr(), state.shape[0], _p(slots), out.data_ptr(), s)
