@@ -17,8 +17,8 @@
 // the one within whose slice the draw falls reads that warp's slice again: its warps an eighth each,
 // and one warp the eighth.
 //
-// Measured (GB300): 128 requests, 4 drafts of 128000 fp32 26.9 us (0.72 of the copy rate); 4 requests of
-// 50021 16.5 us, cold, the latency of the three passes.
+// Measured (GB300): 128 requests, 4 drafts of 128000 fp32 27.1 us (0.71 of the copy rate); 4 requests of
+// 50021 15.5 us, cold, the latency of the three passes.
 #pragma once
 
 #include "lm.cuh"
