@@ -4,6 +4,8 @@ two calls at once, a training step captured and replayed, outputs in place of in
 import pytest
 import torch
 
+import lm_reference as lm
+import ssm_reference as ref
 import stream_compaction_decoupled_gb300 as gb
 import test_gpu_causal_conv as conv
 import test_gpu_selective_scan as scan
@@ -252,3 +254,68 @@ def test_scans_of_rows_on_4_byte_boundaries(size, dt):
 def test_convolutions_of_rows_on_4_byte_boundaries(size, taps, dt):
     conv.run(*size, taps, conv.DT[dt], True, seed=sum(size) + taps)
     conv.run(*size, taps, conv.DT[dt], False, seed=sum(size) + taps, pad=2)
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("n", [13, 16, 40])
+@pytest.mark.parametrize("d", [2050, 4097])
+def test_single_tokens_of_many_rows(d, n, dt):
+    """More rows and channels than fill the device: four rows a thread, the last of them alone; with a
+    row of padding and a slot past the pool among them."""
+    rows = 21
+    q, _, _, _ = scan.inputs(rows, 1, d, n, 2 if d % 2 == 0 else 1, scan.DT[dt], True, d + n, pad=2)
+    one = {k: v[:, 0] if k in ("x", "dt", "b", "c", "z") else v for k, v in q.items()}
+    g = torch.Generator().manual_seed(n)
+    pool = scan.rand(g, (30, d, n))
+    before = pool.clone()
+    slots = torch.randperm(30, generator=g)[:rows].int().cuda()
+    slots[6], slots[17] = -1, 30
+    y = gb.selective_scan_step(state=pool, slots=slots, **one)
+    assert gb.device_error() == gb.ERR_RANGE and gb.device_error() == gb.OK
+    assert not y[6].any() and not y[17].any()
+    live = [r for r in range(rows) if r not in (6, 17)]
+    at = slots[live].long()
+    part = {k: v[live] if k in ("x", "dt", "b", "c", "z") else v for k, v in q.items()}
+    want, last, bound, blast = ref.scan(**part, h0=before[at], starts=None)
+    lm.check(y[live].unsqueeze(1), want, bound, "y")
+    lm.check(pool[at], last, blast, "state")
+    rest = [s for s in range(30) if s not in at.tolist()]
+    assert torch.equal(pool[rest], before[rest])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("offset", [0, 1, 2])
+def test_taps_of_fp32_and_at_odd_places(offset, dt):
+    """The single-token convolution's four taps: fp32 beside 16-bit inputs, and not where one access
+    could read them."""
+    b, d = 6, 264
+    for pd in {scan.DT[dt], torch.float32}:
+        g = torch.Generator().manual_seed(offset)
+        x, bias = conv.rand(g, (b, d), scan.DT[dt]), conv.rand(g, (d,), pd)
+        w = conv.rand(g, (d * 4 + 8,), pd, 0.5)[offset:offset + d * 4].view(d, 4)
+        pool = conv.rand(g, (b, 3, d), scan.DT[dt])
+        before = pool.clone()
+        y = gb.causal_conv_step(x, pool, w, bias)
+        want, last, bound, _ = ref.conv(x.unsqueeze(1), w, bias, before, None)
+        lm.check(y.unsqueeze(1), want, bound, "y")
+        assert torch.equal(lm.wide(pool), last)
+        y, last = gb.causal_conv(x.unsqueeze(1), w, bias, state=before)
+        lm.check(y, want, bound, "y")
+        assert torch.equal(last, pool)
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("size", [(28, 20, 1024, 16), (28, 20, 1022, 14), (28, 20, 1023, 13), (4, 260, 2046, 6),
+                                  (4, 260, 2047, 7)], ids=str)
+def test_scans_that_fill_the_device(size, dt):
+    """Enough rows and channels that two lanes share a pair of them: one part, or several."""
+    b, t, d, n = size
+    q, more, _, _ = scan.inputs(b, t, d, n, 1, scan.DT[dt], True, sum(size))
+    scan.check_forward(q, more, gb.selective_scan(**q, **more))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [(28, 20, 512, 16), (28, 20, 510, 14), (28, 20, 511, 13), (20, 40, 448, 8),
+                                  (13, 20, 510, 18)], ids=str)
+def test_gradients_that_fill_the_device(size, dt):
+    scan.run(*size, 1, scan.DT[dt], True, seed=sum(size))
