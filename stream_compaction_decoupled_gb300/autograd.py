@@ -114,9 +114,10 @@ class _CausalConv(torch.autograd.Function):
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus):
+    def forward(ctx, x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, grads):
+        # needs_input_grad says what requires a gradient, with gradients switched off too.
         y, last, kept = ssm.selective_scan(x, dt, a, b, c, d, z, dt_bias, h0=h0, starts=starts, softplus=softplus,
-                                           keep=any(ctx.needs_input_grad))
+                                           keep=grads and any(ctx.needs_input_grad))
         ctx.save_for_backward(x, dt, a, b, c, d, z, dt_bias, h0, starts, kept)
         ctx.softplus = softplus
         ctx.set_materialize_grads(False)
@@ -127,12 +128,12 @@ class _SelectiveScan(torch.autograd.Function):
     def backward(ctx, dy, dlast):
         x, dt, a, b, c, d, z, dt_bias, h0, starts, kept = ctx.saved_tensors
         if dy is None and dlast is None:
-            return (None,) * 11
+            return (None,) * 12
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else _unit(dy)
         dlast = None if dlast is None else dlast.contiguous()
         g = ssm.selective_scan_backward(dy, x, dt, a, b, c, kept, d, z, dt_bias, starts=starts, dlast=dlast,
                                         softplus=ctx.softplus)
-        return g.dx, g.ddt, g.da, g.db, g.dc, g.dd, g.dz, g.ddt_bias, g.dh0 if h0 is not None else None, None, None
+        return g.dx, g.ddt, g.da, g.db, g.dc, g.dd, g.dz, g.ddt_bias, g.dh0 if h0 is not None else None, None, None, None
 
 
 def recurrence(x, f, i=None, h0=None, starts=None):
@@ -157,4 +158,4 @@ def causal_conv(x, weight, bias=None, state=None, starts=None, silu: bool = True
 
 def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, starts=None, softplus: bool = True):
     """ssm.selective_scan(): (y, last), differentiable in x, dt, a, b, c, d, z, dt_bias and h0."""
-    return _SelectiveScan.apply(x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus)
+    return _SelectiveScan.apply(x, dt, a, b, c, d, z, dt_bias, h0, starts, softplus, torch.is_grad_enabled())

@@ -145,3 +145,24 @@ def test_valid_calls_without_gpu_fail_loudly(lib):
         gb.selective_scan(x, x, torch.zeros(8, 16), torch.zeros(1, 2, 16), torch.zeros(1, 2, 16))
     with pytest.raises(ValueError):
         gb.verify_drafts(torch.zeros((1, 2), dtype=torch.int64), torch.zeros(1, 3, 5), None, torch.zeros(1, 2), torch.zeros(1))
+
+
+@pytest.mark.parametrize("mode,keep", [("enable_grad", True), ("no_grad", False), ("inference_mode", False)])
+def test_states_are_kept_only_for_a_gradient(monkeypatch, mode, keep):
+    """Parameters require gradients while a model generates, too: without a graph nothing is kept."""
+    torch = pytest.importorskip("torch")
+    from stream_compaction_decoupled_gb300 import autograd, ssm
+
+    asked = []
+
+    def scan(x, *args, keep, **kw):
+        asked.append(keep)
+        return x.clone(), x.new_zeros(1), x.new_zeros(1) if keep else None
+
+    monkeypatch.setattr(ssm, "selective_scan", scan)
+    x, a = torch.zeros(1, 4, 2), torch.zeros(2, 3, requires_grad=True)
+    bc = torch.zeros(1, 4, 3)
+    with getattr(torch, mode)():
+        autograd.selective_scan(x, x, a, bc, bc)
+        autograd.selective_scan(x, x, a.detach(), bc, bc)
+    assert asked == [keep, False]
