@@ -1,0 +1,48 @@
+"""GPU: infinities in the selective scan and its gradient.  What is infinite by the definition stays
+an infinity of its sign, in every number of states, channels and tokens; what does not depend on
+one keeps its value."""
+import math
+
+import pytest
+import torch
+
+import lm_reference as lm
+import ssm_reference as ref
+import stream_compaction_decoupled_gb300 as gb
+import test_gpu_selective_scan as scan
+
+pytestmark = pytest.mark.gpu
+
+INF = math.inf
+
+
+def inputs(t, d, n, dtype, seed, rates=1.0):
+    """Everything positive but the rates, so that no infinity of y or a state meets one of the other
+    sign; step sizes of 0.1 to 1."""
+    g = torch.Generator().manual_seed(seed)
+
+    def some(shape, dtype, lo, hi):
+        return (torch.rand(shape, generator=g) * (hi - lo) + lo).to(dtype).cuda()
+
+    q = {"x": some((1, t, d), dtype, 0.25, 1.5), "dt": some((1, t, d), dtype, -2.0, 0.5),
+         "a": -some((d, n), torch.float32, 0.1 * rates, rates), "b": some((1, t, 1, n), dtype, 0.25, 1.5),
+         "c": some((1, t, 1, n), dtype, 0.25, 1.5), "d": some((d,), torch.float32, 0.25, 1.5),
+         "z": some((1, t, d), dtype, 0.25, 1.5), "dt_bias": some((d,), torch.float32, -0.2, 0.0)}
+    more = {"h0": some((1, d, n), torch.float32, 0.25, 1.5), "starts": None}
+    return q, more, some((1, t, d), dtype, 0.25, 1.5), some((1, d, n), torch.float32, 0.25, 1.5)
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("n", [1, 6, 8, 13, 16, 18, 40])
+@pytest.mark.parametrize("t", [21, 24, 300])
+@pytest.mark.parametrize("where", ["x", "dt"])
+def test_states_past_the_last_stay_zero(where, t, n, dt):
+    """An infinite input or step size in some channels: their y and last are infinite from there on."""
+    q, more, _, _ = inputs(t, 24, n, scan.DT[dt], t + n)
+    q[where][0, 5, ::2] = INF
+    y, last, _ = gb.selective_scan(**q, **more)
+    assert (y[0, 5:, ::2] == INF).all() and (last[0, ::2] == INF).all()
+    want, wlast, bound, blast = ref.scan(**q, **more)
+    bound, blast = bound.nan_to_num(0.0), blast.nan_to_num(0.0)  # (of infinities)
+    lm.check(y, want, bound, "y")
+    lm.check(last, wlast, blast, "last")
