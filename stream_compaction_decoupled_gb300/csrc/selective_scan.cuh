@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && L
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 u = mul2(d[r], pair(0, r));
-      if (!whole && t + ln + r * LN >= a.T_) d[r] = u = zero;  // no token: the state stays
+      if (!whole && t + ln + r * LN >= a.T_) d[r] = u = zero;  // no token
       ds[(ln + r * LN) * (32 / LN) + lane / LN] = make_float4(d[r].x, d[r].y, u.x, u.y);
       if constexpr (ENDS) sum = add2(sum, d[r]);
       if constexpr (!ONE) y[r] = zero;
@@ -548,35 +548,38 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && L
           const float2 d2[2] = {make_float2(du.x, du.x), make_float2(du.y, du.y)};
           const float2 u2[2] = {make_float2(du.z, du.z), make_float2(du.w, du.w)};
           float2 acc[2] = {zero, zero};
-#pragma unroll
-          for (int j = 0; j < M / 4; ++j) {
-            const float4 bv = pbv[j];
-            const float2 b2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
-            float2 c2[2];
-            if constexpr (!ENDS && !ANY) {
-              const float4 cv = pbv[4 + j];
-              c2[0] = make_float2(cv.x, cv.y), c2[1] = make_float2(cv.z, cv.w);
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                float2& hh = h[c][2 * j + m];
-                hh = ssc_fma(ssc_decay(rate[c][2 * j + m], d2[c]), hh, mul2(u2[c], b2[m]));
-                if constexpr (!ENDS && !ANY) acc[c] = ssc_fma(hh, c2[m], acc[c]);
-              }
-            }
-          }
-          if constexpr (!ENDS && ANY) {
-            if (PADDED && wild) clear_past(k);
+          // Tokens behind the last are left out, since 0 times a rate or a b may be a NaN.
+          if (!ANY || t + i < a.T_) {
 #pragma unroll
             for (int j = 0; j < M / 4; ++j) {
-              const float4 cv = pbv[4 + j];
-              const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
+              const float4 bv = pbv[j];
+              const float2 b2[2] = {make_float2(bv.x, bv.y), make_float2(bv.z, bv.w)};
+              float2 c2[2];
+              if constexpr (!ENDS && !ANY) {
+                const float4 cv = pbv[4 + j];
+                c2[0] = make_float2(cv.x, cv.y), c2[1] = make_float2(cv.z, cv.w);
+              }
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m) acc[c] = ssc_fma(h[c][2 * j + m], c2[m], acc[c]);
+                for (int m = 0; m < 2; ++m) {
+                  float2& hh = h[c][2 * j + m];
+                  hh = ssc_fma(ssc_decay(rate[c][2 * j + m], d2[c]), hh, mul2(u2[c], b2[m]));
+                  if constexpr (!ENDS && !ANY) acc[c] = ssc_fma(hh, c2[m], acc[c]);
+                }
+              }
+            }
+            if constexpr (!ENDS && ANY) {
+              if (PADDED && wild) clear_past(k);
+#pragma unroll
+              for (int j = 0; j < M / 4; ++j) {
+                const float4 cv = pbv[4 + j];
+                const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                  for (int m = 0; m < 2; ++m) acc[c] = ssc_fma(h[c][2 * j + m], c2[m], acc[c]);
+              }
             }
           }
           if constexpr (!ENDS) {
@@ -601,9 +604,9 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && L
           }
         }
       };
-      constexpr int any = ENDS ? kSscStarts : kSscAny;
-      if (PADDED && wild) tokens(SscKind<any>(), std::false_type());
-      else if (starts || !whole) tokens(SscKind<kSscStarts>(), std::false_type());
+      constexpr int any = ENDS ? kSscStarts : kSscAny;  // (ENDS leaves out the last part)
+      if (!whole || (PADDED && wild)) tokens(SscKind<any>(), std::false_type());
+      else if (starts) tokens(SscKind<kSscStarts>(), std::false_type());
       else if (gated) tokens(SscKind<kSscPlain>(), std::true_type());
       else tokens(SscKind<kSscPlain>(), std::false_type());
       if constexpr (!ONE) put_h(k);

@@ -46,3 +46,28 @@ def test_states_past_the_last_stay_zero(where, t, n, dt):
     bound, blast = bound.nan_to_num(0.0), blast.nan_to_num(0.0)  # (of infinities)
     lm.check(y, want, bound, "y")
     lm.check(last, wlast, blast, "last")
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("size", [(1, 24, 16), (7, 24, 16), (21, 24, 16), (21, 5, 13), (24, 24, 16), (300, 33, 40)], ids=str)
+def test_tokens_behind_the_end_leave_states_of_infinite_rates(size, dt):
+    """A rate of -infinity: its state keeps nothing from token to token, wherever the row ends."""
+    t, d, n = size
+    q, more, _, _ = inputs(t, d, n, scan.DT[dt], sum(size))
+    q["a"][::3, 1] = -INF
+    same = q["a"].clone()
+    same[::3, 1] = -1e30
+    got = gb.selective_scan(**q, **more)
+    want, wlast, bound, blast = ref.scan(**{**q, "a": same}, **more)
+    lm.check(got[0], want, bound, "y")
+    lm.check(got[1], wlast, blast, "last")
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("where", ["b", "x"])
+@pytest.mark.parametrize("t", [1, 7, 21])
+def test_an_infinite_last_token_with_others_behind_it(t, where, dt):
+    q, more, _, _ = inputs(t, 24, 16, scan.DT[dt], t)
+    q[where][0, t - 1] = INF
+    y, last, _ = gb.selective_scan(**q, **more)
+    assert (last == INF).all() and (y[0, t - 1] == INF).all() and torch.isfinite(y[0, :t - 1]).all()
