@@ -121,6 +121,13 @@ __device__ __forceinline__ float2 ssc_decay(float2 a, float2 d) {
   return make_float2(ex2(fmaf(a.x, d.x, kSscCentre)), ex2(fmaf(a.y, d.y, kSscCentre)));
 }
 __device__ __forceinline__ float2 ssc_fma(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+// A state (or what is passed back) through a part: e is what the part makes of zero.  The part's decay, a
+// product of small ones, does not go below fp32's least number: 0 times an infinite state would be a
+// NaN, which no token's decay makes of it.
+__device__ __forceinline__ float2 ssc_through(float2 rate, float sum, float2 h, float2 e) {
+  const float2 decay = ssc_decay(rate, make_float2(sum, sum));
+  return fma2(make_float2(max_nan(decay.x, 0x1p-149f), max_nan(decay.y, 0x1p-149f)), h, e);
+}
 // D and e go into fp32 results (states, dA, dd, dbias) whatever the inputs' type, so that their
 // functions are the fp32 ones; what only 16-bit outputs see (y, dz) is as exact as their type.
 template <class T> __device__ __forceinline__ float2 ssc_step_size(const SscArgs<T>& a, float2 v) {
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && L
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < M / 2; ++j)
-            h[c][j] = dropped ? e[c][j] : fma2(ssc_decay(rate[c][j], make_float2(sum[c], sum[c])), h[c][j], e[c][j]);
+            h[c][j] = dropped ? e[c][j] : ssc_through(rate[c][j], sum[c], h[c][j], e[c][j]);
       }
       if constexpr (PADDED) clear_past(k);
     }
@@ -767,7 +774,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            g[c][j] = dropped ? e[c][j] : fma2(ssc_decay(rate[c][j], make_float2(sum[c], sum[c])), g[c][j], e[c][j]);
+            g[c][j] = dropped ? e[c][j] : ssc_through(rate[c][j], sum[c], g[c][j], e[c][j]);
       }
     }
     if constexpr (!ONE) {

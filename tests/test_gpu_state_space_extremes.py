@@ -32,6 +32,17 @@ def inputs(t, d, n, dtype, seed, rates=1.0):
     return q, more, some((1, t, d), dtype, 0.25, 1.5), some((1, d, n), torch.float32, 0.25, 1.5)
 
 
+def check_gradient(q, more, dy, dlast, same=None, skip=()):
+    """All gradients but `skip` against the definition's, of `same` in place of a."""
+    kept = gb.selective_scan(**q, **more, keep=True)[2]
+    got = gb.selective_scan_backward(dy, **q, kept=kept, dlast=dlast)
+    wants, bounds = ref.scan_grad(dy, **{**q, "a": q["a"] if same is None else same}, **more, dlast=dlast)
+    for name, v, w, e in zip(scan.NAMES, got, wants, bounds):
+        if name not in skip:
+            lm.check(v, w, e, name)
+    return got, wants, bounds
+
+
 @pytest.mark.parametrize("dt", list(scan.DT))
 @pytest.mark.parametrize("n", [1, 6, 8, 13, 16, 18, 40])
 @pytest.mark.parametrize("t", [21, 24, 300])
@@ -71,3 +82,23 @@ def test_an_infinite_last_token_with_others_behind_it(t, where, dt):
     q[where][0, t - 1] = INF
     y, last, _ = gb.selective_scan(**q, **more)
     assert (last == INF).all() and (y[0, t - 1] == INF).all() and torch.isfinite(y[0, :t - 1]).all()
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+def test_an_infinite_state_goes_through_parts(dt):
+    """Rates that bring a part's decay below fp32's range, but no token's: an infinity lasts."""
+    q, more, dy, dlast = inputs(600, 24, 16, scan.DT[dt], 3, rates=40.0)
+    q["x"][0, 5, ::2] = INF
+    y, last, _ = gb.selective_scan(**q, **more)
+    want, wlast, bound, blast = ref.scan(**q, **more)
+    assert (y[0, 5:, ::2] == INF).all() and (last[0, ::2] == INF).all()
+    lm.check(y, want, bound, "y")
+    lm.check(last, wlast, blast, "last")
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+def test_an_infinite_gradient_goes_through_parts(dt):
+    q, more, dy, dlast = inputs(600, 24, 16, scan.DT[dt], 3, rates=40.0)
+    dy[0, -5, ::2] = INF
+    got, _, _ = check_gradient(q, more, dy, dlast)
+    assert (got.dx[0, :-4, ::2] == INF).all() and (got.dh0[0, ::2] == INF).all()
