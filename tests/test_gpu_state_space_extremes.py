@@ -102,3 +102,17 @@ def test_an_infinite_gradient_goes_through_parts(dt):
     dy[0, -5, ::2] = INF
     got, _, _ = check_gradient(q, more, dy, dlast)
     assert (got.dx[0, :-4, ::2] == INF).all() and (got.dh0[0, ::2] == INF).all()
+
+
+SIZES = [(32, 64, 6), (32, 64, 13), (304, 64, 40), (304, 64, 8)]
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("at", [5, -1])
+@pytest.mark.parametrize("where", ["x", "dy"])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_gradient_with_states_past_the_last(size, where, at, dt):
+    t, d, n = size
+    q, more, dy, dlast = inputs(t, d, n, scan.DT[dt], sum(size))
+    (dy if where == "dy" else q["x"])[0, at, ::4] = INF
+    check_gradient(q, more, dy, dlast)
