@@ -960,6 +960,9 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
     cp_async_wait<0>();
     __syncwarp();
     const unsigned char* raw = ring + stage * S::STAGE;
+    // Tokens behind the last are left out, since 0 times a rate, a b or a c may be a NaN.  (No token before
+    // them needs their states.)
+    const int left = a.T_ - t0;
     const bool whole = t0 + L <= a.T_;
     const auto pair = [&](int array, int t) { return P::wide(((const Raw*)(raw + array * S::ARRAY + t * S::ROW))[pr]); };
     // A
@@ -1018,9 +1021,10 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
       if (a.softplus) dd = mul2(dd, sigmoid<float>(add2(pair(1, t), bias)));
       P::store(a.dx + b * a.dxb + u * a.dxt + ch, n, fma2(skip, e, mul2(make_float2(q.x, q.y), along)));
       P::store(a.ddt + b * a.ddtb + u * a.ddtt + ch, n, dd);
-      if (!whole && n <= 0) dd = zero;  // (e is 0 there)
-      dskip_few = fma2(e, x, dskip_few);
-      dbias_few = add2(dbias_few, dd);
+      if (t < left) {
+        dskip_few = fma2(e, x, dskip_few);
+        dbias_few = add2(dbias_few, dd);
+      }
       if (gated) {
         const float2 z = pair(3, t), s = sigmoid<T>(z);
         const float2 slope = fma2(mul2(z, s), fma2(s, make_float2(-1.f, -1.f), make_float2(1.f, 1.f)), s);
@@ -1040,6 +1044,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
           constexpr bool STARTS = decltype(kind)::value != kSscPlain;
 #pragma unroll
           for (int t = L - 1; t >= 0; --t) {
+            if (decltype(kind)::value == kSscAny && t >= left) continue;
             const float4 q = du[t * 8 + pr], cv = *(const float4*)(vk + t * 32 + 16);
             const float2 e = es[t * 8 + pr];
             const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
@@ -1053,7 +1058,8 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
               }
           }
         };
-        if (starts) tokens(SscKind<kSscStarts>());
+        if (!whole) tokens(SscKind<kSscAny>());
+        else if (starts) tokens(SscKind<kSscStarts>());
         else tokens(SscKind<kSscPlain>());
       } else {
         float2 h[2][2];
@@ -1124,6 +1130,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
 #pragma unroll
             for (int i = 3; i >= 0; --i) {
               const int t = 4 * r + i;
+              if (ANY && t >= left) continue;  // what would be its sums is not used
               const float4 cv = *(const float4*)(vk + t * 32 + 16);
               const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)}, e = es[t * 8 + pr];
               const bool start = STARTS && (starts >> t & 1);
@@ -1192,7 +1199,7 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
             __syncwarp();
           }
         };
-        if (wild) tokens(SscKind<kSscAny>());
+        if (!whole || wild) tokens(SscKind<kSscAny>());
         else if (starts) tokens(SscKind<kSscStarts>());
         else tokens(SscKind<kSscPlain>());
         // Sums over the part's tokens go over four tiles, then over as many as there are: a chain of all

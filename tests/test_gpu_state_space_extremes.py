@@ -116,3 +116,21 @@ def test_gradient_with_states_past_the_last(size, where, at, dt):
     q, more, dy, dlast = inputs(t, d, n, scan.DT[dt], sum(size))
     (dy if where == "dy" else q["x"])[0, at, ::4] = INF
     check_gradient(q, more, dy, dlast)
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("where", ["a", "b", "c", "x", "dy"])
+@pytest.mark.parametrize("t", [1, 15, 21, 300])
+def test_gradient_with_tokens_behind_the_end(t, where, dt):
+    q, more, dy, dlast = inputs(t, 64, 16, scan.DT[dt], t)
+    if where != "a":
+        (dy if where == "dy" else q[where])[0, -1] = INF
+        check_gradient(q, more, dy, dlast)
+        return
+    q["a"][::3, 1] = -INF
+    same = q["a"].clone()
+    same[::3, 1] = -1e30
+    # (the step size's gradient has the product of that rate and a decay of 0)
+    got, wants, bounds = check_gradient(q, more, dy, dlast, same, skip=("ddt", "ddt_bias"))
+    lm.check(got.ddt[..., 1::3].contiguous(), wants[1][..., 1::3], bounds[1][..., 1::3], "ddt")
+    lm.check(got.ddt_bias[1::3].contiguous(), wants[7][1::3], bounds[7][1::3], "ddt_bias")
