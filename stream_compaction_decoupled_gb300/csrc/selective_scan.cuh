@@ -743,16 +743,16 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
 #pragma unroll
       for (int j = 0; j < 2; ++j) rate[c][j] = mul2(rate[c][j], make_float2(kLog2e, kLog2e));
   };
-  // States past the last: 0 times an infinity is a NaN, which the sums over states would take.  Where an
-  // input is not finite, what belongs to them is put back to 0.
-  const bool padded = a.N != a.NP;
+  // States and channels past the last: 0 times an infinity is a NaN, which the sums over states and over
+  // channels would take.  Where an input is not finite, what belongs to them is put back to 0.
+  const bool padded = a.N != a.NP, special = padded || (group + 1) * a.DG - first < kSscChannels;
   const auto clear_past = [&](int k, float2 (&v)[2][2]) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int s = k * 16 + ln * M + 2 * j;
-        v[c][j] = make_float2(s < a.N ? v[c][j].x : 0.f, s + 1 < a.N ? v[c][j].y : 0.f);
+        v[c][j] = make_float2(c < count && s < a.N ? v[c][j].x : 0.f, c < count && s + 1 < a.N ? v[c][j].y : 0.f);
       }
   };
   const auto put = [&](int at, const float2 (&v)[2][2]) {
@@ -966,17 +966,21 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
     const bool whole = t0 + L <= a.T_;
     const auto pair = [&](int array, int t) { return P::wide(((const Raw*)(raw + array * S::ARRAY + t * S::ROW))[pr]); };
     // A
-    float size = 0.f;  // not finite where a D x or an e is not
+    float size = 0.f;  // not finite where an input is not
     if constexpr (!ONE) {
       for (int k = threadIdx.x; k < NB * L * 32; k += kSscThreads) {
         const int n = k % 16, second = k / 16 % 2, i = k / 32 % L, n0 = k / (32 * L) * 16 + n;
         const long long u = min(t0 + i, a.T_ - 1);
-        vs[k] = n0 < a.N ? widen(second ? pc[u * a.ct + n0] : pb[u * a.bt + n0]) : 0.f;
+        const float v = n0 < a.N ? widen(second ? pc[u * a.ct + n0] : pb[u * a.bt + n0]) : 0.f;
+        vs[k] = v;
+        if (!CARRY) size += fabsf(v);
       }
     } else {
       const int c = threadIdx.x * 4;
       const T* from = (const T*)(vring + stage * S::VECTORS) + (warp * 4 * 32 + lane * 4);
-      *(float4*)(vs + c) = make_float4(widen(from[0]), widen(from[1]), widen(from[2]), widen(from[3]));
+      const float4 v = make_float4(widen(from[0]), widen(from[1]), widen(from[2]), widen(from[3]));
+      *(float4*)(vs + c) = v;
+      if (!CARRY && special) size = (fabsf(v.x) + fabsf(v.y)) + (fabsf(v.z) + fabsf(v.w));
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -987,14 +991,14 @@ __global__ void __launch_bounds__(kSscThreads, 2) ssc_backward_kernel(const __gr
         e = mul2(e, mul2(z, sigmoid<float>(z)));
       }
       float2 u = CARRY ? zero : mul2(d, pair(0, t));
-      if (!CARRY && padded) size += (fabsf(u.x) + fabsf(u.y)) + (fabsf(e.x) + fabsf(e.y));
+      if (!CARRY && special) size += (fabsf(u.x) + fabsf(u.y)) + (fabsf(e.x) + fabsf(e.y));
       if (!whole && t0 + t >= a.T_) d = e = u = zero;
       du[t * 8 + pr] = make_float4(d.x, d.y, u.x, u.y);
       es[t * 8 + pr] = e;
       if constexpr (CARRY) sum_d = add2(sum_d, d);
     }
     bool wild = false;
-    if (!CARRY && padded) {
+    if (!CARRY && special) {
       wild = __syncthreads_or(!(size < __int_as_float(0x7f800000)));
     } else {
       __syncthreads();

@@ -134,3 +134,14 @@ def test_gradient_with_tokens_behind_the_end(t, where, dt):
     got, wants, bounds = check_gradient(q, more, dy, dlast, same, skip=("ddt", "ddt_bias"))
     lm.check(got.ddt[..., 1::3].contiguous(), wants[1][..., 1::3], bounds[1][..., 1::3], "ddt")
     lm.check(got.ddt_bias[1::3].contiguous(), wants[7][1::3], bounds[7][1::3], "ddt_bias")
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("at", [5, -1])
+@pytest.mark.parametrize("where", ["b", "c"])
+@pytest.mark.parametrize("size", [(32, 24, 16), (32, 5, 16), (32, 33, 13), (21, 1, 32), (300, 70, 16), (32, 20, 40)], ids=str)
+def test_gradient_with_channels_past_the_last(size, where, at, dt):
+    t, d, n = size
+    q, more, dy, dlast = inputs(t, d, n, scan.DT[dt], sum(size))
+    q[where][0, at] = INF
+    check_gradient(q, more, dy, dlast)
