@@ -160,67 +160,102 @@ constexpr int kSscMaxStates = 128;
 struct SscSplit {
   long long parts, tiles;
 };
-// At most so many parts: a part goes through all before it first, so that many make it longer than
-// they make the tokens of one shorter (forward, 1 x 32768 x 128 bf16: 64 parts 113 us, 128 102, 256
-// 129; the bound is 128).
-// Rows below 8 tiles are not worth a second launch.
-inline long long ssc_most_parts(long long tiles) {
-  const long long root = (long long)sqrt(8.0 * (double)tiles);
-  return tiles < 8 ? 1 : root < tiles / 2 ? root : tiles / 2;
+constexpr long long kSscSms = 152;  // GB300's: the scratch is sized without asking a device
+// Shared memory of a block of 4 warps, states in NB blocks of 16, values of es bytes.
+constexpr size_t ssc_forward_bytes(int es, int lanes, int NB) {
+  return 4 * (size_t)((es == 2 ? 3 : 2) * (3 * 8 * (64 / lanes) * es + NB * 8 * 32 * es) + NB * 8 * 32 * 4 + 8 * (32 / lanes) * 16 +
+                      (NB > 1 ? NB * 16 / lanes * 256 : 0));
 }
-inline SscSplit ssc_parts(long long tiles, long long parts) {
-  const long long most = ssc_most_parts(tiles);
-  if (parts > most) parts = most;
-  if (parts < 1) parts = 1;
-  const long long each = (tiles + parts - 1) / parts;
-  return {tiles ? (tiles + each - 1) / each : 1, each};
+constexpr size_t ssc_backward_bytes(int es, int NB) {
+  return 4 * (size_t)(2 * (4 * 16 * 16 * es + 1024) + 2048 + 1024 + 3072 + 3072 + 2048 + (NB > 1 ? NB * 2048 : 0)) +
+         2 * 16 * 32 * es + NB * 2048;
 }
-// The gradient: a block takes 64 channels, two blocks fit an SM.  Where the rows and channels give
-// enough blocks, a row is one chain (8 x 2048 x 2048 bf16, 256 blocks: 819 us, in 4 parts 898); some
-// are split four times over the device, since what is left at the end is then short (128 blocks: 608
-// us, in 2 parts 511, in 9 462), few until it is full (1 x 8192 x 2048, 32 blocks: in 9 parts 472 us, in
-// 14 501).
-inline SscSplit ssc_backward_split(long long B, long long T, long long D, long long G) {
+// Blocks an SM holds: by registers `bound`, by shared memory what goes into 228 KB (with 1 KB a block of
+// the system's).
+constexpr int ssc_resident(size_t bytes, int bound) {
+  return 228 * 1024 / (bytes + 1024) < (size_t)bound ? (int)(228 * 1024 / (bytes + 1024)) : bound;
+}
+// What a split costs, in the time that a tile takes a block alone on its SM.  k blocks of an SM take
+// 1 + share (k - 1) a tile, and each block `start` tiles' time to begin; the first pass, over all parts but
+// the last, takes `again` of that; each part goes through all before it first, `part` for each of them;
+// `launch` is the second launch's.
+struct SscCost {
+  double share, again, part, launch, start;
+};
+inline double ssc_waves(long long blocks, int resident, double share) {
+  const long long most = resident * kSscSms, rest = blocks % most;
+  const double all = 1 + share * (resident - 1), last = rest ? 1 + share * (double)((rest - 1) / kSscSms) : 0;
+  return (double)(blocks / most) * all + last;
+}
+// The split that costs least, of those whose blocks are one to 16 for each SM: parts of 2 tiles at least, and
+// not so many that the way through the parts before one becomes as long as a part.
+// units: blocks, where a row is one part; two waves of them fill the device anyway.
+inline SscSplit ssc_best_split(long long tiles, long long units, int resident, const SscCost& c, double& cost) {
+  SscSplit best = {1, tiles};
+  cost = ((double)tiles + c.start) * ssc_waves(units, resident, c.share);
+  if (tiles < 8 || units >= 2 * resident * kSscSms) return best;
+  const long long root = (long long)sqrt(8.0 * (double)tiles), most = root < tiles / 2 ? root : tiles / 2;
+  for (long long each_sm = 1, tried = 1; each_sm <= 16 && tried < most; ++each_sm) {
+    const long long fit = each_sm * kSscSms / units, p = fit < most ? fit : most;
+    if (p <= tried) continue;
+    tried = p;
+    const long long each = (tiles + p - 1) / p, parts = (tiles + each - 1) / each;
+    const double waves = ssc_waves(units * parts, resident, c.share) + c.again * ssc_waves(units * (parts - 1), resident, c.share);
+    const double x = ((double)each + c.start) * waves + c.part * (double)parts + c.launch;
+    if (x < cost) cost = x, best = {parts, each};
+  }
+  return best;
+}
+// The gradient: a block takes 64 channels.  (bf16, us: 7 x 2048 x 1024, 16 states, 112 blocks, one part 621, 2
+// 519, 8 400; 8 x 2048 x 2048, 256 blocks, one 825, in 4 parts 898; 4 x 1024 x 2048, 128 states, of which a
+// block fills an SM, one part 2979, 8 3392.)
+inline SscSplit ssc_backward_split(long long B, long long T, long long D, long long N, long long G, int es) {
+  const int NB = (int)((N + 15) / 16);
   const long long units = B * G * ((D / G + kSscChannels - 1) / kSscChannels);
-  return ssc_parts((T + kSscTile - 1) / kSscTile, units >= 220 ? 1 : (units < 128 ? 1 : 4) * 304 / units);
+  double cost;
+  return ssc_best_split((T + kSscTile - 1) / kSscTile, units, ssc_resident(ssc_backward_bytes(es, NB), 2),
+                        {0.3, 0.25, 0.05, 2.0 / NB, 0.5}, cost);
 }
 
-// Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 /
-// lanes channels each; 4 blocks fit an SM.  Where the rows and channels give enough blocks, a row
-// is one chain (more parts cost a second pass over all parts but the last: 16 x 1024 x 2048 bf16,
-// gated, 256 blocks: 211 us, in 4 parts 252).  Else it is split until the device is full (8 x 2048
-// x 2048, 128 blocks: 313 us, in 4 parts 276), or, from 64 blocks on, twice over, by parts of the
-// same length where there are some (in 8 256, in 9 270; 4 x 2048 x 2048 315, in 9 parts 152, in 16
-// 150); fewer blocks once (1 x 32768 x 2048, 16 blocks: in 32 596, in 38 510), with 4 lanes where 2
-// cannot fill it (1 x 2048 x 1024, 16 parts: 49 us, with 4 lanes 43).
+// Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 / lanes
+// channels each.  (bf16, us: 8 x 2048 x 2048, 16 states, 128 blocks, one part 305, 2 317, 4 287, 8 266; 12 x
+// 1024 x 2048, 32 states, 384 blocks, one 373, 4 535; 4 x 1024 x 2048, 128 states, of which a block fills an SM,
+// one 696, 8 1049, 16 1337.)  A tile takes 4 lanes 0.72 of the time that it takes 2, for half the channels; more than 16
+// states are always 4 lanes', and so are rows that are read value by value (2 lanes take twice as long there:
+// 1 x 2048 x 1023, 13 states, bf16 in 32 parts 78 us, with 4 lanes 57; 8 x 1024 x 2047 in 2 parts 375 and 270).
 struct SscForwardPlan {
   SscSplit split;
   int lanes;
 };
-inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, long long G) {
+inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, long long N, long long G, int es, bool singles) {
   const long long tiles = (T + kSscTile - 1) / kSscTile;
+  const int NB = (int)((N + 15) / 16);
+  const SscCost c = {0.25, 0.8, 0.1, 2.0 / NB, 1.25};
   const auto blocks = [&](int lanes) {
     const long long width = 64 / lanes;
     return (B * G * ((D / G + width - 1) / width) + 3) / 4;
   };
-  int lanes = 2;
-  long long parts = 1;
-  if (blocks(2) < 220) {
-    if (blocks(2) * ssc_most_parts(tiles) < 456) lanes = 4;
-    parts = 608 / blocks(lanes);
-    if (blocks(2) >= 64) {
-      const long long twice = 1216 / blocks(2);
-      for (parts = twice; tiles % parts != 0 && 4 * parts > 3 * twice;) --parts;
-      if (tiles % parts != 0) parts = twice;
-    }
-  }
-  return {ssc_parts(tiles, parts), lanes};
+  double cost, cost2;
+  const SscForwardPlan four = {ssc_best_split(tiles, blocks(4), ssc_resident(ssc_forward_bytes(es, 4, NB), NB > 1 ? 3 : 4), c, cost), 4};
+  if (NB > 1 || singles) return four;
+  const SscForwardPlan two = {ssc_best_split(tiles, blocks(2), 4, c, cost2), 2};
+  return 0.72 * cost < cost2 ? four : two;
 }
-inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, bool backward) {
-  const SscSplit s = backward ? ssc_backward_split(B, T, D, G) : ssc_forward_plan(B, T, D, G).split;
-  size_t floats = (size_t)B * (s.parts - 1) * (D * N + D + 1);
+// Parts that scratch has to hold: of values of es bytes however the rows lie, or (es = 0) of any type.
+inline long long ssc_most_parts(long long B, long long T, long long D, long long N, long long G, int es, bool backward) {
+  if (es == 0) {
+    const long long two = ssc_most_parts(B, T, D, N, G, 2, backward), four = ssc_most_parts(B, T, D, N, G, 4, backward);
+    return two > four ? two : four;
+  }
+  if (backward) return ssc_backward_split(B, T, D, N, G, es).parts;
+  const long long a = ssc_forward_plan(B, T, D, N, G, es, false).split.parts, b = N <= 16 && es == 2 ? ssc_forward_plan(B, T, D, N, G, es, true).split.parts : a;
+  return a > b ? a : b;
+}
+inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, int es, bool backward) {
+  const long long parts = ssc_most_parts(B, T, D, N, G, es, backward);
+  size_t floats = (size_t)B * (parts - 1) * (D * N + D + 1);
   if (backward) {
-    floats += (size_t)B * s.parts * D * (N + 2);
+    floats += (size_t)B * parts * D * (N + 2);
     floats += 2 * (size_t)((D / G + kSscChannels - 1) / kSscChannels) * B * T * G * N;
   }
   return round_up(floats * sizeof(float), 256);

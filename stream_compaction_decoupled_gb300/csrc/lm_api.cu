@@ -396,7 +396,7 @@ int gb_causal_conv_step(int dtype, int param_dtype, int64_t batch, int64_t chann
 size_t gb_selective_scan_temp_bytes(int64_t batch, int64_t length, int64_t channels, int64_t states, int64_t groups,
                                     int backward) {
   if (batch <= 0 || channels <= 0 || check_ssc(GB_F32, batch, length, channels, states, groups, 0)) return 0;
-  return gbs::ssc_temp_bytes(batch, length, channels, states, groups, backward != 0);
+  return gbs::ssc_temp_bytes(batch, length, channels, states, groups, 0, backward != 0);
 }
 
 int gb_selective_scan(int dtype, int64_t batch, int64_t length, int64_t channels, int64_t states, int64_t group_count,
@@ -423,7 +423,7 @@ int gb_selective_scan(int dtype, int64_t batch, int64_t length, int64_t channels
   LaunchCtx ctx;
   rc = gbs::abi_ctx(stream, ctx);
   if (rc) return rc;
-  const size_t need = gbs::ssc_temp_bytes(batch, length, channels, states, group_count, false);
+  const size_t need = gbs::ssc_temp_bytes(batch, length, channels, states, group_count, (int)es, false);
   gbs::Temp t;
   if (need) {
     rc = gbs::abi_temp(temp, temp_bytes, need, ctx.stream, t);
@@ -470,7 +470,7 @@ int gb_selective_scan_backward(int dtype, int64_t batch, int64_t length, int64_t
     return finish(e);
   }
   gbs::Temp t;
-  rc = gbs::abi_temp(temp, temp_bytes, gbs::ssc_temp_bytes(batch, length, channels, states, group_count, true),
+  rc = gbs::abi_temp(temp, temp_bytes, gbs::ssc_temp_bytes(batch, length, channels, states, group_count, (int)es, true),
                      ctx.stream, t);
   if (rc) return rc;
   j.temp = t.p;

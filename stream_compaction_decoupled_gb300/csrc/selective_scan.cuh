@@ -241,7 +241,7 @@ template <int KIND> using SscKind = std::integral_constant<int, KIND>;
 // bf16, 8 states: 269 -> 276 us).  Not in ENDS, which stores nothing of the states past the last.
 // ENDS: only the states that the part ends with, from a state of zero, and its sum of D.
 template <class T, SscMode MODE, bool ONE, bool ENDS, bool PADDED, int LN>
-__global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && LN == 2) ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
+__global__ void __launch_bounds__(kSscThreads, ONE ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
   using S = SscLane<T, MODE, LN>;
   using P = typename S::P;
@@ -1537,6 +1537,7 @@ template <class T, SscMode MODE, bool ONE, int LN> cudaError_t ssc_forward(const
   const auto grid = [&](long long parts) { return (units * parts + kSscThreads / 32 - 1) / (kSscThreads / 32); };
   using S = SscLane<T, MODE, LN>;
   const int NB = ONE ? 1 : a.NP / 16;
+  static_assert(4 * S::warp_bytes(1) == ssc_forward_bytes(sizeof(T), LN, 1) && 4 * S::warp_bytes(8) == ssc_forward_bytes(sizeof(T), LN, 8), "planned with");
   const size_t smem = (size_t)(kSscThreads / 32) * S::warp_bytes(NB);
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
@@ -1549,12 +1550,13 @@ template <class T, SscMode MODE, bool ONE, int LN> cudaError_t ssc_forward(const
 }
 
 template <class T, SscMode MODE, bool ONE> cudaError_t ssc_backward(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.G);
+  const SscSplit split = ssc_backward_split(j.B, j.T, j.D, j.N, j.G, sizeof(T));
   const SscArgs<T> a = ssc_args<T>(j, split);
   const long long units = j.B * a.G * a.blocks;
   profile_before(ctx);
   cudaError_t e = cudaSuccess;
   using S = SscBack<T, MODE>;
+  static_assert(S::bytes(1, false) == ssc_backward_bytes(sizeof(T), 1) && S::bytes(8, false) == ssc_backward_bytes(sizeof(T), 8), "planned with");
   if (split.parts > 1)
     e = ssc_launch(ssc_backward_kernel<T, MODE, ONE, true>, units * (split.parts - 1), S::bytes(a.NP / 16, true), a, ctx);
   if (e == cudaSuccess)
@@ -1577,9 +1579,12 @@ template <class T, SscMode MODE, bool ONE> cudaError_t ssc_backward(const Select
 }
 
 template <class T, SscMode MODE> cudaError_t ssc_forward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
-  const SscForwardPlan plan = ssc_forward_plan(j.B, j.T, j.D, j.G);
+  const SscForwardPlan plan = ssc_forward_plan(j.B, j.T, j.D, j.N, j.G, sizeof(T), MODE == kSscSingles);
   if (j.N > 16) return ssc_forward<T, MODE, false, 4>(j, plan, ctx);
-  return plan.lanes == 2 ? ssc_forward<T, MODE, true, 2>(j, plan, ctx) : ssc_forward<T, MODE, true, 4>(j, plan, ctx);
+  if constexpr (MODE != kSscSingles) {
+    if (plan.lanes == 2) return ssc_forward<T, MODE, true, 2>(j, plan, ctx);
+  }
+  return ssc_forward<T, MODE, true, 4>(j, plan, ctx);
 }
 // Whether what is read starts in pieces of V values; written: of a pair.
 template <class T> bool ssc_pieces(const SelectiveScanJob& j, int V, std::initializer_list<const SeqArray*> read,
