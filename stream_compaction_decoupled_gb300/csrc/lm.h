@@ -218,11 +218,13 @@ inline SscSplit ssc_backward_split(long long B, long long T, long long D, long l
 }
 
 // Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 / lanes
-// channels each.  (bf16, us: 8 x 2048 x 2048, 16 states, 128 blocks, one part 305, 2 317, 4 287, 8 266; 12 x
-// 1024 x 2048, 32 states, 384 blocks, one 373, 4 535; 4 x 1024 x 2048, 128 states, of which a block fills an SM,
-// one 696, 8 1049, 16 1337.)  A tile takes 4 lanes 0.72 of the time that it takes 2, for half the channels; more than 16
-// states are always 4 lanes', and so are rows that are read value by value (2 lanes take twice as long there:
-// 1 x 2048 x 1023, 13 states, bf16 in 32 parts 78 us, with 4 lanes 57; 8 x 1024 x 2047 in 2 parts 375 and 270).
+// channels each.  (bf16, us: 8 x 2048 x 2048, 16 states, 128 blocks, one part 305, 2 317, 4 287, 8 266;
+// 12 x 1024 x 2048, 32 states, 384 blocks, one 373, 4 535; 4 x 1024 x 2048, 128 states, of which a block
+// fills an SM, one 696, 8 1049, 16 1337.)  A tile takes 4 lanes 0.72 of the time that it takes 2, for half
+// the channels; more than 16 states are always 4 lanes'.  Rows that are read value by value wait more than
+// they compute, so that blocks hardly slow each other, and 4 lanes take 0.57 (bf16, 13 states, us:
+// 1 x 2048 x 1023, one part, 2 lanes 958, 4 551; 8 x 2048 x 2047, 2 lanes in 8 parts 547, 4 in 2 500;
+// 24 x 1024 x 2047, one part, 549 and 618).
 struct SscForwardPlan {
   SscSplit split;
   int lanes;
@@ -230,16 +232,16 @@ struct SscForwardPlan {
 inline SscForwardPlan ssc_forward_plan(long long B, long long T, long long D, long long N, long long G, int es, bool singles) {
   const long long tiles = (T + kSscTile - 1) / kSscTile;
   const int NB = (int)((N + 15) / 16);
-  const SscCost c = {0.25, 0.8, 0.1, 2.0 / NB, 1.25};
+  const SscCost c = singles ? SscCost{0.05, 0.7, 0.15, 2.0 / NB, 0} : SscCost{0.25, 0.8, 0.1, 2.0 / NB, 1.25};
   const auto blocks = [&](int lanes) {
     const long long width = 64 / lanes;
     return (B * G * ((D / G + width - 1) / width) + 3) / 4;
   };
   double cost, cost2;
   const SscForwardPlan four = {ssc_best_split(tiles, blocks(4), ssc_resident(ssc_forward_bytes(es, 4, NB), NB > 1 ? 3 : 4), c, cost), 4};
-  if (NB > 1 || singles) return four;
-  const SscForwardPlan two = {ssc_best_split(tiles, blocks(2), 4, c, cost2), 2};
-  return 0.72 * cost < cost2 ? four : two;
+  if (NB > 1) return four;
+  const SscForwardPlan two = {ssc_best_split(tiles, blocks(2), singles ? 3 : 4, c, cost2), 2};
+  return (singles ? 0.57 : 0.72) * cost < cost2 ? four : two;
 }
 // Parts that scratch has to hold: of values of es bytes however the rows lie, or (es = 0) of any type.
 inline long long ssc_most_parts(long long B, long long T, long long D, long long N, long long G, int es, bool backward) {
@@ -248,7 +250,8 @@ inline long long ssc_most_parts(long long B, long long T, long long D, long long
     return two > four ? two : four;
   }
   if (backward) return ssc_backward_split(B, T, D, N, G, es).parts;
-  const long long a = ssc_forward_plan(B, T, D, N, G, es, false).split.parts, b = N <= 16 && es == 2 ? ssc_forward_plan(B, T, D, N, G, es, true).split.parts : a;
+  const long long a = ssc_forward_plan(B, T, D, N, G, es, false).split.parts;
+  const long long b = es == 2 ? ssc_forward_plan(B, T, D, N, G, es, true).split.parts : a;
   return a > b ? a : b;
 }
 inline size_t ssc_temp_bytes(long long B, long long T, long long D, long long N, long long G, int es, bool backward) {

@@ -67,7 +67,7 @@ template <class T> struct SscArgs {
 // How rows are read: by asynchronous copies of 16 bytes (WHOLE), of 4 (WORDS: any fp32 rows, and
 // 16-bit ones with even widths, strides and counts of states on 4-byte boundaries), or value by value
 // through registers (SINGLES, 16 bits only).  8 x 2048 tokens, 16 states, WORDS and SINGLES: 2046
-// channels bf16 295 and 547 us, the gradient 864 and 1235; 4 x 2048 x 2001 fp32 205 and 252, 552 and 589.
+// channels bf16 310 and 515 us, the gradient 870 and 1211; 4 x 2048 x 2001 fp32 212 and 252, 544 and 589.
 enum SscMode { kSscWhole, kSscWords, kSscSingles };
 
 // Two neighbouring channels of a row, as they lie in memory.
@@ -241,7 +241,7 @@ template <int KIND> using SscKind = std::integral_constant<int, KIND>;
 // bf16, 8 states: 269 -> 276 us).  Not in ENDS, which stores nothing of the states past the last.
 // ENDS: only the states that the part ends with, from a state of zero, and its sum of D.
 template <class T, SscMode MODE, bool ONE, bool ENDS, bool PADDED, int LN>
-__global__ void __launch_bounds__(kSscThreads, ONE ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
+__global__ void __launch_bounds__(kSscThreads, ONE && !(MODE == kSscSingles && LN == 2) ? 4 : 3) ssc_forward_kernel(const __grid_constant__ SscArgs<T> a) {
   pdl_entry();
   using S = SscLane<T, MODE, LN>;
   using P = typename S::P;
@@ -1581,10 +1581,7 @@ template <class T, SscMode MODE, bool ONE> cudaError_t ssc_backward(const Select
 template <class T, SscMode MODE> cudaError_t ssc_forward_any(const SelectiveScanJob& j, const LaunchCtx& ctx) {
   const SscForwardPlan plan = ssc_forward_plan(j.B, j.T, j.D, j.N, j.G, sizeof(T), MODE == kSscSingles);
   if (j.N > 16) return ssc_forward<T, MODE, false, 4>(j, plan, ctx);
-  if constexpr (MODE != kSscSingles) {
-    if (plan.lanes == 2) return ssc_forward<T, MODE, true, 2>(j, plan, ctx);
-  }
-  return ssc_forward<T, MODE, true, 4>(j, plan, ctx);
+  return plan.lanes == 2 ? ssc_forward<T, MODE, true, 2>(j, plan, ctx) : ssc_forward<T, MODE, true, 4>(j, plan, ctx);
 }
 // Whether what is read starts in pieces of V values; written: of a pair.
 template <class T> bool ssc_pieces(const SelectiveScanJob& j, int V, std::initializer_list<const SeqArray*> read,

@@ -71,7 +71,7 @@ def test_parts_hold_all_tiles_and_the_scratch_all_parts(ask):
         for es, row in by.items():
             for parts, each in (row[0:2], row[3:5], row[6:8]):
                 assert parts >= 1 and parts * each >= tiles and (parts == 1 or ((parts - 1) * each < tiles and each >= 2))
-            assert row[2] in (2, 4) and row[5] == 4 and (n <= 16 or row[2] == 4)
+            assert {row[2], row[5]} <= {2, 4} and (n <= 16 or row[2] == row[5] == 4)
             for parts in (row[0], row[3]) if es == 2 else (row[0],):
                 assert row[8] >= 4 * b * (parts - 1) * (d * n + d + 1)
             assert any_type[0] >= row[8] and any_type[1] >= row[9]
