@@ -545,7 +545,8 @@ int gb_causal_conv_step(int dtype, int param_dtype, int64_t batch, int64_t chann
  *   y_t = (sum over states of c_t h_t + d x_t) z_t sigmoid(z_t), without the last factor
  *   where z is NULL.
  * b and c are (batch, length, groups, states); channel k uses group k / (channels / groups).
- *   a             (channels, states) fp32, contiguous
+ *   a             (channels, states) fp32, contiguous; below -2.3e38 as -infinity, with which a
+ *                 state keeps nothing (D_t > 0)
  *   d, dt_bias    (channels) fp32, or NULL: 0
  *   strides       host array: (batch, time) of x, dt, z, y, then (batch, time, group) of b, c;
  *                 or NULL: contiguous
@@ -577,6 +578,7 @@ size_t gb_selective_scan_temp_bytes(int64_t batch, int64_t length, int64_t chann
  *   da        (channels, states) fp32; dd, ddt_bias (channels) fp32 or NULL: not written
  *   dh0       (batch, channels, states) fp32, contiguous, or NULL: the gradient of h0
  *   temp      scratch of gb_selective_scan_temp_bytes(..., 1) bytes, 256-byte aligned, or NULL
+ * Where a is -infinity ddt is NaN: it has the product of a and a decay of 0.
  */
 int gb_selective_scan_backward(int dtype, int64_t batch, int64_t length, int64_t channels, int64_t states,
                                int64_t groups, const void* dy, const void* x, const void* dt, const float* a,
@@ -616,8 +618,9 @@ int gb_selective_scan_step(int dtype, int64_t batch, int64_t channels, int64_t s
  *   out           (batch, drafts + 1) int32, contiguous: the n accepted drafts, the token drawn,
  *                 and -1 behind it
  * Probabilities need not sum to 1; negative ones and NaNs count as 0 (with an infinite one it is
- * not said which token is drawn).  Where r is 0 everywhere the token is -1.  A length outside 0 .. drafts is taken as the nearest within, a draft outside
- * the vocabulary is not accepted; both are reported as GB_ERR_RANGE by gb_device_error.
+ * not said which token is drawn).  Where r is 0 everywhere the token is -1.  A length outside
+ * 0 .. drafts is taken as the nearest within, a draft outside the vocabulary is not accepted; both
+ * are reported as GB_ERR_RANGE by gb_device_error.
  */
 int gb_verify_drafts(int dtype, int64_t batch, int64_t drafts, int64_t vocab, const void* tokens, int token_dtype,
                      const void* target, const void* draft, const int64_t* strides, const float* accept,

@@ -25,17 +25,21 @@
 // The gradient: a block of 4 warps takes 64 channels and tiles of 16 tokens, from the last to the
 // first; a warp 16 channels, 4 lanes a pair of channels and 4 states of both a lane.  A tile's states
 // are computed again from the one kept before it.  The warps meet twice a tile, for B and C and for
-// the sums over channels.  Issue and shared memory bound it about equally: of some 236 instructions
-// and 58 passes a token and warp, 8 passes bring D, D x, B and C forward and 6 C and e back, 12 and
+// the sums over channels.  Issue and shared memory bound it about equally: of some 240 instructions
+// and 53 passes a token and warp, 8 passes bring D, D x, B and C forward and 6 C and e back, 12 and
 // 8 instructions are the lanes' parts of the sums over states, 7 and 28 the sums over channels.
 //
 // The tokens of a row are one chain.  Where the rows and channels are too few for the device,
 // they are split into parts: a first kernel finds what each part makes of a state of zero, and
 // with exp(A sum D) each part knows where it starts (the gradient: from the other end).
 //
+// The states and channels of a full tile that do not exist, and its tokens behind the last, keep zeros
+// beside finite inputs.  Beside an infinity they would be NaNs, so that tiles with one are gone through with
+// those places put back to 0, and tokens behind the last are left out.
+//
 // Measured (GB300, cold caches): 8 x 2048 x 2048, 16 states, bf16, gated, with starts and kept
-// states 274 us (0.7 instructions a cycle and scheduler, an eighth of the copy rate), its gradient
-// 823 us (0.55, and 0.56 of shared memory's cycles); 1 x 32768 x 2048 continued 536 us; one
+// states 274 us (0.7 instructions a cycle and scheduler, 0.15 of the copy rate), its gradient
+// 829 us (0.56, and half of shared memory's cycles); 1 x 32768 x 2048 continued 534 us; one
 // token, 64 x 4096, 17.5 us.
 #pragma once
 
@@ -182,7 +186,7 @@ template <class T> struct SscWarp {
   }
 };
 
-// M values of two channels of a (D, N) array, in pairs of states; `other` where there are none.
+// M values of two channels of a (D, N) array, in pairs of states; 0 where there are none.
 template <int M, bool VEC> __device__ __forceinline__ void ssc_load_states(const float* p, int n0, int N, int count, float2 (&v)[2][M / 2]) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -1359,7 +1363,8 @@ template <class T> struct SscStepArgs {
 // Four lanes a channel, four neighbouring states of each 16 a lane (VEC: as one access of 16
 // bytes, and B and C as one of four values).  ROWS = 4: four rows, which share the channel's A and
 // keep more loads in flight; what is done once a row and channel is done by one lane for each row.
-// 64 rows x 4096 channels x 16 states bf16: bound by issue and by the latency of its one pass.
+// 64 rows x 4096 channels x 16 states bf16: 14.3 us of the device, 5.3 of bytes; the latency of one pass from the
+// slot to the state and back, at the 512 threads an SM that 126 registers leave (0.37 instructions a cycle).
 template <class T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(128) ssc_step_kernel(const __grid_constant__ SscStepArgs<T> a) {
   static_assert(ROWS == 1 || ROWS == 4, "a row a lane, or one row");
