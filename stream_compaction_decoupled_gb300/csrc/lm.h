@@ -218,7 +218,7 @@ inline SscSplit ssc_backward_split(long long B, long long T, long long D, long l
 }
 
 // Forward: parts of the tokens, and lanes that share two channels.  A block's 4 warps take 64 / lanes
-// channels each.  (bf16, us: 8 x 2048 x 2048, 16 states, 128 blocks, one part 305, 2 317, 4 287, 8 266;
+// channels each.  (bf16, no kept states, us: 8 x 2048 x 2048 x 16, 128 blocks, one part 305, 4 287, 8 266;
 // 12 x 1024 x 2048, 32 states, 384 blocks, one 373, 4 535; 4 x 1024 x 2048, 128 states, of which a block
 // fills an SM, one 696, 8 1049, 16 1337.)  A tile takes 4 lanes 0.72 of the time that it takes 2, for half
 // the channels; more than 16 states are always 4 lanes'.  Rows that are read value by value wait more than
