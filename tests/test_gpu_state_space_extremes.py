@@ -145,3 +145,29 @@ def test_gradient_with_channels_past_the_last(size, where, at, dt):
     q, more, dy, dlast = inputs(t, d, n, scan.DT[dt], sum(size))
     q[where][0, at] = INF
     check_gradient(q, more, dy, dlast)
+
+
+@pytest.mark.parametrize("dt", list(scan.DT))
+@pytest.mark.parametrize("size", [(21, 24, 13), (40, 10, 16), (40, 66, 40), (300, 34, 6), (300, 64, 16)], ids=str)
+def test_infinities_of_one_document_among_others(size, dt):
+    """Two rows, two groups of channels; an infinite input in one row's first document, dropped by the
+    next document's start, in the same tile or in another."""
+    t, d, n = size
+    q, _, dy, _ = inputs(2 * t, d, 2 * n, scan.DT[dt], sum(size))
+    q = {k: v.unflatten(1, (2, t)).squeeze(0) if k in ("x", "dt", "z", "b", "c") else v for k, v in q.items()}
+    q["b"], q["c"] = (q[k].squeeze(2).unflatten(-1, (2, n)) for k in ("b", "c"))
+    q["a"] = q["a"][:, :n].contiguous()
+    dy = dy.unflatten(1, (2, t)).squeeze(0)
+    starts = torch.zeros((2, t), dtype=torch.uint8, device="cuda")
+    starts[:, 9] = starts[0, t - 2] = starts[1, 0] = 1
+    q["x"][1, 5, ::2] = INF
+    more = {"h0": None, "starts": starts}
+    y, last, kept = gb.selective_scan(**q, **more, keep=True)
+    want, wlast, bound, blast = ref.scan(**q, **more)
+    lm.check(y, want, bound, "y")
+    lm.check(last, wlast, blast, "last")
+    assert (y[1, 5:9, ::2] == INF).all() and torch.isfinite(y[1, 9:]).all() and torch.isfinite(last).all()
+    got = gb.selective_scan_backward(dy, **q, kept=kept, starts=starts)
+    wants, bounds = ref.scan_grad(dy, **q, **more, dlast=None)
+    for name, v, w, e in zip(scan.NAMES, got, wants, bounds):
+        lm.check(v, w, e, name)
