@@ -167,7 +167,7 @@ constexpr size_t ssc_forward_bytes(int es, int lanes, int NB) {
                       (NB > 1 ? NB * 16 / lanes * 256 : 0));
 }
 constexpr size_t ssc_backward_bytes(int es, int NB) {
-  return 4 * (size_t)(2 * (4 * 16 * 16 * es + 1024) + 2048 + 1024 + 3072 + 3072 + 2048 + (NB > 1 ? NB * 2048 : 0)) +
+  return 4 * (size_t)(2 * (4 * 16 * 16 * es + 1024) + 2048 + 1024 + 2 * 3 * 1024 + 2048 + (NB > 1 ? NB * 2048 : 0)) +
          2 * 16 * 32 * es + NB * 2048;
 }
 // Blocks an SM holds: by registers `bound`, by shared memory what goes into 228 KB (with 1 KB a block of
